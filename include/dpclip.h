@@ -423,6 +423,143 @@ dp_status dp_unfold2d(void* stream, const void* a, const dp_conv2d* conv, dp_dty
 size_t dp_conv_workspace_bytes(const dp_conv2d* conv, dp_dtype dtype, int64_t B, int64_t p, int32_t has_bias,
                                dp_mode mode, int32_t kappa);
 
+/*
+ * Root-mean-square norm with the residual's addition, over the last dimension:
+ *
+ *   s = x + residual      u = s / sqrt(mean(s^2) + eps)      out = u * gain
+ *
+ * in fp32, each output rounded once to dtype (out is formed from the sum
+ * before its rounding to dtype). A row of zeros gives zeros when eps > 0.
+ *
+ *  x, residual  [rows, d], dtype; residual may be NULL (s = x).
+ *  gain         [d], gain_dtype (DP_F32 or DP_BF16).
+ *  d            1 <= d <= 32768.
+ *  eps          finite, >= 0.
+ *  out          [rows, d], dtype; may be x or residual.
+ *  sum_out      [rows, d], dtype: s (what the backward pass reads); may be
+ *               NULL, x or residual, not out.
+ * Tensors aligned to their element; rows are read 16 bytes at a time when d
+ * is a multiple of 16 bytes and every tensor is 16-byte aligned.
+ */
+dp_status dp_rms_norm(void* stream, const void* x, const void* residual, const void* gain, dp_dtype dtype,
+                      dp_dtype gain_dtype, int64_t rows, int64_t d, float eps, void* out, void* sum_out);
+
+/*
+ * Its backward pass, with the gain's gradient of every sample (what the
+ * per-sample clipping takes: a gain layer is the linear layer A = 1 [B, 1, 1],
+ * G = gain_rows [B, 1, d] of dp_ghost_norm and dp_clipped_sum_noise):
+ *
+ *   h = dy * gain      dx = dsum + (h - u * mean(h * u)) / sqrt(mean(s^2) + eps)
+ *   gain_rows[b] = sum_t dy[b][t] * u[b][t]
+ *
+ *  dy, s, dsum  [B, T, d], dtype. s: the forward's sum; dsum: the gradient
+ *               that reaches s past the norm (the residual stream), or NULL.
+ *  dx           [B, T, d], dtype, or NULL: the gradient of x and of residual;
+ *               may be dy or dsum.
+ *  gain_rows    [B, d] fp32, or NULL. dx and gain_rows are not both NULL.
+ *  workspace    at least dp_rms_norm_workspace_bytes(...) bytes when gain_rows
+ *               is not NULL (partial sums of samples spread over workgroups).
+ */
+dp_status dp_rms_norm_backward(void* stream, const void* dy, const void* s, const void* dsum, const void* gain,
+                               dp_dtype dtype, dp_dtype gain_dtype, int64_t B, int64_t T, int64_t d, float eps,
+                               void* workspace, size_t ws_bytes, void* dx, float* gain_rows);
+size_t dp_rms_norm_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t d);
+
+/*
+ * Distillation loss from a teacher's top logits, one value per sample:
+ *
+ *   loss[b] = tau^2 * sum_t weight[b][t] * sum_k q_k (log q_k - log p_{ids_k})
+ *
+ * with p = softmax(logits[b][t] / tau) over the V words and q the softmax of
+ * the token's used teacher logits / tau. Place k of a token is used when
+ * 0 <= ids < V and its teacher logit is not -inf; places naming the same word
+ * add up. A token without a used place, or with weight 0, adds 0 whatever its
+ * logits hold.
+ *
+ *  logits   [B, T, V], dtype, 16-byte aligned.
+ *  ids      [B, T, K] int64; teacher [B, T, K], dtype. 1 <= K <= 2048.
+ *  tau      temperature, finite, > 0.
+ *  weight   [B, T] fp32, or NULL (1 everywhere).
+ *  loss     [B] fp32.
+ *  lse      [B, T] fp32: log sum_j exp(logits_j / tau), for the backward pass.
+ *  workspace  at least dp_distill_workspace_bytes(...) bytes.
+ */
+dp_status dp_distill_loss(void* stream, const void* logits, const int64_t* ids, const void* teacher, dp_dtype dtype,
+                          int64_t B, int64_t T, int64_t V, int64_t K, float tau, const float* weight,
+                          void* workspace, size_t ws_bytes, float* loss, float* lse);
+
+/*
+ * Its gradient, the output gradient G of the layer that made the logits:
+ *
+ *   grad[b][t][j] = dloss[b] * weight[b][t] * tau * (p_j - sum_{k: ids_k = j} q_k)
+ *
+ *  lse      as dp_distill_loss left it.
+ *  dloss    [B] fp32, or NULL (1 everywhere: the summed per-sample losses).
+ *  grad     [B, T, V], dtype, 16-byte aligned; may be logits.
+ */
+dp_status dp_distill_loss_backward(void* stream, const void* logits, const int64_t* ids, const void* teacher,
+                                   dp_dtype dtype, int64_t B, int64_t T, int64_t V, int64_t K, float tau,
+                                   const float* weight, const float* dloss, const float* lse, void* grad);
+size_t dp_distill_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t V, int64_t K);
+
+/*
+ * Products grouped by expert, with ragged sizes. R rows are sorted by expert
+ * and, within an expert, by sample; `segments` (device memory, [E*B + 1]
+ * int64, ascending, at most R) holds the row ranges: sample b's rows in
+ * expert e are [segments[e*B + b], segments[e*B + b + 1]). Any range may be
+ * empty. Rows before segments[0] and from segments[E*B] on belong to no
+ * expert: they are not read, and output rows there are left as they were. The
+ * sizes are only read on the device, so a call does not wait for them.
+ *
+ * dp_grouped_matmul, for expert weights W [E, p, d] (a torch Linear's layout
+ * per expert) and the rows r of expert e:
+ *   transpose == 0:  Y[r] = W_e X[r]       X [R, d], Y [R, p]   (forward)
+ *   transpose != 0:  Y[r] = W_e^T X[r]     X [R, p], Y [R, d]   (gradient of the rows)
+ *
+ *  X, W, Y, dtype  one number type, 16-byte aligned; fp32 accumulation, one
+ *           rounding. Y overlaps neither X nor W.
+ *  R, E, B, d, p  1 <= d, p <= 2^20; R and E*B below 2^31.
+ *  workspace  at least dp_grouped_workspace_bytes(...) bytes (may be NULL when
+ *           that is 0).
+ */
+dp_status dp_grouped_matmul(void* stream, const void* X, const void* W, dp_dtype dtype, const int64_t* segments,
+                            int64_t R, int64_t E, int64_t B, int64_t d, int64_t p, int32_t transpose, void* workspace,
+                            size_t ws_bytes, void* Y);
+
+/*
+ * Per-sample squared gradient norms of an expert layer, over all its experts:
+ * sqnorm[b] (+)= sum_e || sum_{r in (e, b)} A_r G_r^T ||_F^2, by the ghost
+ * identity of dp_ghost_norm on each (expert, sample) range.
+ *
+ *  A [R, d] rows that entered the experts, G [R, p] output gradients.
+ *  sqnorm   [B] fp32, overwritten (accumulate == 0) or added to.
+ */
+dp_status dp_grouped_norm(void* stream, const void* A, const void* G, dp_dtype dtype, const int64_t* segments,
+                          int64_t R, int64_t E, int64_t B, int64_t d, int64_t p, void* workspace, size_t ws_bytes,
+                          float* sqnorm, int32_t accumulate);
+
+/*
+ * Clipped, noised mean gradients of an expert layer:
+ *
+ *   out[e] = (sum_b c[b] * sum_{r in (e, b)} A_r G_r^T + (sigma*C) * z_e) * (1/denom)
+ *
+ * as dp_clipped_sum_noise forms it for one layer; an expert without rows gets
+ * the noise alone. The noise is that of a layer of E*d rows: z_e[m][n] is
+ * element (e*d + m, n) of dp_clipped_sum_noise's z_w. ceil(E*d/4)*p < 2^32.
+ *
+ *  A, G, segments, R, E, B, d, p  as in dp_grouped_norm.
+ *  c, C, sigma, denom, seed, layer_id, step  as in dp_clipped_sum_noise.
+ *  out      [E, d, p] fp32 (per expert the transpose of W_e's gradient).
+ */
+dp_status dp_grouped_clipped_sum_noise(void* stream, const void* A, const void* G, dp_dtype dtype,
+                                       const int64_t* segments, int64_t R, int64_t E, int64_t B, int64_t d, int64_t p,
+                                       const float* c, float C, float sigma, float denom, uint64_t seed,
+                                       uint32_t layer_id, uint32_t step, void* workspace, size_t ws_bytes,
+                                       float* out);
+/* Workspace bytes that the dp_grouped_* calls need for these sizes (the
+ * largest of the three). Returns 0 for invalid arguments. */
+size_t dp_grouped_workspace_bytes(dp_dtype dtype, int64_t R, int64_t E, int64_t B, int64_t d, int64_t p);
+
 /* Workspace bytes that dp_ghost_norm and dp_clipped_sum_noise need for this
  * layer shape (the larger of the two). Returns 0 for invalid arguments. */
 size_t dp_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t d, int64_t p,

@@ -35,6 +35,16 @@ The functions mirror the C ABI in ``include/dpclip.h``:
                               bias_out=None, workspace=None)
     dp_conv_workspace_bytes(conv, dtype, B, p, has_bias=False, mode=MODE_MIXED, kappa=1) -> int
     dp_unfold2d(a, conv, out=None) -> U [B, T, d]
+    dp_rms_norm(x, gain, eps, out, residual=None, sum_out=None)
+    dp_rms_norm_backward(dy, s, gain, eps, dx=None, dsum=None, gain_rows=None, workspace=None)
+    dp_rms_norm_workspace_bytes(dtype, B, T, d) -> int
+    dp_distill_loss(logits, ids, teacher, tau, loss, lse, weight=None, workspace=None)
+    dp_distill_loss_backward(logits, ids, teacher, tau, lse, grad, weight=None, dloss=None)
+    dp_distill_workspace_bytes(dtype, B, T, V, K) -> int
+    dp_grouped_matmul(X, W, segments, out, transpose=False, workspace=None)
+    dp_grouped_norm(A, G, segments, sqnorm, accumulate=False, workspace=None)
+    dp_grouped_clipped_sum_noise(A, G, segments, c, C, sigma, denom, seed, layer_id, step, out, workspace=None)
+    dp_grouped_workspace_bytes(dtype, R, E, B, d, p) -> int
 
 The dp_conv_* calls take a convolution layer's folded input a [B, C_in, H, W]
 and its geometry (``conv_geometry(C_in, H, W, kernel_size, stride, padding,
@@ -64,7 +74,10 @@ EXPORTS = ("dp_ghost_norm", "dp_ghost_norm_layers", "dp_ghost_norm_clip_layers",
            "dp_clip_factors", "dp_clipped_sum_accumulate", "dp_noise_mean", "dp_accumulate_workspace_bytes",
            "dp_clipped_sum_accumulate_layers", "dp_layers_accumulate_workspace_bytes", "dp_clipped_sum_noise", "dp_adaptive_threshold",
            "dp_workspace_bytes", "dp_choose_path", "dp_status_string", "dp_abi_version",
-           "dp_conv_norm", "dp_conv_clipped_sum_noise", "dp_conv_workspace_bytes", "dp_unfold2d")
+           "dp_conv_norm", "dp_conv_clipped_sum_noise", "dp_conv_workspace_bytes", "dp_unfold2d",
+           "dp_rms_norm", "dp_rms_norm_backward", "dp_rms_norm_workspace_bytes",
+           "dp_distill_loss", "dp_distill_loss_backward", "dp_distill_workspace_bytes",
+           "dp_grouped_matmul", "dp_grouped_norm", "dp_grouped_clipped_sum_noise", "dp_grouped_workspace_bytes")
 
 _lib = None
 
@@ -159,6 +172,29 @@ def _declare(lib):
     lib.dp_conv_workspace_bytes.restype = ctypes.c_size_t
     lib.dp_unfold2d.argtypes = [vp, vp, cp, c_i32, c_i64, vp]
     lib.dp_unfold2d.restype = c_i32
+    sz = ctypes.c_size_t
+    lib.dp_rms_norm.argtypes = [vp, vp, vp, vp, c_i32, c_i32, c_i64, c_i64, f, vp, vp]
+    lib.dp_rms_norm.restype = c_i32
+    lib.dp_rms_norm_backward.argtypes = [vp, vp, vp, vp, vp, c_i32, c_i32, c_i64, c_i64, c_i64, f, vp, sz, vp, fp]
+    lib.dp_rms_norm_backward.restype = c_i32
+    lib.dp_rms_norm_workspace_bytes.argtypes = [c_i32, c_i64, c_i64, c_i64]
+    lib.dp_rms_norm_workspace_bytes.restype = sz
+    lib.dp_distill_loss.argtypes = [vp, vp, vp, vp, c_i32, c_i64, c_i64, c_i64, c_i64, f, fp, vp, sz, fp, fp]
+    lib.dp_distill_loss.restype = c_i32
+    lib.dp_distill_loss_backward.argtypes = [vp, vp, vp, vp, c_i32, c_i64, c_i64, c_i64, c_i64, f, fp, fp, fp, vp]
+    lib.dp_distill_loss_backward.restype = c_i32
+    lib.dp_distill_workspace_bytes.argtypes = [c_i32, c_i64, c_i64, c_i64, c_i64]
+    lib.dp_distill_workspace_bytes.restype = sz
+    sizes = [c_i64] * 5
+    lib.dp_grouped_matmul.argtypes = [vp, vp, vp, c_i32, vp, *sizes, c_i32, vp, sz, vp]
+    lib.dp_grouped_matmul.restype = c_i32
+    lib.dp_grouped_norm.argtypes = [vp, vp, vp, c_i32, vp, *sizes, vp, sz, fp, c_i32]
+    lib.dp_grouped_norm.restype = c_i32
+    lib.dp_grouped_clipped_sum_noise.argtypes = [vp, vp, vp, c_i32, vp, *sizes, fp, f, f, f, c_u64, c_u32, c_u32, vp,
+                                                 sz, fp]
+    lib.dp_grouped_clipped_sum_noise.restype = c_i32
+    lib.dp_grouped_workspace_bytes.argtypes = [c_i32, *sizes]
+    lib.dp_grouped_workspace_bytes.restype = sz
     lib.dp_abi_version.argtypes = []
     lib.dp_abi_version.restype = c_i32
     return lib
@@ -593,3 +629,203 @@ def dp_conv_clipped_sum_noise(a, G, conv: DpConv2d, c, C: float, sigma: float, d
         _stream(stream), _ptr(a), _ptr(G), ctypes.byref(conv), dt, B, p, _ptr(c), float(C), float(sigma),
         float(denom), int(seed) & 0xFFFFFFFFFFFFFFFF, int(layer_id) & 0xFFFFFFFF, int(step) & 0xFFFFFFFF, _ptr(ws),
         nbytes, _ptr(out), _ptr(bias_out)))
+
+
+# ---- language-model operators
+
+
+def _lm_tensors(stream, *named):
+    """Checks of the language-model calls' tensors, given as (name, tensor or
+    None, dtypes, shape or None): a contiguous GPU tensor of one of the dtypes
+    and of that shape, on the device that is current and that `stream` belongs
+    to (a launch from another device's context would run on the wrong one)."""
+    import torch
+    current = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t, dtypes, shape in named:
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous GPU tensor")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} must be of dtype {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.device.index != current:
+            raise ValueError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{current}")
+    if stream is not None and stream.device.index != current:
+        raise ValueError(f"stream belongs to cuda:{stream.device.index}, the current device is cuda:{current}")
+
+
+def _act_dtypes(t, name):
+    """The number type of a call, as the only one its other tensors may have."""
+    _dtype_code(t)
+    return (t.dtype,)
+
+
+def _lm_workspace(workspace, nbytes, device, stream):
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0
+        workspace = _scratch(nbytes, device, stream)
+    _lm_tensors(stream, ("workspace", workspace, (workspace.dtype,), None))
+    return workspace, _ws_bytes(workspace)
+
+
+def dp_rms_norm_workspace_bytes(dtype: int, B: int, T: int, d: int) -> int:
+    return int(lib().dp_rms_norm_workspace_bytes(dtype, B, T, d))
+
+
+def dp_rms_norm(x, gain, eps: float, out, residual=None, sum_out=None, stream=None):
+    """out = s / sqrt(mean(s^2) + eps) * gain over the last dimension, s = x
+    (+ residual); s itself into sum_out. gain is float32 or bfloat16."""
+    import torch
+    if x.dim() < 1 or x.numel() < 1:
+        raise ValueError("x must have at least one element")
+    dt = _act_dtypes(x, "x")
+    d = int(x.shape[-1])
+    _lm_tensors(stream, ("x", x, dt, None), ("residual", residual, dt, x.shape), ("out", out, dt, x.shape),
+                ("sum_out", sum_out, dt, x.shape), ("gain", gain, (torch.float32, torch.bfloat16), (d,)))
+    if sum_out is not None and sum_out.data_ptr() == out.data_ptr():
+        raise ValueError("sum_out and out must be different tensors")
+    _check("dp_rms_norm", lib().dp_rms_norm(_stream(stream), _ptr(x), _ptr(residual), _ptr(gain), _dtype_code(x),
+                                            _dtype_code(gain), x.numel() // d, d, float(eps), _ptr(out),
+                                            _ptr(sum_out)))
+
+
+def dp_rms_norm_backward(dy, s, gain, eps: float, dx=None, dsum=None, gain_rows=None, workspace=None, stream=None):
+    """Backward pass of dp_rms_norm from s [B, T, d] (or [B, d]): dx (the
+    gradient of x and of residual, dsum joined in) and gain_rows [B, d], the
+    gain's gradient of every sample; either may be None."""
+    import torch
+    if s.dim() < 2 or s.numel() < 1:
+        raise ValueError("s [B, ..., d] with at least one element expected")
+    dt = _act_dtypes(s, "s")
+    B, d = int(s.shape[0]), int(s.shape[-1])
+    T = s.numel() // (B * d)
+    _lm_tensors(stream, ("s", s, dt, None), ("dy", dy, dt, s.shape), ("dsum", dsum, dt, s.shape),
+                ("dx", dx, dt, s.shape), ("gain", gain, (torch.float32, torch.bfloat16), (d,)),
+                ("gain_rows", gain_rows, (torch.float32,), (B, d)))
+    if dx is None and gain_rows is None:
+        raise ValueError("dx or gain_rows is required")
+    ws, nbytes = _lm_workspace(workspace, dp_rms_norm_workspace_bytes(_dtype_code(s), B, T, d)
+                               if gain_rows is not None else 0, s.device, stream)
+    _check("dp_rms_norm_backward", lib().dp_rms_norm_backward(
+        _stream(stream), _ptr(dy), _ptr(s), _ptr(dsum), _ptr(gain), _dtype_code(s), _dtype_code(gain), B, T, d,
+        float(eps), _ptr(ws), nbytes, _ptr(dx), _ptr(gain_rows)))
+
+
+def dp_distill_workspace_bytes(dtype: int, B: int, T: int, V: int, K: int) -> int:
+    return int(lib().dp_distill_workspace_bytes(dtype, B, T, V, K))
+
+
+def _distill(logits, ids, teacher, weight, stream):
+    import torch
+    if logits.dim() != 3 or ids.dim() != 3 or ids.shape[:2] != logits.shape[:2]:
+        raise ValueError(f"logits [B, T, V] and ids [B, T, K] expected, got {tuple(logits.shape)} and "
+                         f"{tuple(ids.shape)}")
+    dt = _act_dtypes(logits, "logits")
+    B, T, V = (int(v) for v in logits.shape)
+    _lm_tensors(stream, ("logits", logits, dt, None), ("ids", ids, (torch.int64,), None),
+                ("teacher", teacher, dt, ids.shape), ("weight", weight, (torch.float32,), (B, T)))
+    return _dtype_code(logits), B, T, V, int(ids.shape[2])
+
+
+def dp_distill_loss(logits, ids, teacher, tau: float, loss, lse, weight=None, workspace=None, stream=None):
+    """Per-sample distillation loss [B] of logits [B, T, V] from a teacher's
+    top logits (ids [B, T, K] int64, -1 where unused; teacher [B, T, K]) at
+    temperature tau; lse [B, T] is kept for the backward pass."""
+    import torch
+    dt, B, T, V, K = _distill(logits, ids, teacher, weight, stream)
+    _lm_tensors(stream, ("loss", loss, (torch.float32,), (B,)), ("lse", lse, (torch.float32,), (B, T)))
+    ws, nbytes = _lm_workspace(workspace, dp_distill_workspace_bytes(dt, B, T, V, K), logits.device, stream)
+    _check("dp_distill_loss", lib().dp_distill_loss(
+        _stream(stream), _ptr(logits), _ptr(ids), _ptr(teacher), dt, B, T, V, K, float(tau), _ptr(weight), _ptr(ws),
+        nbytes, _ptr(loss), _ptr(lse)))
+
+
+def dp_distill_loss_backward(logits, ids, teacher, tau: float, lse, grad, weight=None, dloss=None, stream=None):
+    """Gradient of sum_b dloss[b] * loss[b] (dloss None: of the sum) with
+    respect to the logits into grad [B, T, V], which may be logits itself."""
+    import torch
+    dt, B, T, V, K = _distill(logits, ids, teacher, weight, stream)
+    _lm_tensors(stream, ("lse", lse, (torch.float32,), (B, T)), ("grad", grad, (logits.dtype,), logits.shape),
+                ("dloss", dloss, (torch.float32,), (B,)))
+    _check("dp_distill_loss_backward", lib().dp_distill_loss_backward(
+        _stream(stream), _ptr(logits), _ptr(ids), _ptr(teacher), dt, B, T, V, K, float(tau), _ptr(weight),
+        _ptr(dloss), _ptr(lse), _ptr(grad)))
+
+
+def dp_grouped_workspace_bytes(dtype: int, R: int, E: int, B: int, d: int, p: int) -> int:
+    return int(lib().dp_grouped_workspace_bytes(dtype, R, E, B, d, p))
+
+
+def _grouped_batch(segments, E, B=None):
+    """The batch size of a segments tensor [E*B + 1] (sample b's rows in
+    expert e: segments[e*B + b] .. segments[e*B + b + 1])."""
+    import torch
+    n = segments.numel() - 1
+    if segments.dtype != torch.int64 or segments.dim() != 1 or E < 1 or n < E or n % E or (B is not None and n != E * B):
+        want = "E*B + 1" if B is None else f"{E * B + 1}"
+        raise ValueError(f"segments must be an int64 vector of {want} elements (E = {E})")
+    return n // E
+
+
+def dp_grouped_matmul(X, W, segments, out, transpose: bool = False, workspace=None, stream=None):
+    """out[r] = W[e] @ X[r] (transpose: W[e].T @ X[r]) for the rows r of
+    expert e; W [E, p, d], rows sorted by expert as segments says."""
+    import torch
+    if X.dim() != 2 or W.dim() != 3:
+        raise ValueError(f"X [R, ...] and W [E, p, d] expected, got {tuple(X.shape)} and {tuple(W.shape)}")
+    dt = _act_dtypes(X, "X")
+    E, p, d = (int(v) for v in W.shape)
+    R = int(X.shape[0])
+    B = _grouped_batch(segments, E)
+    _lm_tensors(stream, ("X", X, dt, (R, p if transpose else d)), ("W", W, dt, None),
+                ("out", out, dt, (R, d if transpose else p)), ("segments", segments, (torch.int64,), None))
+    code = _dtype_code(X)
+    ws, nbytes = _lm_workspace(workspace, dp_grouped_workspace_bytes(code, R, E, B, d, p), X.device, stream)
+    _check("dp_grouped_matmul", lib().dp_grouped_matmul(
+        _stream(stream), _ptr(X), _ptr(W), code, _ptr(segments), R, E, B, d, p, int(bool(transpose)), _ptr(ws), nbytes,
+        _ptr(out)))
+
+
+def _grouped_layer(A, G, segments, B, stream):
+    import torch
+    if A.dim() != 2 or G.dim() != 2 or A.shape[0] != G.shape[0]:
+        raise ValueError(f"A [R, d] and G [R, p] expected, got {tuple(A.shape)} and {tuple(G.shape)}")
+    dt = _act_dtypes(A, "A")
+    _lm_tensors(stream, ("A", A, dt, None), ("G", G, dt, None), ("segments", segments, (torch.int64,), None))
+    if (segments.numel() - 1) % B:
+        raise ValueError(f"segments must have E*B + 1 elements, B = {B}")
+    E = (segments.numel() - 1) // B
+    _grouped_batch(segments, E, B)
+    return _dtype_code(A), int(A.shape[0]), E, int(A.shape[1]), int(G.shape[1])
+
+
+def dp_grouped_norm(A, G, segments, sqnorm, accumulate: bool = False, workspace=None, stream=None):
+    """Per-sample squared gradient norms of an expert layer over all its
+    experts into sqnorm [B], from its rows A [R, d] and output gradients
+    G [R, p], sorted by (expert, sample) as segments [E*B + 1] says."""
+    import torch
+    _lm_tensors(stream, ("sqnorm", sqnorm, (torch.float32,), None))
+    B = sqnorm.numel()
+    dt, R, E, d, p = _grouped_layer(A, G, segments, B, stream)
+    ws, nbytes = _lm_workspace(workspace, dp_grouped_workspace_bytes(dt, R, E, B, d, p), A.device, stream)
+    _check("dp_grouped_norm", lib().dp_grouped_norm(
+        _stream(stream), _ptr(A), _ptr(G), dt, _ptr(segments), R, E, B, d, p, _ptr(ws), nbytes, _ptr(sqnorm),
+        int(bool(accumulate))))
+
+
+def dp_grouped_clipped_sum_noise(A, G, segments, c, C: float, sigma: float, denom: float, seed: int, layer_id: int,
+                                 step: int, out, workspace=None, stream=None):
+    """Clipped noised mean gradients of an expert layer into out [E, d, p]."""
+    import torch
+    _lm_tensors(stream, ("c", c, (torch.float32,), None))
+    B = c.numel()
+    dt, R, E, d, p = _grouped_layer(A, G, segments, B, stream)
+    _lm_tensors(stream, ("out", out, (torch.float32,), (E, d, p)))
+    ws, nbytes = _lm_workspace(workspace, dp_grouped_workspace_bytes(dt, R, E, B, d, p), A.device, stream)
+    _check("dp_grouped_clipped_sum_noise", lib().dp_grouped_clipped_sum_noise(
+        _stream(stream), _ptr(A), _ptr(G), dt, _ptr(segments), R, E, B, d, p, _ptr(c), float(C), float(sigma),
+        float(denom), int(seed) & 0xFFFFFFFFFFFFFFFF, int(layer_id) & 0xFFFFFFFF, int(step) & 0xFFFFFFFF, _ptr(ws),
+        nbytes, _ptr(out)))
