@@ -477,7 +477,8 @@ size_t dp_rms_norm_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t
  * logits hold.
  *
  *  logits   [B, T, V], dtype, 16-byte aligned.
- *  ids      [B, T, K] int64; teacher [B, T, K], dtype. 1 <= K <= 2048.
+ *  ids      [B, T, K] int64; teacher [B, T, K], teacher_dtype (DP_F32 or
+ *           DP_BF16). 1 <= K <= 2048.
  *  tau      temperature, finite, > 0.
  *  weight   [B, T] fp32, or NULL (1 everywhere).
  *  loss     [B] fp32.
@@ -485,7 +486,7 @@ size_t dp_rms_norm_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t
  *  workspace  at least dp_distill_workspace_bytes(...) bytes.
  */
 dp_status dp_distill_loss(void* stream, const void* logits, const int64_t* ids, const void* teacher, dp_dtype dtype,
-                          int64_t B, int64_t T, int64_t V, int64_t K, float tau, const float* weight,
+                          dp_dtype teacher_dtype, int64_t B, int64_t T, int64_t V, int64_t K, float tau, const float* weight,
                           void* workspace, size_t ws_bytes, float* loss, float* lse);
 
 /*
@@ -498,7 +499,8 @@ dp_status dp_distill_loss(void* stream, const void* logits, const int64_t* ids, 
  *  grad     [B, T, V], dtype, 16-byte aligned; may be logits.
  */
 dp_status dp_distill_loss_backward(void* stream, const void* logits, const int64_t* ids, const void* teacher,
-                                   dp_dtype dtype, int64_t B, int64_t T, int64_t V, int64_t K, float tau,
+                                   dp_dtype dtype, dp_dtype teacher_dtype, int64_t B, int64_t T, int64_t V,
+                                   int64_t K, float tau,
                                    const float* weight, const float* dloss, const float* lse, void* grad);
 size_t dp_distill_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t V, int64_t K);
 

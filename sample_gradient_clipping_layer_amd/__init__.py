@@ -179,9 +179,10 @@ def _declare(lib):
     lib.dp_rms_norm_backward.restype = c_i32
     lib.dp_rms_norm_workspace_bytes.argtypes = [c_i32, c_i64, c_i64, c_i64]
     lib.dp_rms_norm_workspace_bytes.restype = sz
-    lib.dp_distill_loss.argtypes = [vp, vp, vp, vp, c_i32, c_i64, c_i64, c_i64, c_i64, f, fp, vp, sz, fp, fp]
+    lib.dp_distill_loss.argtypes = [vp, vp, vp, vp, c_i32, c_i32, c_i64, c_i64, c_i64, c_i64, f, fp, vp, sz, fp, fp]
     lib.dp_distill_loss.restype = c_i32
-    lib.dp_distill_loss_backward.argtypes = [vp, vp, vp, vp, c_i32, c_i64, c_i64, c_i64, c_i64, f, fp, fp, fp, vp]
+    lib.dp_distill_loss_backward.argtypes = [vp, vp, vp, vp, c_i32, c_i32, c_i64, c_i64, c_i64, c_i64, f, fp, fp,
+                                             fp, vp]
     lib.dp_distill_loss_backward.restype = c_i32
     lib.dp_distill_workspace_bytes.argtypes = [c_i32, c_i64, c_i64, c_i64, c_i64]
     lib.dp_distill_workspace_bytes.restype = sz
@@ -726,7 +727,7 @@ def _distill(logits, ids, teacher, weight, stream):
     dt = _act_dtypes(logits, "logits")
     B, T, V = (int(v) for v in logits.shape)
     _lm_tensors(stream, ("logits", logits, dt, None), ("ids", ids, (torch.int64,), None),
-                ("teacher", teacher, dt, ids.shape), ("weight", weight, (torch.float32,), (B, T)))
+                ("teacher", teacher, (torch.float32, torch.bfloat16), ids.shape), ("weight", weight, (torch.float32,), (B, T)))
     return _dtype_code(logits), B, T, V, int(ids.shape[2])
 
 
@@ -739,8 +740,8 @@ def dp_distill_loss(logits, ids, teacher, tau: float, loss, lse, weight=None, wo
     _lm_tensors(stream, ("loss", loss, (torch.float32,), (B,)), ("lse", lse, (torch.float32,), (B, T)))
     ws, nbytes = _lm_workspace(workspace, dp_distill_workspace_bytes(dt, B, T, V, K), logits.device, stream)
     _check("dp_distill_loss", lib().dp_distill_loss(
-        _stream(stream), _ptr(logits), _ptr(ids), _ptr(teacher), dt, B, T, V, K, float(tau), _ptr(weight), _ptr(ws),
-        nbytes, _ptr(loss), _ptr(lse)))
+        _stream(stream), _ptr(logits), _ptr(ids), _ptr(teacher), dt, _dtype_code(teacher), B, T, V, K, float(tau),
+        _ptr(weight), _ptr(ws), nbytes, _ptr(loss), _ptr(lse)))
 
 
 def dp_distill_loss_backward(logits, ids, teacher, tau: float, lse, grad, weight=None, dloss=None, stream=None):
@@ -751,8 +752,8 @@ def dp_distill_loss_backward(logits, ids, teacher, tau: float, lse, grad, weight
     _lm_tensors(stream, ("lse", lse, (torch.float32,), (B, T)), ("grad", grad, (logits.dtype,), logits.shape),
                 ("dloss", dloss, (torch.float32,), (B,)))
     _check("dp_distill_loss_backward", lib().dp_distill_loss_backward(
-        _stream(stream), _ptr(logits), _ptr(ids), _ptr(teacher), dt, B, T, V, K, float(tau), _ptr(weight),
-        _ptr(dloss), _ptr(lse), _ptr(grad)))
+        _stream(stream), _ptr(logits), _ptr(ids), _ptr(teacher), dt, _dtype_code(teacher), B, T, V, K, float(tau),
+        _ptr(weight), _ptr(dloss), _ptr(lse), _ptr(grad)))
 
 
 def dp_grouped_workspace_bytes(dtype: int, R: int, E: int, B: int, d: int, p: int) -> int:

@@ -139,13 +139,13 @@ size_t dp_distill_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t 
 }
 
 dp_status dp_distill_loss(void* stream, const void* logits, const int64_t* ids, const void* teacher, dp_dtype dtype,
-                          int64_t B, int64_t T, int64_t V, int64_t K, float tau, const float* weight,
+                          dp_dtype teacher_dtype, int64_t B, int64_t T, int64_t V, int64_t K, float tau, const float* weight,
                           void* workspace, size_t ws_bytes, float* loss, float* lse) {
   if (!logits || !ids || !teacher || !loss || !lse) return DP_ERR_NULL;
   dp_status s = check_distill(B, T, V, K, tau);
   if (s != DP_OK) return s;
-  if (!dtype_ok(dtype)) return DP_ERR_DTYPE;
-  if (!aligned(logits, 16) || !aligned(ids, 8) || !aligned(teacher, elem_bytes(dtype)) || !aligned(weight, 4) ||
+  if (!dtype_ok(dtype) || !dtype_ok(teacher_dtype)) return DP_ERR_DTYPE;
+  if (!aligned(logits, 16) || !aligned(ids, 8) || !aligned(teacher, elem_bytes(teacher_dtype)) || !aligned(weight, 4) ||
       !aligned(loss, 4) || !aligned(lse, 4))
     return DP_ERR_ALIGN;
   const DistillWs w = distill_ws(B, T, V);
@@ -157,6 +157,7 @@ dp_status dp_distill_loss(void* stream, const void* logits, const int64_t* ids, 
   a.logits = logits;
   a.ids = ids;
   a.teacher = teacher;
+  a.teacher_bf16 = teacher_dtype == DP_BF16;
   a.weight = weight;
   a.tau = tau;
   a.B = B;
@@ -171,13 +172,14 @@ dp_status dp_distill_loss(void* stream, const void* logits, const int64_t* ids, 
 }
 
 dp_status dp_distill_loss_backward(void* stream, const void* logits, const int64_t* ids, const void* teacher,
-                                   dp_dtype dtype, int64_t B, int64_t T, int64_t V, int64_t K, float tau,
+                                   dp_dtype dtype, dp_dtype teacher_dtype, int64_t B, int64_t T, int64_t V,
+                                   int64_t K, float tau,
                                    const float* weight, const float* dloss, const float* lse, void* grad) {
   if (!logits || !ids || !teacher || !lse || !grad) return DP_ERR_NULL;
   dp_status s = check_distill(B, T, V, K, tau);
   if (s != DP_OK) return s;
-  if (!dtype_ok(dtype)) return DP_ERR_DTYPE;
-  if (!aligned(logits, 16) || !aligned(grad, 16) || !aligned(ids, 8) || !aligned(teacher, elem_bytes(dtype)) ||
+  if (!dtype_ok(dtype) || !dtype_ok(teacher_dtype)) return DP_ERR_DTYPE;
+  if (!aligned(logits, 16) || !aligned(grad, 16) || !aligned(ids, 8) || !aligned(teacher, elem_bytes(teacher_dtype)) ||
       !aligned(weight, 4) || !aligned(dloss, 4) || !aligned(lse, 4))
     return DP_ERR_ALIGN;
   s = device_ready();
@@ -186,6 +188,7 @@ dp_status dp_distill_loss_backward(void* stream, const void* logits, const int64
   a.logits = logits;
   a.ids = ids;
   a.teacher = teacher;
+  a.teacher_bf16 = teacher_dtype == DP_BF16;
   a.weight = weight;
   a.tau = tau;
   a.B = B;

@@ -132,25 +132,29 @@ struct Span {
   }
 };
 
+// Teacher logit i, fp32 or bf16.
+__device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t i) {
+  return a.teacher_bf16 ? to_f32(static_cast<const bf16s*>(a.teacher)[i]) : static_cast<const float*>(a.teacher)[i];
+}
+
 // The loss of one token from its student statistics, by the whole block.
 template <typename T>
 __device__ float token_loss(const DistillArgs& a, int64_t row, Run r, float* red) {
   const float w = a.weight ? a.weight[row] : 1.0f;
   if (w == 0.0f) return 0.0f;  // uniform over the block
   const T* z = static_cast<const T*>(a.logits) + row * a.V;
-  const T* t = static_cast<const T*>(a.teacher) + row * a.K;
   const int64_t* id = a.ids + row * a.K;
   const float inv_tau = 1.0f / a.tau;
   float tm = -INFINITY;
   for (int64_t k = threadIdx.x; k < a.K; k += kDt)
-    if (id[k] >= 0 && id[k] < a.V) tm = fmaxf(tm, to_f32(t[k]));
+    if (id[k] >= 0 && id[k] < a.V) tm = fmaxf(tm, teacher_at(a, row * a.K + k));
   tm = block_max(tm, red);
   if (tm == -INFINITY) return 0.0f;  // no used place
   float total = 0.f, s = 0.f;
   for (int64_t k = threadIdx.x; k < a.K; k += kDt) {
     const int64_t j = id[k];
     if (j < 0 || j >= a.V) continue;
-    const float dt = (to_f32(t[k]) - tm) * inv_tau;
+    const float dt = (teacher_at(a, row * a.K + k) - tm) * inv_tau;
     const float e = __builtin_exp2f(dt * kLog2e);
     if (e == 0.0f) continue;  // no mass there: its logits (infinite ones among them) do not count
     total += e;
@@ -271,7 +275,6 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
     if (v0 >= v1) continue;  // uniform
     const T* z = static_cast<const T*>(a.logits) + row * a.V;
     T* g = static_cast<T*>(a.grad) + row * a.V;
-    const T* t = static_cast<const T*>(a.teacher) + row * a.K;
     const int64_t* id = a.ids + row * a.K;
     float f = a.weight ? a.weight[row] : 1.0f;
     if (a.dloss) f *= a.dloss[row / a.T];
@@ -280,7 +283,7 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
     float tm = -INFINITY;
     if (f != 0.0f)
       for (int k = threadIdx.x; k < K; k += kDt)
-        if (id[k] >= 0 && id[k] < a.V) tm = fmaxf(tm, to_f32(t[k]));
+        if (id[k] >= 0 && id[k] < a.V) tm = fmaxf(tm, teacher_at(a, row * a.K + k));
     tm = block_max(tm, red);
     const bool any = f != 0.0f && tm != -INFINITY;
     float total = 0.f;
@@ -290,7 +293,7 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
         float e = 0.f;
         if (k < K && id[k] >= 0 && id[k] < a.V) {
           w = (int32_t)id[k];
-          e = __builtin_exp2f((to_f32(t[k]) - tm) * inv_tau * kLog2e);
+          e = __builtin_exp2f((teacher_at(a, row * a.K + k) - tm) * inv_tau * kLog2e);
         }
         ids[k] = w;
         qs[k] = e;

@@ -54,6 +54,7 @@ struct DistillArgs {
   const void* logits;
   const int64_t* ids;
   const void* teacher;
+  int teacher_bf16;
   const float* weight;  // [B][T] or null
   float tau;
   int64_t B, T, V, K;

@@ -1,5 +1,6 @@
 """Privacy engine front end: per-sample clipping and Gaussian noise for the
-Linear and Conv2d layers of a torch model, through the C ABI.
+Linear, Conv2d, RMSNorm and ExpertLinear layers of a torch model, through the
+C ABI.
 
 "Scalable and Efficient Training of Large CNNs with DP", App. E (the privacy
 engine with its 'ghost' and 'ghost-mixed' modes) and Sec. 3 (ghost norm, then
@@ -17,6 +18,13 @@ stored), and with conv_input="unfolded" torch unfolds each input (at
 ResNet-18 shapes torch's unfold alone takes several times the whole
 clipping path).
 
+A root-mean-square norm's gain (layers.RMSNorm, torch.nn.RMSNorm) has the
+per-sample gradient sum_t dy u, which dp_rms_norm_backward leaves as [B, d]
+rows: the linear layer A = 1 [B, 1, 1], G = rows [B, 1, d] of the multi-layer
+calls. layers.ExpertLinear's rows are grouped by (expert, sample) and take the
+dp_grouped_* calls. Both add to the same per-sample norms and share the clip
+factors.
+
 Only argument marshalling and layout changes happen here; every step of the
 clipping path runs in libdpclip.
 """
@@ -27,7 +35,9 @@ import torch.nn.functional as F
 
 from . import (DP_BF16, DP_F32, MODE_EXPLICIT, MODE_GHOST, MODE_MIXED, MODE_TIME, conv_geometry, dp_clip_factors,
                dp_clipped_sum_noise_layers, dp_conv_clipped_sum_noise, dp_conv_norm, dp_conv_workspace_bytes,
-               dp_ghost_norm_clip_layers, dp_ghost_norm_layers, dp_layers_workspace_bytes, dp_unfold2d)
+               dp_ghost_norm_clip_layers, dp_ghost_norm_layers, dp_grouped_clipped_sum_noise, dp_grouped_norm,
+               dp_grouped_workspace_bytes, dp_layers_workspace_bytes, dp_rms_norm_backward, dp_unfold2d)
+from .layers import ExpertLinear, RMSNorm
 
 MODES = {"ghost-mixed": MODE_MIXED, "ghost": MODE_GHOST, "explicit": MODE_EXPLICIT, "time": MODE_TIME}
 
@@ -37,12 +47,17 @@ class _Layer:
         self.module = module
         self.a = None   # the module's input of the last forward pass
         self.g = None   # dL/d(output) of the last backward pass
+        self.segments = None  # ExpertLinear: its rows' (expert, sample) ranges
+
+
+_COVERED = (torch.nn.Linear, torch.nn.Conv2d, torch.nn.RMSNorm, RMSNorm, ExpertLinear)
 
 
 class PrivacyEngine:
     """Flat (global) per-sample clipping at bound C with noise multiplier
-    sigma for every nn.Linear and nn.Conv2d (groups = 1) with trainable
-    parameters in `model`.
+    sigma for every nn.Linear, nn.Conv2d (groups = 1), nn.RMSNorm,
+    layers.RMSNorm and layers.ExpertLinear with trainable parameters in
+    `model`.
 
     Usage, per step:
         out = model(x)                       # hooks keep the layer inputs
@@ -75,7 +90,9 @@ class PrivacyEngine:
         self.layers: list[_Layer] = []
         covered = set()
         for m in model.modules():
-            if isinstance(m, (torch.nn.Linear, torch.nn.Conv2d)) and any(p.requires_grad for p in m.parameters()):
+            if isinstance(m, _COVERED) and any(p.requires_grad for p in m.parameters()):
+                if isinstance(m, torch.nn.RMSNorm) and len(m.normalized_shape) != 1:
+                    raise ValueError("RMSNorm must be over the last dimension")
                 if isinstance(m, torch.nn.Conv2d) and m.groups != 1:
                     raise ValueError("Conv2d with groups != 1 is not supported")
                 if isinstance(m, torch.nn.Conv2d) and m.padding_mode != "zeros":
@@ -88,11 +105,14 @@ class PrivacyEngine:
                 covered.update(id(p) for p in m.parameters())
         others = [n for n, p in model.named_parameters() if p.requires_grad and id(p) not in covered]
         if others:
-            raise ValueError(f"trainable parameters outside Linear/Conv2d layers: {others}")
+            raise ValueError("trainable parameters outside Linear, Conv2d, RMSNorm and ExpertLinear layers: "
+                             f"{others}")
         if not self.layers:
-            raise ValueError("no Linear or Conv2d layer with trainable parameters")
+            raise ValueError("no Linear, Conv2d, RMSNorm or ExpertLinear layer with trainable parameters")
         self._handles = []
         for L in self.layers:
+            if isinstance(L.module, (RMSNorm, ExpertLinear)):
+                L.module.private = True  # their backward passes leave the weight's gradient to step()
             self._handles.append(L.module.register_forward_hook(self._forward_hook(L)))
             self._handles.append(L.module.register_full_backward_hook(self._backward_hook(L)))
         self.last_norms = None  # per-sample norms of the last step
@@ -104,12 +124,17 @@ class PrivacyEngine:
                 raise RuntimeError("a module ran twice in one forward pass")
             L.a = inputs[0].detach()
             L.g = None
+            if isinstance(module, ExpertLinear):
+                L.segments = inputs[1]
+            elif isinstance(module, RMSNorm):
+                module.gain_rows = None
         return hook
 
     @staticmethod
     def _backward_hook(L):
         def hook(module, grad_input, grad_output):
-            L.g = grad_output[0].detach()
+            g = grad_output[0]  # None: an RMSNorm of which only the sum was used
+            L.g = None if g is None else g.detach()
         return hook
 
     def detach(self):
@@ -117,6 +142,9 @@ class PrivacyEngine:
         for h in self._handles:
             h.remove()
         self._handles = []
+        for L in self.layers:
+            if isinstance(L.module, (RMSNorm, ExpertLinear)):
+                L.module.private = False
 
     @staticmethod
     def _padding(m):
@@ -125,15 +153,37 @@ class PrivacyEngine:
     def _is_folded(self, L):
         return self.folded and isinstance(L.module, torch.nn.Conv2d)
 
+    def _gain_operands(self, L):
+        """(A = 1 [B, 1, 1], G = the gain's per-sample gradients [B, 1, d]) of a
+        norm layer, in float32."""
+        m, a, g = L.module, L.a, L.g
+        if a is None or (g is None and getattr(m, "gain_rows", None) is None):
+            raise RuntimeError("step() needs one forward and one backward pass of every layer first")
+        if isinstance(m, RMSNorm):
+            rows = m.gain_rows
+            if rows is None:
+                raise RuntimeError("an RMSNorm's backward pass did not run")
+        else:
+            dt = a.dtype if a.dtype in (torch.float32, torch.bfloat16) else torch.float32
+            rows = torch.empty(a.shape[0], a.shape[-1], dtype=torch.float32, device=a.device)
+            eps = m.eps if m.eps is not None else torch.finfo(a.dtype).eps  # torch's default
+            dp_rms_norm_backward(g.to(dt).contiguous(), a.to(dt).contiguous(), m.weight.detach(), eps,
+                                 gain_rows=rows)
+        B = rows.shape[0]
+        return torch.ones(B, 1, 1, dtype=torch.float32, device=rows.device), rows.view(B, 1, -1)
+
     def _operands(self, L):
         """(A [B, T, d], G [B, T, p]) of one layer, contiguous, in the activation dtype;
-        for a conv layer taken folded, (a [B, C_in, H, W], G [B, T, p], geometry)."""
+        for a conv layer taken folded, (a [B, C_in, H, W], G [B, T, p], geometry);
+        for an expert layer its rows (A [R, d], G [R, p])."""
         m, a, g = L.module, L.a, L.g
         if a is None or g is None:
             raise RuntimeError("step() needs one forward and one backward pass of every layer first")
         B = a.shape[0]
         dt = a.dtype if a.dtype in (torch.float32, torch.bfloat16) else torch.float32
-        if isinstance(m, torch.nn.Linear):
+        if isinstance(m, ExpertLinear):
+            A, G = a, g
+        elif isinstance(m, torch.nn.Linear):
             A = a.reshape(B, -1, a.shape[-1])
             G = g.reshape(B, -1, g.shape[-1])
         elif self._is_folded(L):
@@ -157,41 +207,65 @@ class PrivacyEngine:
 
         The noise stream of a layer is its index in the engine's layer list
         (the model's module order), whichever call serves it."""
-        ops = [self._operands(L) for L in self.layers]
-        B = ops[0][0].shape[0]
+        gains = [k for k, L in enumerate(self.layers) if isinstance(L.module, (RMSNorm, torch.nn.RMSNorm))]
+        experts = [k for k, L in enumerate(self.layers) if isinstance(L.module, ExpertLinear)]
+        ops = [self._gain_operands(L) if k in gains else self._operands(L) for k, L in enumerate(self.layers)]
+        batch = {op[0].shape[0] if k not in experts
+                 else (self.layers[k].segments.numel() - 1) // self.layers[k].module.weight.shape[0]
+                 for k, op in enumerate(ops)}
+        if len(batch) != 1:
+            raise RuntimeError(f"all layers must share one batch size, got {sorted(batch)}")
+        B = batch.pop()
         dev = ops[0][0].device
-        dtypes = {op[0].dtype for op in ops}
-        if len(dtypes) != 1:
+        dtypes = {op[0].dtype for k, op in enumerate(ops) if k not in gains}
+        if len(dtypes) > 1:
             raise RuntimeError("all layers must share one activation dtype")
-        dt = DP_BF16 if ops[0][0].dtype == torch.bfloat16 else DP_F32
+        dt = DP_BF16 if dtypes == {torch.bfloat16} else DP_F32
         denom = float(B) if denom is None else float(denom)
-        has_bias = [L.module.bias is not None and L.module.bias.requires_grad for L in self.layers]
-        dense = [k for k, op in enumerate(ops) if len(op) == 2]   # [B, T, d] operands: multi-layer calls
-        folded = [k for k, op in enumerate(ops) if len(op) == 3]  # folded conv inputs: dp_conv_* calls
+        has_bias = [getattr(L.module, "bias", None) is not None and L.module.bias.requires_grad for L in self.layers]
+        others = set(gains) | set(experts)
+        # [B, T, d] operands: multi-layer calls; folded conv inputs: dp_conv_* calls
+        dense = [k for k, op in enumerate(ops) if len(op) == 2 and k not in others]
+        folded = [k for k, op in enumerate(ops) if len(op) == 3]
         sq = torch.empty(B, dtype=torch.float32, device=dev)
         c = torch.empty(B, dtype=torch.float32, device=dev)
         norms = torch.empty(B, dtype=torch.float32, device=dev)
         ws = None
+        started = False  # sq holds the layers so far
         if dense:
             dops, dhb = [ops[k] for k in dense], [has_bias[k] for k in dense]
             ws = torch.empty(max(256, dp_layers_workspace_bytes(dops, has_bias=dhb, mode=self.mode,
                                                                 kappa=self.kappa)), dtype=torch.uint8, device=dev)
-            if folded:
+            if folded or others:
                 dp_ghost_norm_layers(dops, sq, has_bias=dhb, mode=self.mode, kappa=self.kappa, workspace=ws)
             else:  # every layer in this call: its kernels form the clip factors too (the same bits)
                 dp_ghost_norm_clip_layers(dops, sq, self.C, c, norms, has_bias=dhb, mode=self.mode,
                                           kappa=self.kappa, workspace=ws)
+            started = True
         wsc = {}
         for k in folded:
             a, G, geo = ops[k]
             wsc[k] = torch.empty(max(256, dp_conv_workspace_bytes(geo, dt, B, G.shape[2], has_bias[k], self.mode,
                                                                   self.kappa)), dtype=torch.uint8, device=dev)
             dp_conv_norm(a, G, geo, sq, has_bias=has_bias[k], mode=self.mode, kappa=self.kappa,
-                         accumulate=bool(dense) or k != folded[0], workspace=wsc[k])
-        if folded:
+                         accumulate=started, workspace=wsc[k])
+            started = True
+        if gains:
+            gops = [ops[k] for k in gains]
+            dp_ghost_norm_layers(gops, sq, accumulate=started)
+            started = True
+        for k in experts:
+            A, G = ops[k]
+            E, p, d = self.layers[k].module.weight.shape
+            wsc[k] = torch.empty(max(256, dp_grouped_workspace_bytes(dt, A.shape[0], E, B, d, p)), dtype=torch.uint8,
+                                 device=dev)
+            dp_grouped_norm(A, G, self.layers[k].segments, sq, accumulate=started, workspace=wsc[k])
+            started = True
+        if folded or others:
             dp_clip_factors(sq, self.C, c, norms)
-        d_of = [op[2].C_in * op[2].kh * op[2].kw if len(op) == 3 else op[0].shape[2] for op in ops]
-        outs = [torch.empty(d_of[k], op[1].shape[2], dtype=torch.float32, device=dev) for k, op in enumerate(ops)]
+        outs = [torch.empty(self.layers[k].module.weight.transpose(1, 2).shape if k in experts
+                            else ((op[2].C_in * op[2].kh * op[2].kw if len(op) == 3 else op[0].shape[2]),
+                                  op[1].shape[2]), dtype=torch.float32, device=dev) for k, op in enumerate(ops)]
         bouts = [torch.empty(op[1].shape[2], dtype=torch.float32, device=dev) if hb else None
                  for op, hb in zip(ops, has_bias)]
         if dense:
@@ -203,12 +277,23 @@ class PrivacyEngine:
             a, G, geo = ops[k]
             dp_conv_clipped_sum_noise(a, G, geo, c, self.C, self.sigma, denom, self.seed, k, step, outs[k],
                                       bias_out=bouts[k], workspace=wsc[k])
+        if gains:
+            dp_clipped_sum_noise_layers([ops[k] for k in gains], c, self.C, self.sigma, denom, self.seed, step,
+                                        [outs[k] for k in gains], layer_ids=gains)
+        for k in experts:
+            A, G = ops[k]
+            dp_grouped_clipped_sum_noise(A, G, self.layers[k].segments, c, self.C, self.sigma, denom, self.seed, k,
+                                         step, outs[k], workspace=wsc[k])
         for L, out, bout in zip(self.layers, outs, bouts):
             w = L.module.weight
-            if w.requires_grad:
+            if isinstance(L.module, ExpertLinear):
+                w.grad = out.transpose(1, 2).to(w.dtype).contiguous()  # [E, p, d]
+            elif w.requires_grad:
                 w.grad = out.t().reshape(w.shape).to(w.dtype).contiguous()  # [p, d] (conv: [C_out, C_in, kH, kW])
             if bout is not None:
                 L.module.bias.grad = bout.to(L.module.bias.dtype)
-            L.a = L.g = None
+            L.a = L.g = L.segments = None
+            if isinstance(L.module, RMSNorm):
+                L.module.gain_rows = None
         self.last_norms = norms
         return norms
