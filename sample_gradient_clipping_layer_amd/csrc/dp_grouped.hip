@@ -67,23 +67,24 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
 
 // ---- operand tiles in LDS
 //
-// A chunk is 128 bytes of K per feature: 64 bf16 or 32 fp32. KCONT operands
-// hold K along their rows: LDS rows are features, 128 bytes each. The others
-// hold features along their rows: LDS rows are the chunk's K rows. Both are
-// windows of a row-major matrix, stored in 16-byte pieces; piece q of LDS row
-// r sits at position q ^ swz(r), which puts every fragment read on 64
+// A chunk is KB bytes of K per feature (128: 64 bf16 or 32 fp32). KCONT
+// operands hold K along their rows: LDS rows are features, KB bytes each. The
+// others hold features along their rows: LDS rows are the chunk's K rows.
+// Both are windows of a row-major matrix, stored in 16-byte pieces; piece q of
+// LDS row r sits at position q ^ swz(r), which puts every fragment read on 64
 // distinct banks.
-template <typename T, bool KCONT, int NF>
+template <typename T, bool KCONT, int NF, int KB = 128>
 struct Opnd {
   static constexpr int SZ = sizeof(T);
   static constexpr int P = elem_traits<T>::per16;
-  static constexpr int KC = 128 / SZ;               // K per chunk
-  static constexpr int ROWB = KCONT ? 128 : NF * SZ;  // LDS row bytes
+  static constexpr int KC = KB / SZ;                 // K per chunk
+  static constexpr int ROWB = KCONT ? KB : NF * SZ;  // LDS row bytes
   static constexpr int NROWS = KCONT ? NF : KC;
-  static constexpr int BYTES = NF * 128;
+  static constexpr int BYTES = NF * KB;
   static constexpr int PIECES = ROWB / 16;
+  static_assert(KB == 64 || KB == 128, "chunk depth");
   static __device__ __forceinline__ int swz(int r) {
-    if constexpr (KCONT) return (r >> 1) & 7;
+    if constexpr (KCONT) return KB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
     else if constexpr (SZ == 2) return 4 * (r & 3);
     else return 8 * ((r >> 2) & 1);
   }
@@ -99,6 +100,13 @@ struct Win {
   int64_t rows;  // valid rows
   int64_t cols;  // valid columns (elements)
 };
+
+// Between a wave's LDS writes and its reads of what other lanes wrote (and
+// before the next writes over it): in order in hardware, kept so by the compiler.
+__device__ __forceinline__ void lds_wave_fence() { asm volatile("" ::: "memory"); }
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 
 // 16 bytes per lane from a buffer straight into LDS; lanes whose offset lies
 // at or past num_records write zeros.
@@ -171,22 +179,22 @@ struct Filler {
 // Reading MFMA fragments: a step is 32 bytes of K per feature (16 bf16: one
 // MFMA; 8 fp32: four of K = 2). Lane l holds feature l % 32 of each 32-block;
 // its 16 bytes are K piece 2*step + l/32.
-template <typename T, int NF, int NB>
+template <typename T, int NF, int NB, int KB = 128>
 struct ReadK {  // KCONT
-  using O = Opnd<T, true, NF>;
-  int off[4];
+  using O = Opnd<T, true, NF, KB>;
+  int off[KB / 32];
   __device__ __forceinline__ void init(int w0, int lane) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      off[s] = (w0 + (lane & 31)) * 128 + 16 * ((2 * s + (lane >> 5)) ^ (((lane & 31) >> 1) & 7));
+    for (int s = 0; s < KB / 32; ++s)
+      off[s] = (w0 + (lane & 31)) * KB + 16 * ((2 * s + (lane >> 5)) ^ O::swz(lane & 31));
   }
   __device__ __forceinline__ u32x4 get(uint32_t sbase, int s, int blk) const {
-    return *(lds_u32x4*)(uintptr_t)(sbase + off[s] + blk * 4096);
+    return *(lds_u32x4*)(uintptr_t)(sbase + off[s] + blk * 32 * KB);
   }
 };
-template <typename T, int NF, int NB>
+template <typename T, int NF, int NB, int KB = 128>
 struct ReadF {  // features along the rows
-  using O = Opnd<T, false, NF>;
+  using O = Opnd<T, false, NF, KB>;
   int off[NB];
   __device__ __forceinline__ void init(int w0, int lane) {
 #pragma unroll
@@ -223,8 +231,8 @@ struct ReadF {  // features along the rows
     }
   }
 };
-template <typename T, bool KCONT, int NF, int NB>
-using ReadOf = std::conditional_t<KCONT, ReadK<T, NF, NB>, ReadF<T, NF, NB>>;
+template <typename T, bool KCONT, int NF, int NB, int KB>
+using ReadOf = std::conditional_t<KCONT, ReadK<T, NF, NB, KB>, ReadF<T, NF, NB, KB>>;
 
 template <typename T>
 __device__ __forceinline__ f32x16 mma_step(u32x4 a, u32x4 b, f32x16 c) {
@@ -289,21 +297,26 @@ struct MatmulArgs {
   int64_t B, E, R, K, N;
   int64_t slots;  // R / BM + E
   int64_t ntn;    // column tiles
+  int64_t ks;     // K splits
+  int64_t kper;   // K per split, whole chunks
+  float* part;    // ks > 1: partial products [ks][R][N]
 };
 
 constexpr int64_t kSlotGroup = 4;  // row tiles that neighbouring workgroups share a weight tile over
 
-template <typename T, bool TRANS, int BM, int BN, int WGM, int WGN, int ST, bool DMA>
+template <typename T, bool TRANS, int BM, int BN, int WGM, int WGN, int KB, int ST, bool DMA, bool SPLIT>
 __global__ __launch_bounds__(64 * WGM * WGN) void k_grouped_matmul(MatmulArgs a) {
-  constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, NBM = WM / 32, NBN = WN / 32;
-  using OX = Opnd<T, true, BM>;
-  using OW = Opnd<T, !TRANS, BN>;
+  constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, NBM = WM / 32, NBN = WN / 32, NS = KB / 32;
+  using OX = Opnd<T, true, BM, KB>;
+  using OW = Opnd<T, !TRANS, BN, KB>;
   constexpr int KC = OX::KC, STAGE = OX::BYTES + OW::BYTES;
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
 
   const int64_t items = a.slots * a.ntn;
-  const int64_t w = xcd_item(blockIdx.x, items);
-  if (w >= items) return;
+  int64_t w = xcd_item(blockIdx.x, items * a.ks);
+  if (w >= items * a.ks) return;
+  const int64_t sp = SPLIT ? w / items : 0;
+  if (SPLIT) w -= sp * items;
   const int64_t sg = w / (kSlotGroup * a.ntn), rem = w - sg * kSlotGroup * a.ntn;
   const int64_t in_group = a.slots - sg * kSlotGroup < kSlotGroup ? a.slots - sg * kSlotGroup : kSlotGroup;
   const int64_t tn = rem / in_group, slot = sg * kSlotGroup + (rem - tn * in_group);
@@ -311,11 +324,13 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_grouped_matmul(MatmulArgs a)
   if (!find_group<BM>(a.seg, a.B, a.E, a.R, slot, &gr)) return;  // whole workgroup
   const int64_t row0 = uniform64(gr.row0), rows = uniform64(gr.rows), e = uniform64(gr.g);
   const int64_t n0 = tn * BN;
+  const int64_t kb0 = SPLIT ? sp * a.kper : 0;
+  const int64_t klen = SPLIT ? (a.K - kb0 < a.kper ? a.K - kb0 : a.kper) : a.K;  // > 0: checked on the host
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WGM, wn = wave / WGM;
-  const T* X = static_cast<const T*>(a.X) + row0 * a.K;
-  const T* W = static_cast<const T*>(a.W) + e * a.K * a.N + (TRANS ? n0 : n0 * a.K);
+  const T* X = static_cast<const T*>(a.X) + row0 * a.K + kb0;
+  const T* W = static_cast<const T*>(a.W) + e * a.K * a.N + (TRANS ? kb0 * a.N + n0 : n0 * a.K + kb0);
   const int64_t xb = a.K * (int64_t)sizeof(T), wb = (TRANS ? a.N : a.K) * (int64_t)sizeof(T);
   const int64_t mrows = rows < BM ? rows : BM;
 
@@ -323,36 +338,72 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_grouped_matmul(MatmulArgs a)
   Filler<OW, T, NW> fw;
   fx.init(xb, wave, lane);
   fw.init(wb, wave, lane);
-  ReadOf<T, true, BM, NBM> rx;
-  ReadOf<T, !TRANS, BN, NBN> rw;
+  ReadOf<T, true, BM, NBM, KB> rx;
+  ReadOf<T, !TRANS, BN, NBN, KB> rw;
   rx.init(wm * WM, lane);
   rw.init(wn * WN, lane);
-  auto xwin = [&](int64_t k0) { return Win<T>{X + k0, xb, mrows, a.K - k0}; };
+  auto xwin = [&](int64_t k0) { return Win<T>{X + k0, xb, mrows, klen - k0}; };
   auto wwin = [&](int64_t k0) {
-    return TRANS ? Win<T>{W + k0 * a.N, wb, a.K - k0, a.N - n0} : Win<T>{W + k0, wb, a.N - n0, a.K - k0};
+    return TRANS ? Win<T>{W + k0 * a.N, wb, klen - k0, a.N - n0} : Win<T>{W + k0, wb, a.N - n0, klen - k0};
   };
 
   f32x16 acc[NBN][NBM];
   zero_acc(acc);
-  const int nq = (int)((a.K + KC - 1) / KC);
+  const int nq = (int)((klen + KC - 1) / KC);
   const uint32_t l0 = lds_addr(lds);
-  auto issue = [&](int q) {
-    const uint32_t sb = l0 + (uint32_t)(q % ST) * STAGE;
-    fx.dma(xwin((int64_t)q * KC), sb, wave);
-    fw.dma(wwin((int64_t)q * KC), sb + OX::BYTES, wave);
+  struct Frags {
+    u32x4 w[NBN], x[NBM];
+  };
+  auto read = [&](uint32_t sb, int s, Frags& f) {
+#pragma unroll
+    for (int j = 0; j < NBN; ++j) f.w[j] = rw.get(sb + OX::BYTES, s, j);
+#pragma unroll
+    for (int i = 0; i < NBM; ++i) f.x[i] = rx.get(sb, s, i);
+  };
+  auto mma = [&](const Frags& f) {
+#pragma unroll
+    for (int j = 0; j < NBN; ++j)
+#pragma unroll
+      for (int i = 0; i < NBM; ++i) acc[j][i] = mma_step<T>(f.w[j], f.x[i], acc[j][i]);
   };
   if constexpr (DMA) {
     constexpr int LPC = Filler<OX, T, NW>::LOADS + Filler<OW, T, NW>::LOADS;
+    auto issue = [&](int q) {
+      const uint32_t sb = l0 + (uint32_t)(q % ST) * STAGE;
+      fx.dma(xwin((int64_t)q * KC), sb, wave);
+      fw.dma(wwin((int64_t)q * KC), sb + OX::BYTES, wave);
+    };
+    auto stage_of = [&](int q) { return l0 + (uint32_t)(q % ST) * STAGE; };
+    // chunk q landed for every wave, and every wave is done with chunk q - 1, whose stage takes chunk q + ST - 1
+    auto arrive = [&](int q) {
+      const int later = nq - 1 - q < ST - 2 ? nq - 1 - q : ST - 2;
+      wait_chunks<LPC, ST - 2>(later);
+      lds_barrier();
+      if (q + ST - 1 < nq) issue(q + ST - 1);
+    };
 #pragma unroll
     for (int q = 0; q < ST - 1; ++q)
       if (q < nq) issue(q);
-    for (int q = 0; q < nq; ++q) {
-      const int later = nq - 1 - q < ST - 2 ? nq - 1 - q : ST - 2;
-      wait_chunks<LPC, ST - 2>(later);
-      lds_barrier();  // chunk q landed for every wave; every wave is done with chunk q-1
-      if (q + ST - 1 < nq) issue(q + ST - 1);
-      const uint32_t sb = l0 + (uint32_t)(q % ST) * STAGE;
-      chunk_mma<T, NBN, NBM>(sb + OX::BYTES, sb, rw, rx, 4, acc);
+    // step s + 1's fragments are read while step s is on the matrix cores, across chunks too
+    Frags f[2];
+    arrive(0);
+    read(stage_of(0), 0, f[0]);
+    for (int q = 0; q + 1 < nq; ++q) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if (s + 1 < NS) {
+          read(stage_of(q), s + 1, f[(s + 1) & 1]);
+        } else {
+          arrive(q + 1);
+          read(stage_of(q + 1), 0, f[0]);
+        }
+        mma(f[s & 1]);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if (s + 1 < NS) read(stage_of(nq - 1), s + 1, f[(s + 1) & 1]);
+      mma(f[s & 1]);
     }
   } else {
     for (int q = 0; q < nq; ++q) {
@@ -360,18 +411,24 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_grouped_matmul(MatmulArgs a)
       fx.regs(xwin((int64_t)q * KC), lds, wave, lane);
       fw.regs(wwin((int64_t)q * KC), lds + OX::BYTES, wave, lane);
       __syncthreads();
-      chunk_mma<T, NBN, NBM>(l0 + OX::BYTES, l0, rw, rx, 4, acc);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        Frags f;
+        read(l0, s, f);
+        mma(f);
+      }
     }
   }
 
   // ---- rows of Y: lane l holds row l % 32 of each row block, columns in fours
-  T* Y = static_cast<T*>(a.Y);
-  const bool vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * sizeof(T) - 1)) == 0;
+  using D = std::conditional_t<SPLIT, float, T>;
+  D* Y = SPLIT ? reinterpret_cast<D*>(a.part) + sp * a.R * a.N : static_cast<D*>(a.Y);
+  const bool vec = a.N % 4 == 0;
 #pragma unroll
   for (int i = 0; i < NBM; ++i) {
     const int64_t m = wm * WM + i * 32 + (lane & 31);
     if (m >= mrows) continue;
-    T* yr = Y + (row0 + m) * a.N;
+    D* yr = Y + (row0 + m) * a.N;
 #pragma unroll
     for (int j = 0; j < NBN; ++j)
 #pragma unroll
@@ -380,7 +437,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_grouped_matmul(MatmulArgs a)
         const f32x16& c = acc[j][i];
         if (vec) {
           if (n >= a.N) continue;
-          if constexpr (sizeof(T) == 2)
+          if constexpr (sizeof(D) == 2)
             *reinterpret_cast<uint2*>(yr + n) = make_uint2(pack_bf16(c[4 * q], c[4 * q + 1]),
                                                            pack_bf16(c[4 * q + 2], c[4 * q + 3]));
           else
@@ -389,11 +446,239 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_grouped_matmul(MatmulArgs a)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             if (n + r < a.N) {
-              if constexpr (sizeof(T) == 2) yr[n + r].u = f32_to_bf16(c[4 * q + r]);
+              if constexpr (sizeof(D) == 2) yr[n + r].u = f32_to_bf16(c[4 * q + r]);
               else yr[n + r] = c[4 * q + r];
             }
         }
       }
+  }
+}
+
+// The 256 x 256 tile of bf16 products, for up to 64 experts: one workgroup per
+// CU (128 KB of stages) that goes over its tiles in turn, as one stream of
+// chunks. The loads run ST - 1 chunks ahead of the products, into the next
+// tile where this one ends, so that neither the search for a tile nor its
+// first loads stand alone; only the writing of a tile's rows does, with the
+// next tile's loads in flight.
+//
+// Lane e of each wave holds expert e's row range and tile count, so a tile's
+// expert is found without memory, and the tiles are numbered without gaps.
+//
+// Each wave writes its 64 x 128 part of the tile through 4 KB of LDS of its
+// own (no barrier): 32 x 64 values at a time, 8-byte units swizzled by the
+// row, read back as 16-byte pieces and stored 128 contiguous bytes per row.
+template <bool TRANS>
+__global__ __launch_bounds__(512) void k_grouped_matmul_big(MatmulArgs a) {
+  using T = bf16s;
+  constexpr int BM = 256, BN = 256, WGM = 4, WGN = 2, NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN;
+  constexpr int NBM = WM / 32, NBN = WN / 32, KB = 64, ST = 4;
+  using OX = Opnd<T, true, BM, KB>;
+  using OW = Opnd<T, !TRANS, BN, KB>;
+  using FX = Filler<OX, T, NW>;
+  using FW = Filler<OW, T, NW>;
+  constexpr int KC = OX::KC, STAGE = OX::BYTES + OW::BYTES, LPC = FX::LOADS + FW::LOADS;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WGM, wn = wave / WGM;
+
+  // ---- the experts' rows and tiles
+  int off = 0, end = 0;
+  if (lane < a.E) {
+    off = (int)clamp_row(a.seg[(int64_t)lane * a.B], a.R);
+    end = (int)clamp_row(a.seg[(int64_t)(lane + 1) * a.B], a.R);
+  }
+  const int mine = end > off ? (end - off + BM - 1) / BM : 0;
+  int incl = mine;  // tiles of experts 0 .. lane
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d, kWave);
+    if (lane >= d) incl += v;
+  }
+  const int64_t slots = __builtin_amdgcn_readlane(incl, 63);
+  // this workgroup's items: its XCD's contiguous range, strided by the XCD's workgroups
+  const int64_t items = slots * a.ntn, per = (items + 7) / 8, wgs = gridDim.x >> 3, xcd = blockIdx.x & 7;
+  const int64_t w_end = (xcd + 1) * per < items ? (xcd + 1) * per : items;
+  int64_t w = xcd * per + (blockIdx.x >> 3);
+  if (w >= w_end) return;  // whole workgroup
+
+  struct Tile {
+    int64_t row0, mrows, e, n0;
+  };
+  auto tile_of = [&](int64_t item) {
+    const int64_t sg = item / (kSlotGroup * a.ntn), rem = item - sg * kSlotGroup * a.ntn;
+    const int64_t left = slots - sg * kSlotGroup, in_group = left < kSlotGroup ? left : kSlotGroup;
+    const int64_t tn = rem / in_group;
+    const int slot = (int)(sg * kSlotGroup + (rem - tn * in_group));
+    const int e = __popcll(__ballot(incl <= slot));  // the experts whose tiles all come before this one
+    const int t = slot - (__builtin_amdgcn_readlane(incl, e) - __builtin_amdgcn_readlane(mine, e));
+    const int row0 = __builtin_amdgcn_readlane(off, e) + t * BM;
+    const int rows = __builtin_amdgcn_readlane(end, e) - row0;
+    return Tile{row0, rows < BM ? rows : BM, e, tn * BN};
+  };
+
+  const int64_t xb = a.K * (int64_t)sizeof(T), wb = (TRANS ? a.N : a.K) * (int64_t)sizeof(T);
+  FX fx;
+  FW fw;
+  fx.init(xb, wave, lane);
+  fw.init(wb, wave, lane);
+  ReadOf<T, true, BM, NBM, KB> rx;
+  ReadOf<T, !TRANS, BN, NBN, KB> rw;
+  rx.init(wm * WM, lane);
+  rw.init(wn * WN, lane);
+  const int nq = (int)((a.K + KC - 1) / KC);
+  const uint32_t l0 = lds_addr(lds), eb = l0 + ST * STAGE + wave * 4096;
+
+  // ---- the loads' side: the next chunk to load and where it goes
+  Tile lt;
+  const T *lx, *lw;
+  int lk = 0;                // K left to load of its tile; <= 0 past the last tile: the loads go on, of empty windows
+  uint32_t ls = l0;          // stage
+  uint32_t xrows_b, wrows_b; // X: bytes of the rows before the window's last; W: the same, or (TRANS) its row's bytes
+  int wcols;                 // TRANS: columns of W from n0 on
+  auto load_tile = [&]() {
+    lt = tile_of(w);
+    lx = static_cast<const T*>(a.X) + lt.row0 * a.K;
+    lw = static_cast<const T*>(a.W) + lt.e * a.K * a.N + (TRANS ? lt.n0 : lt.n0 * a.K);
+    lk = (int)a.K;
+    xrows_b = (uint32_t)((lt.mrows - 1) * xb);
+    const int64_t n = a.N - lt.n0;
+    wrows_b = TRANS ? (uint32_t)(n * 2) : (uint32_t)(((n < BN ? n : BN) - 1) * wb);
+    wcols = (int)n;
+  };
+  auto xload = [&](int P) {
+    const u32x4 srd = make_srd(lx, lk > 0 ? xrows_b + 2u * (uint32_t)lk : 0u);
+    dma16_buf(srd, fx.qp[P] < lk ? fx.voff[P] : 0x80000000u, ls + (wave + NW * P) * 1024);
+  };
+  auto wload = [&](int P) {
+    const uint32_t krows = (uint32_t)(lk < KC ? lk : KC);
+    const uint32_t bytes = TRANS ? (krows - 1) * (uint32_t)wb + wrows_b : wrows_b + 2u * (uint32_t)lk;
+    const u32x4 srd = make_srd(lw, lk > 0 ? bytes : 0u);
+    dma16_buf(srd, fw.qp[P] < (TRANS ? wcols : lk) ? fw.voff[P] : 0x80000000u, ls + OX::BYTES + (wave + NW * P) * 1024);
+  };
+  auto load_next = [&]() {  // after a chunk's X and W parts
+    ls = ls == l0 + (ST - 1) * STAGE ? l0 : ls + STAGE;
+    lx += KC;
+    lw += TRANS ? KC * a.N : KC;
+    lk -= KC;
+    if (lk <= 0) {
+      w += wgs;
+      if (w < w_end) load_tile();
+    }
+  };
+  load_tile();
+
+  struct Frags {
+    u32x4 w[NBN], x[NBM];
+  };
+  auto read1 = [&](uint32_t sb, int s, Frags& f, int k) {  // the k-th of a step's fragments, in the order of their use
+    if (k == 0) f.w[0] = rw.get(sb + OX::BYTES, s, 0);
+    else if (k <= NBM) f.x[k - 1] = rx.get(sb, s, k - 1);
+    else f.w[k - NBM] = rw.get(sb + OX::BYTES, s, k - NBM);
+  };
+  f32x16 acc[NBN][NBM];
+  // One step: the products of `f`, and between them the reads of the next step's fragments and this wave's
+  // share of a later chunk's loads (its X or its W part). A burst of either would hold up the products.
+  auto step = [&](const Frags& f, Frags& g, uint32_t sb, int s, auto wpart) {
+#pragma unroll
+    for (int k = 0; k < NBN * NBM; ++k) {
+      const int j = k / NBM, i = k % NBM;
+      acc[j][i] = mma_step<T>(f.w[j], f.x[i], acc[j][i]);
+      if (k < NBN + NBM) read1(sb, s, g, k);
+      if (k % 4 == 1) {
+        if constexpr (decltype(wpart)::value) wload(k / 4);
+        else xload(k / 4);
+      }
+    }
+    if constexpr (decltype(wpart)::value) load_next();
+  };
+  static_assert(4 * FX::LOADS == NBM * NBN && 4 * FW::LOADS == NBM * NBN, "a load every four products");
+
+#pragma unroll
+  for (int q = 0; q < ST - 1; ++q) {
+#pragma unroll
+    for (int i = 0; i < FX::LOADS; ++i) xload(i);
+#pragma unroll
+    for (int i = 0; i < FW::LOADS; ++i) wload(i);
+    load_next();
+  }
+#pragma unroll
+  for (int i = 0; i < FX::LOADS; ++i) xload(i);
+  // Wait for the stream's next chunk, for every wave; every wave is then done with the chunk before it. Behind
+  // it in flight are ST - 2 whole chunks, at the first wait also the X part of one more, and after a tile's
+  // end the stores of its rows.
+  constexpr int kStores = NBM * (NBN / 2) * 4;
+  wait_vmcnt<LPC*(ST - 2) + FX::LOADS>();
+  lds_barrier();
+  Frags f0, f1;
+#pragma unroll
+  for (int k = 0; k < NBN + NBM; ++k) read1(l0, 0, f0, k);
+  uint32_t cs = l0;  // the chunk being multiplied
+  bool stored = false;
+  for (int64_t cw = xcd * per + (blockIdx.x >> 3); cw < w_end; cw += wgs) {
+    zero_acc(acc);
+    for (int q = 0; q < nq; ++q) {
+      step(f0, f1, cs, 1, std::true_type{});
+      if (stored) {
+        wait_vmcnt<LPC*(ST - 2) + kStores>();
+        stored = false;
+      } else {
+        wait_vmcnt<LPC*(ST - 2)>();
+      }
+      lds_barrier();
+      cs = cs == l0 + (ST - 1) * STAGE ? l0 : cs + STAGE;
+      step(f1, f0, cs, 0, std::false_type{});
+    }
+    // ---- this wave's rows: accumulator lane l holds row l % 32, columns 8q + 4(l / 32) .. + 3 of a 32-block
+    const Tile ct = tile_of(cw);
+    const uint32_t yb = (uint32_t)(ct.mrows * a.N * 2);
+    const __amdgpu_buffer_rsrc_t ysrd =
+        __builtin_amdgcn_make_buffer_rsrc(static_cast<T*>(a.Y) + ct.row0 * a.N, 0, yb, 0x00020000);
+    const int r = lane & 31, fr = (r >> 1) & 15;
+#pragma unroll
+    for (int i = 0; i < NBM; ++i)
+#pragma unroll
+      for (int h = 0; h < NBN / 2; ++h) {
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16& c = acc[2 * h + jj][i];
+            const int unit = jj * 8 + 2 * q + (lane >> 5);
+            u32x2 v;
+            v[0] = pack_bf16(c[4 * q], c[4 * q + 1]);
+            v[1] = pack_bf16(c[4 * q + 2], c[4 * q + 3]);
+            *(lds_u32x2*)(uintptr_t)(eb + r * 128 + 8 * (unit ^ fr)) = v;
+          }
+        lds_wave_fence();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int rr = 8 * t + (lane >> 3), pp = lane & 7, f2 = (rr >> 1) & 15;
+          u32x4 v = *(lds_u32x4*)(uintptr_t)(eb + rr * 128 + 16 * (pp ^ (f2 >> 1)));
+          if (f2 & 1) v = u32x4{v[2], v[3], v[0], v[1]};
+          const int64_t m = wm * WM + i * 32 + rr, n = ct.n0 + wn * WN + h * 64 + 8 * pp;
+          // always issued (the waits count the stores); rows and columns outside the tile are dropped
+          const uint32_t vo = m < ct.mrows && n < a.N ? (uint32_t)((m * a.N + n) * 2) : 0x80000000u;
+          __builtin_amdgcn_raw_buffer_store_b128(v, ysrd, vo, 0, 0);
+        }
+        lds_wave_fence();
+      }
+    stored = true;
+  }
+  wait_vmcnt<0>();  // the empty loads past the last tile: none may land after this workgroup's LDS is given away
+}
+
+// Y = the splits' partial products, added in order, for the rows that belong
+// to an expert.
+template <typename T>
+__global__ __launch_bounds__(256) void k_grouped_join(MatmulArgs a) {
+  const int64_t lo = clamp_row(a.seg[0], a.R), hi = clamp_row(a.seg[a.E * a.B], a.R);
+  const int64_t n = a.R * a.N;
+  for (int64_t i = lo * a.N + (int64_t)blockIdx.x * 256 + threadIdx.x; i < hi * a.N; i += (int64_t)gridDim.x * 256) {
+    float s = 0.f;
+#pragma unroll 4
+    for (int64_t k = 0; k < a.ks; ++k) s += a.part[k * n + i];
+    if constexpr (sizeof(T) == 2) static_cast<T*>(a.Y)[i].u = f32_to_bf16(s);
+    else static_cast<T*>(a.Y)[i] = s;
   }
 }
 
@@ -513,193 +798,711 @@ __global__ __launch_bounds__(64) void k_grouped_norm_finish(GNormArgs a, float* 
 }
 
 // ---------------------------------------------------------------------------
-// Clipped sums. A list of K pieces is formed first: piece t of segment g
-// covers up to KC rows of one sample and carries its clip factor, at slot
-// off_g / KC + g + t (rows = 0 where a slot is unused).
+// Clipped sums: out_e = sum_r c_r a_r g_r^T over the rows r of expert e, c_r
+// the clip factor of the row's sample. bf16 products leave no room for the
+// factor in an operand (c g rounded to bf16 would cost 2^-9 of the sum), so it
+// enters in one of three ways:
+//   ratio  (bf16, samples with about 32 rows or more per expert) K runs over
+//          pieces of up to 32 rows of one sample, the accumulators hold the
+//          sum divided by the current factor and are rescaled where the
+//          factor changes (one fp32 rounding per sample);
+//   split  (bf16, shorter ranges) K runs over the expert's rows as they lie; a
+//          chunk's A operand becomes c a = hi + mid + lo, three bf16 values
+//          that hold the 24 bits of the fp32 product (two would leave an error
+//          of 2^-17), and takes three products;
+//   fold   (bf16, 128 x 128 tiles) pieces as for ratio, each sample's product
+//          in a second accumulator set, added as acc += c tmp;
+//   scale  (fp32) the A operand is multiplied by c in fp32.
+
+// Piece t of segment g covers up to kPieceRows rows of one sample and carries
+// its clip factor, at slot off_g / kPieceRows + g + t (rows = 0: unused slot).
+constexpr int kPieceRows = 32;
 struct Piece {
   int32_t row0, rows;
-  int32_t last;  // last piece of its segment
   float c;
+  int32_t pad;
 };
 struct GSumArgs {
   const void *A, *G;
   const int64_t* seg;
-  const Piece* pieces;
+  const Piece* pieces;  // ratio
+  const float* crow;    // split, scale: factor of every row [R]
   int64_t R, E, B, d, p;
   int64_t mt, nt, ks;
-  float* ws;  // partials [ks][E*d][p]
+  NoiseArgs na;
+  float* out;    // ks == 1: the result [E*d][p], noise and mean applied
+  float* part;   // else the splits' sums [ks][E*d][p]
+  int fused;     // the epilogue writes out
+  int32_t* queue;  // next item of each XCD's list, past the workgroups' first ones
 };
 
-template <int KC>
 __global__ __launch_bounds__(256) void k_grouped_pieces(const int64_t* __restrict__ seg, int64_t R, int64_t E,
                                                         int64_t B, const float* __restrict__ c, int64_t slots,
-                                                        Piece* __restrict__ out) {
+                                                        Piece* __restrict__ out, int32_t* __restrict__ queue) {
   const int64_t slot = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (blockIdx.x == 0 && threadIdx.x < 8) queue[threadIdx.x] = 0;
   if (slot >= slots) return;
-  // the last g with off_g / KC + g <= slot, by each thread on its own
+  // the last g with off_g / kPieceRows + g <= slot, by each thread on its own
   int64_t g = 0, hi = E * B;
   while (hi - g > 1) {
     const int64_t mid = (g + hi) / 2;
-    if (clamp_row(seg[mid], R) / KC + mid <= slot) g = mid;
+    if (clamp_row(seg[mid], R) / kPieceRows + mid <= slot) g = mid;
     else hi = mid;
   }
   const int64_t off = clamp_row(seg[g], R), end = clamp_row(seg[g + 1], R);
-  const int64_t t = slot - (off / KC + g), row0 = off + t * KC;
-  Piece pc{0, 0, 0, 0.f};
+  const int64_t t = slot - (off / kPieceRows + g), row0 = off + t * kPieceRows;
+  Piece pc{0, 0, 0.f, 0};
   if (t >= 0 && row0 < end) {
     pc.row0 = (int32_t)row0;
-    pc.rows = (int32_t)(end - row0 < KC ? end - row0 : KC);
-    pc.last = row0 + KC >= end;
+    pc.rows = (int32_t)(end - row0 < kPieceRows ? end - row0 : kPieceRows);
     pc.c = c[g % B];
   }
   out[slot] = pc;
 }
 
-// One workgroup per (expert, tile of [d, p], split of the expert's pieces):
-// every piece's product accumulates unscaled and is folded in as
-// acc += c * tmp in fp32 at the end of its sample, so the clip factor is
-// applied exactly.
-template <typename T, int BM, int BN, int WGM, int WGN, int ST, bool DMA>
-__global__ __launch_bounds__(64 * WGM * WGN) void k_grouped_sum(GSumArgs a) {
-  constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, NBM = WM / 32, NBN = WN / 32;
-  using OA = Opnd<T, false, BM>;
-  using OG = Opnd<T, false, BN>;
-  constexpr int KC = OA::KC, STAGE = OA::BYTES + OG::BYTES;
-  extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
-
-  const int64_t tiles = a.mt * a.nt, items = a.E * tiles * a.ks;
-  const int64_t w = xcd_item(blockIdx.x, items);
-  if (w >= items) return;
-  const int64_t sp = w / (a.E * tiles), r0 = w - sp * a.E * tiles;
-  const int64_t e = r0 / tiles, t = r0 - e * tiles;
-  const int64_t tm = t % a.mt, tn = t / a.mt;
-  const int64_t m0 = tm * BM, n0 = tn * BN;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave % WGM, wn = wave / WGM;
-
-  // this split's slots
-  const int64_t g0 = e * a.B, g1 = (e + 1) * a.B;
-  const int64_t o0 = uniform64(clamp_row(a.seg[g0], a.R)), o1 = uniform64(clamp_row(a.seg[g1], a.R));
-  const int64_t s0 = o0 / KC + g0, s1 = o1 / KC + g1;
-  const int64_t per = (s1 - s0 + a.ks - 1) / a.ks;
-  const int64_t b0 = s0 + sp * per, b1 = b0 + per < s1 ? b0 + per : s1;
-
-  const T* A = static_cast<const T*>(a.A) + m0;
-  const T* G = static_cast<const T*>(a.G) + n0;
-  const int64_t ab = a.d * (int64_t)sizeof(T), gb = a.p * (int64_t)sizeof(T);
-  Filler<OA, T, NW> fa;
-  Filler<OG, T, NW> fg;
-  fa.init(ab, wave, lane);
-  fg.init(gb, wave, lane);
-  ReadF<T, BM, NBM> ra;
-  ReadF<T, BN, NBN> rg;
-  ra.init(wm * WM, lane);
-  rg.init(wn * WN, lane);
-
-  f32x16 acc[NBM][NBN], tmp[NBM][NBN];
-  zero_acc(acc);
-  zero_acc(tmp);
-  const uint32_t l0 = lds_addr(lds);
-
-  // The pieces in use, 64 slots at a time: lane i holds slot base + i. Two
-  // walkers go over them, one for the loads and one for the products.
-  struct Walk {
-    int64_t base;
-    uint64_t mask;
-    Piece mine;
-  };
-  auto load64 = [&](Walk& wk) {
-    wk.mine = Piece{0, 0, 0, 0.f};
-    if (wk.base + lane < b1) wk.mine = a.pieces[wk.base + lane];
-    wk.mask = __ballot(wk.mine.rows > 0);
-  };
-  auto next = [&](Walk& wk, Piece* pc) -> bool {
-    while (wk.mask == 0) {
-      wk.base += 64;
-      if (wk.base >= b1) return false;
-      load64(wk);
+// The clip factor of every row; 0 for rows outside the segments.
+__global__ __launch_bounds__(256) void k_grouped_row_factors(const int64_t* __restrict__ seg, int64_t R, int64_t E,
+                                                             int64_t B, const float* __restrict__ c,
+                                                             float* __restrict__ crow, int32_t* __restrict__ queue) {
+  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (blockIdx.x == 0 && threadIdx.x < 8) queue[threadIdx.x] = 0;
+  if (row >= R) return;
+  float v = 0.f;
+  if (row >= seg[0] && row < seg[E * B]) {
+    int64_t g = 0, hi = E * B;  // the last segment that starts at or before the row
+    while (hi - g > 1) {
+      const int64_t mid = (g + hi) / 2;
+      if (seg[mid] <= row) g = mid;
+      else hi = mid;
     }
-    const int i = __ffsll((unsigned long long)wk.mask) - 1;
-    wk.mask &= wk.mask - 1;
-    pc->row0 = __builtin_amdgcn_readlane(wk.mine.row0, i);
-    pc->rows = __builtin_amdgcn_readlane(wk.mine.rows, i);
-    pc->last = __builtin_amdgcn_readlane(wk.mine.last, i);
-    pc->c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wk.mine.c), i));
-    return true;
-  };
-  auto awin = [&](const Piece& pc) { return Win<T>{A + pc.row0 * a.d, ab, pc.rows, a.d - m0}; };
-  auto gwin = [&](const Piece& pc) { return Win<T>{G + pc.row0 * a.p, gb, pc.rows, a.p - n0}; };
-  auto steps_of = [&](const Piece& pc) { return (pc.rows + KC / 4 - 1) / (KC / 4); };
-
-  bool open = false;
-  float cur = 0.f;
-  auto fold = [&]() {
-#pragma unroll
-    for (int i = 0; i < NBM; ++i)
-#pragma unroll
-      for (int j = 0; j < NBN; ++j)
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          acc[i][j][k] = __builtin_fmaf(cur, tmp[i][j][k], acc[i][j][k]);
-          tmp[i][j][k] = 0.f;
-        }
-    open = false;
-  };
-  if (b0 < b1) {
-    Walk wl{b0, 0, {}};
-    load64(wl);
-    if constexpr (DMA) {
-      static_assert(ST == 2, "one piece ahead");
-      Piece cp, np;
-      bool have = next(wl, &cp);
-      int q = 0;
-      if (have) {
-        fa.dma(awin(cp), l0, wave);
-        fg.dma(gwin(cp), l0 + OA::BYTES, wave);
-      }
-      while (have) {
-        wait_vmcnt<0>();
-        lds_barrier();
-        const bool more = next(wl, &np);
-        const uint32_t sb = l0 + (uint32_t)(q & 1) * STAGE, sn = l0 + (uint32_t)((q + 1) & 1) * STAGE;
-        if (more) {
-          fa.dma(awin(np), sn, wave);
-          fg.dma(gwin(np), sn + OA::BYTES, wave);
-        }
-        chunk_mma<T, NBM, NBN>(sb, sb + OA::BYTES, ra, rg, steps_of(cp), tmp);
-        cur = cp.c;
-        open = true;
-        if (cp.last) fold();
-        cp = np;
-        have = more;
-        ++q;
-      }
-    } else {
-      Piece cp;
-      while (next(wl, &cp)) {
-        __syncthreads();
-        fa.regs(awin(cp), lds, wave, lane);
-        fg.regs(gwin(cp), lds + OA::BYTES, wave, lane);
-        __syncthreads();
-        chunk_mma<T, NBM, NBN>(l0, l0 + OA::BYTES, ra, rg, steps_of(cp), tmp);
-        cur = cp.c;
-        open = true;
-        if (cp.last) fold();
-      }
-    }
-    if (open) fold();
+    v = c[g % B];
   }
+  crow[row] = v;
+}
 
-  float* out = a.ws + (sp * a.E + e) * a.d * a.p;
+// c a of eight (k, feature) elements as three bf16 terms; ck: the eight rows' factors.
+__device__ __forceinline__ void split_scaled(u32x4 a, const f32x4 (&ck)[2], u32x4 (&t)[3]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float y0 = __uint_as_float(a[e] << 16) * ck[e >> 1][2 * (e & 1)];
+    float y1 = __uint_as_float(a[e] & 0xFFFF0000u) * ck[e >> 1][2 * (e & 1) + 1];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t h = pack_bf16(y0, y1);
+      t[k][e] = h;
+      y0 -= __uint_as_float(h << 16);  // exact
+      y1 -= __uint_as_float(h & 0xFFFF0000u);
+    }
+  }
+}
+
+// 4 bytes per lane from a buffer straight into LDS
+__device__ __forceinline__ void dma4_buf(u32x4 srd, uint32_t voff, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(srd),
+               "s"(lds_base)
+               : "memory", "m0");
+}
+
+// A wave's accumulators to the result: (S + sc z) * inv_denom, or S itself as
+// a split's partial (sc = 0, inv_denom = 1 there). Half a 32x32 block at a time
+// goes through 2 KB of the wave's own LDS (16 rows of 32 fp32), so that rows
+// are stored 128 bytes at a time, and the four rows of a quad, which share a
+// Philox block, are drawn by one lane (d is a multiple of 4 where noise is
+// added here, so quads start at multiples of 4 of the flat row e*d + m).
+struct Emit {
+  float* dst;  // [d][p]
+  int64_t d, p, e;
+  bool vec;  // 16-byte stores
+};
+template <int NBM, int NBN>
+__device__ __forceinline__ void emit_tile(const f32x16 (&acc)[NBM][NBN], const Emit& o, const NoiseArgs& na,
+                                          uint32_t scratch, int64_t m0, int64_t n0, int lane) {
+  typedef __attribute__((address_space(3))) float lds_f;
 #pragma unroll
   for (int i = 0; i < NBM; ++i)
 #pragma unroll
     for (int j = 0; j < NBN; ++j)
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int64_t m = m0 + wm * WM + i * 32 + acc_row(k, lane), n = n0 + wn * WN + j * 32 + acc_col(lane);
-        if (m < a.d && n < a.p) out[m * a.p + n] = acc[i][j][k];
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            *(lds_f*)(uintptr_t)(scratch + 128 * (8 * q + 4 * (lane >> 5) + r) + 4 * (lane & 31)) =
+                acc[i][j][8 * h + 4 * q + r];
+        lds_wave_fence();
+        const int64_t mb = m0 + 32 * i + 16 * h, nb = n0 + 32 * j;
+        if (na.sc == 0.0f) {
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            const int row = 8 * t + (lane >> 3), c4 = 4 * (lane & 7);
+            f32x4 v = __builtin_bit_cast(f32x4, *(lds_u32x4*)(uintptr_t)(scratch + 128 * row + 4 * c4));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = noised_mean_spec(v[k], 0.0f, 0.0f, na.inv_denom);
+            const int64_t m = mb + row, n = nb + c4;
+            if (m >= o.d || n >= o.p) continue;
+            float* dst = o.dst + m * o.p + n;
+            if (o.vec) {
+              *reinterpret_cast<f32x4*>(dst) = v;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (n + k < o.p) dst[k] = v[k];
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            const int quad = 2 * t + (lane >> 5);
+            const int64_t m = mb + 4 * quad, n = nb + (lane & 31);
+            if (m >= o.d || n >= o.p) continue;
+            const f32x4 z = normals4((uint32_t)(((o.e * o.d + m) >> 2) * o.p + n), 2u * na.layer, na.step, 0u, na.k0,
+                                     na.k1);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float S = *(lds_f*)(uintptr_t)(scratch + 128 * (4 * quad + r) + 4 * (lane & 31));
+              if (m + r < o.d) o.dst[(m + r) * o.p + n] = noised_mean_spec(S, na.sc, z[r], na.inv_denom);
+            }
+          }
+        }
+        lds_wave_fence();
       }
+}
+
+__device__ __forceinline__ Emit emit_at(const GSumArgs& a, int64_t e, int64_t sp) {
+  float* dst = a.fused ? a.out + e * a.d * a.p : a.part + (sp * a.E + e) * a.d * a.p;
+  return Emit{dst, a.d, a.p, e, a.p % 4 == 0 && (reinterpret_cast<uintptr_t>(a.fused ? a.out : a.part) & 15) == 0};
+}
+
+// bf16, 256 x 256 tiles, one workgroup per CU over its (expert, split, tile)
+// items in turn, as one stream of 32-row chunks (the structure of
+// k_grouped_matmul_big; both operands are read with transposing LDS reads).
+// XCD x takes its share of every expert's tiles, experts with more rows
+// first, and its workgroups take the next item off the XCD's list as they
+// come free: uneven experts even out, and the workgroups share operand tiles
+// in their L2. (Which workgroup forms an item does not enter its result.)
+template <bool RATIO>
+__global__ __launch_bounds__(512) void k_grouped_sum_big(GSumArgs a) {
+  using T = bf16s;
+  constexpr int BM = 256, BN = 256, WGM = 4, WGN = 2, NW = 8, WM = 64, WN = 128, NBM = 2, NBN = 4, KB = 64, ST = 4;
+  using OA = Opnd<T, false, BM, KB>;
+  using OG = Opnd<T, false, BN, KB>;
+  using FA = Filler<OA, T, NW>;
+  using FG = Filler<OG, T, NW>;
+  static_assert(OA::KC == kPieceRows, "a chunk holds a piece");
+  constexpr int KC = 32, CB = RATIO ? 0 : NW * 128;  // split: the rows' factors, a copy per wave
+  constexpr int STAGE = OA::BYTES + OG::BYTES + CB, LPC = FA::LOADS + FG::LOADS + (RATIO ? 0 : 1);
+  extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WGM, wn = wave / WGM;
+
+  // ---- experts by rows, the largest first (up to 64 of them; more keep their order)
+  int order = lane;
+  if (a.E <= 64) {
+    int mine = -1;
+    if (lane < a.E) mine = (int)(clamp_row(a.seg[(int64_t)(lane + 1) * a.B], a.R) - clamp_row(a.seg[(int64_t)lane * a.B], a.R));
+    int rank = 0;
+    for (int j = 0; j < (int)a.E; ++j) {
+      const int o = __builtin_amdgcn_readlane(mine, j);
+      rank += o > mine || (o == mine && j < lane);
+    }
+    // lane r <- the expert of rank r
+    for (int j = 0; j < (int)a.E; ++j)
+      if (__builtin_amdgcn_readlane(rank, j) == lane) order = j;
+  }
+
+  // ---- items: (expert by rank, split, tile of this XCD's share), tiles fastest
+  const int64_t tiles = a.mt * a.nt, per = (tiles + 7) / 8, wgs = gridDim.x >> 3, xcd = blockIdx.x & 7;
+  const int share_t = (int)(tiles - xcd * per < per ? tiles - xcd * per : per);
+  const int nlocal = share_t > 0 ? (int)(a.E * a.ks) * share_t : 0;
+  if ((int)(blockIdx.x >> 3) >= nlocal) return;  // whole workgroup
+  struct Item {
+    int64_t e, sp, m0, n0;
+  };
+  auto item_at = [&](int l) {
+    const int ri = l / share_t, er = ri / (int)a.ks;
+    const int64_t t = xcd * per + (l - ri * share_t);
+    Item it;
+    it.sp = ri - er * (int)a.ks;
+    it.e = a.E <= 64 ? __builtin_amdgcn_readlane(order, er) : er;
+    it.m0 = (t % a.mt) * BM;
+    it.n0 = (t / a.mt) * BN;
+    return it;
+  };
+
+  const int64_t ab = a.d * 2, gb = a.p * 2;
+  FA fa;
+  FG fg;
+  fa.init(ab, wave, lane);
+  fg.init(gb, wave, lane);
+  ReadF<T, BM, NBM, KB> ra;
+  ReadF<T, BN, NBN, KB> rg;
+  ra.init(wm * WM, lane);
+  rg.init(wn * WN, lane);
+  const uint32_t l0 = lds_addr(lds);
+
+  // ---- the loads' side. Its chunk: rows [lrow, lrow + lrows) of item lit; lrows = 0: an empty window (past the
+  // last item, for an expert without rows, or for a sample with factor 0, whose rows add nothing).
+  __shared__ int next_item[2];
+  int litem = (int)(blockIdx.x >> 3), turn = 0;
+  bool first = true;
+  if (threadIdx.x == 0) next_item[0] = (int)wgs + atomicAdd(a.queue + xcd, 1);
+  __syncthreads();
+  Item lit{0, 0, 0, 0};
+  int64_t lrow = 0;
+  int lrows = 0;
+  bool lopen = false;        // the item has chunks left
+  int64_t lpos = 0, lend = 0;  // ratio: slot window and end; split: next row and end
+  uint64_t lmask = 0;
+  Piece lmine{0, 0, 0.f, 0};
+  uint32_t ls = l0;
+  struct Desc {
+    float c;
+    int end;   // last chunk of its item
+    int item;  // -1: past the last
+  };
+  auto load64 = [&]() {
+    lmine = Piece{0, 0, 0.f, 0};
+    if (lpos + lane < lend) lmine = a.pieces[lpos + lane];
+    lmask = __ballot(lmine.rows > 0);
+  };
+  auto skip_unused = [&]() {
+    while (lmask == 0 && lpos + 64 < lend) {
+      lpos += 64;
+      load64();
+    }
+  };
+  auto fetch = [&]() -> Desc {  // the next chunk
+    Desc ds{0.f, 0, -1};
+    lrows = 0;
+    if (!lopen) {
+      // The item after this one is taken off the list now, by the first wave, and read by all when this one's
+      // chunks have been fetched: at least one barrier later.
+      if (first) {
+        first = false;
+      } else if (litem >= 0) {
+        litem = __builtin_amdgcn_readfirstlane(next_item[turn]);
+        turn ^= 1;
+        if (wave == 0 && lane == 0) next_item[turn] = (int)wgs + atomicAdd(a.queue + xcd, 1);
+      }
+      if (litem < 0 || litem >= nlocal) {
+        litem = -1;
+        return ds;
+      }
+      lit = item_at(litem);
+      const int64_t g0 = lit.e * a.B, g1 = g0 + a.B;
+      const int64_t o0 = uniform64(clamp_row(a.seg[g0], a.R)), o1 = uniform64(clamp_row(a.seg[g1], a.R));
+      // the split's share of the expert's slots, or of its rows in whole chunks
+      const int64_t s0 = RATIO ? o0 / KC + g0 : 0, s1 = RATIO ? o1 / KC + g1 : (o1 - o0 + KC - 1) / KC;
+      const int64_t share = (s1 - s0 + a.ks - 1) / a.ks;
+      const int64_t b0 = s0 + lit.sp * share, b1 = b0 + share < s1 ? b0 + share : s1;
+      lpos = RATIO ? b0 : o0 + b0 * KC;
+      lend = RATIO ? b1 : (o0 + b1 * KC < o1 ? o0 + b1 * KC : o1);
+      if constexpr (RATIO) {
+        lmask = 0;
+        if (lpos < lend) {
+          load64();
+          skip_unused();
+        }
+      }
+    }
+    ds.item = litem;
+    if constexpr (RATIO) {
+      if (lmask == 0) {  // no rows in this item: one empty chunk
+        lopen = false;
+        ds.end = 1;
+        return ds;
+      }
+      const int i = __ffsll((unsigned long long)lmask) - 1;
+      lmask &= lmask - 1;
+      lrow = __builtin_amdgcn_readlane(lmine.row0, i);
+      lrows = __builtin_amdgcn_readlane(lmine.rows, i);
+      ds.c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lmine.c), i));
+      if (ds.c == 0.0f) lrows = 0;
+      skip_unused();
+      lopen = lmask != 0;
+    } else {
+      if (lpos < lend) {
+        lrow = lpos;
+        lrows = (int)(lend - lpos < KC ? lend - lpos : KC);
+        lpos += KC;
+      }
+      lopen = lpos < lend;
+    }
+    ds.end = !lopen;
+    return ds;
+  };
+  auto aload = [&](int P) {
+    const u32x4 srd = make_srd(static_cast<const T*>(a.A) + lrow * a.d + lit.m0,
+                               lrows > 0 ? (uint32_t)((lrows - 1) * ab + (a.d - lit.m0) * 2) : 0u);
+    dma16_buf(srd, fa.qp[P] < (int)(a.d - lit.m0) ? fa.voff[P] : 0x80000000u, ls + (wave + NW * P) * 1024);
+  };
+  auto gload = [&](int P) {
+    const u32x4 srd = make_srd(static_cast<const T*>(a.G) + lrow * a.p + lit.n0,
+                               lrows > 0 ? (uint32_t)((lrows - 1) * gb + (a.p - lit.n0) * 2) : 0u);
+    dma16_buf(srd, fg.qp[P] < (int)(a.p - lit.n0) ? fg.voff[P] : 0x80000000u,
+              ls + OA::BYTES + (wave + NW * P) * 1024);
+  };
+  auto cload = [&]() {
+    if constexpr (!RATIO) {
+      const u32x4 srd = make_srd(a.crow + lrow, 4u * (uint32_t)lrows);
+      if (lane < KC) dma4_buf(srd, 4u * lane, ls + OA::BYTES + OG::BYTES + wave * 128);
+    }
+  };
+  auto next_stage = [&](uint32_t st) { return st == l0 + (ST - 1) * STAGE ? l0 : st + STAGE; };
+
+  struct Frags {
+    u32x4 a[NBM], g[NBN];
+  };
+  // the k-th of a step's fragments, in the order of their use
+  auto read1 = [&](uint32_t sb, int s, Frags& f, int k) {
+    if (k < NBM) f.a[k] = ra.get(sb, s, k);
+    else f.g[k - NBM] = rg.get(sb + OA::BYTES, s, k - NBM);
+  };
+  f32x16 acc[NBM][NBN];
+  // One step (16 rows): as in k_grouped_matmul_big, the next step's reads and a later chunk's loads between the
+  // products. With split, sb/s of the fragments in hand give the rows' factors.
+  auto step = [&](const Frags& f, uint32_t csb, int cstep, Frags& g, uint32_t sb, int s, auto gpart) {
+    u32x4 t[NBM][3];
+    if constexpr (!RATIO) {
+      f32x4 ck[2];
+      const uint32_t cb = csb + OA::BYTES + OG::BYTES + wave * 128 + 4 * (16 * cstep + 8 * (lane >> 5));
+      ck[0] = __builtin_bit_cast(f32x4, *(lds_u32x4*)(uintptr_t)cb);
+      ck[1] = __builtin_bit_cast(f32x4, *(lds_u32x4*)(uintptr_t)(cb + 16));
+#pragma unroll
+      for (int i = 0; i < NBM; ++i) split_scaled(f.a[i], ck, t[i]);
+    }
+#pragma unroll
+    for (int k = 0; k < NBM * NBN; ++k) {
+      const int j = k / NBM, i = k % NBM;
+      if constexpr (RATIO) {
+        acc[i][j] = mfma32_bf16(f.a[i], f.g[j], acc[i][j]);
+      } else {
+#pragma unroll
+        for (int u = 2; u >= 0; --u) acc[i][j] = mfma32_bf16(t[i][u], f.g[j], acc[i][j]);  // the small terms first
+      }
+      if (k < NBN + NBM) read1(sb, s, g, k);
+      if (k % 4 == 1) {
+        if constexpr (decltype(gpart)::value) gload(k / 4);
+        else aload(k / 4);
+      }
+    }
+    if constexpr (decltype(gpart)::value) {
+      cload();
+      ls = next_stage(ls);
+    }
+  };
+  static_assert(4 * FA::LOADS == NBM * NBN && 4 * FG::LOADS == NBM * NBN, "a load every four products");
+
+  // ---- the stream: descriptors of the chunk being multiplied and the ones in flight
+  Desc q0 = fetch();
+  auto issue_all = [&]() {
+#pragma unroll
+    for (int i = 0; i < FA::LOADS; ++i) aload(i);
+#pragma unroll
+    for (int i = 0; i < FG::LOADS; ++i) gload(i);
+    cload();
+    ls = next_stage(ls);
+  };
+  issue_all();
+  lds_barrier();  // between fetches: see there
+  Desc q1 = fetch();
+  issue_all();
+  lds_barrier();
+  Desc q2 = fetch();
+  issue_all();
+  lds_barrier();
+  Desc q3 = fetch();
+#pragma unroll
+  for (int i = 0; i < FA::LOADS; ++i) aload(i);
+  static_assert(ST == 4, "three chunks ahead");
+  wait_vmcnt<LPC*(ST - 2) + FA::LOADS>();
+  lds_barrier();
+  Frags f0, f1;
+#pragma unroll
+  for (int k = 0; k < NBN + NBM; ++k) read1(l0, 0, f0, k);
+  uint32_t cs = l0;
+
+  while (q0.item >= 0) {
+    const Item it = item_at(q0.item);
+    const Emit em = emit_at(a, it.e, it.sp);
+    zero_acc(acc);
+    float prev = 0.f, ref = 0.f;  // ratio: the factor acc is in units of, and that of the run's first sample
+    bool flushed = false;
+    // this lane's elements inside [0, d) x [0, p): element = f(element, its place in the result)
+    auto for_elems = [&](auto f) {
+      // an opaque copy of the row stride: the addresses are formed where they are used (rarely), not ahead of
+      // the loop and held in registers through it
+      int64_t ps = a.p;
+      asm volatile("" : "+s"(ps));
+      const int64_t lr = it.m0 + wm * WM + 4 * (lane >> 5), lc = it.n0 + wn * WN + (lane & 31);
+      float* const base = em.dst + lr * ps + lc;
+      const int64_t rem_r = a.d - lr, rem_c = a.p - lc;
+#pragma unroll
+      for (int i = 0; i < NBM; ++i)
+#pragma unroll
+        for (int j = 0; j < NBN; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int ro = i * 32 + 8 * (k >> 2) + (k & 3), co = j * 32;
+            if (ro < rem_r && co < rem_c) acc[i][j][k] = f(acc[i][j][k], base + ro * ps + co);
+          }
+    };
+    while (true) {
+      if constexpr (RATIO) {
+        if (q0.c != 0.0f && q0.c != prev) {
+          if (prev != 0.0f) {
+            const float mag = fabsf(q0.c), rmag = fabsf(ref);
+            float r;
+            if (mag < rmag * 0x1p-32f || mag > rmag * 0x1p32f) {
+              // factors this far apart would overflow the quotient: bank the sum so far in the result's place
+              for_elems([&](float v, float* o) {
+                *o = flushed ? *o + v * prev : v * prev;
+                return v;
+              });
+              flushed = true;
+              ref = q0.c;
+              r = 0.0f;
+            } else {
+              r = prev / q0.c;
+            }
+#pragma unroll
+            for (int i = 0; i < NBM; ++i)
+#pragma unroll
+              for (int j = 0; j < NBN; ++j)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) acc[i][j][k] *= r;
+          } else {
+            ref = q0.c;
+          }
+          prev = q0.c;
+        }
+      }
+      step(f0, cs, 0, f1, cs, 1, std::true_type{});
+      const Desc q4 = fetch();
+      wait_vmcnt<LPC*(ST - 2)>();
+      lds_barrier();
+      const uint32_t nx = next_stage(cs);
+      step(f1, cs, 1, f0, nx, 0, std::false_type{});
+      cs = nx;
+      const int end = q0.end;
+      q0 = q1;
+      q1 = q2;
+      q2 = q3;
+      q3 = q4;
+      if (end) break;
+    }
+    if constexpr (RATIO) {
+      // back to units of 1, and the banked part (if any)
+#pragma unroll
+      for (int i = 0; i < NBM; ++i)
+#pragma unroll
+        for (int j = 0; j < NBN; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) acc[i][j][k] *= prev;
+      if (flushed) for_elems([&](float v, const float* o) { return v + *o; });
+    }
+    emit_tile<NBM, NBN>(acc, em, a.na, l0 + ST * STAGE + wave * 2048, it.m0 + wm * WM, it.n0 + wn * WN, lane);
+  }
+  wait_vmcnt<0>();  // the empty loads past the last item: none may land after this workgroup's LDS is given away
+}
+
+// Any widths and both types, 128 x 128 tiles, one workgroup per (expert, split,
+// tile). FOLD: pieces of one sample; else the expert's rows as they lie (scale
+// for fp32, split for bf16).
+template <typename T, bool FOLD, bool DMA>
+__global__ __launch_bounds__(256) void k_grouped_sum(GSumArgs a) {
+  constexpr int BM = 128, BN = 128, WGM = 2, NW = 4, WM = 64, WN = 64, NBM = 2, NBN = 2, ST = 2;
+  constexpr bool SPLIT = !FOLD && sizeof(T) == 2;
+  constexpr int KB = FOLD ? 64 : 128;
+  using OA = Opnd<T, false, BM, KB>;
+  using OG = Opnd<T, false, BN, KB>;
+  constexpr int KC = OA::KC, STAGE = OA::BYTES + OG::BYTES + (FOLD ? 0 : NW * 256);
+  static_assert(!FOLD || (sizeof(T) == 2 && KC == kPieceRows), "fold: bf16 pieces");
+  constexpr int NC = 32 / sizeof(T);  // rows per step
+  extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
+  // XCD x takes its share of the tiles of every (expert, split)
+  const int64_t tiles = a.mt * a.nt, per = (tiles + 7) / 8, local = blockIdx.x >> 3;
+  const int64_t es = local / per, t = (blockIdx.x & 7) * per + (local - es * per);
+  if (t >= tiles) return;
+  const int64_t e = es / a.ks, sp = es - e * a.ks;
+  const int64_t m0 = (t % a.mt) * BM, n0 = (t / a.mt) * BN;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WGM, wn = wave / WGM;
+
+  // this split's share of the expert's slots (FOLD) or chunks
+  const int64_t g0 = e * a.B, g1 = g0 + a.B;
+  const int64_t o0 = uniform64(clamp_row(a.seg[g0], a.R)), o1 = uniform64(clamp_row(a.seg[g1], a.R));
+  const int64_t s0 = FOLD ? o0 / KC + g0 : 0, s1 = FOLD ? o1 / KC + g1 : (o1 > o0 ? (o1 - o0 + KC - 1) / KC : 0);
+  const int64_t share = (s1 - s0 + a.ks - 1) / a.ks;
+  const int64_t c0 = s0 + sp * share, c1 = c0 + share < s1 ? c0 + share : s1;
+
+  const int64_t ab = a.d * (int64_t)sizeof(T), gb = a.p * (int64_t)sizeof(T);
+  Filler<OA, T, NW> fa;
+  Filler<OG, T, NW> fg;
+  fa.init(ab, wave, lane);
+  fg.init(gb, wave, lane);
+  ReadF<T, BM, NBM, KB> ra;
+  ReadF<T, BN, NBN, KB> rg;
+  ra.init(wm * WM, lane);
+  rg.init(wn * WN, lane);
+  const uint32_t l0 = lds_addr(lds);
+
+  f32x16 acc[NBM][NBN];
+  zero_acc(acc);
+  const T* A = static_cast<const T*>(a.A) + m0;
+  const T* G = static_cast<const T*>(a.G) + n0;
+  auto awin = [&](int64_t row, int64_t rows) { return Win<T>{A + row * a.d, ab, rows, a.d - m0}; };
+  auto gwin = [&](int64_t row, int64_t rows) { return Win<T>{G + row * a.p, gb, rows, a.p - n0}; };
+
+  if constexpr (FOLD) {
+    f32x16 tmp[NBM][NBN];
+    zero_acc(tmp);
+    float cur = 0.f;
+    auto fold = [&]() {
+#pragma unroll
+      for (int i = 0; i < NBM; ++i)
+#pragma unroll
+        for (int j = 0; j < NBN; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            acc[i][j][k] = __builtin_fmaf(cur, tmp[i][j][k], acc[i][j][k]);
+            tmp[i][j][k] = 0.f;
+          }
+    };
+    // the pieces in use, 64 slots at a time: lane i holds slot pos + i
+    int64_t pos = c0;
+    uint64_t mask = 0;
+    Piece mine{0, 0, 0.f, 0};
+    auto load64 = [&]() {
+      mine = Piece{0, 0, 0.f, 0};
+      if (pos + lane < c1) mine = a.pieces[pos + lane];
+      mask = __ballot(mine.rows > 0 && mine.c != 0.0f);  // a factor of 0: its rows add nothing
+    };
+    auto next = [&](Piece* pc) -> bool {
+      while (mask == 0) {
+        pos += 64;
+        if (pos >= c1) return false;
+        load64();
+      }
+      const int i = __ffsll((unsigned long long)mask) - 1;
+      mask &= mask - 1;
+      pc->row0 = __builtin_amdgcn_readlane(mine.row0, i);
+      pc->rows = __builtin_amdgcn_readlane(mine.rows, i);
+      pc->c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine.c), i));
+      return true;
+    };
+    auto use = [&](const Piece& pc, uint32_t sb) {
+      if (!(pc.c == cur)) {  // another factor (or NaN): what was gathered under the last one is folded in
+        fold();
+        cur = pc.c;
+      }
+      chunk_mma<T, NBM, NBN>(sb, sb + OA::BYTES, ra, rg, pc.rows > 16 ? 2 : 1, tmp);
+    };
+    if (c0 < c1) {
+      load64();
+      Piece cp, np{0, 0, 0.f, 0};
+      bool have = next(&cp);
+      if constexpr (DMA) {
+        auto issue = [&](const Piece& pc, uint32_t sb) {
+          fa.dma(awin(pc.row0, pc.rows), sb, wave);
+          fg.dma(gwin(pc.row0, pc.rows), sb + OA::BYTES, wave);
+        };
+        uint32_t sb = l0, sn = l0 + STAGE;
+        if (have) issue(cp, sb);
+        while (have) {
+          wait_vmcnt<0>();
+          lds_barrier();
+          const bool more = next(&np);
+          if (more) issue(np, sn);
+          use(cp, sb);
+          cp = np;
+          have = more;
+          const uint32_t x = sb;
+          sb = sn;
+          sn = x;
+        }
+      } else {
+        while (have) {
+          __syncthreads();
+          fa.regs(awin(cp.row0, cp.rows), lds, wave, lane);
+          fg.regs(gwin(cp.row0, cp.rows), lds + OA::BYTES, wave, lane);
+          __syncthreads();
+          use(cp, l0);
+          have = next(&cp);
+        }
+      }
+      fold();
+    }
+  } else {
+    auto chunk = [&](uint32_t sb) {
+      const uint32_t cb = sb + OA::BYTES + OG::BYTES + wave * 256;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        u32x4 fragA[NBM], fragG[NBN];
+#pragma unroll
+        for (int i = 0; i < NBM; ++i) fragA[i] = ra.get(sb, s, i);
+#pragma unroll
+        for (int j = 0; j < NBN; ++j) fragG[j] = rg.get(sb + OA::BYTES, s, j);
+        const uint32_t cl = cb + 4 * (NC * s + NC / 2 * (lane >> 5));
+        f32x4 ck[2];
+        ck[0] = __builtin_bit_cast(f32x4, *(lds_u32x4*)(uintptr_t)cl);
+        if constexpr (SPLIT) {
+          ck[1] = __builtin_bit_cast(f32x4, *(lds_u32x4*)(uintptr_t)(cl + 16));
+#pragma unroll
+          for (int i = 0; i < NBM; ++i) {
+            u32x4 tr[3];
+            split_scaled(fragA[i], ck, tr);
+#pragma unroll
+            for (int u = 2; u >= 0; --u)
+#pragma unroll
+              for (int j = 0; j < NBN; ++j) acc[i][j] = mfma32_bf16(tr[u], fragG[j], acc[i][j]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NBM; ++i)
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4) fragA[i][e4] = __float_as_uint(__uint_as_float(fragA[i][e4]) * ck[0][e4]);
+#pragma unroll
+          for (int i = 0; i < NBM; ++i)
+#pragma unroll
+            for (int j = 0; j < NBN; ++j) acc[i][j] = mma_step<T>(fragA[i], fragG[j], acc[i][j]);
+        }
+      }
+    };
+    auto crows = [&](int64_t q, uint32_t dst) {  // the chunk's factors (KC <= 64 of them), a copy per wave
+      const int64_t row = o0 + q * KC, left = o1 - row < KC ? o1 - row : KC;
+      dma4_buf(make_srd(a.crow + row, 4u * (uint32_t)left), 4u * lane, dst + wave * 256);
+    };
+    auto rows_of = [&](int64_t q) { return o1 - (o0 + q * KC); };
+    if constexpr (DMA) {
+      auto issue = [&](int64_t q) {
+        const uint32_t sb = l0 + (uint32_t)((q - c0) % ST) * STAGE;
+        fa.dma(awin(o0 + q * KC, rows_of(q)), sb, wave);
+        fg.dma(gwin(o0 + q * KC, rows_of(q)), sb + OA::BYTES, wave);
+        crows(q, sb + OA::BYTES + OG::BYTES);
+      };
+      if (c0 < c1) issue(c0);
+      for (int64_t q = c0; q < c1; ++q) {
+        wait_vmcnt<0>();
+        lds_barrier();
+        if (q + 1 < c1) issue(q + 1);
+        chunk(l0 + (uint32_t)((q - c0) % ST) * STAGE);
+      }
+    } else {
+      for (int64_t q = c0; q < c1; ++q) {
+        __syncthreads();
+        crows(q, l0 + OA::BYTES + OG::BYTES);
+        fa.regs(awin(o0 + q * KC, rows_of(q)), lds, wave, lane);
+        fg.regs(gwin(o0 + q * KC, rows_of(q)), lds + OA::BYTES, wave, lane);
+        wait_vmcnt<0>();
+        __syncthreads();
+        chunk(l0);
+      }
+    }
+  }
+  __syncthreads();  // the stages are free: the epilogue's scratch lies over them
+  emit_tile<NBM, NBN>(acc, emit_at(a, e, sp), a.na, l0 + wave * 2048, m0 + wm * WM, n0 + wn * WN, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -716,35 +1519,100 @@ hipError_t dyn_lds(F* f, int bytes) {
   return hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <typename T, bool TRANS, int BM, int BN, int WGM, int WGN, int ST, bool DMA>
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Tile of a product by the average rows per expert: 256 x 256 tiles read the
+// fewest operand bytes per product; with few rows per expert a tile of 32
+// rows wastes none on empty ones, and K is split so that about two workgroups
+// per CU share the weights' reading.
+struct MatmulPlan {
+  int bm, bn;
+  int64_t ks, kper;
+};
+MatmulPlan matmul_plan(int dtype, int64_t R, int64_t E, int64_t K, int64_t N) {
+  const bool dma = K % (dtype == 1 ? 8 : 4) == 0 && N % (dtype == 1 ? 8 : 4) == 0;
+  const int64_t per = R / E;
+  MatmulPlan m{128, 128, 1, K};
+  if (!dma) return m;
+  if (per <= 32) {
+    m.bm = 32;
+    const int64_t kc = dtype == 1 ? 64 : 32;
+    const int64_t tiles = (R / 32 + std::min(E, R)) * ((N + 127) / 128);
+    const int64_t chunks = (K + kc - 1) / kc;
+    const int64_t want = std::max<int64_t>(1, std::min(512 / tiles, chunks / 4));
+    m.kper = (chunks + want - 1) / want * kc;
+    m.ks = (K + m.kper - 1) / m.kper;
+  } else if (dtype == 1 && per >= 192 && E <= 64) {
+    m.bm = m.bn = 256;
+  }
+  return m;
+}
+
+template <typename T, bool TRANS, int BM, int BN, int WGM, int WGN, int KB, int ST, bool DMA, bool SPLIT>
 hipError_t run_matmul(hipStream_t st, MatmulArgs a) {
-  auto* f = &k_grouped_matmul<T, TRANS, BM, BN, WGM, WGN, ST, DMA>;
-  constexpr int LDS = (DMA ? ST : 1) * (BM + BN) * 128;
+  auto* f = &k_grouped_matmul<T, TRANS, BM, BN, WGM, WGN, KB, ST, DMA, SPLIT>;
+  constexpr int LDS = (DMA ? ST : 1) * (BM + BN) * KB;
   a.slots = a.R / BM + a.E;
   a.ntn = (a.N + BN - 1) / BN;
   hipError_t e = dyn_lds(f, LDS);
   if (e != hipSuccess) return e;
-  f<<<dim3((unsigned)xcd_grid(a.slots * a.ntn)), 64 * WGM * WGN, LDS, st>>>(a);
+  f<<<dim3((unsigned)xcd_grid(a.slots * a.ntn * a.ks)), 64 * WGM * WGN, LDS, st>>>(a);
+  return hipGetLastError();
+}
+
+template <bool TRANS>
+hipError_t run_matmul_big(hipStream_t st, MatmulArgs a) {
+  auto* f = &k_grouped_matmul_big<TRANS>;
+  constexpr int LDS = 4 * 512 * 64 + 8 * 4096;
+  a.ntn = (a.N + 255) / 256;
+  hipError_t e = dyn_lds(f, LDS);
+  if (e != hipSuccess) return e;
+  f<<<dim3((unsigned)std::min<int64_t>(256, xcd_grid((a.R / 256 + a.E) * a.ntn))), 512, LDS, st>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, bool TRANS>
-hipError_t matmul_t(hipStream_t st, int dtype, const MatmulArgs& a) {
-  const bool dma = dma_ok(dtype, {a.K, a.N});
-  if (!dma) return run_matmul<T, TRANS, 128, 128, 2, 2, 2, false>(st, a);
-  return run_matmul<T, TRANS, 128, 128, 2, 2, 2, true>(st, a);
+hipError_t matmul_t(hipStream_t st, int dtype, MatmulArgs a) {
+  const MatmulPlan m = matmul_plan(dtype, a.R, a.E, a.K, a.N);
+  a.ks = m.ks;
+  a.kper = m.kper;
+  if (!dma_ok(dtype, {a.K, a.N})) return run_matmul<T, TRANS, 128, 128, 2, 2, 128, 2, false, false>(st, a);
+  if (m.bm == 32) {
+    if (a.ks == 1) return run_matmul<T, TRANS, 32, 128, 1, 4, 128, 3, true, false>(st, a);
+    hipError_t e = run_matmul<T, TRANS, 32, 128, 1, 4, 128, 3, true, true>(st, a);
+    if (e != hipSuccess) return e;
+    const int64_t blocks = std::min<int64_t>((a.R * a.N + 255) / 256, 4096);
+    k_grouped_join<T><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  if constexpr (sizeof(T) == 2) {
+    if (m.bm == 256) return run_matmul_big<TRANS>(st, a);
+  }
+  return run_matmul<T, TRANS, 128, 128, 2, 2, 128, 2, true, false>(st, a);
 }
 
 int64_t norm_slots(const GroupedArgs& g, int ts) { return g.R / ts + g.E * g.B; }
-int64_t piece_rows(int dtype) { return dtype == 1 ? 64 : 32; }
-int64_t piece_slots(int dtype, const GroupedArgs& g) { return g.R / piece_rows(dtype) + g.E * g.B; }
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+int64_t piece_slots(const GroupedArgs& g) { return g.R / kPieceRows + g.E * g.B; }
 
-int64_t sum_splits(int dtype, const GroupedArgs& g) {
-  const int64_t tiles = ((g.d + 127) / 128) * ((g.p + 127) / 128) * g.E;
-  const int64_t want = (512 + tiles - 1) / tiles;
-  const int64_t most = std::max<int64_t>(1, g.R / g.E / 256);
-  return std::max<int64_t>(1, std::min(want, most));
+// The clipped sum's kernel, tile and K splits. 256 x 256 tiles (bf16, aligned
+// widths) where the layer is wide enough to fill them; the splits make at
+// least two items per CU, each of at least 512 rows.
+struct SumPlan {
+  bool big, pieces, dma, fused;
+  int64_t mt, nt, ks;
+};
+SumPlan sum_plan(int dtype, const GroupedArgs& g) {
+  SumPlan s{};
+  s.dma = dma_ok(dtype, {g.d, g.p});
+  s.big = dtype == 1 && s.dma && g.d >= 192 && g.p >= 192;
+  s.pieces = dtype == 1 && g.R / (g.E * g.B) >= 16;
+  const int64_t t = s.big ? 256 : 128;
+  s.mt = (g.d + t - 1) / t;
+  s.nt = (g.p + t - 1) / t;
+  const int64_t items = s.mt * s.nt * g.E, rows = g.R / g.E;
+  s.ks = std::max<int64_t>(1, std::min((512 + items - 1) / items, rows / (s.big ? 512 : 256)));
+  s.fused = s.ks == 1 && g.d % 4 == 0;
+  return s;
 }
 
 template <typename T, int TS, int WG>
@@ -770,26 +1638,33 @@ hipError_t run_norm(hipStream_t st, int dtype, GNormArgs a, float* sqnorm, int a
   return hipGetLastError();
 }
 
-template <typename T, bool DMA>
-hipError_t run_sum(hipStream_t st, const GSumArgs& a) {
-  auto* f = &k_grouped_sum<T, 128, 128, 2, 2, 2, DMA>;
-  constexpr int LDS = (DMA ? 2 : 1) * 256 * 128;
-  hipError_t e = dyn_lds(f, LDS);
+template <typename F>
+hipError_t run_sum(F* f, hipStream_t st, const GSumArgs& a, int64_t grid, int threads, int lds) {
+  hipError_t e = dyn_lds(f, lds);
   if (e != hipSuccess) return e;
-  f<<<dim3((unsigned)xcd_grid(a.E * a.mt * a.nt * a.ks)), 256, LDS, st>>>(a);
+  f<<<dim3((unsigned)grid), threads, lds, st>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t grouped_matmul_ws_bytes(int, const GroupedArgs&) { return 0; }
+size_t grouped_matmul_ws_bytes(int dtype, const GroupedArgs& g) {
+  size_t need = 0;
+  for (int tr = 0; tr < 2; ++tr) {
+    const int64_t K = tr ? g.p : g.d, N = tr ? g.d : g.p;
+    const MatmulPlan m = matmul_plan(dtype, g.R, g.E, K, N);
+    if (m.ks > 1) need = std::max(need, round256((size_t)m.ks * (size_t)g.R * (size_t)N * sizeof(float)));
+  }
+  return need;
+}
 
 hipError_t launch_grouped_matmul(hipStream_t st, int dtype, const GroupedArgs& g, const void* X, const void* W,
-                                 bool transpose, void*, void* Y) {
+                                 bool transpose, void* ws, void* Y) {
   MatmulArgs a{};
   a.X = X;
   a.W = W;
   a.Y = Y;
+  a.part = static_cast<float*>(ws);
   a.seg = g.seg;
   a.B = g.B;
   a.E = g.E;
@@ -818,43 +1693,70 @@ hipError_t launch_grouped_norm(hipStream_t st, int dtype, const GroupedArgs& g, 
                     : run_norm<float, 128, 2>(st, dtype, a, sqnorm, accumulate);
 }
 
+// workspace: the XCDs' item queues, the piece list or the rows' factors, then the splits' sums
+constexpr size_t kQueueBytes = 256;
+size_t sum_list_bytes(const SumPlan& s, const GroupedArgs& g) {
+  return kQueueBytes + round256(s.pieces ? (size_t)piece_slots(g) * sizeof(Piece) : (size_t)g.R * sizeof(float));
+}
 size_t grouped_sum_ws_bytes(int dtype, const GroupedArgs& g) {
-  return round256((size_t)piece_slots(dtype, g) * sizeof(Piece)) +
-         round256((size_t)sum_splits(dtype, g) * (size_t)g.E * (size_t)g.d * (size_t)g.p * sizeof(float));
+  const SumPlan s = sum_plan(dtype, g);
+  return sum_list_bytes(s, g) +
+         (s.fused ? 0 : round256((size_t)s.ks * (size_t)g.E * (size_t)g.d * (size_t)g.p * sizeof(float)));
 }
 
 hipError_t launch_grouped_sum(hipStream_t st, int dtype, const GroupedArgs& g, const void* A, const void* G,
                               const float* c, void* ws, const NoiseArgs& na, float* out) {
-  const int64_t slots = piece_slots(dtype, g);
-  Piece* pieces = static_cast<Piece*>(ws);
-  const unsigned pb = (unsigned)((slots + 255) / 256);
-  if (dtype == 1)
-    k_grouped_pieces<64><<<pb, 256, 0, st>>>(g.seg, g.R, g.E, g.B, c, slots, pieces);
-  else
-    k_grouped_pieces<32><<<pb, 256, 0, st>>>(g.seg, g.R, g.E, g.B, c, slots, pieces);
+  const SumPlan s = sum_plan(dtype, g);
+  GSumArgs a{};
+  a.queue = static_cast<int32_t*>(ws);
+  void* list = static_cast<char*>(ws) + kQueueBytes;
+  if (s.pieces) {
+    Piece* pieces = static_cast<Piece*>(list);
+    const int64_t slots = piece_slots(g);
+    k_grouped_pieces<<<dim3((unsigned)((slots + 255) / 256)), 256, 0, st>>>(g.seg, g.R, g.E, g.B, c, slots, pieces,
+                                                                            a.queue);
+    a.pieces = pieces;
+  } else {
+    float* crow = static_cast<float*>(list);
+    k_grouped_row_factors<<<dim3((unsigned)((g.R + 255) / 256)), 256, 0, st>>>(g.seg, g.R, g.E, g.B, c, crow, a.queue);
+    a.crow = crow;
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  GSumArgs a{};
   a.A = A;
   a.G = G;
   a.seg = g.seg;
-  a.pieces = pieces;
   a.R = g.R;
   a.E = g.E;
   a.B = g.B;
   a.d = g.d;
   a.p = g.p;
-  a.mt = (g.d + 127) / 128;
-  a.nt = (g.p + 127) / 128;
-  a.ks = sum_splits(dtype, g);
-  a.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + round256((size_t)slots * sizeof(Piece)));
-  const bool dma = dma_ok(dtype, {g.d, g.p});
-  if (dtype == 1)
-    e = dma ? run_sum<bf16s, true>(st, a) : run_sum<bf16s, false>(st, a);
-  else
-    e = dma ? run_sum<float, true>(st, a) : run_sum<float, false>(st, a);
-  if (e != hipSuccess) return e;
-  return launch_split_reduce(st, a.ks, a.ws, g.E * g.d, g.p, na, out);
+  a.mt = s.mt;
+  a.nt = s.nt;
+  a.ks = s.ks;
+  a.na = s.fused ? na : make_noise_args(0.0f, 1.0f, 0, 0, 0);
+  a.out = out;
+  a.fused = s.fused;
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + sum_list_bytes(s, g));
+  if (s.big) {
+    const int64_t grid = std::min<int64_t>(256, xcd_grid(s.mt * s.nt * s.ks * g.E));
+    e = s.pieces ? run_sum(&k_grouped_sum_big<true>, st, a, grid, 512, 4 * 32768 + 8 * 2048)
+                 : run_sum(&k_grouped_sum_big<false>, st, a, grid, 512, 4 * (32768 + 1024) + 8 * 2048);
+  } else {
+    const int64_t grid = g.E * s.ks * xcd_grid(s.mt * s.nt);
+    const int st_n = s.dma ? 2 : 1;
+    if (dtype == 1 && s.pieces)
+      e = s.dma ? run_sum(&k_grouped_sum<bf16s, true, true>, st, a, grid, 256, st_n * 16384)
+                : run_sum(&k_grouped_sum<bf16s, true, false>, st, a, grid, 256, st_n * 16384);
+    else if (dtype == 1)
+      e = s.dma ? run_sum(&k_grouped_sum<bf16s, false, true>, st, a, grid, 256, st_n * (32768 + 1024))
+                : run_sum(&k_grouped_sum<bf16s, false, false>, st, a, grid, 256, st_n * (32768 + 1024));
+    else
+      e = s.dma ? run_sum(&k_grouped_sum<float, false, true>, st, a, grid, 256, st_n * (32768 + 1024))
+                : run_sum(&k_grouped_sum<float, false, false>, st, a, grid, 256, st_n * (32768 + 1024));
+  }
+  if (e != hipSuccess || s.fused) return e;
+  return launch_split_reduce(st, a.ks, a.part, g.E * g.d, g.p, na, out);
 }
 
 bool grouped_fits(int dtype, const GroupedArgs& g) {
@@ -862,7 +1764,8 @@ bool grouped_fits(int dtype, const GroupedArgs& g) {
   const int64_t cols = (std::max(g.d, g.p) + 127) / 128;
   if ((g.R / 32 + g.E) * cols + 8 >= kMax) return false;
   if (g.R / 32 + g.E * g.B + 8 >= kMax) return false;
-  return g.E * ((g.d + 127) / 128) * ((g.p + 127) / 128) * sum_splits(dtype, g) + 8 < kMax;
+  const SumPlan s = sum_plan(dtype, g);
+  return g.E * s.ks * xcd_grid(s.mt * s.nt) < kMax;
 }
 
 }  // namespace dpk
