@@ -639,9 +639,11 @@ def _lm_tensors(stream, *named):
     """Checks of the language-model calls' tensors, given as (name, tensor or
     None, dtypes, shape or None): a contiguous GPU tensor of one of the dtypes
     and of that shape, on the device that is current and that `stream` belongs
-    to (a launch from another device's context would run on the wrong one)."""
+    to (a launch from another device's context would run on the wrong one).
+    Returns the HIP stream handle. These calls serve single tokens too, where
+    the host's time counts: the checks use torch's cheapest queries."""
     import torch
-    current = torch.cuda.current_device() if torch.cuda.is_available() else None
+    device = None
     for name, t, dtypes, shape in named:
         if t is None:
             continue
@@ -649,12 +651,17 @@ def _lm_tensors(stream, *named):
             raise ValueError(f"{name} must be a contiguous GPU tensor")
         if t.dtype not in dtypes:
             raise TypeError(f"{name} must be of dtype {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-        if shape is not None and tuple(t.shape) != tuple(shape):
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-        if t.device.index != current:
-            raise ValueError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{current}")
-    if stream is not None and stream.device.index != current:
-        raise ValueError(f"stream belongs to cuda:{stream.device.index}, the current device is cuda:{current}")
+        if device is None:
+            device = torch._C._cuda_getDevice()
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{device}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device.index != device:
+        raise ValueError(f"stream belongs to cuda:{stream.device.index}, the current device is cuda:{device}")
+    return stream.cuda_stream
 
 
 def _act_dtypes(t, name):
@@ -663,13 +670,21 @@ def _act_dtypes(t, name):
     return (t.dtype,)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _lm_workspace(workspace, nbytes, device, stream):
+    """(address, bytes) of the caller's workspace, or of one allocated for the
+    call when it is None; `nbytes()` is the size needed."""
     if workspace is None:
-        if nbytes == 0:
-            return None, 0
-        workspace = _scratch(nbytes, device, stream)
-    _lm_tensors(stream, ("workspace", workspace, (workspace.dtype,), None))
-    return workspace, _ws_bytes(workspace)
+        need = nbytes()
+        if need == 0:
+            return None, 0, None
+        workspace = _scratch(need, device, stream)
+    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous GPU tensor on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def dp_rms_norm_workspace_bytes(dtype: int, B: int, T: int, d: int) -> int:
@@ -683,14 +698,14 @@ def dp_rms_norm(x, gain, eps: float, out, residual=None, sum_out=None, stream=No
     if x.dim() < 1 or x.numel() < 1:
         raise ValueError("x must have at least one element")
     dt = _act_dtypes(x, "x")
-    d = int(x.shape[-1])
-    _lm_tensors(stream, ("x", x, dt, None), ("residual", residual, dt, x.shape), ("out", out, dt, x.shape),
-                ("sum_out", sum_out, dt, x.shape), ("gain", gain, (torch.float32, torch.bfloat16), (d,)))
+    d = x.shape[-1]
+    st = _lm_tensors(stream, ("x", x, dt, None), ("residual", residual, dt, x.shape), ("out", out, dt, x.shape),
+                     ("sum_out", sum_out, dt, x.shape), ("gain", gain, (torch.float32, torch.bfloat16), (d,)))
     if sum_out is not None and sum_out.data_ptr() == out.data_ptr():
         raise ValueError("sum_out and out must be different tensors")
-    _check("dp_rms_norm", lib().dp_rms_norm(_stream(stream), _ptr(x), _ptr(residual), _ptr(gain), _dtype_code(x),
-                                            _dtype_code(gain), x.numel() // d, d, float(eps), _ptr(out),
-                                            _ptr(sum_out)))
+    _check("dp_rms_norm", lib().dp_rms_norm(st, x.data_ptr(), _addr(residual), gain.data_ptr(), _dtype_code(x),
+                                            _dtype_code(gain), x.numel() // d, d, eps, out.data_ptr(),
+                                            _addr(sum_out)))
 
 
 def dp_rms_norm_backward(dy, s, gain, eps: float, dx=None, dsum=None, gain_rows=None, workspace=None, stream=None):
@@ -701,59 +716,59 @@ def dp_rms_norm_backward(dy, s, gain, eps: float, dx=None, dsum=None, gain_rows=
     if s.dim() < 2 or s.numel() < 1:
         raise ValueError("s [B, ..., d] with at least one element expected")
     dt = _act_dtypes(s, "s")
-    B, d = int(s.shape[0]), int(s.shape[-1])
+    B, d = s.shape[0], s.shape[-1]
     T = s.numel() // (B * d)
-    _lm_tensors(stream, ("s", s, dt, None), ("dy", dy, dt, s.shape), ("dsum", dsum, dt, s.shape),
-                ("dx", dx, dt, s.shape), ("gain", gain, (torch.float32, torch.bfloat16), (d,)),
-                ("gain_rows", gain_rows, (torch.float32,), (B, d)))
+    st = _lm_tensors(stream, ("s", s, dt, None), ("dy", dy, dt, s.shape), ("dsum", dsum, dt, s.shape),
+                     ("dx", dx, dt, s.shape), ("gain", gain, (torch.float32, torch.bfloat16), (d,)),
+                     ("gain_rows", gain_rows, (torch.float32,), (B, d)))
     if dx is None and gain_rows is None:
         raise ValueError("dx or gain_rows is required")
-    ws, nbytes = _lm_workspace(workspace, dp_rms_norm_workspace_bytes(_dtype_code(s), B, T, d)
-                               if gain_rows is not None else 0, s.device, stream)
+    code = _dtype_code(s)
+    ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_rms_norm_workspace_bytes(code, B, T, d)
+                                      if gain_rows is not None else 0, s.device, stream)
     _check("dp_rms_norm_backward", lib().dp_rms_norm_backward(
-        _stream(stream), _ptr(dy), _ptr(s), _ptr(dsum), _ptr(gain), _dtype_code(s), _dtype_code(gain), B, T, d,
-        float(eps), _ptr(ws), nbytes, _ptr(dx), _ptr(gain_rows)))
+        st, dy.data_ptr(), s.data_ptr(), _addr(dsum), gain.data_ptr(), code, _dtype_code(gain), B, T, d, eps, ws, nbytes,
+        _addr(dx), _addr(gain_rows)))
 
 
 def dp_distill_workspace_bytes(dtype: int, B: int, T: int, V: int, K: int) -> int:
     return int(lib().dp_distill_workspace_bytes(dtype, B, T, V, K))
 
 
-def _distill(logits, ids, teacher, weight, stream):
+def _distill(logits, ids, teacher, weight, stream, *more):
     import torch
     if logits.dim() != 3 or ids.dim() != 3 or ids.shape[:2] != logits.shape[:2]:
         raise ValueError(f"logits [B, T, V] and ids [B, T, K] expected, got {tuple(logits.shape)} and "
                          f"{tuple(ids.shape)}")
     dt = _act_dtypes(logits, "logits")
-    B, T, V = (int(v) for v in logits.shape)
-    _lm_tensors(stream, ("logits", logits, dt, None), ("ids", ids, (torch.int64,), None),
-                ("teacher", teacher, (torch.float32, torch.bfloat16), ids.shape), ("weight", weight, (torch.float32,), (B, T)))
-    return _dtype_code(logits), B, T, V, int(ids.shape[2])
+    B, T, V = logits.shape
+    f32 = (torch.float32,)
+    st = _lm_tensors(stream, ("logits", logits, dt, None), ("ids", ids, (torch.int64,), None),
+                     ("teacher", teacher, (torch.float32, torch.bfloat16), ids.shape), ("weight", weight, f32, (B, T)),
+                     *((n, t, f32, (B, T)[:k]) if k else (n, t, dt, logits.shape) for n, t, k in more))
+    return st, _dtype_code(logits), B, T, V, ids.shape[2]
 
 
 def dp_distill_loss(logits, ids, teacher, tau: float, loss, lse, weight=None, workspace=None, stream=None):
     """Per-sample distillation loss [B] of logits [B, T, V] from a teacher's
     top logits (ids [B, T, K] int64, -1 where unused; teacher [B, T, K]) at
     temperature tau; lse [B, T] is kept for the backward pass."""
-    import torch
-    dt, B, T, V, K = _distill(logits, ids, teacher, weight, stream)
-    _lm_tensors(stream, ("loss", loss, (torch.float32,), (B,)), ("lse", lse, (torch.float32,), (B, T)))
-    ws, nbytes = _lm_workspace(workspace, dp_distill_workspace_bytes(dt, B, T, V, K), logits.device, stream)
+    st, dt, B, T, V, K = _distill(logits, ids, teacher, weight, stream, ("loss", loss, 1), ("lse", lse, 2))
+    ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_distill_workspace_bytes(dt, B, T, V, K), logits.device,
+                                      stream)
     _check("dp_distill_loss", lib().dp_distill_loss(
-        _stream(stream), _ptr(logits), _ptr(ids), _ptr(teacher), dt, _dtype_code(teacher), B, T, V, K, float(tau),
-        _ptr(weight), _ptr(ws), nbytes, _ptr(loss), _ptr(lse)))
+        st, logits.data_ptr(), ids.data_ptr(), teacher.data_ptr(), dt, _dtype_code(teacher), B, T, V, K, tau,
+        _addr(weight), ws, nbytes, loss.data_ptr(), lse.data_ptr()))
 
 
 def dp_distill_loss_backward(logits, ids, teacher, tau: float, lse, grad, weight=None, dloss=None, stream=None):
     """Gradient of sum_b dloss[b] * loss[b] (dloss None: of the sum) with
     respect to the logits into grad [B, T, V], which may be logits itself."""
-    import torch
-    dt, B, T, V, K = _distill(logits, ids, teacher, weight, stream)
-    _lm_tensors(stream, ("lse", lse, (torch.float32,), (B, T)), ("grad", grad, (logits.dtype,), logits.shape),
-                ("dloss", dloss, (torch.float32,), (B,)))
+    st, dt, B, T, V, K = _distill(logits, ids, teacher, weight, stream, ("lse", lse, 2), ("grad", grad, 0),
+                                  ("dloss", dloss, 1))
     _check("dp_distill_loss_backward", lib().dp_distill_loss_backward(
-        _stream(stream), _ptr(logits), _ptr(ids), _ptr(teacher), dt, _dtype_code(teacher), B, T, V, K, float(tau),
-        _ptr(weight), _ptr(dloss), _ptr(lse), _ptr(grad)))
+        st, logits.data_ptr(), ids.data_ptr(), teacher.data_ptr(), dt, _dtype_code(teacher), B, T, V, K, tau,
+        _addr(weight), _addr(dloss), lse.data_ptr(), grad.data_ptr()))
 
 
 def dp_grouped_workspace_bytes(dtype: int, R: int, E: int, B: int, d: int, p: int) -> int:
@@ -778,55 +793,54 @@ def dp_grouped_matmul(X, W, segments, out, transpose: bool = False, workspace=No
     if X.dim() != 2 or W.dim() != 3:
         raise ValueError(f"X [R, ...] and W [E, p, d] expected, got {tuple(X.shape)} and {tuple(W.shape)}")
     dt = _act_dtypes(X, "X")
-    E, p, d = (int(v) for v in W.shape)
-    R = int(X.shape[0])
+    E, p, d = W.shape
+    R = X.shape[0]
     B = _grouped_batch(segments, E)
-    _lm_tensors(stream, ("X", X, dt, (R, p if transpose else d)), ("W", W, dt, None),
-                ("out", out, dt, (R, d if transpose else p)), ("segments", segments, (torch.int64,), None))
+    st = _lm_tensors(stream, ("X", X, dt, (R, p if transpose else d)), ("W", W, dt, None),
+                     ("out", out, dt, (R, d if transpose else p)), ("segments", segments, (torch.int64,), None))
     code = _dtype_code(X)
-    ws, nbytes = _lm_workspace(workspace, dp_grouped_workspace_bytes(code, R, E, B, d, p), X.device, stream)
+    ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_grouped_workspace_bytes(code, R, E, B, d, p), X.device,
+                                      stream)
     _check("dp_grouped_matmul", lib().dp_grouped_matmul(
-        _stream(stream), _ptr(X), _ptr(W), code, _ptr(segments), R, E, B, d, p, int(bool(transpose)), _ptr(ws), nbytes,
-        _ptr(out)))
+        st, X.data_ptr(), W.data_ptr(), code, segments.data_ptr(), R, E, B, d, p, 1 if transpose else 0, ws, nbytes,
+        out.data_ptr()))
 
 
-def _grouped_layer(A, G, segments, B, stream):
+def _grouped_layer(A, G, segments, vec, name, stream):
+    """Checks of an expert layer's rows, segments and the [B] vector `vec`."""
     import torch
     if A.dim() != 2 or G.dim() != 2 or A.shape[0] != G.shape[0]:
         raise ValueError(f"A [R, d] and G [R, p] expected, got {tuple(A.shape)} and {tuple(G.shape)}")
     dt = _act_dtypes(A, "A")
-    _lm_tensors(stream, ("A", A, dt, None), ("G", G, dt, None), ("segments", segments, (torch.int64,), None))
-    if (segments.numel() - 1) % B:
-        raise ValueError(f"segments must have E*B + 1 elements, B = {B}")
+    st = _lm_tensors(stream, ("A", A, dt, None), ("G", G, dt, None), ("segments", segments, (torch.int64,), None),
+                     (name, vec, (torch.float32,), None))
+    B = vec.numel()
+    if B < 1 or (segments.numel() - 1) % B:
+        raise ValueError(f"segments must have E*B + 1 elements, B = {B} (the elements of {name})")
     E = (segments.numel() - 1) // B
     _grouped_batch(segments, E, B)
-    return _dtype_code(A), int(A.shape[0]), E, int(A.shape[1]), int(G.shape[1])
+    return st, _dtype_code(A), A.shape[0], E, B, A.shape[1], G.shape[1]
 
 
 def dp_grouped_norm(A, G, segments, sqnorm, accumulate: bool = False, workspace=None, stream=None):
     """Per-sample squared gradient norms of an expert layer over all its
     experts into sqnorm [B], from its rows A [R, d] and output gradients
     G [R, p], sorted by (expert, sample) as segments [E*B + 1] says."""
-    import torch
-    _lm_tensors(stream, ("sqnorm", sqnorm, (torch.float32,), None))
-    B = sqnorm.numel()
-    dt, R, E, d, p = _grouped_layer(A, G, segments, B, stream)
-    ws, nbytes = _lm_workspace(workspace, dp_grouped_workspace_bytes(dt, R, E, B, d, p), A.device, stream)
+    st, dt, R, E, B, d, p = _grouped_layer(A, G, segments, sqnorm, "sqnorm", stream)
+    ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_grouped_workspace_bytes(dt, R, E, B, d, p), A.device, stream)
     _check("dp_grouped_norm", lib().dp_grouped_norm(
-        _stream(stream), _ptr(A), _ptr(G), dt, _ptr(segments), R, E, B, d, p, _ptr(ws), nbytes, _ptr(sqnorm),
-        int(bool(accumulate))))
+        st, A.data_ptr(), G.data_ptr(), dt, segments.data_ptr(), R, E, B, d, p, ws, nbytes, sqnorm.data_ptr(),
+        1 if accumulate else 0))
 
 
 def dp_grouped_clipped_sum_noise(A, G, segments, c, C: float, sigma: float, denom: float, seed: int, layer_id: int,
                                  step: int, out, workspace=None, stream=None):
     """Clipped noised mean gradients of an expert layer into out [E, d, p]."""
     import torch
-    _lm_tensors(stream, ("c", c, (torch.float32,), None))
-    B = c.numel()
-    dt, R, E, d, p = _grouped_layer(A, G, segments, B, stream)
+    st, dt, R, E, B, d, p = _grouped_layer(A, G, segments, c, "c", stream)
     _lm_tensors(stream, ("out", out, (torch.float32,), (E, d, p)))
-    ws, nbytes = _lm_workspace(workspace, dp_grouped_workspace_bytes(dt, R, E, B, d, p), A.device, stream)
+    ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_grouped_workspace_bytes(dt, R, E, B, d, p), A.device, stream)
     _check("dp_grouped_clipped_sum_noise", lib().dp_grouped_clipped_sum_noise(
-        _stream(stream), _ptr(A), _ptr(G), dt, _ptr(segments), R, E, B, d, p, _ptr(c), float(C), float(sigma),
-        float(denom), int(seed) & 0xFFFFFFFFFFFFFFFF, int(layer_id) & 0xFFFFFFFF, int(step) & 0xFFFFFFFF, _ptr(ws),
-        nbytes, _ptr(out)))
+        st, A.data_ptr(), G.data_ptr(), dt, segments.data_ptr(), R, E, B, d, p, c.data_ptr(), C, sigma, denom,
+        int(seed) & 0xFFFFFFFFFFFFFFFF, int(layer_id) & 0xFFFFFFFF, int(step) & 0xFFFFFFFF, ws, nbytes,
+        out.data_ptr()))

@@ -20,6 +20,8 @@
 #include "dp_lm.hpp"
 #include "dp_noise.hpp"
 
+#include <cmath>
+
 namespace dpk {
 
 namespace {
@@ -127,6 +129,28 @@ __device__ __forceinline__ u32x4 make_srd(const T* base, uint32_t bytes) {
   return s;
 }
 
+// 16 bytes of elements [col, col + P) of a row of K, zero past K and where !ok;
+// rows of odd widths start at any element.
+template <typename T>
+__device__ __forceinline__ u32x4 load_piece(const T* __restrict__ row, int64_t col, int64_t K, bool ok) {
+  constexpr int P = elem_traits<T>::per16;
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (!ok || col >= K) return v;
+  if (col + P <= K) {
+    __builtin_memcpy(&v, row + col, 16);
+    return v;
+  }
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < P - 1; ++e)
+    if (col + e < K) {
+      const uint32_t bits = raw_bits(row[col + e]);
+      if constexpr (P == 8) w[e >> 1] |= bits << (16 * (e & 1));
+      else w[e] = bits;
+    }
+  return u32x4{w[0], w[1], w[2], w[3]};
+}
+
 // Filling one operand's LDS image of a window with NW waves.
 template <typename O, typename T, int NW>
 struct Filler {
@@ -154,25 +178,19 @@ struct Filler {
     for (int i = 0; i < LOADS; ++i)
       dma16_buf(srd, qp[i] < cols ? voff[i] : 0x80000000u, lds + (wave + NW * i) * 1024);
   }
-  // through registers, element by element where needed: any alignment
-  __device__ __forceinline__ void regs(const Win<T>& w, unsigned char* lds, int wave, int lane) const {
+  // Through registers (any alignment): load, and after the LDS image's readers are done, store.
+  __device__ __forceinline__ void load(const Win<T>& w, u32x4 (&v)[LOADS], int wave, int lane) const {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      const int byte = (wave + NW * i) * 1024 + 16 * lane;
-      const int r = byte / O::ROWB;
-      uint32_t v[4] = {0u, 0u, 0u, 0u};
-      if (r < w.rows) {
-        const T* src = reinterpret_cast<const T*>(reinterpret_cast<const char*>(w.base) + (int64_t)r * w.ldb);
-#pragma unroll
-        for (int e = 0; e < O::P; ++e) {
-          uint32_t bits = 0u;
-          if (qp[i] + e < w.cols) bits = raw_bits(src[qp[i] + e]);
-          if constexpr (O::P == 8) v[e >> 1] |= bits << (16 * (e & 1));
-          else v[e] = bits;
-        }
-      }
-      *reinterpret_cast<u32x4*>(lds + byte) = u32x4{v[0], v[1], v[2], v[3]};
+      const int r = ((wave + NW * i) * 1024 + 16 * lane) / O::ROWB;
+      v[i] = load_piece(reinterpret_cast<const T*>(reinterpret_cast<const char*>(w.base) + (int64_t)r * w.ldb),
+                        qp[i], w.cols, r < w.rows);
     }
+  }
+  __device__ __forceinline__ void store(const u32x4 (&v)[LOADS], unsigned char* lds, int wave, int lane) const {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i)
+      *reinterpret_cast<u32x4*>(lds + (wave + NW * i) * 1024 + 16 * lane) = v[i];
   }
 };
 
@@ -406,11 +424,16 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_grouped_matmul(MatmulArgs a)
       mma(f[s & 1]);
     }
   } else {
+    u32x4 vx[Filler<OX, T, NW>::LOADS], vw[Filler<OW, T, NW>::LOADS];
+    fx.load(xwin(0), vx, wave, lane);
+    fw.load(wwin(0), vw, wave, lane);
     for (int q = 0; q < nq; ++q) {
       __syncthreads();
-      fx.regs(xwin((int64_t)q * KC), lds, wave, lane);
-      fw.regs(wwin((int64_t)q * KC), lds + OX::BYTES, wave, lane);
+      fx.store(vx, lds, wave, lane);
+      fw.store(vw, lds + OX::BYTES, wave, lane);
       __syncthreads();
+      fx.load(xwin((int64_t)(q + 1) * KC), vx, wave, lane);  // past the last chunk: an empty window
+      fw.load(wwin((int64_t)(q + 1) * KC), vw, wave, lane);
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         Frags f;
@@ -683,27 +706,35 @@ __global__ __launch_bounds__(256) void k_grouped_join(MatmulArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Norms: one workgroup per (segment, row tile of TS rows); it takes the Gram
-// tiles (t, u), u >= t, of its segment in turn: both Grams' 32x32 blocks in
-// registers, their elementwise product summed, counted twice off the
-// diagonal. The tile's value goes to partial[slot].
+// Norms. Both Grams of a pair of row tiles in registers, their elementwise
+// product summed, off-diagonal pairs counted twice.
 struct GNormArgs {
   const void *A, *G;
   const int64_t* seg;
   int64_t R, E, B, d, p;
-  float* partial;  // [slots]
-  int64_t slots;   // R / TS + E * B
+  float* partial;   // tiles: [slots * J]; packed: a value per row [R]
+  int32_t* row_seg; // packed: a row's segment, -1 for none [R]
+  int64_t slots;    // R / 128 + E * B
+  int64_t J;        // workgroups a row tile's pairs are dealt to
 };
 
-template <typename T, int TS, int WG, bool DMA>
-__global__ __launch_bounds__(64 * WG * WG) void k_grouped_norm(GNormArgs a) {
-  constexpr int NW = WG * WG, WT = TS / WG, NB = WT / 32;
+// Segments of about 64 rows or more: row tiles of 128 within a segment.
+// Workgroup (tile t, j) takes the pairs (t, u), u - t = j, j + J, ...: a long
+// segment's pairs spread over J workgroups (one after another they were the
+// launch's critical path: 276 -> 172 us at 256 segments of 128 rows on
+// average, d + p = 6400). A wave whose 64 x 64 part lies below the diagonal
+// or past the segment only takes part in the loads.
+template <typename T, bool DMA>
+__global__ __launch_bounds__(256) void k_grouped_norm(GNormArgs a) {
+  constexpr int TS = 128, WG = 2, NW = 4, WT = 64, NB = 2;
   using O = Opnd<T, true, TS>;
   constexpr int KC = O::KC, STAGE = 2 * O::BYTES, ST = 2;
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
   __shared__ float red[NW];
 
-  const int64_t slot = xcd_item(blockIdx.x, a.slots);
+  // XCD x takes every eighth run of four row tiles, whose pairs share rows in its L2
+  const int64_t local = blockIdx.x >> 3, run = local / (4 * a.J), in_run = local - run * 4 * a.J;
+  const int64_t slot = (run * 8 + (blockIdx.x & 7)) * 4 + in_run / a.J, j = in_run % a.J;
   if (slot >= a.slots) return;
   Group gr;
   if (!find_group<TS>(a.seg, 1, a.E * a.B, a.R, slot, &gr)) return;  // an unused slot: nothing reads its partial
@@ -717,9 +748,10 @@ __global__ __launch_bounds__(64 * WG * WG) void k_grouped_norm(GNormArgs a) {
 
   const int64_t trows = rows < TS ? rows : TS;
   float total = 0.f;
-  for (int64_t u = 0; u * TS < rows; ++u) {
+  for (int64_t u = j; u * TS < rows; u += a.J) {
     const int64_t urows = rows - u * TS < TS ? rows - u * TS : TS;
     const bool diag = u == 0;
+    const bool active = !(diag && wm > wn) && wm * WT < trows && wn * WT < urows;
     f32x16 ga[NB][NB], gg[NB][NB];
     zero_acc(ga);
     zero_acc(gg);
@@ -745,15 +777,20 @@ __global__ __launch_bounds__(64 * WG * WG) void k_grouped_norm(GNormArgs a) {
           lds_barrier();
           if (q + 1 < nq) issue(q + 1);
           const uint32_t sb = l0 + (uint32_t)(q % ST) * STAGE;
-          chunk_mma<T, NB, NB>(sb, diag ? sb : sb + O::BYTES, rm, rn, 4, acc);
+          if (active) chunk_mma<T, NB, NB>(sb, diag ? sb : sb + O::BYTES, rm, rn, 4, acc);
         }
       } else {
+        u32x4 vt[Filler<O, T, NW>::LOADS], vu[Filler<O, T, NW>::LOADS];
+        f.load(wt(0), vt, wave, lane);
+        if (!diag) f.load(wu(0), vu, wave, lane);
         for (int q = 0; q < nq; ++q) {
           __syncthreads();
-          f.regs(wt(q), lds, wave, lane);
-          if (!diag) f.regs(wu(q), lds + O::BYTES, wave, lane);
+          f.store(vt, lds, wave, lane);
+          if (!diag) f.store(vu, lds + O::BYTES, wave, lane);
           __syncthreads();
-          chunk_mma<T, NB, NB>(l0, diag ? l0 : l0 + O::BYTES, rm, rn, 4, acc);
+          f.load(wt(q + 1), vt, wave, lane);  // past the last chunk: an empty window
+          if (!diag) f.load(wu(q + 1), vu, wave, lane);
+          if (active) chunk_mma<T, NB, NB>(l0, diag ? l0 : l0 + O::BYTES, rm, rn, 4, acc);
         }
       }
     };
@@ -763,10 +800,10 @@ __global__ __launch_bounds__(64 * WG * WG) void k_grouped_norm(GNormArgs a) {
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
+      for (int k = 0; k < NB; ++k)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) s = __builtin_fmaf(ga[i][j][k], gg[i][j][k], s);
-    total += diag ? s : 2.0f * s;
+        for (int e = 0; e < 16; ++e) s = __builtin_fmaf(ga[i][k][e], gg[i][k][e], s);
+    if (active) total += diag && wm == wn ? s : 2.0f * s;
   }
   total = wave_sum(total);
   if (lane == 0) red[wave] = total;
@@ -775,22 +812,112 @@ __global__ __launch_bounds__(64 * WG * WG) void k_grouped_norm(GNormArgs a) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NW; ++i) s += red[i];
-    a.partial[slot] = s;
+    a.partial[slot * a.J + j] = s;
   }
 }
 
-// sqnorm[b] (+)= the values of the sample's tiles, in tile order per
-// segment, one lane per segment, the segments joined in a fixed order. One
-// wave per sample.
-template <int TS>
+// Shorter segments: row tiles of 32 consecutive rows whatever their segments,
+// both Grams of a tile with itself masked to pairs of one segment, and with
+// the following tiles as far as the tile's last segment reaches. The rows go
+// from memory straight into fragments (a Gram of a tile with itself takes one
+// load per product), K dealt to the four waves and joined through LDS. Each
+// row's share of its segment's value goes to partial[row].
+template <typename T>
+__global__ __launch_bounds__(256) void k_grouped_norm_packed(GNormArgs a) {
+  constexpr int P = elem_traits<T>::per16, U = 4;
+  __shared__ float gram[2][4][32 * 33];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 31, g = lane >> 5;
+  const int orow = threadIdx.x >> 3, ocol = (threadIdx.x & 7) * 4;  // this thread's four elements of the product
+  for (int64_t t = blockIdx.x; t * 32 < a.R; t += gridDim.x) {
+    const int64_t trow = t * 32 + r;
+    const bool tok = trow < a.R && a.row_seg[trow] >= 0;
+    const int oseg = t * 32 + orow < a.R ? a.row_seg[t * 32 + orow] : -1;
+    const int last = a.row_seg[t * 32 + 31 < a.R ? t * 32 + 31 : a.R - 1];
+    float value = 0.f;
+    for (int64_t u = t;; ++u) {
+      if (u > t && (u * 32 >= a.R || last < 0 || a.row_seg[u * 32] != last)) break;  // uniform
+      const int64_t urow = u * 32 + r;
+      const bool uok = urow < a.R && a.row_seg[urow] >= 0;
+      f32x16 acc[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[m][k] = 0.f;
+        const int64_t K = m ? a.p : a.d;
+        const T* X = static_cast<const T*>(m ? a.G : a.A);
+        const T* xt = X + (tok ? trow : 0) * K;
+        const T* xu = X + (uok ? urow : 0) * K;
+        const int64_t steps = (K + 2 * P - 1) / (2 * P);
+        for (int64_t s = wave * U; s < steps; s += 4 * U) {
+          u32x4 ft[U], fu[U];
+#pragma unroll
+          for (int i = 0; i < U; ++i) ft[i] = load_piece(xt, (2 * (s + i) + g) * P, K, tok);
+          if (u != t) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) fu[i] = load_piece(xu, (2 * (s + i) + g) * P, K, uok);
+          } else {
+#pragma unroll
+            for (int i = 0; i < U; ++i) fu[i] = ft[i];
+          }
+#pragma unroll
+          for (int i = 0; i < U; ++i) acc[m] = mma_step<T>(ft[i], fu[i], acc[m]);
+        }
+      }
+      __syncthreads();  // the previous pair's elements are read
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) gram[m][wave][acc_row(k, lane) * 33 + r] = acc[m][k];
+      __syncthreads();
+      float s = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int64_t col = u * 32 + ocol + c;
+        const int at = orow * 33 + ocol + c;
+        const float x = (gram[0][0][at] + gram[0][1][at]) + (gram[0][2][at] + gram[0][3][at]);
+        const float y = (gram[1][0][at] + gram[1][1][at]) + (gram[1][2][at] + gram[1][3][at]);
+        if (col < a.R && oseg >= 0 && a.row_seg[col] == oseg) s = __builtin_fmaf(x, y, s);
+      }
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) s += __shfl_xor(s, off, kWave);
+      value += u == t ? s : 2.0f * s;
+    }
+    if ((threadIdx.x & 7) == 0 && t * 32 + orow < a.R) a.partial[t * 32 + orow] = value;
+  }
+}
+
+__global__ __launch_bounds__(256) void k_grouped_row_segments(const int64_t* __restrict__ seg, int64_t R, int64_t n,
+                                                              int32_t* __restrict__ row_seg) {
+  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (row >= R) return;
+  int64_t g = -1;
+  if (row >= seg[0] && row < seg[n]) {
+    int64_t hi = n;  // the last segment that starts at or before the row
+    g = 0;
+    while (hi - g > 1) {
+      const int64_t mid = (g + hi) / 2;
+      if (seg[mid] <= row) g = mid;
+      else hi = mid;
+    }
+  }
+  row_seg[row] = (int32_t)g;
+}
+
+// sqnorm[b] (+)= the values of the sample's tiles (or, packed, rows), in order
+// within a segment, one lane per segment, the segments joined in a fixed
+// order. One wave per sample.
+template <bool PACKED>
 __global__ __launch_bounds__(64) void k_grouped_norm_finish(GNormArgs a, float* __restrict__ sqnorm, int accumulate) {
   for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
     float s = 0.f;
     for (int64_t e = threadIdx.x; e < a.E; e += 64) {
       const int64_t g = e * a.B + b;
       const int64_t off = clamp_row(a.seg[g], a.R), end = clamp_row(a.seg[g + 1], a.R);
-      const int64_t base = off / TS + g;
-      for (int64_t t = 0; off + t * TS < end; ++t) s += a.partial[base + t];
+      const int64_t first = PACKED ? off : (off / 128 + g) * a.J;
+      const int64_t n = end <= off ? 0 : PACKED ? end - off : (end - off + 127) / 128 * a.J;
+#pragma unroll 8
+      for (int64_t t = 0; t < n; ++t) s += a.partial[first + t];
     }
     s = wave_sum(s);
     if (threadIdx.x == 0) sqnorm[b] = accumulate ? sqnorm[b] + s : s;
@@ -1423,13 +1550,22 @@ __global__ __launch_bounds__(256) void k_grouped_sum(GSumArgs a) {
           sn = x;
         }
       } else {
+        u32x4 va[Filler<OA, T, NW>::LOADS], vg[Filler<OG, T, NW>::LOADS];
+        auto load = [&](const Piece& pc) {
+          fa.load(awin(pc.row0, pc.rows), va, wave, lane);
+          fg.load(gwin(pc.row0, pc.rows), vg, wave, lane);
+        };
+        if (have) load(cp);
         while (have) {
           __syncthreads();
-          fa.regs(awin(cp.row0, cp.rows), lds, wave, lane);
-          fg.regs(gwin(cp.row0, cp.rows), lds + OA::BYTES, wave, lane);
+          fa.store(va, lds, wave, lane);
+          fg.store(vg, lds + OA::BYTES, wave, lane);
           __syncthreads();
+          const bool more = next(&np);
+          if (more) load(np);
           use(cp, l0);
-          have = next(&cp);
+          cp = np;
+          have = more;
         }
       }
       fold();
@@ -1490,13 +1626,21 @@ __global__ __launch_bounds__(256) void k_grouped_sum(GSumArgs a) {
         chunk(l0 + (uint32_t)((q - c0) % ST) * STAGE);
       }
     } else {
+      u32x4 va[Filler<OA, T, NW>::LOADS], vg[Filler<OG, T, NW>::LOADS];
+      float vc = 0.f;  // lane l < KC: the factor of the chunk's row l
+      auto load = [&](int64_t q) {
+        fa.load(awin(o0 + q * KC, rows_of(q)), va, wave, lane);
+        fg.load(gwin(o0 + q * KC, rows_of(q)), vg, wave, lane);
+        vc = lane < KC && lane < rows_of(q) ? a.crow[o0 + q * KC + lane] : 0.f;
+      };
+      if (c0 < c1) load(c0);
       for (int64_t q = c0; q < c1; ++q) {
         __syncthreads();
-        crows(q, l0 + OA::BYTES + OG::BYTES);
-        fa.regs(awin(o0 + q * KC, rows_of(q)), lds, wave, lane);
-        fg.regs(gwin(o0 + q * KC, rows_of(q)), lds + OA::BYTES, wave, lane);
-        wait_vmcnt<0>();
+        fa.store(va, lds, wave, lane);
+        fg.store(vg, lds + OA::BYTES, wave, lane);
+        *reinterpret_cast<float*>(lds + OA::BYTES + OG::BYTES + wave * 256 + 4 * lane) = vc;
         __syncthreads();
+        if (q + 1 < c1) load(q + 1);
         chunk(l0);
       }
     }
@@ -1514,8 +1658,10 @@ bool dma_ok(int dtype, std::initializer_list<int64_t> widths) {
   return true;
 }
 
+// More than 64 KB of LDS per workgroup has to be asked for.
 template <typename F>
 hipError_t dyn_lds(F* f, int bytes) {
+  if (bytes <= 64 * 1024) return hipSuccess;
   return hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
@@ -1591,12 +1737,20 @@ hipError_t matmul_t(hipStream_t st, int dtype, MatmulArgs a) {
   return run_matmul<T, TRANS, 128, 128, 2, 2, 128, 2, true, false>(st, a);
 }
 
-int64_t norm_slots(const GroupedArgs& g, int ts) { return g.R / ts + g.E * g.B; }
+// The norm's kernel by the average rows per segment, and the workgroups per
+// row tile (enough for segments three times as long as the average).
+struct NormPlan {
+  bool packed;
+  int64_t J;
+};
+NormPlan norm_plan(const GroupedArgs& g) {
+  const int64_t avg = g.R / (g.E * g.B);
+  return NormPlan{avg < 64, std::max<int64_t>(1, std::min<int64_t>(16, (3 * avg + 127) / 128))};
+}
 int64_t piece_slots(const GroupedArgs& g) { return g.R / kPieceRows + g.E * g.B; }
 
-// The clipped sum's kernel, tile and K splits. 256 x 256 tiles (bf16, aligned
-// widths) where the layer is wide enough to fill them; the splits make at
-// least two items per CU, each of at least 512 rows.
+// The clipped sum's kernel, tile and K splits: 256 x 256 tiles (bf16, aligned
+// widths) where the layer is wide enough to fill them.
 struct SumPlan {
   bool big, pieces, dma, fused;
   int64_t mt, nt, ks;
@@ -1609,32 +1763,59 @@ SumPlan sum_plan(int dtype, const GroupedArgs& g) {
   const int64_t t = s.big ? 256 : 128;
   s.mt = (g.d + t - 1) / t;
   s.nt = (g.p + t - 1) / t;
-  const int64_t items = s.mt * s.nt * g.E, rows = g.R / g.E;
-  s.ks = std::max<int64_t>(1, std::min((512 + items - 1) / items, rows / (s.big ? 512 : 256)));
+  // K splits: the fewest rounds of items over the CUs (one 256 x 256 tile or two 128 x 128 tiles at a time; the
+  // times are those measured per 32-row chunk and per item), against the traffic of the splits' partial sums
+  const double slots = s.big ? 256 : 512, chunk_us = s.big ? 0.95 : 1.5, item_us = s.big ? 8 : 5;
+  const double out_us = (double)g.E * g.d * g.p * 8.0 / 4.5e6;  // written and read once, 4.5 TB/s
+  const int64_t chunks = std::max<int64_t>(1, g.R / g.E / 32);
+  double best = 1e30;
+  for (int64_t ks = 1; ks <= 64 && (ks == 1 || ks * 2 <= chunks); ks = ks < 4 ? ks + 1 : ks * 3 / 2) {
+    const double items = (double)(s.mt * s.nt * g.E * ks);
+    const double us = std::ceil(items / slots) * (std::ceil((double)chunks / ks) * chunk_us + item_us) +
+                      (ks > 1 ? ks * out_us + 8.0 : 0.0);
+    if (us < best) {
+      best = us;
+      s.ks = ks;
+    }
+  }
   s.fused = s.ks == 1 && g.d % 4 == 0;
   return s;
 }
 
-template <typename T, int TS, int WG>
-hipError_t run_norm(hipStream_t st, int dtype, GNormArgs a, float* sqnorm, int accumulate) {
-  a.slots = a.R / TS + a.E * a.B;
+template <typename T>
+hipError_t run_norm(hipStream_t st, int dtype, GNormArgs a, const NormPlan& pl, float* sqnorm, int accumulate) {
+  const unsigned fin = (unsigned)std::min<int64_t>(a.B, 1 << 20);
+  if (pl.packed) {
+    k_grouped_row_segments<<<dim3((unsigned)((a.R + 255) / 256)), 256, 0, st>>>(a.seg, a.R, a.E * a.B, a.row_seg);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t tiles = (a.R + 31) / 32;
+    k_grouped_norm_packed<T><<<dim3((unsigned)std::min<int64_t>(tiles, 1 << 20)), 256, 0, st>>>(a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    k_grouped_norm_finish<true><<<fin, 64, 0, st>>>(a, sqnorm, accumulate);
+    return hipGetLastError();
+  }
+  a.J = pl.J;
+  a.slots = a.R / 128 + a.E * a.B;
   const bool dma = dma_ok(dtype, {a.d, a.p});
-  const int lds = (dma ? 2 : 1) * 2 * TS * 128;
+  const int lds = (dma ? 2 : 1) * 2 * 128 * 128;
+  const unsigned grid = (unsigned)((a.slots + 31) / 32 * 32 * a.J);
   hipError_t e;
   if (dma) {
-    auto* f = &k_grouped_norm<T, TS, WG, true>;
+    auto* f = &k_grouped_norm<T, true>;
     e = dyn_lds(f, lds);
     if (e != hipSuccess) return e;
-    f<<<dim3((unsigned)xcd_grid(a.slots)), 64 * WG * WG, lds, st>>>(a);
+    f<<<dim3(grid), 256, lds, st>>>(a);
   } else {
-    auto* f = &k_grouped_norm<T, TS, WG, false>;
+    auto* f = &k_grouped_norm<T, false>;
     e = dyn_lds(f, lds);
     if (e != hipSuccess) return e;
-    f<<<dim3((unsigned)xcd_grid(a.slots)), 64 * WG * WG, lds, st>>>(a);
+    f<<<dim3(grid), 256, lds, st>>>(a);
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_grouped_norm_finish<TS><<<dim3((unsigned)std::min<int64_t>(a.B, 1 << 20)), 64, 0, st>>>(a, sqnorm, accumulate);
+  k_grouped_norm_finish<false><<<fin, 64, 0, st>>>(a, sqnorm, accumulate);
   return hipGetLastError();
 }
 
@@ -1675,7 +1856,11 @@ hipError_t launch_grouped_matmul(hipStream_t st, int dtype, const GroupedArgs& g
   return transpose ? matmul_t<float, true>(st, dtype, a) : matmul_t<float, false>(st, dtype, a);
 }
 
-size_t grouped_norm_ws_bytes(int, const GroupedArgs& g) { return round256((size_t)norm_slots(g, 128) * sizeof(float)); }
+size_t grouped_norm_ws_bytes(int, const GroupedArgs& g) {
+  const NormPlan pl = norm_plan(g);
+  if (pl.packed) return 2 * round256((size_t)g.R * sizeof(float));
+  return round256((size_t)(g.R / 128 + g.E * g.B) * (size_t)pl.J * sizeof(float));
+}
 
 hipError_t launch_grouped_norm(hipStream_t st, int dtype, const GroupedArgs& g, const void* A, const void* G, void* ws,
                                float* sqnorm, int accumulate) {
@@ -1689,8 +1874,10 @@ hipError_t launch_grouped_norm(hipStream_t st, int dtype, const GroupedArgs& g, 
   a.d = g.d;
   a.p = g.p;
   a.partial = static_cast<float*>(ws);
-  return dtype == 1 ? run_norm<bf16s, 128, 2>(st, dtype, a, sqnorm, accumulate)
-                    : run_norm<float, 128, 2>(st, dtype, a, sqnorm, accumulate);
+  a.row_seg = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + round256((size_t)g.R * sizeof(float)));
+  const NormPlan pl = norm_plan(g);
+  return dtype == 1 ? run_norm<bf16s>(st, dtype, a, pl, sqnorm, accumulate)
+                    : run_norm<float>(st, dtype, a, pl, sqnorm, accumulate);
 }
 
 // workspace: the XCDs' item queues, the piece list or the rows' factors, then the splits' sums
@@ -1763,7 +1950,7 @@ bool grouped_fits(int dtype, const GroupedArgs& g) {
   constexpr int64_t kMax = ((int64_t)1 << 32) / 512;
   const int64_t cols = (std::max(g.d, g.p) + 127) / 128;
   if ((g.R / 32 + g.E) * cols + 8 >= kMax) return false;
-  if (g.R / 32 + g.E * g.B + 8 >= kMax) return false;
+  if ((g.R / 128 + g.E * g.B + 32) * norm_plan(g).J >= kMax || g.R / 32 + g.E * g.B + 8 >= kMax) return false;
   const SumPlan s = sum_plan(dtype, g);
   return g.E * s.ks * xcd_grid(s.mt * s.nt) < kMax;
 }
