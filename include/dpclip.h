@@ -438,8 +438,7 @@ size_t dp_conv_workspace_bytes(const dp_conv2d* conv, dp_dtype dtype, int64_t B,
  *  out          [rows, d], dtype; may be x or residual.
  *  sum_out      [rows, d], dtype: s (what the backward pass reads); may be
  *               NULL, x or residual, not out.
- * Tensors aligned to their element; rows are read 16 bytes at a time when d
- * is a multiple of 16 bytes and every tensor is 16-byte aligned.
+ * Tensors aligned to their element.
  */
 dp_status dp_rms_norm(void* stream, const void* x, const void* residual, const void* gain, dp_dtype dtype,
                       dp_dtype gain_dtype, int64_t rows, int64_t d, float eps, void* out, void* sum_out);

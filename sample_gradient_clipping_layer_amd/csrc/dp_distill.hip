@@ -29,6 +29,10 @@ namespace {
 constexpr int kDt = 256;  // threads per block
 constexpr float kLog2e = 1.4426950408889634f;
 
+// 2^x by the hardware's instruction: within one step, results below 2^-126
+// flushed to 0 (they are terms of sums of order 1, or probabilities).
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
 // (m, s): s = sum of 2^((z - m) k) over the values seen, k = log2(e)/tau. The
 // initial maximum is finite, so that no difference of infinities arises.
 struct Run {
@@ -37,11 +41,11 @@ struct Run {
 __device__ __forceinline__ Run run_empty() { return Run{-FLT_MAX, 0.f}; }
 __device__ __forceinline__ Run run_join(Run a, Run b, float k) {
   const float m = fmaxf(a.m, b.m);
-  return Run{m, a.s * __builtin_exp2f((a.m - m) * k) + b.s * __builtin_exp2f((b.m - m) * k)};
+  return Run{m, a.s * exp2_hw((a.m - m) * k) + b.s * exp2_hw((b.m - m) * k)};
 }
 __device__ __forceinline__ void run_one(Run& r, float z, float k) {
   const float m = fmaxf(r.m, z);
-  r.s = r.s * __builtin_exp2f((r.m - m) * k) + __builtin_exp2f((z - m) * k);
+  r.s = r.s * exp2_hw((r.m - m) * k) + exp2_hw((z - m) * k);
   r.m = m;
 }
 // P values at once: one rescale for all of them.
@@ -50,9 +54,9 @@ __device__ __forceinline__ void run_many(Run& r, const float* z, float k) {
   float m = r.m;
 #pragma unroll
   for (int e = 0; e < P; ++e) m = fmaxf(m, z[e]);
-  float s = r.s * __builtin_exp2f((r.m - m) * k);
+  float s = r.s * exp2_hw((r.m - m) * k);
 #pragma unroll
-  for (int e = 0; e < P; ++e) s += __builtin_exp2f((z[e] - m) * k);
+  for (int e = 0; e < P; ++e) s += exp2_hw((z[e] - m) * k);
   r.m = m;
   r.s = s;
 }
@@ -155,7 +159,7 @@ __device__ float token_loss(const DistillArgs& a, int64_t row, Run r, float* red
     const int64_t j = id[k];
     if (j < 0 || j >= a.V) continue;
     const float dt = (teacher_at(a, row * a.K + k) - tm) * inv_tau;
-    const float e = __builtin_exp2f(dt * kLog2e);
+    const float e = exp2_hw(dt * kLog2e);
     if (e == 0.0f) continue;  // no mass there: its logits (infinite ones among them) do not count
     total += e;
     s += e * (dt - (to_f32(z[j]) - r.m) * inv_tau);
@@ -293,7 +297,7 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
         float e = 0.f;
         if (k < K && id[k] >= 0 && id[k] < a.V) {
           w = (int32_t)id[k];
-          e = __builtin_exp2f((teacher_at(a, row * a.K + k) - tm) * inv_tau * kLog2e);
+          e = exp2_hw((teacher_at(a, row * a.K + k) - tm) * inv_tau * kLog2e);
         }
         ids[k] = w;
         qs[k] = e;
@@ -315,7 +319,7 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
     if (K > 0) __syncthreads();
     // ---- p_j f over the split
     auto p_of = [&](float zz) {
-      return any ? f * __builtin_exp2f(__builtin_fmaf(zz, inv_tau, -shift) * kLog2e) : 0.0f;
+      return any ? f * exp2_hw(__builtin_fmaf(zz, inv_tau, -shift) * kLog2e) : 0.0f;
     };
     const Span<T> sn(z, v0, v1);
     auto put1 = [&](int64_t j, float v) {
@@ -349,14 +353,16 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
       return o;
     };
     if (any) {
-      constexpr int U = 4;
+      // eight vectors in flight per thread, past the caches both ways (4096 x 50257 bf16: 186 us with four,
+      // 182 with eight, 170 without caching)
+      constexpr int U = 8;
       int64_t i = threadIdx.x;
       for (; i + (U - 1) * kDt < sn.vecs; i += U * kDt) {
         u32x4 raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = vz[i + u * kDt];
+        for (int u = 0; u < U; ++u) raw[u] = __builtin_nontemporal_load(vz + i + u * kDt);
 #pragma unroll
-        for (int u = 0; u < U; ++u) vg[i + u * kDt] = vec(raw[u]);
+        for (int u = 0; u < U; ++u) __builtin_nontemporal_store(vec(raw[u]), vg + i + u * kDt);
       }
       for (; i < sn.vecs; i += kDt) vg[i] = vec(vz[i]);
     } else {

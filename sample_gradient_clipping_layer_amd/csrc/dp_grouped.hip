@@ -712,13 +712,19 @@ struct GNormArgs {
   const void *A, *G;
   const int64_t* seg;
   int64_t R, E, B, d, p;
-  float* partial;   // tiles: [slots * J]; packed: a value per row [R]
+  float* partial;   // tiles: [slots * J]; packed: J values per row [R][J]
   int32_t* row_seg; // packed: a row's segment, -1 for none [R]
-  int64_t slots;    // R / 128 + E * B
+  int64_t slots;    // R / TS + E * B
   int64_t J;        // workgroups a row tile's pairs are dealt to
 };
 
-// Segments of about 64 rows or more: row tiles of 128 within a segment.
+template <typename T>
+constexpr int norm_tile() {
+  return sizeof(T) == 2 ? 128 : 64;
+}
+
+// Segments of about 64 rows or more: row tiles of TS within a segment (128 for
+// bf16, where memory bounds; 64 for fp32, where the products do).
 // Workgroup (tile t, j) takes the pairs (t, u), u - t = j, j + J, ...: a long
 // segment's pairs spread over J workgroups (one after another they were the
 // launch's critical path: 276 -> 172 us at 256 segments of 128 rows on
@@ -726,7 +732,7 @@ struct GNormArgs {
 // or past the segment only takes part in the loads.
 template <typename T, bool DMA>
 __global__ __launch_bounds__(256) void k_grouped_norm(GNormArgs a) {
-  constexpr int TS = 128, WG = 2, NW = 4, WT = 64, NB = 2;
+  constexpr int TS = norm_tile<T>(), WG = 2, NW = 4, WT = TS / 2, NB = WT / 32;
   using O = Opnd<T, true, TS>;
   constexpr int KC = O::KC, STAGE = 2 * O::BYTES, ST = 2;
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
@@ -829,13 +835,15 @@ __global__ __launch_bounds__(256) void k_grouped_norm_packed(GNormArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, g = lane >> 5;
   const int orow = threadIdx.x >> 3, ocol = (threadIdx.x & 7) * 4;  // this thread's four elements of the product
-  for (int64_t t = blockIdx.x; t * 32 < a.R; t += gridDim.x) {
+  const int64_t J = a.J;
+  for (int64_t item = blockIdx.x; item < (a.R + 31) / 32 * J; item += gridDim.x) {
+    const int64_t t = item / J, j = item - t * J;  // pairs (t, t + j), (t, t + j + J), ...
     const int64_t trow = t * 32 + r;
     const bool tok = trow < a.R && a.row_seg[trow] >= 0;
     const int oseg = t * 32 + orow < a.R ? a.row_seg[t * 32 + orow] : -1;
     const int last = a.row_seg[t * 32 + 31 < a.R ? t * 32 + 31 : a.R - 1];
     float value = 0.f;
-    for (int64_t u = t;; ++u) {
+    for (int64_t u = t + j;; u += J) {
       if (u > t && (u * 32 >= a.R || last < 0 || a.row_seg[u * 32] != last)) break;  // uniform
       const int64_t urow = u * 32 + r;
       const bool uok = urow < a.R && a.row_seg[urow] >= 0;
@@ -883,7 +891,7 @@ __global__ __launch_bounds__(256) void k_grouped_norm_packed(GNormArgs a) {
       for (int off = 4; off > 0; off >>= 1) s += __shfl_xor(s, off, kWave);
       value += u == t ? s : 2.0f * s;
     }
-    if ((threadIdx.x & 7) == 0 && t * 32 + orow < a.R) a.partial[t * 32 + orow] = value;
+    if ((threadIdx.x & 7) == 0 && t * 32 + orow < a.R) a.partial[(t * 32 + orow) * J + j] = value;
   }
 }
 
@@ -907,15 +915,15 @@ __global__ __launch_bounds__(256) void k_grouped_row_segments(const int64_t* __r
 // sqnorm[b] (+)= the values of the sample's tiles (or, packed, rows), in order
 // within a segment, one lane per segment, the segments joined in a fixed
 // order. One wave per sample.
-template <bool PACKED>
+template <bool PACKED, int TS>
 __global__ __launch_bounds__(64) void k_grouped_norm_finish(GNormArgs a, float* __restrict__ sqnorm, int accumulate) {
   for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
     float s = 0.f;
     for (int64_t e = threadIdx.x; e < a.E; e += 64) {
       const int64_t g = e * a.B + b;
       const int64_t off = clamp_row(a.seg[g], a.R), end = clamp_row(a.seg[g + 1], a.R);
-      const int64_t first = PACKED ? off : (off / 128 + g) * a.J;
-      const int64_t n = end <= off ? 0 : PACKED ? end - off : (end - off + 127) / 128 * a.J;
+      const int64_t first = (PACKED ? off : off / TS + g) * a.J;
+      const int64_t n = end <= off ? 0 : (PACKED ? end - off : (end - off + TS - 1) / TS) * a.J;
 #pragma unroll 8
       for (int64_t t = 0; t < n; ++t) s += a.partial[first + t];
     }
@@ -1139,25 +1147,25 @@ __global__ __launch_bounds__(512) void k_grouped_sum_big(GSumArgs a) {
   }
 
   // ---- items: (expert by rank, split, tile of this XCD's share), tiles fastest
-  const int64_t tiles = a.mt * a.nt, per = (tiles + 7) / 8, wgs = gridDim.x >> 3, xcd = blockIdx.x & 7;
-  const int share_t = (int)(tiles - xcd * per < per ? tiles - xcd * per : per);
-  const int nlocal = share_t > 0 ? (int)(a.E * a.ks) * share_t : 0;
+  const int tiles = (int)(a.mt * a.nt), per = (tiles + 7) / 8, wgs = (int)(gridDim.x >> 3), xcd = (int)(blockIdx.x & 7);
+  const int share_t = tiles - xcd * per < per ? tiles - xcd * per : per;
+  const int nlocal = share_t > 0 ? (int)a.E * (int)a.ks * share_t : 0;
   if ((int)(blockIdx.x >> 3) >= nlocal) return;  // whole workgroup
   struct Item {
-    int64_t e, sp, m0, n0;
+    int e, sp, m0, n0;
   };
   auto item_at = [&](int l) {
-    const int ri = l / share_t, er = ri / (int)a.ks;
-    const int64_t t = xcd * per + (l - ri * share_t);
+    const uint32_t ri = (uint32_t)l / (uint32_t)share_t, er = ri / (uint32_t)a.ks;
+    const uint32_t t = (uint32_t)(xcd * per) + ((uint32_t)l - ri * (uint32_t)share_t), tn = t / (uint32_t)a.mt;
     Item it;
-    it.sp = ri - er * (int)a.ks;
-    it.e = a.E <= 64 ? __builtin_amdgcn_readlane(order, er) : er;
-    it.m0 = (t % a.mt) * BM;
-    it.n0 = (t / a.mt) * BN;
+    it.sp = (int)(ri - er * (uint32_t)a.ks);
+    it.e = a.E <= 64 ? __builtin_amdgcn_readlane(order, (int)er) : (int)er;
+    it.m0 = (int)(t - tn * (uint32_t)a.mt) * BM;
+    it.n0 = (int)tn * BN;
     return it;
   };
 
-  const int64_t ab = a.d * 2, gb = a.p * 2;
+  const uint32_t ab = (uint32_t)a.d * 2u, gb = (uint32_t)a.p * 2u;
   FA fa;
   FG fg;
   fa.init(ab, wave, lane);
@@ -1168,25 +1176,29 @@ __global__ __launch_bounds__(512) void k_grouped_sum_big(GSumArgs a) {
   rg.init(wn * WN, lane);
   const uint32_t l0 = lds_addr(lds);
 
-  // ---- the loads' side. Its chunk: rows [lrow, lrow + lrows) of item lit; lrows = 0: an empty window (past the
-  // last item, for an expert without rows, or for a sample with factor 0, whose rows add nothing).
+  // ---- the loads' side: buffers of its chunk (no bytes: an empty window, for chunks past the last item, experts
+  // without rows, and samples with factor 0, whose rows add nothing), and where its item stands
   __shared__ int next_item[2];
   int litem = (int)(blockIdx.x >> 3), turn = 0;
   bool first = true;
-  if (threadIdx.x == 0) next_item[0] = (int)wgs + atomicAdd(a.queue + xcd, 1);
+  if (threadIdx.x == 0) next_item[0] = wgs + atomicAdd(a.queue + xcd, 1);
   __syncthreads();
-  Item lit{0, 0, 0, 0};
-  int64_t lrow = 0;
-  int lrows = 0;
-  bool lopen = false;        // the item has chunks left
-  int64_t lpos = 0, lend = 0;  // ratio: slot window and end; split: next row and end
+  const char *abase = nullptr, *gbase = nullptr;  // the item's first columns
+  uint32_t acols = 0, gcols = 0;                  // bytes of them to the row's end
+  uint32_t va[FA::LOADS], vg[FG::LOADS];          // the lane's offsets; past num_records where its columns do not exist
+#pragma unroll
+  for (int i = 0; i < FA::LOADS; ++i) va[i] = 0x80000000u;
+#pragma unroll
+  for (int i = 0; i < FG::LOADS; ++i) vg[i] = 0x80000000u;
+  u32x4 sa = make_srd(static_cast<const char*>(nullptr), 0u), sg = sa, sc = sa;
+  bool lopen = false;       // the item has chunks left
+  int lpos = 0, lend = 0;   // ratio: slot window and end; split: next row and end
   uint64_t lmask = 0;
   Piece lmine{0, 0, 0.f, 0};
   uint32_t ls = l0;
   struct Desc {
     float c;
-    int end;   // last chunk of its item
-    int item;  // -1: past the last
+    int id;  // 2 * item + (last chunk of its item); -1: past the last
   };
   auto load64 = [&]() {
     lmine = Piece{0, 0, 0.f, 0};
@@ -1199,82 +1211,84 @@ __global__ __launch_bounds__(512) void k_grouped_sum_big(GSumArgs a) {
       load64();
     }
   };
-  auto fetch = [&]() -> Desc {  // the next chunk
-    Desc ds{0.f, 0, -1};
-    lrows = 0;
-    if (!lopen) {
-      // The item after this one is taken off the list now, by the first wave, and read by all when this one's
-      // chunks have been fetched: at least one barrier later.
-      if (first) {
-        first = false;
-      } else if (litem >= 0) {
-        litem = __builtin_amdgcn_readfirstlane(next_item[turn]);
-        turn ^= 1;
-        if (wave == 0 && lane == 0) next_item[turn] = (int)wgs + atomicAdd(a.queue + xcd, 1);
-      }
-      if (litem < 0 || litem >= nlocal) {
-        litem = -1;
-        return ds;
-      }
-      lit = item_at(litem);
-      const int64_t g0 = lit.e * a.B, g1 = g0 + a.B;
-      const int64_t o0 = uniform64(clamp_row(a.seg[g0], a.R)), o1 = uniform64(clamp_row(a.seg[g1], a.R));
-      // the split's share of the expert's slots, or of its rows in whole chunks
-      const int64_t s0 = RATIO ? o0 / KC + g0 : 0, s1 = RATIO ? o1 / KC + g1 : (o1 - o0 + KC - 1) / KC;
-      const int64_t share = (s1 - s0 + a.ks - 1) / a.ks;
-      const int64_t b0 = s0 + lit.sp * share, b1 = b0 + share < s1 ? b0 + share : s1;
-      lpos = RATIO ? b0 : o0 + b0 * KC;
-      lend = RATIO ? b1 : (o0 + b1 * KC < o1 ? o0 + b1 * KC : o1);
-      if constexpr (RATIO) {
-        lmask = 0;
-        if (lpos < lend) {
-          load64();
-          skip_unused();
-        }
+  auto window = [&](int row, int rows) {
+    const uint32_t n = (uint32_t)rows;
+    sa = make_srd(abase + (uint64_t)(uint32_t)row * ab, n ? (n - 1) * ab + acols : 0u);
+    sg = make_srd(gbase + (uint64_t)(uint32_t)row * gb, n ? (n - 1) * gb + gcols : 0u);
+    if constexpr (!RATIO) sc = make_srd(a.crow + row, 4u * n);
+  };
+  auto open_item = [&]() -> bool {
+    // The item after this one is taken off the list now, by the first wave, and read by all when this one's
+    // chunks have been fetched: at least one barrier later.
+    if (first) {
+      first = false;
+    } else if (litem >= 0) {
+      litem = __builtin_amdgcn_readfirstlane(next_item[turn]);
+      turn ^= 1;
+      if (threadIdx.x == 0) next_item[turn] = wgs + atomicAdd(a.queue + xcd, 1);
+    }
+    if (litem < 0 || litem >= nlocal) {
+      litem = -1;
+      return false;
+    }
+    const Item it = item_at(litem);
+    abase = static_cast<const char*>(a.A) + 2 * it.m0;
+    gbase = static_cast<const char*>(a.G) + 2 * it.n0;
+    acols = ab - 2u * (uint32_t)it.m0;
+    gcols = gb - 2u * (uint32_t)it.n0;
+#pragma unroll
+    for (int i = 0; i < FA::LOADS; ++i) va[i] = 2u * (uint32_t)fa.qp[i] < acols ? fa.voff[i] : 0x80000000u;
+#pragma unroll
+    for (int i = 0; i < FG::LOADS; ++i) vg[i] = 2u * (uint32_t)fg.qp[i] < gcols ? fg.voff[i] : 0x80000000u;
+    const int g0 = it.e * (int)a.B, g1 = g0 + (int)a.B;
+    const int o0 = __builtin_amdgcn_readfirstlane((int)clamp_row(a.seg[g0], a.R));
+    const int o1 = __builtin_amdgcn_readfirstlane((int)clamp_row(a.seg[g1], a.R));
+    // the split's share of the expert's slots, or of its rows in whole chunks
+    const int s0 = RATIO ? o0 / KC + g0 : 0, s1 = RATIO ? o1 / KC + g1 : (o1 - o0 + KC - 1) / KC;
+    const int share = (s1 - s0 + (int)a.ks - 1) / (int)a.ks;
+    const int b0 = s0 + it.sp * share, b1 = b0 + share < s1 ? b0 + share : s1;
+    lpos = RATIO ? b0 : o0 + b0 * KC;
+    lend = RATIO ? b1 : (b1 < s1 ? o0 + b1 * KC : o1);
+    lmask = 0;
+    if constexpr (RATIO) {
+      if (lpos < lend) {
+        load64();
+        skip_unused();
       }
     }
-    ds.item = litem;
+    return true;
+  };
+  auto fetch = [&]() -> Desc {  // the next chunk
+    if (!lopen && !open_item()) {
+      window(0, 0);
+      return Desc{0.f, -1};
+    }
+    float c = 0.f;
     if constexpr (RATIO) {
-      if (lmask == 0) {  // no rows in this item: one empty chunk
-        lopen = false;
-        ds.end = 1;
-        return ds;
+      int row = 0, rows = 0;
+      if (lmask != 0) {  // else: no rows in this item, one empty chunk
+        const int i = __ffsll((unsigned long long)lmask) - 1;
+        lmask &= lmask - 1;
+        row = __builtin_amdgcn_readlane(lmine.row0, i);
+        c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lmine.c), i));
+        rows = c == 0.0f ? 0 : __builtin_amdgcn_readlane(lmine.rows, i);
+        if (lmask == 0) skip_unused();
       }
-      const int i = __ffsll((unsigned long long)lmask) - 1;
-      lmask &= lmask - 1;
-      lrow = __builtin_amdgcn_readlane(lmine.row0, i);
-      lrows = __builtin_amdgcn_readlane(lmine.rows, i);
-      ds.c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lmine.c), i));
-      if (ds.c == 0.0f) lrows = 0;
-      skip_unused();
+      window(row, rows);
       lopen = lmask != 0;
     } else {
-      if (lpos < lend) {
-        lrow = lpos;
-        lrows = (int)(lend - lpos < KC ? lend - lpos : KC);
-        lpos += KC;
-      }
+      const int left = lend - lpos;
+      window(lpos, left <= 0 ? 0 : left < KC ? left : KC);
+      lpos += KC;
       lopen = lpos < lend;
     }
-    ds.end = !lopen;
-    return ds;
+    return Desc{c, 2 * litem + (lopen ? 0 : 1)};
   };
-  auto aload = [&](int P) {
-    const u32x4 srd = make_srd(static_cast<const T*>(a.A) + lrow * a.d + lit.m0,
-                               lrows > 0 ? (uint32_t)((lrows - 1) * ab + (a.d - lit.m0) * 2) : 0u);
-    dma16_buf(srd, fa.qp[P] < (int)(a.d - lit.m0) ? fa.voff[P] : 0x80000000u, ls + (wave + NW * P) * 1024);
-  };
-  auto gload = [&](int P) {
-    const u32x4 srd = make_srd(static_cast<const T*>(a.G) + lrow * a.p + lit.n0,
-                               lrows > 0 ? (uint32_t)((lrows - 1) * gb + (a.p - lit.n0) * 2) : 0u);
-    dma16_buf(srd, fg.qp[P] < (int)(a.p - lit.n0) ? fg.voff[P] : 0x80000000u,
-              ls + OA::BYTES + (wave + NW * P) * 1024);
-  };
+  auto aload = [&](int P) { dma16_buf(sa, va[P], ls + (wave + NW * P) * 1024); };
+  auto gload = [&](int P) { dma16_buf(sg, vg[P], ls + OA::BYTES + (wave + NW * P) * 1024); };
   auto cload = [&]() {
-    if constexpr (!RATIO) {
-      const u32x4 srd = make_srd(a.crow + lrow, 4u * (uint32_t)lrows);
-      if (lane < KC) dma4_buf(srd, 4u * lane, ls + OA::BYTES + OG::BYTES + wave * 128);
-    }
+    if constexpr (!RATIO)
+      if (lane < KC) dma4_buf(sc, 4u * lane, ls + OA::BYTES + OG::BYTES + wave * 128);
   };
   auto next_stage = [&](uint32_t st) { return st == l0 + (ST - 1) * STAGE ? l0 : st + STAGE; };
 
@@ -1289,7 +1303,9 @@ __global__ __launch_bounds__(512) void k_grouped_sum_big(GSumArgs a) {
   f32x16 acc[NBM][NBN];
   // One step (16 rows): as in k_grouped_matmul_big, the next step's reads and a later chunk's loads between the
   // products. With split, sb/s of the fragments in hand give the rows' factors.
-  auto step = [&](const Frags& f, uint32_t csb, int cstep, Frags& g, uint32_t sb, int s, auto gpart) {
+  // Ratio, at a sample's first step: each block is rescaled by r while its predecessor's product runs.
+  auto step = [&](const Frags& f, uint32_t csb, int cstep, Frags& g, uint32_t sb, int s, auto gpart, bool rescale,
+                  float r) {
     u32x4 t[NBM][3];
     if constexpr (!RATIO) {
       f32x4 ck[2];
@@ -1303,6 +1319,10 @@ __global__ __launch_bounds__(512) void k_grouped_sum_big(GSumArgs a) {
     for (int k = 0; k < NBM * NBN; ++k) {
       const int j = k / NBM, i = k % NBM;
       if constexpr (RATIO) {
+        if (decltype(gpart)::value && rescale) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) acc[i][j][x] *= r;
+        }
         acc[i][j] = mfma32_bf16(f.a[i], f.g[j], acc[i][j]);
       } else {
 #pragma unroll
@@ -1350,8 +1370,8 @@ __global__ __launch_bounds__(512) void k_grouped_sum_big(GSumArgs a) {
   for (int k = 0; k < NBN + NBM; ++k) read1(l0, 0, f0, k);
   uint32_t cs = l0;
 
-  while (q0.item >= 0) {
-    const Item it = item_at(q0.item);
+  while (q0.id >= 0) {
+    const Item it = item_at(q0.id >> 1);
     const Emit em = emit_at(a, it.e, it.sp);
     zero_acc(acc);
     float prev = 0.f, ref = 0.f;  // ratio: the factor acc is in units of, and that of the run's first sample
@@ -1376,43 +1396,38 @@ __global__ __launch_bounds__(512) void k_grouped_sum_big(GSumArgs a) {
           }
     };
     while (true) {
+      bool rescale = false;
+      float r = 1.0f;
       if constexpr (RATIO) {
         if (q0.c != 0.0f && q0.c != prev) {
           if (prev != 0.0f) {
             const float mag = fabsf(q0.c), rmag = fabsf(ref);
-            float r;
+            rescale = true;
+            r = prev / q0.c;
             if (mag < rmag * 0x1p-32f || mag > rmag * 0x1p32f) {
               // factors this far apart would overflow the quotient: bank the sum so far in the result's place
               for_elems([&](float v, float* o) {
                 *o = flushed ? *o + v * prev : v * prev;
-                return v;
+                return 0.0f;
               });
               flushed = true;
               ref = q0.c;
-              r = 0.0f;
-            } else {
-              r = prev / q0.c;
+              rescale = false;
             }
-#pragma unroll
-            for (int i = 0; i < NBM; ++i)
-#pragma unroll
-              for (int j = 0; j < NBN; ++j)
-#pragma unroll
-                for (int k = 0; k < 16; ++k) acc[i][j][k] *= r;
           } else {
             ref = q0.c;
           }
           prev = q0.c;
         }
       }
-      step(f0, cs, 0, f1, cs, 1, std::true_type{});
+      step(f0, cs, 0, f1, cs, 1, std::true_type{}, rescale, r);
       const Desc q4 = fetch();
       wait_vmcnt<LPC*(ST - 2)>();
       lds_barrier();
       const uint32_t nx = next_stage(cs);
-      step(f1, cs, 1, f0, nx, 0, std::false_type{});
+      step(f1, cs, 1, f0, nx, 0, std::false_type{}, false, 1.0f);
       cs = nx;
-      const int end = q0.end;
+      const int end = q0.id & 1;
       q0 = q1;
       q1 = q2;
       q2 = q3;
@@ -1741,11 +1756,12 @@ hipError_t matmul_t(hipStream_t st, int dtype, MatmulArgs a) {
 // row tile (enough for segments three times as long as the average).
 struct NormPlan {
   bool packed;
-  int64_t J;
+  int64_t ts, J;
 };
-NormPlan norm_plan(const GroupedArgs& g) {
-  const int64_t avg = g.R / (g.E * g.B);
-  return NormPlan{avg < 64, std::max<int64_t>(1, std::min<int64_t>(16, (3 * avg + 127) / 128))};
+NormPlan norm_plan(int dtype, const GroupedArgs& g) {
+  const int64_t avg = g.R / (g.E * g.B), ts = dtype == 1 ? norm_tile<bf16s>() : norm_tile<float>();
+  if (avg < 64) return NormPlan{true, 32, 1 + (avg + 15) / 16};
+  return NormPlan{false, ts, std::max<int64_t>(1, std::min<int64_t>(16, (3 * avg + ts - 1) / ts))};
 }
 int64_t piece_slots(const GroupedArgs& g) { return g.R / kPieceRows + g.E * g.B; }
 
@@ -1756,50 +1772,58 @@ struct SumPlan {
   int64_t mt, nt, ks;
 };
 SumPlan sum_plan(int dtype, const GroupedArgs& g) {
-  SumPlan s{};
-  s.dma = dma_ok(dtype, {g.d, g.p});
-  s.big = dtype == 1 && s.dma && g.d >= 192 && g.p >= 192;
-  s.pieces = dtype == 1 && g.R / (g.E * g.B) >= 16;
-  const int64_t t = s.big ? 256 : 128;
-  s.mt = (g.d + t - 1) / t;
-  s.nt = (g.p + t - 1) / t;
-  // K splits: the fewest rounds of items over the CUs (one 256 x 256 tile or two 128 x 128 tiles at a time; the
-  // times are those measured per 32-row chunk and per item), against the traffic of the splits' partial sums
-  const double slots = s.big ? 256 : 512, chunk_us = s.big ? 0.95 : 1.5, item_us = s.big ? 8 : 5;
-  const double out_us = (double)g.E * g.d * g.p * 8.0 / 4.5e6;  // written and read once, 4.5 TB/s
+  SumPlan best{};
+  double best_us = 1e30;
+  const bool dma = dma_ok(dtype, {g.d, g.p}), pieces = dtype == 1 && g.R / (g.E * g.B) >= 16;
+  const double out_us = (double)g.E * g.d * g.p * 8.0 / 4.5e6;  // a split's sums written and read once, 4.5 TB/s
   const int64_t chunks = std::max<int64_t>(1, g.R / g.E / 32);
-  double best = 1e30;
-  for (int64_t ks = 1; ks <= 64 && (ks == 1 || ks * 2 <= chunks); ks = ks < 4 ? ks + 1 : ks * 3 / 2) {
-    const double items = (double)(s.mt * s.nt * g.E * ks);
-    const double us = std::ceil(items / slots) * (std::ceil((double)chunks / ks) * chunk_us + item_us) +
-                      (ks > 1 ? ks * out_us + 8.0 : 0.0);
-    if (us < best) {
-      best = us;
-      s.ks = ks;
+  for (int big = 0; big < 2; ++big) {
+    if (big && !(dtype == 1 && dma && g.d >= 192 && g.p >= 192)) continue;
+    SumPlan s{};
+    s.big = big;
+    s.pieces = pieces;
+    s.dma = dma;
+    const int64_t t = big ? 256 : 128;
+    s.mt = (g.d + t - 1) / t;
+    s.nt = (g.p + t - 1) / t;
+    // rounds of items over the CUs (one 256 x 256 tile or two 128 x 128 tiles at a time), each the time of its
+    // 32-row chunks and a fixed part, as measured; then the traffic of the splits' sums and their reduce launch
+    const double slots = big ? 256 : 512, item_us = big ? 20 : 6;
+    const double chunk_us = big ? (pieces ? 1.1 : 1.7) : dtype == 1 ? (pieces ? 1.3 : 2.5) : dma ? 4.0 : 6.5;
+    for (int64_t ks = 1; ks <= 64 && (ks == 1 || ks * 2 <= chunks); ks = ks < 4 ? ks + 1 : ks * 3 / 2) {
+      const double items = (double)(s.mt * s.nt * g.E * ks);
+      const double us = std::ceil(items / slots) * (std::ceil((double)chunks / ks) * chunk_us + item_us) +
+                        (ks > 1 ? ks * out_us + 14.0 : 0.0);
+      if (us < best_us) {
+        best_us = us;
+        s.ks = ks;
+        best = s;
+      }
     }
   }
-  s.fused = s.ks == 1 && g.d % 4 == 0;
-  return s;
+  best.fused = best.ks == 1 && g.d % 4 == 0;
+  return best;
 }
 
 template <typename T>
 hipError_t run_norm(hipStream_t st, int dtype, GNormArgs a, const NormPlan& pl, float* sqnorm, int accumulate) {
   const unsigned fin = (unsigned)std::min<int64_t>(a.B, 1 << 20);
+  a.J = pl.J;
   if (pl.packed) {
     k_grouped_row_segments<<<dim3((unsigned)((a.R + 255) / 256)), 256, 0, st>>>(a.seg, a.R, a.E * a.B, a.row_seg);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t tiles = (a.R + 31) / 32;
-    k_grouped_norm_packed<T><<<dim3((unsigned)std::min<int64_t>(tiles, 1 << 20)), 256, 0, st>>>(a);
+    const int64_t items = (a.R + 31) / 32 * a.J;
+    k_grouped_norm_packed<T><<<dim3((unsigned)std::min<int64_t>(items, 1 << 20)), 256, 0, st>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_grouped_norm_finish<true><<<fin, 64, 0, st>>>(a, sqnorm, accumulate);
+    k_grouped_norm_finish<true, 32><<<fin, 64, 0, st>>>(a, sqnorm, accumulate);
     return hipGetLastError();
   }
-  a.J = pl.J;
-  a.slots = a.R / 128 + a.E * a.B;
+  constexpr int TS = norm_tile<T>();
+  a.slots = a.R / TS + a.E * a.B;
   const bool dma = dma_ok(dtype, {a.d, a.p});
-  const int lds = (dma ? 2 : 1) * 2 * 128 * 128;
+  const int lds = (dma ? 2 : 1) * 2 * TS * 128;
   const unsigned grid = (unsigned)((a.slots + 31) / 32 * 32 * a.J);
   hipError_t e;
   if (dma) {
@@ -1815,7 +1839,7 @@ hipError_t run_norm(hipStream_t st, int dtype, GNormArgs a, const NormPlan& pl, 
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_grouped_norm_finish<false><<<fin, 64, 0, st>>>(a, sqnorm, accumulate);
+  k_grouped_norm_finish<false, TS><<<fin, 64, 0, st>>>(a, sqnorm, accumulate);
   return hipGetLastError();
 }
 
@@ -1856,10 +1880,10 @@ hipError_t launch_grouped_matmul(hipStream_t st, int dtype, const GroupedArgs& g
   return transpose ? matmul_t<float, true>(st, dtype, a) : matmul_t<float, false>(st, dtype, a);
 }
 
-size_t grouped_norm_ws_bytes(int, const GroupedArgs& g) {
-  const NormPlan pl = norm_plan(g);
-  if (pl.packed) return 2 * round256((size_t)g.R * sizeof(float));
-  return round256((size_t)(g.R / 128 + g.E * g.B) * (size_t)pl.J * sizeof(float));
+size_t grouped_norm_ws_bytes(int dtype, const GroupedArgs& g) {
+  const NormPlan pl = norm_plan(dtype, g);
+  if (pl.packed) return round256((size_t)g.R * (size_t)pl.J * sizeof(float)) + round256((size_t)g.R * sizeof(int32_t));
+  return round256((size_t)(g.R / pl.ts + g.E * g.B) * (size_t)pl.J * sizeof(float));
 }
 
 hipError_t launch_grouped_norm(hipStream_t st, int dtype, const GroupedArgs& g, const void* A, const void* G, void* ws,
@@ -1874,8 +1898,9 @@ hipError_t launch_grouped_norm(hipStream_t st, int dtype, const GroupedArgs& g, 
   a.d = g.d;
   a.p = g.p;
   a.partial = static_cast<float*>(ws);
-  a.row_seg = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + round256((size_t)g.R * sizeof(float)));
-  const NormPlan pl = norm_plan(g);
+  const NormPlan pl = norm_plan(dtype, g);
+  a.row_seg = reinterpret_cast<int32_t*>(static_cast<char*>(ws) +
+                                         round256((size_t)g.R * (size_t)pl.J * sizeof(float)));
   return dtype == 1 ? run_norm<bf16s>(st, dtype, a, pl, sqnorm, accumulate)
                     : run_norm<float>(st, dtype, a, pl, sqnorm, accumulate);
 }
@@ -1894,6 +1919,7 @@ size_t grouped_sum_ws_bytes(int dtype, const GroupedArgs& g) {
 hipError_t launch_grouped_sum(hipStream_t st, int dtype, const GroupedArgs& g, const void* A, const void* G,
                               const float* c, void* ws, const NoiseArgs& na, float* out) {
   const SumPlan s = sum_plan(dtype, g);
+  const bool fused = s.fused || (s.ks == 1 && na.sc == 0.0f);  // without noise the quads do not matter
   GSumArgs a{};
   a.queue = static_cast<int32_t*>(ws);
   void* list = static_cast<char*>(ws) + kQueueBytes;
@@ -1921,9 +1947,9 @@ hipError_t launch_grouped_sum(hipStream_t st, int dtype, const GroupedArgs& g, c
   a.mt = s.mt;
   a.nt = s.nt;
   a.ks = s.ks;
-  a.na = s.fused ? na : make_noise_args(0.0f, 1.0f, 0, 0, 0);
+  a.na = fused ? na : make_noise_args(0.0f, 1.0f, 0, 0, 0);
   a.out = out;
-  a.fused = s.fused;
+  a.fused = fused;
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + sum_list_bytes(s, g));
   if (s.big) {
     const int64_t grid = std::min<int64_t>(256, xcd_grid(s.mt * s.nt * s.ks * g.E));
@@ -1942,7 +1968,7 @@ hipError_t launch_grouped_sum(hipStream_t st, int dtype, const GroupedArgs& g, c
       e = s.dma ? run_sum(&k_grouped_sum<float, false, true>, st, a, grid, 256, st_n * (32768 + 1024))
                 : run_sum(&k_grouped_sum<float, false, false>, st, a, grid, 256, st_n * (32768 + 1024));
   }
-  if (e != hipSuccess || s.fused) return e;
+  if (e != hipSuccess || fused) return e;
   return launch_split_reduce(st, a.ks, a.part, g.E * g.d, g.p, na, out);
 }
 
@@ -1950,7 +1976,8 @@ bool grouped_fits(int dtype, const GroupedArgs& g) {
   constexpr int64_t kMax = ((int64_t)1 << 32) / 512;
   const int64_t cols = (std::max(g.d, g.p) + 127) / 128;
   if ((g.R / 32 + g.E) * cols + 8 >= kMax) return false;
-  if ((g.R / 128 + g.E * g.B + 32) * norm_plan(g).J >= kMax || g.R / 32 + g.E * g.B + 8 >= kMax) return false;
+  const NormPlan n = norm_plan(dtype, g);
+  if ((g.R / n.ts + g.E * g.B + 32) * n.J >= kMax || g.R / 32 + g.E * g.B + 8 >= kMax) return false;
   const SumPlan s = sum_plan(dtype, g);
   return g.E * s.ks * xcd_grid(s.mt * s.nt) < kMax;
 }

@@ -29,52 +29,59 @@ namespace {
 __device__ __forceinline__ void put(float& d, float v) { d = v; }
 __device__ __forceinline__ void put(bf16s& d, float v) { d.u = f32_to_bf16(v); }
 
-// The columns a lane holds: E elements, either E/P vectors of 16 bytes (VEC)
-// or E single elements (rows that are not 16-byte aligned), the row's LPR
-// lanes side by side.
-template <typename T, bool VEC, int E, int LPR>
+// The columns a lane holds: E elements as vectors of 16 bytes, the row's LPR
+// lanes side by side. Rows may start at any element (odd widths, views): the
+// hardware takes unaligned 16-byte accesses, and the row's last vector is
+// taken element by element when it is not whole (WHOLE: it always is). (Single-element accesses for
+// such rows took 16.6 us instead of 8 for a backward pass of 1001 x 1001 fp32.)
+template <typename T, bool WHOLE, int E, int LPR>
 struct RowMap {
-  static constexpr int P = VEC ? elem_traits<T>::per16 : 1;
+  static constexpr int P = elem_traits<T>::per16;
   static constexpr int N = E / P;
-  static __device__ __forceinline__ int64_t col(int j, int lane) { return ((int64_t)j * LPR + lane) * P; }
+  static __device__ __forceinline__ int col(int j, int lane) { return (j * LPR + lane) * P; }  // d <= 32768
+
+  using Raw = u32x4[N];
 
   // elements past d read as 0
-  static __device__ __forceinline__ void load(const T* __restrict__ row, int64_t d, int lane, float* v) {
-    if constexpr (VEC) {
-      u32x4 raw[N];
+  static __device__ __forceinline__ void fetch(const T* __restrict__ row, int d, int lane, Raw& raw) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        raw[j] = u32x4{0u, 0u, 0u, 0u};
-        const int64_t c = col(j, lane);
-        if (c < d) raw[j] = *reinterpret_cast<const u32x4*>(row + c);
-      }
+    for (int j = 0; j < N; ++j) {
+      raw[j] = u32x4{0u, 0u, 0u, 0u};
+      const int c = col(j, lane);
+      if (WHOLE ? c < d : c + P <= d) {
+        __builtin_memcpy(&raw[j], row + c, 16);
+      } else if (!WHOLE && c < d) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if constexpr (P == 8) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[j * 8 + 2 * e] = __uint_as_float(raw[j][e] << 16);
-            v[j * 8 + 2 * e + 1] = __uint_as_float(raw[j][e] & 0xFFFF0000u);
+        for (int e = 0; e < P - 1; ++e)
+          if (c + e < d) {
+            const uint32_t bits = raw_bits(row[c + e]);
+            if constexpr (P == 8) raw[j][e >> 1] |= bits << (16 * (e & 1));
+            else raw[j][e] = bits;
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[j * 4 + e] = __uint_as_float(raw[j][e]);
-        }
       }
-    } else {
+    }
+  }
+  static __device__ __forceinline__ void unpack(const Raw& raw, float* v) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int64_t c = col(j, lane);
-        v[j] = c < d ? to_f32(row[c]) : 0.f;
+    for (int j = 0; j < N; ++j) {
+      if constexpr (P == 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[j * 8 + 2 * e] = __uint_as_float(raw[j][e] << 16);
+          v[j * 8 + 2 * e + 1] = __uint_as_float(raw[j][e] & 0xFFFF0000u);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j * 4 + e] = __uint_as_float(raw[j][e]);
       }
     }
   }
 
-  static __device__ __forceinline__ void store(T* __restrict__ row, int64_t d, int lane, const float* v) {
-    if constexpr (VEC) {
+  static __device__ __forceinline__ void store(T* __restrict__ row, int d, int lane, const float* v) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int64_t c = col(j, lane);
+    for (int j = 0; j < N; ++j) {
+      const int c = col(j, lane);
+      if (WHOLE ? c < d : c + P <= d) {
         u32x4 raw;
         if constexpr (P == 8) {
 #pragma unroll
@@ -83,30 +90,49 @@ struct RowMap {
 #pragma unroll
           for (int e = 0; e < 4; ++e) raw[e] = __float_as_uint(v[j * 4 + e]);
         }
-        if (c < d) *reinterpret_cast<u32x4*>(row + c) = raw;
-      }
-    } else {
+        __builtin_memcpy(row + c, &raw, 16);
+      } else if (!WHOLE && c < d) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int64_t c = col(j, lane);
-        if (c < d) put(row[c], v[j]);
+        for (int e = 0; e < P - 1; ++e)
+          if (c + e < d) put(row[c + e], v[j * P + e]);
       }
     }
   }
 
-  // the gain (fp32 or bf16, any 16-byte alignment not assumed)
-  static __device__ __forceinline__ void load_gain(const void* gain, int gain_bf16, int64_t d, int lane, float* v) {
+  static __device__ __forceinline__ void store_f32(float* __restrict__ row, int d, int lane, const float* v) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int64_t c = col(j, lane);
+      const int c = col(j, lane);
+      if (WHOLE ? c < d : c + P <= d) {
+        __builtin_memcpy(row + c, v + j * P, 4 * P);
+      } else if (!WHOLE && c < d) {
 #pragma unroll
-      for (int e = 0; e < P; ++e) {
-        float g = 0.f;
-        if (c + e < d)
-          g = gain_bf16 ? to_f32(static_cast<const bf16s*>(gain)[c + e]) : static_cast<const float*>(gain)[c + e];
-        v[j * P + e] = g;
+        for (int e = 0; e < P - 1; ++e)
+          if (c + e < d) row[c + e] = v[j * P + e];
       }
     }
+  }
+
+  // the gain, fp32 or bf16
+  template <typename GT>
+  static __device__ __forceinline__ void load_gain_as(const GT* __restrict__ gain, int d, int lane, float* v) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int c = col(j, lane);
+      if (WHOLE ? c < d : c + P <= d) {
+        GT raw[P];
+        __builtin_memcpy(raw, gain + c, sizeof(raw));
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[j * P + e] = to_f32(raw[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[j * P + e] = !WHOLE && c + e < d ? to_f32(gain[c + e]) : 0.f;
+      }
+    }
+  }
+  static __device__ __forceinline__ void load_gain(const void* gain, int gain_bf16, int d, int lane, float* v) {
+    if (gain_bf16) load_gain_as(static_cast<const bf16s*>(gain), d, lane, v);
+    else load_gain_as(static_cast<const float*>(gain), d, lane, v);
   }
 };
 
@@ -143,47 +169,50 @@ constexpr int rms_threads() {
   return WPR == 16 ? 1024 : 256;
 }
 
-template <typename T, bool VEC, int E, int WPR>
+template <typename T, bool WHOLE, int E, int WPR>
 __global__ __launch_bounds__(rms_threads<WPR>()) void k_rms_norm(RmsArgs a) {
   constexpr int NW = rms_threads<WPR>() / 64, GROUPS = NW / WPR, LPR = 64 * WPR;
-  using M = RowMap<T, VEC, E, LPR>;
+  using M = RowMap<T, WHOLE, E, LPR>;
   __shared__ float red[64];
   const int wave = threadIdx.x >> 6;
   const int group = WPR == 1 ? wave : 0;
   const int lane = WPR == 1 ? (threadIdx.x & 63) : threadIdx.x;
   int phase = 0;
   float g[E];
-  M::load_gain(a.gain, a.gain_bf16, a.d, lane, g);
+  M::load_gain(a.gain, a.gain_bf16, (int)a.d, lane, g);
   const float inv_d = 1.0f / (float)a.d;
   // WPR > 1: one group, so every wave of the block takes the same rows
   for (int64_t row = (int64_t)blockIdx.x * GROUPS + group; row < a.rows; row += (int64_t)gridDim.x * GROUPS) {
+    typename M::Raw rx, rr;
+    M::fetch(static_cast<const T*>(a.x) + row * a.d, (int)a.d, lane, rx);
+    if (a.residual) M::fetch(static_cast<const T*>(a.residual) + row * a.d, (int)a.d, lane, rr);
     float v[E];
-    M::load(static_cast<const T*>(a.x) + row * a.d, a.d, lane, v);
+    M::unpack(rx, v);
     if (a.residual) {
       float r[E];
-      M::load(static_cast<const T*>(a.residual) + row * a.d, a.d, lane, r);
+      M::unpack(rr, r);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] += r[e];
     }
     float ss = 0.f, unused = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
-    if (a.sum_out) M::store(static_cast<T*>(a.sum_out) + row * a.d, a.d, lane, v);
+    if (a.sum_out) M::store(static_cast<T*>(a.sum_out) + row * a.d, (int)a.d, lane, v);
     row_sum2<WPR>(ss, unused, red, wave, phase);
     const float rstd = 1.0f / sqrtf(__builtin_fmaf(ss, inv_d, a.eps));
     // y from the sum before its rounding to the storage type
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = v[e] * rstd * g[e];
-    M::store(static_cast<T*>(a.out) + row * a.d, a.d, lane, v);
+    M::store(static_cast<T*>(a.out) + row * a.d, (int)a.d, lane, v);
   }
 }
 
 // Work items: (sample, chunk of its rows); with `own_groups` every group of
 // a block takes a sample of its own (chunks == 1).
-template <typename T, bool VEC, int E, int WPR>
+template <typename T, bool WHOLE, int E, int WPR>
 __global__ __launch_bounds__(rms_threads<WPR>()) void k_rms_norm_backward(RmsBackArgs a) {
   constexpr int NW = rms_threads<WPR>() / 64, GROUPS = NW / WPR, LPR = 64 * WPR;
-  using M = RowMap<T, VEC, E, LPR>;
+  using M = RowMap<T, WHOLE, E, LPR>;
   __shared__ float red[64];
   __shared__ float part[GROUPS > 1 ? (GROUPS - 1) * E * 64 : 1];
   const int wave = threadIdx.x >> 6;
@@ -191,7 +220,8 @@ __global__ __launch_bounds__(rms_threads<WPR>()) void k_rms_norm_backward(RmsBac
   const int lane = WPR == 1 ? (threadIdx.x & 63) : threadIdx.x;
   int phase = 0;
   float g[E];
-  M::load_gain(a.gain, a.gain_bf16, a.d, lane, g);
+  // 1024-thread blocks have 128 registers a lane: the gain is read again for every row there (from L2)
+  if constexpr (WPR < 16) M::load_gain(a.gain, a.gain_bf16, (int)a.d, lane, g);
   const float inv_d = 1.0f / (float)a.d;
   const int64_t per_block = a.own_groups ? GROUPS : 1;
   const int64_t items = a.B * a.chunks;
@@ -206,9 +236,14 @@ __global__ __launch_bounds__(rms_threads<WPR>()) void k_rms_norm_backward(RmsBac
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     for (int64_t t = t0 + (a.own_groups ? 0 : group); t < t1; t += (a.own_groups ? 1 : GROUPS)) {
       const int64_t off = (b * a.T + t) * a.d;
+      typename M::Raw rs, rh, ro;
+      M::fetch(static_cast<const T*>(a.s) + off, (int)a.d, lane, rs);
+      M::fetch(static_cast<const T*>(a.dy) + off, (int)a.d, lane, rh);
+      if (WPR < 16 && a.dsum) M::fetch(static_cast<const T*>(a.dsum) + off, (int)a.d, lane, ro);
+      if constexpr (WPR == 16) M::load_gain(a.gain, a.gain_bf16, (int)a.d, lane, g);
       float s[E], h[E];
-      M::load(static_cast<const T*>(a.s) + off, a.d, lane, s);
-      M::load(static_cast<const T*>(a.dy) + off, a.d, lane, h);
+      M::unpack(rs, s);
+      M::unpack(rh, h);
       float ss = 0.f, hs = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -221,14 +256,15 @@ __global__ __launch_bounds__(rms_threads<WPR>()) void k_rms_norm_backward(RmsBac
         const float along = hs * inv_d * rstd * rstd;  // mean(h u) * rstd, for u = s * rstd
         float o[E];
         if (a.dsum) {
-          M::load(static_cast<const T*>(a.dsum) + off, a.d, lane, o);
+          if (WPR == 16) M::fetch(static_cast<const T*>(a.dsum) + off, (int)a.d, lane, ro);
+          M::unpack(ro, o);
         } else {
 #pragma unroll
           for (int e = 0; e < E; ++e) o[e] = 0.f;
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(rstd, h[e] * g[e] - s[e] * along, o[e]);
-        M::store(static_cast<T*>(a.dx) + off, a.d, lane, o);
+        M::store(static_cast<T*>(a.dx) + off, (int)a.d, lane, o);
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(h[e], s[e] * rstd, acc[e]);
@@ -243,7 +279,7 @@ __global__ __launch_bounds__(rms_threads<WPR>()) void k_rms_norm_backward(RmsBac
         }
         __syncthreads();
         if (group == 0) {
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < GROUPS - 1; ++k)
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] += part[(k * E + e) * 64 + lane];
@@ -254,13 +290,7 @@ __global__ __launch_bounds__(rms_threads<WPR>()) void k_rms_norm_backward(RmsBac
     }
     if (writes) {
       float* dst = (a.chunks == 1 ? a.gain_rows : a.partial) + item * a.d;
-#pragma unroll
-      for (int j = 0; j < M::N; ++j)
-#pragma unroll
-        for (int e = 0; e < M::P; ++e) {
-          const int64_t c = M::col(j, lane) + e;
-          if (c < a.d) dst[c] = acc[j * M::P + e];
-        }
+      M::store_f32(dst, (int)a.d, lane, acc);
     }
   }
 }
@@ -284,7 +314,7 @@ namespace {
 constexpr int64_t kRmsBlocks = 256 * 8;  // blocks that fill the 256 CUs; more rows than that are looped over
 
 // One instantiation per (elements per lane, waves per row) the width needs.
-template <typename T, bool VEC, typename F>
+template <typename F>
 hipError_t rms_dispatch(int64_t d, F f) {
   if (d <= 512) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
   if (d <= 1024) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
@@ -298,51 +328,42 @@ hipError_t rms_dispatch(int64_t d, F f) {
 
 int rms_groups(int64_t d) { return d <= 2048 ? 4 : 1; }
 
-template <typename T, bool VEC>
+template <typename T, bool WHOLE>
 hipError_t launch_fwd(hipStream_t st, const RmsArgs& a) {
-  return rms_dispatch<T, VEC>(a.d, [&](auto e, auto w) {
+  return rms_dispatch(a.d, [&](auto e, auto w) {
     constexpr int E = decltype(e)::value, WPR = decltype(w)::value;
     const int64_t groups = rms_groups(a.d);
     const int64_t blocks = std::min<int64_t>((a.rows + groups - 1) / groups, kRmsBlocks);
-    k_rms_norm<T, VEC, E, WPR><<<dim3((unsigned)blocks), rms_threads<WPR>(), 0, st>>>(a);
+    k_rms_norm<T, WHOLE, E, WPR><<<dim3((unsigned)blocks), rms_threads<WPR>(), 0, st>>>(a);
     return hipGetLastError();
   });
 }
 
-template <typename T, bool VEC>
+template <typename T, bool WHOLE>
 hipError_t launch_bwd(hipStream_t st, const RmsBackArgs& a) {
-  return rms_dispatch<T, VEC>(a.d, [&](auto e, auto w) {
+  return rms_dispatch(a.d, [&](auto e, auto w) {
     constexpr int E = decltype(e)::value, WPR = decltype(w)::value;
     const int64_t per = a.own_groups ? rms_groups(a.d) : 1;
     const int64_t blocks = std::min<int64_t>((a.B * a.chunks + per - 1) / per, kRmsBlocks);
-    k_rms_norm_backward<T, VEC, E, WPR><<<dim3((unsigned)blocks), rms_threads<WPR>(), 0, st>>>(a);
+    k_rms_norm_backward<T, WHOLE, E, WPR><<<dim3((unsigned)blocks), rms_threads<WPR>(), 0, st>>>(a);
     return hipGetLastError();
   });
-}
-
-bool vec_ok(int dtype, int64_t d, std::initializer_list<const void*> ptrs) {
-  if (d % (dtype == 1 ? 8 : 4)) return false;
-  for (const void* p : ptrs)
-    if (reinterpret_cast<uintptr_t>(p) & 15) return false;
-  return true;
 }
 
 }  // namespace
 
-// How a sample's rows are spread over workgroups: chunks of at least 16 rows
-// (4 per wave; fewer would leave the partial sums' traffic, 4 d bytes per
-// chunk written and read, above a tenth of the rows'), as many as it takes
-// for about four workgroups per CU.
+// How a sample's rows are spread over workgroups: as many chunks as it takes
+// for about four workgroups per CU, each of at least four rows (one per wave).
 int64_t rms_chunks(int64_t B, int64_t T) {
   const int64_t want = (1024 + B - 1) / B;
-  const int64_t most = (T + 15) / 16;
+  const int64_t most = (T + 3) / 4;
   return std::max<int64_t>(1, std::min(want, most));
 }
 
 hipError_t launch_rms_norm(hipStream_t st, int dtype, const RmsArgs& a) {
-  const bool v = vec_ok(dtype, a.d, {a.x, a.residual, a.out, a.sum_out});
-  if (dtype == 1) return v ? launch_fwd<bf16s, true>(st, a) : launch_fwd<bf16s, false>(st, a);
-  return v ? launch_fwd<float, true>(st, a) : launch_fwd<float, false>(st, a);
+  const bool whole = a.d % (dtype == 1 ? 8 : 4) == 0;
+  if (dtype == 1) return whole ? launch_fwd<bf16s, true>(st, a) : launch_fwd<bf16s, false>(st, a);
+  return whole ? launch_fwd<float, true>(st, a) : launch_fwd<float, false>(st, a);
 }
 
 hipError_t launch_rms_norm_backward(hipStream_t st, int dtype, RmsBackArgs a) {
@@ -354,12 +375,12 @@ hipError_t launch_rms_norm_backward(hipStream_t st, int dtype, RmsBackArgs a) {
   a.chunk_rows = (a.T + a.chunks - 1) / a.chunks;
   // samples of few rows: a wave each, no sum across waves
   a.own_groups = a.chunks == 1 && a.d <= 2048 && (a.T < 8 || a.B >= 4096);
-  const bool v = vec_ok(dtype, a.d, {a.dy, a.s, a.dsum, a.dx});
+  const bool whole = a.d % (dtype == 1 ? 8 : 4) == 0;
   hipError_t e;
   if (dtype == 1)
-    e = v ? launch_bwd<bf16s, true>(st, a) : launch_bwd<bf16s, false>(st, a);
+    e = whole ? launch_bwd<bf16s, true>(st, a) : launch_bwd<bf16s, false>(st, a);
   else
-    e = v ? launch_bwd<float, true>(st, a) : launch_bwd<float, false>(st, a);
+    e = whole ? launch_bwd<float, true>(st, a) : launch_bwd<float, false>(st, a);
   if (e != hipSuccess || !a.gain_rows || a.chunks == 1) return e;
   const int64_t blocks = std::min<int64_t>((a.B * a.d + 255) / 256, kRmsBlocks);
   k_rms_gain_finish<<<dim3((unsigned)blocks), 256, 0, st>>>(a.partial, a.B, a.chunks, a.d, a.gain_rows);
