@@ -1682,31 +1682,42 @@ hipError_t dyn_lds(F* f, int bytes) {
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Tile of a product by the average rows per expert: 256 x 256 tiles read the
-// fewest operand bytes per product; with few rows per expert a tile of 32
-// rows wastes none on empty ones, and K is split so that about two workgroups
-// per CU share the weights' reading.
+// Tile and K splits of a product: the least of the measured times per chunk
+// of 32 K and per item, in rounds of items over the CUs, plus the traffic of the
+// splits' partial products and their joining launch. 256 x 256 tiles (bf16)
+// read the fewest operand bytes per product; 128 x 128 tiles run two to a CU;
+// tiles of 32 rows waste little on experts with few rows, and K can be split
+// for them, so that single tokens' weights are read by the whole GPU.
 struct MatmulPlan {
-  int bm, bn;
+  int bm;
   int64_t ks, kper;
 };
 MatmulPlan matmul_plan(int dtype, int64_t R, int64_t E, int64_t K, int64_t N) {
-  const bool dma = K % (dtype == 1 ? 8 : 4) == 0 && N % (dtype == 1 ? 8 : 4) == 0;
-  const int64_t per = R / E;
-  MatmulPlan m{128, 128, 1, K};
-  if (!dma) return m;
-  if (per <= 32) {
-    m.bm = 32;
-    const int64_t kc = dtype == 1 ? 64 : 32;
-    const int64_t tiles = (R / 32 + std::min(E, R)) * ((N + 127) / 128);
-    const int64_t chunks = (K + kc - 1) / kc;
-    const int64_t want = std::max<int64_t>(1, std::min(512 / tiles, chunks / 4));
-    m.kper = (chunks + want - 1) / want * kc;
-    m.ks = (K + m.kper - 1) / m.kper;
-  } else if (dtype == 1 && per >= 192 && E <= 64) {
-    m.bm = m.bn = 256;
+  const bool bf16 = dtype == 1, dma = dma_ok(dtype, {K, N});
+  MatmulPlan best{128, 1, K};
+  if (!dma) return best;
+  const int64_t kc = bf16 ? 64 : 32;  // K per chunk of the smaller tiles
+  const double k32 = std::ceil((double)K / 32);
+  double best_us = 1e30;
+  auto consider = [&](int bm, int bn, int64_t ks, int64_t kper, double chunk_us, double item_us, int per_cu) {
+    const double tiles = ((double)R / bm + 0.5 * (double)std::min(E, R)) * (double)((N + bn - 1) / bn) * (double)ks;
+    // workgroups that share a CU share its matrix cores
+    const double share = tiles <= 256 ? 1.0 / per_cu : 1.0;
+    const double us = std::ceil(tiles / (256.0 * per_cu)) * (k32 / (double)ks * chunk_us * share + item_us) +
+                      (ks > 1 ? (double)ks * R * N * 8.0 / 4.5e6 + 5.0 : 0.0);
+    if (us < best_us) {
+      best_us = us;
+      best = MatmulPlan{bm, ks, kper};
+    }
+  };
+  if (bf16 && E <= 64 && K >= 128) consider(256, 256, 1, K, 1.0, 9.0, 1);
+  consider(128, 128, 1, K, bf16 ? 0.66 : 4.8, 5.0, 2);
+  const int64_t chunks = (K + kc - 1) / kc;
+  for (int64_t want = 1; want <= 32 && want * 2 <= std::max<int64_t>(2, chunks); want *= 2) {
+    const int64_t kper = (chunks + want - 1) / want * kc, ks = (K + kper - 1) / kper;
+    consider(32, 128, ks, kper, bf16 ? 0.3 : 1.35, 5.0, 2);
   }
-  return m;
+  return best;
 }
 
 template <typename T, bool TRANS, int BM, int BN, int WGM, int WGN, int KB, int ST, bool DMA, bool SPLIT>
