@@ -58,7 +58,7 @@ __device__ __forceinline__ bool find_group(const int64_t* __restrict__ seg, int6
   out->tile = t;
   out->row0 = off + t * TS;
   out->rows = end - out->row0;
-  return out->rows > 0;
+  return t >= 0 && out->rows > 0;  // t < 0 only where the offsets do not ascend
 }
 
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
@@ -1068,21 +1068,24 @@ __device__ __forceinline__ void emit_tile(const f32x16 (&acc)[NBM][NBN], const E
         lds_wave_fence();
         const int64_t mb = m0 + 32 * i + 16 * h, nb = n0 + 32 * j;
         if (na.sc == 0.0f) {
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t) {
-            const int row = 8 * t + (lane >> 3), c4 = 4 * (lane & 7);
-            f32x4 v = __builtin_bit_cast(f32x4, *(lds_u32x4*)(uintptr_t)(scratch + 128 * row + 4 * c4));
+          f32x4 v[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = noised_mean_spec(v[k], 0.0f, 0.0f, na.inv_denom);
-            const int64_t m = mb + row, n = nb + c4;
+          for (int t = 0; t < 2; ++t)
+            v[t] = __builtin_bit_cast(
+                f32x4, *(lds_u32x4*)(uintptr_t)(scratch + 128 * (8 * t + (lane >> 3)) + 16 * (lane & 7)));
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int64_t m = mb + 8 * t + (lane >> 3), n = nb + 4 * (lane & 7);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[t][k] = noised_mean_spec(v[t][k], 0.0f, 0.0f, na.inv_denom);
             if (m >= o.d || n >= o.p) continue;
             float* dst = o.dst + m * o.p + n;
             if (o.vec) {
-              *reinterpret_cast<f32x4*>(dst) = v;
+              __builtin_nontemporal_store(v[t], reinterpret_cast<f32x4*>(dst));
             } else {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (n + k < o.p) dst[k] = v[k];
+                if (n + k < o.p) dst[k] = v[t][k];
             }
           }
         } else {
@@ -1987,6 +1990,10 @@ bool grouped_fits(int dtype, const GroupedArgs& g) {
   constexpr int64_t kMax = ((int64_t)1 << 32) / 512;
   const int64_t cols = (std::max(g.d, g.p) + 127) / 128;
   if ((g.R / 32 + g.E) * cols + 8 >= kMax) return false;
+  for (int tr = 0; tr < 2; ++tr) {
+    const MatmulPlan m = matmul_plan(dtype, g.R, g.E, tr ? g.p : g.d, tr ? g.d : g.p);
+    if ((g.R / m.bm + g.E) * cols * m.ks + 8 >= kMax) return false;
+  }
   const NormPlan n = norm_plan(dtype, g);
   if ((g.R / n.ts + g.E * g.B + 32) * n.J >= kMax || g.R / 32 + g.E * g.B + 8 >= kMax) return false;
   const SumPlan s = sum_plan(dtype, g);
