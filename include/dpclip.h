@@ -493,9 +493,12 @@ dp_status dp_distill_loss(void* stream, const void* logits, const int64_t* ids, 
  *
  *   grad[b][t][j] = dloss[b] * weight[b][t] * tau * (p_j - sum_{k: ids_k = j} q_k)
  *
- *  lse      as dp_distill_loss left it.
+ *  lse      as dp_distill_loss left it. (A token with |lse| >= 1024 has its
+ *           logits read a second time: lse has no room for the sum there. A
+ *           token whose logits all hold the type's lowest value gets p = 1/V.)
  *  dloss    [B] fp32, or NULL (1 everywhere: the summed per-sample losses).
- *  grad     [B, T, V], dtype, 16-byte aligned; may be logits.
+ *  grad     [B, T, V], dtype, 16-byte aligned; may be logits, and overlaps
+ *           nothing else.
  */
 dp_status dp_distill_loss_backward(void* stream, const void* logits, const int64_t* ids, const void* teacher,
                                    dp_dtype dtype, dp_dtype teacher_dtype, int64_t B, int64_t T, int64_t V,
@@ -549,7 +552,9 @@ dp_status dp_grouped_norm(void* stream, const void* A, const void* G, dp_dtype d
  * element (e*d + m, n) of dp_clipped_sum_noise's z_w. ceil(E*d/4)*p < 2^32.
  *
  *  A, G, segments, R, E, B, d, p  as in dp_grouped_norm.
- *  c, C, sigma, denom, seed, layer_id, step  as in dp_clipped_sum_noise.
+ *  c, C, sigma, denom, seed, layer_id, step  as in dp_clipped_sum_noise. The
+ *           rows of a sample with factor 0 have to be finite: whether 0 * inf
+ *           shows in out depends on the sizes.
  *  out      [E, d, p] fp32 (per expert the transpose of W_e's gradient).
  */
 dp_status dp_grouped_clipped_sum_noise(void* stream, const void* A, const void* G, dp_dtype dtype,

@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kDt = 256;  // threads per block
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFarLse = 1024.0f;  // from here on the backward forms a row's statistics again
 
 // 2^x by the hardware's instruction: within one step, results below 2^-126
 // flushed to 0 (they are terms of sums of order 1, or probabilities).
@@ -173,12 +174,44 @@ __device__ float token_loss(const DistillArgs& a, int64_t row, Run r, float* red
 
 __device__ __forceinline__ float lse_of(Run r, float tau) { return r.m / tau + logf(r.s); }
 
+// A thread's part of a row's words [v0, v1).
+template <typename T>
+__device__ __forceinline__ Run run_span(const T* z, int64_t v0, int64_t v1, float k) {
+  constexpr int P = elem_traits<T>::per16;
+  Run r = run_empty();
+  if (v0 >= v1) return r;
+  const Span<T> sn(z, v0, v1);
+  const int64_t j = v0 + threadIdx.x;
+  if (j < sn.head) run_one(r, to_f32(z[j]), k);
+  const u32x4* vz = reinterpret_cast<const u32x4*>(z + sn.head);
+  constexpr int U = 4;  // vectors in flight per thread
+  int64_t i = threadIdx.x;
+  for (; i + (U - 1) * kDt < sn.vecs; i += U * kDt) {
+    u32x4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = vz[i + u * kDt];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v[P];
+      unpack16<P>(raw[u], v);
+      run_many<P>(r, v, k);
+    }
+  }
+  for (; i < sn.vecs; i += kDt) {
+    float v[P];
+    unpack16<P>(vz[i], v);
+    run_many<P>(r, v, k);
+  }
+  const int64_t jt = sn.tail0 + threadIdx.x;
+  if (jt < v1) run_one(r, to_f32(z[jt]), k);
+  return r;
+}
+
 }  // namespace
 
 // One block per (token, split).
 template <typename T>
 __global__ __launch_bounds__(kDt) void k_distill_stats(DistillArgs a) {
-  constexpr int P = elem_traits<T>::per16;
   __shared__ float red[2 * kDt / 64];
   const float k = kLog2e / a.tau;
   const int64_t items = a.B * a.T * a.splits;
@@ -187,33 +220,7 @@ __global__ __launch_bounds__(kDt) void k_distill_stats(DistillArgs a) {
     const int64_t row = item / a.splits, sp = item - row * a.splits;
     const int64_t v0 = sp * len, v1 = v0 + len < a.V ? v0 + len : a.V;
     const T* z = static_cast<const T*>(a.logits) + row * a.V;
-    Run r = run_empty();
-    if (v0 < v1) {
-      const Span<T> sn(z, v0, v1);
-      const int64_t j = v0 + threadIdx.x;
-      if (j < sn.head) run_one(r, to_f32(z[j]), k);
-      const u32x4* vz = reinterpret_cast<const u32x4*>(z + sn.head);
-      constexpr int U = 4;  // vectors in flight per thread
-      int64_t i = threadIdx.x;
-      for (; i + (U - 1) * kDt < sn.vecs; i += U * kDt) {
-        u32x4 raw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = vz[i + u * kDt];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float v[P];
-          unpack16<P>(raw[u], v);
-          run_many<P>(r, v, k);
-        }
-      }
-      for (; i < sn.vecs; i += kDt) {
-        float v[P];
-        unpack16<P>(vz[i], v);
-        run_many<P>(r, v, k);
-      }
-      const int64_t jt = sn.tail0 + threadIdx.x;
-      if (jt < v1) run_one(r, to_f32(z[jt]), k);
-    }
+    Run r = run_span(z, v0, v1, k);
     r = block_join(r, k, red);
     if (a.splits > 1) {
       if (threadIdx.x == 0) a.part[item] = make_float2(r.m, r.s);
@@ -266,7 +273,7 @@ __global__ __launch_bounds__(kDt) void k_distill_sum(const float* __restrict__ r
 template <typename T>
 __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
   constexpr int P = elem_traits<T>::per16;
-  __shared__ float red[kDt / 64];
+  __shared__ float red[2 * kDt / 64];
   __shared__ __attribute__((aligned(16))) int32_t ids[kDistillMaxTop + 4];
   __shared__ __attribute__((aligned(16))) float qs[kDistillMaxTop + 4];
   const float inv_tau = 1.0f / a.tau;
@@ -306,7 +313,15 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
     }
     total = block_add(total, red);  // its barriers also publish ids and qs
     const float inv_total = any ? 1.0f / total : 0.0f;
-    const float shift = any ? a.lse[row] : 0.0f;
+    // log p_j = (z_j - m) / tau - shift. m = 0 and shift = lse, whose rounding costs p 2^-24 |lse|. Where that
+    // would show (rows of a mask's value, down to the type's lowest, have no room for log V in lse) m and the
+    // logarithm of the sum are formed again from the row.
+    float shift = any ? a.lse[row] : 0.0f, m = 0.0f;
+    if (!(fabsf(shift) < kFarLse)) {
+      const Run r = block_join(run_span(z, 0, a.V, kLog2e * inv_tau), kLog2e * inv_tau, red);
+      m = r.m;
+      shift = logf(r.s);
+    }
     // ---- the used words of this split: their logits, before anything is written
     constexpr int KPT = kDistillMaxTop / kDt;  // places per thread
     float pv[KPT];
@@ -319,7 +334,7 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
     if (K > 0) __syncthreads();
     // ---- p_j f over the split
     auto p_of = [&](float zz) {
-      return any ? f * exp2_hw(__builtin_fmaf(zz, inv_tau, -shift) * kLog2e) : 0.0f;
+      return any ? f * exp2_hw(__builtin_fmaf(zz - m, inv_tau, -shift) * kLog2e) : 0.0f;
     };
     const Span<T> sn(z, v0, v1);
     auto put1 = [&](int64_t j, float v) {
@@ -429,7 +444,8 @@ hipError_t launch_distill_loss(hipStream_t st, int dtype, DistillArgs a) {
 
 hipError_t launch_distill_backward(hipStream_t st, int dtype, DistillArgs a) {
   const int64_t rows = a.B * a.T;
-  a.splits = distill_splits(rows, a.V);
+  // in place a row is one block's: it may be read a second time, before anything of it is overwritten
+  a.splits = a.grad == a.logits ? 1 : distill_splits(rows, a.V);
   const unsigned blocks = (unsigned)std::min<int64_t>(rows * a.splits, 1 << 20);
   if (dtype == 1)
     k_distill_backward<bf16s><<<blocks, kDt, 0, st>>>(a);
