@@ -727,14 +727,14 @@ constexpr int norm_tile() {
 // bf16, where memory bounds; 64 for fp32, where the products do).
 // Workgroup (tile t, j) takes the pairs (t, u), u - t = j, j + J, ...: a long
 // segment's pairs spread over J workgroups (one after another they were the
-// launch's critical path: 276 -> 172 us at 256 segments of 128 rows on
-// average, d + p = 6400). A wave whose 64 x 64 part lies below the diagonal
+// launch's critical path: 276 -> 181 us at 256 segments of 128 rows on
+// average, d + p = 6400; 151 with the deeper stages of the diagonal). A wave whose 64 x 64 part lies below the diagonal
 // or past the segment only takes part in the loads.
 template <typename T, bool DMA>
-__global__ __launch_bounds__(256) void k_grouped_norm(GNormArgs a) {
+__global__ __launch_bounds__(256, DMA ? 2 : 1) void k_grouped_norm(GNormArgs a) {
   constexpr int TS = norm_tile<T>(), WG = 2, NW = 4, WT = TS / 2, NB = WT / 32;
   using O = Opnd<T, true, TS>;
-  constexpr int KC = O::KC, STAGE = 2 * O::BYTES, ST = 2;
+  constexpr int KC = O::KC;
   extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
   __shared__ float red[NW];
 
@@ -761,47 +761,59 @@ __global__ __launch_bounds__(256) void k_grouped_norm(GNormArgs a) {
     f32x16 ga[NB][NB], gg[NB][NB];
     zero_acc(ga);
     zero_acc(gg);
-    auto gram = [&](const T* M, int64_t K, f32x16 (&acc)[NB][NB]) {
+    // Pairs of a tile with itself load one operand, and use the other's LDS for two more stages: three chunks in
+    // flight instead of one.
+    auto gram = [&](const T* M, int64_t K, f32x16 (&acc)[NB][NB], auto dg) {
+      constexpr bool DIAG = decltype(dg)::value;
+      constexpr int ST = DIAG ? 4 : 2, STAGE = (DIAG ? 1 : 2) * O::BYTES, UOFF = DIAG ? 0 : O::BYTES;
+      using F = Filler<O, T, NW>;
       const T* Mt = M + row0 * K;
       const T* Mu = M + (row0 + u * TS) * K;
       const int64_t kb = K * (int64_t)sizeof(T);
-      Filler<O, T, NW> f;
+      F f;
       f.init(kb, wave, lane);
       const int nq = (int)((K + KC - 1) / KC);
       auto wt = [&](int q) { return Win<T>{Mt + (int64_t)q * KC, kb, trows, K - (int64_t)q * KC}; };
       auto wu = [&](int q) { return Win<T>{Mu + (int64_t)q * KC, kb, urows, K - (int64_t)q * KC}; };
       if constexpr (DMA) {
+        constexpr int LPC = F::LOADS * (DIAG ? 1 : 2);
+        auto stage_of = [&](int q) { return l0 + (uint32_t)(q % ST) * STAGE; };
         auto issue = [&](int q) {
-          const uint32_t sb = l0 + (uint32_t)(q % ST) * STAGE;
-          f.dma(wt(q), sb, wave);
-          if (!diag) f.dma(wu(q), sb + O::BYTES, wave);
+          f.dma(wt(q), stage_of(q), wave);
+          if constexpr (!DIAG) f.dma(wu(q), stage_of(q) + UOFF, wave);
         };
         lds_barrier();  // every wave is done with the stages of the previous Gram
-        issue(0);
+#pragma unroll
+        for (int q = 0; q < ST - 1; ++q)
+          if (q < nq) issue(q);
         for (int q = 0; q < nq; ++q) {
-          wait_vmcnt<0>();
+          wait_chunks<LPC, ST - 2>(nq - 1 - q < ST - 2 ? nq - 1 - q : ST - 2);
           lds_barrier();
-          if (q + 1 < nq) issue(q + 1);
-          const uint32_t sb = l0 + (uint32_t)(q % ST) * STAGE;
-          if (active) chunk_mma<T, NB, NB>(sb, diag ? sb : sb + O::BYTES, rm, rn, 4, acc);
+          if (q + ST - 1 < nq) issue(q + ST - 1);
+          if (active) chunk_mma<T, NB, NB>(stage_of(q), stage_of(q) + UOFF, rm, rn, 4, acc);
         }
       } else {
-        u32x4 vt[Filler<O, T, NW>::LOADS], vu[Filler<O, T, NW>::LOADS];
+        u32x4 vt[F::LOADS], vu[F::LOADS];
         f.load(wt(0), vt, wave, lane);
-        if (!diag) f.load(wu(0), vu, wave, lane);
+        if constexpr (!DIAG) f.load(wu(0), vu, wave, lane);
         for (int q = 0; q < nq; ++q) {
           __syncthreads();
           f.store(vt, lds, wave, lane);
-          if (!diag) f.store(vu, lds + O::BYTES, wave, lane);
+          if constexpr (!DIAG) f.store(vu, lds + UOFF, wave, lane);
           __syncthreads();
           f.load(wt(q + 1), vt, wave, lane);  // past the last chunk: an empty window
-          if (!diag) f.load(wu(q + 1), vu, wave, lane);
-          if (active) chunk_mma<T, NB, NB>(l0, diag ? l0 : l0 + O::BYTES, rm, rn, 4, acc);
+          if constexpr (!DIAG) f.load(wu(q + 1), vu, wave, lane);
+          if (active) chunk_mma<T, NB, NB>(l0, l0 + UOFF, rm, rn, 4, acc);
         }
       }
     };
-    gram(static_cast<const T*>(a.A), a.d, ga);
-    gram(static_cast<const T*>(a.G), a.p, gg);
+    if (diag) {
+      gram(static_cast<const T*>(a.A), a.d, ga, std::true_type{});
+      gram(static_cast<const T*>(a.G), a.p, gg, std::true_type{});
+    } else {
+      gram(static_cast<const T*>(a.A), a.d, ga, std::false_type{});
+      gram(static_cast<const T*>(a.G), a.p, gg, std::false_type{});
+    }
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
@@ -912,23 +924,33 @@ __global__ __launch_bounds__(256) void k_grouped_row_segments(const int64_t* __r
   row_seg[row] = (int32_t)g;
 }
 
-// sqnorm[b] (+)= the values of the sample's tiles (or, packed, rows), in order
-// within a segment, one lane per segment, the segments joined in a fixed
-// order. One wave per sample.
+// sqnorm[b] (+)= the values of the sample's tiles (or, packed, rows). One
+// workgroup per sample: 16 groups of 16 lanes take the experts in turn, a
+// lane every sixteenth value of a segment; the lanes' sums are joined in a
+// fixed order. (One lane per segment, its values one after another: 14 us at
+// 5 experts of 12 rows, 45 values each.)
 template <bool PACKED, int TS>
-__global__ __launch_bounds__(64) void k_grouped_norm_finish(GNormArgs a, float* __restrict__ sqnorm, int accumulate) {
+__global__ __launch_bounds__(256) void k_grouped_norm_finish(GNormArgs a, float* __restrict__ sqnorm, int accumulate) {
+  __shared__ float red[4];
+  const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
   for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
     float s = 0.f;
-    for (int64_t e = threadIdx.x; e < a.E; e += 64) {
+    for (int64_t e = sub; e < a.E; e += 16) {
       const int64_t g = e * a.B + b;
       const int64_t off = clamp_row(a.seg[g], a.R), end = clamp_row(a.seg[g + 1], a.R);
       const int64_t first = (PACKED ? off : off / TS + g) * a.J;
       const int64_t n = end <= off ? 0 : (PACKED ? end - off : (end - off + TS - 1) / TS) * a.J;
-#pragma unroll 8
-      for (int64_t t = 0; t < n; ++t) s += a.partial[first + t];
+#pragma unroll 4
+      for (int64_t t = l; t < n; t += 16) s += a.partial[first + t];
     }
     s = wave_sum(s);
-    if (threadIdx.x == 0) sqnorm[b] = accumulate ? sqnorm[b] + s : s;
+    __syncthreads();  // the previous sample's sums are read
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s = (red[0] + red[1]) + (red[2] + red[3]);
+      sqnorm[b] = accumulate ? sqnorm[b] + s : s;
+    }
   }
 }
 
@@ -1667,6 +1689,28 @@ __global__ __launch_bounds__(256) void k_grouped_sum(GSumArgs a) {
   emit_tile<NBM, NBN>(acc, emit_at(a, e, sp), a.na, l0 + wave * 2048, m0 + wm * WM, n0 + wn * WN, lane);
 }
 
+// The splits' sums added in order, noise and mean applied, for widths without
+// 16-byte vectors: a thread takes one column of a row quad, lanes side by side
+// (the layers' reduce gives a thread 4 x 4 elements, 16 loads of 4 bytes a
+// split: 20 us against 6 at six splits of 1665 x 517).
+__global__ __launch_bounds__(256) void k_grouped_reduce(GSumArgs a, NoiseArgs na) {
+  const int64_t rows = a.E * a.d, n = (rows + 3) / 4 * a.p, stride = rows * a.p;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t q = i / a.p, at = 4 * q * a.p + (i - q * a.p);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int64_t k = 0; k < a.ks; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (4 * q + r < rows) s[r] += a.part[k * stride + at + r * a.p];
+    f32x4 z = {0.f, 0.f, 0.f, 0.f};
+    if (na.sc != 0.0f) z = normals4((uint32_t)i, 2u * na.layer, na.step, 0u, na.k0, na.k1);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (4 * q + r < rows) a.out[at + r * a.p] = noised_mean_spec(s[r], na.sc, z[r], na.inv_denom);
+  }
+}
+
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -1831,7 +1875,7 @@ hipError_t run_norm(hipStream_t st, int dtype, GNormArgs a, const NormPlan& pl, 
     k_grouped_norm_packed<T><<<dim3((unsigned)std::min<int64_t>(items, 1 << 20)), 256, 0, st>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_grouped_norm_finish<true, 32><<<fin, 64, 0, st>>>(a, sqnorm, accumulate);
+    k_grouped_norm_finish<true, 32><<<fin, 256, 0, st>>>(a, sqnorm, accumulate);
     return hipGetLastError();
   }
   constexpr int TS = norm_tile<T>();
@@ -1853,7 +1897,7 @@ hipError_t run_norm(hipStream_t st, int dtype, GNormArgs a, const NormPlan& pl, 
   }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_grouped_norm_finish<false, TS><<<fin, 64, 0, st>>>(a, sqnorm, accumulate);
+  k_grouped_norm_finish<false, TS><<<fin, 256, 0, st>>>(a, sqnorm, accumulate);
   return hipGetLastError();
 }
 
@@ -1983,6 +2027,11 @@ hipError_t launch_grouped_sum(hipStream_t st, int dtype, const GroupedArgs& g, c
                 : run_sum(&k_grouped_sum<float, false, false>, st, a, grid, 256, st_n * (32768 + 1024));
   }
   if (e != hipSuccess || fused) return e;
+  if (g.p % 4) {
+    const int64_t n = (g.E * g.d + 3) / 4 * g.p;
+    k_grouped_reduce<<<dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 16)), 256, 0, st>>>(a, na);
+    return hipGetLastError();
+  }
   return launch_split_reduce(st, a.ks, a.part, g.E * g.d, g.p, na, out);
 }
 
