@@ -55,14 +55,7 @@ dp_status check_distill(int64_t B, int64_t T, int64_t V, int64_t K, float tau) {
   return DP_OK;
 }
 
-struct DistillWs {
-  size_t row_loss, part;  // bytes of the two regions, in this order
-};
-DistillWs distill_ws(int64_t B, int64_t T, int64_t V) {
-  const int64_t rows = B * T, splits = dpk::distill_splits(rows, V);
-  return {T > 1 ? round256((size_t)rows * sizeof(float)) : 0,
-          splits > 1 ? round256((size_t)rows * (size_t)splits * sizeof(float2)) : 0};
-}
+size_t distill_ws_bytes(int64_t B, int64_t T) { return T > 1 ? round256((size_t)B * (size_t)T * sizeof(float)) : 0; }
 
 dp_status check_grouped(dp_dtype dtype, const dpk::GroupedArgs& g) {
   if (g.R < 1 || g.E < 1 || g.B < 1 || g.d < 1 || g.p < 1) return DP_ERR_SHAPE;
@@ -134,8 +127,7 @@ dp_status dp_rms_norm_backward(void* stream, const void* dy, const void* s, cons
 
 size_t dp_distill_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t V, int64_t K) {
   if (!dtype_ok(dtype) || check_distill(B, T, V, K, 1.0f) != DP_OK) return 0;
-  const DistillWs w = distill_ws(B, T, V);
-  return w.row_loss + w.part;
+  return distill_ws_bytes(B, T);
 }
 
 dp_status dp_distill_loss(void* stream, const void* logits, const int64_t* ids, const void* teacher, dp_dtype dtype,
@@ -148,8 +140,7 @@ dp_status dp_distill_loss(void* stream, const void* logits, const int64_t* ids, 
   if (!aligned(logits, 16) || !aligned(ids, 8) || !aligned(teacher, elem_bytes(teacher_dtype)) || !aligned(weight, 4) ||
       !aligned(loss, 4) || !aligned(lse, 4))
     return DP_ERR_ALIGN;
-  const DistillWs w = distill_ws(B, T, V);
-  s = check_workspace(workspace, ws_bytes, w.row_loss + w.part);
+  s = check_workspace(workspace, ws_bytes, distill_ws_bytes(B, T));
   if (s != DP_OK) return s;
   s = device_ready();
   if (s != DP_OK) return s;
@@ -167,7 +158,6 @@ dp_status dp_distill_loss(void* stream, const void* logits, const int64_t* ids, 
   a.loss = loss;
   a.lse = lse;
   a.row_loss = static_cast<float*>(workspace);
-  a.part = reinterpret_cast<float2*>(static_cast<char*>(workspace) + w.row_loss);
   return hip_status(dpk::launch_distill_loss(static_cast<hipStream_t>(stream), dtype, a));
 }
 

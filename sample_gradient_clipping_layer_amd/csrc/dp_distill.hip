@@ -14,9 +14,10 @@
 // maximum and sum per thread, joined across the block at the end. The
 // logarithm's argument is kept as (z - max) in raw logits, so that rows holding
 // the type's lowest value neither overflow nor give NaN. Where tokens are few,
-// a row is split over several workgroups whose (max, sum) pairs go through
-// the workspace to a second kernel. Sums over a sample's tokens run in a fixed
-// order in a kernel of their own; nothing is atomic.
+// each takes a workgroup of 1024 threads (a row of 50257 bf16 is then six
+// loads of a thread, all in flight together, and the loss is one launch).
+// Sums over a sample's tokens run in a fixed order in a kernel of their own;
+// nothing is atomic.
 #include "dp_common.hpp"
 #include "dp_lm.hpp"
 
@@ -72,6 +73,7 @@ __device__ __forceinline__ Run wave_join(Run r, float k) {
 }
 
 // Joined over the block; the same value in every thread. Contains barriers.
+template <int NT>
 __device__ __forceinline__ Run block_join(Run r, float k, float* red) {
   r = wave_join(r, k);
   __syncthreads();
@@ -80,11 +82,14 @@ __device__ __forceinline__ Run block_join(Run r, float k, float* red) {
     red[2 * (threadIdx.x >> 6) + 1] = r.s;
   }
   __syncthreads();
-  r = Run{red[0], red[1]};
+  float m = red[0], s = 0.f;
 #pragma unroll
-  for (int w = 1; w < kDt / 64; ++w) r = run_join(r, Run{red[2 * w], red[2 * w + 1]}, k);
-  return r;
+  for (int w = 1; w < NT / 64; ++w) m = fmaxf(m, red[2 * w]);
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) s += red[2 * w + 1] * exp2_hw((red[2 * w] - m) * k);
+  return Run{m, s};
 }
+template <int NT>
 __device__ __forceinline__ float block_max(float v, float* red) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
@@ -93,9 +98,10 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   __syncthreads();
   v = red[0];
 #pragma unroll
-  for (int w = 1; w < kDt / 64; ++w) v = fmaxf(v, red[w]);
+  for (int w = 1; w < NT / 64; ++w) v = fmaxf(v, red[w]);
   return v;
 }
+template <int NT>
 __device__ __forceinline__ float block_add(float v, float* red) {
   v = wave_sum(v);
   __syncthreads();
@@ -103,7 +109,7 @@ __device__ __forceinline__ float block_add(float v, float* red) {
   __syncthreads();
   v = red[0];
 #pragma unroll
-  for (int w = 1; w < kDt / 64; ++w) v += red[w];
+  for (int w = 1; w < NT / 64; ++w) v += red[w];
   return v;
 }
 
@@ -142,31 +148,52 @@ __device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t i) {
   return a.teacher_bf16 ? to_f32(static_cast<const bf16s*>(a.teacher)[i]) : static_cast<const float*>(a.teacher)[i];
 }
 
+// A token's weight and the place of its first K that this thread holds, read
+// ahead of the student's statistics.
+struct FirstPlace {
+  float weight, teacher;
+  int64_t id;
+};
+__device__ __forceinline__ FirstPlace first_place(const DistillArgs& a, int64_t row) {
+  FirstPlace f{1.0f, 0.0f, -1};
+  if (a.weight) f.weight = a.weight[row];
+  if (threadIdx.x < a.K) {
+    f.id = a.ids[row * a.K + threadIdx.x];
+    f.teacher = teacher_at(a, row * a.K + threadIdx.x);
+  }
+  return f;
+}
+
 // The loss of one token from its student statistics, by the whole block.
-template <typename T>
-__device__ float token_loss(const DistillArgs& a, int64_t row, Run r, float* red) {
-  const float w = a.weight ? a.weight[row] : 1.0f;
+template <typename T, int NT>
+__device__ float token_loss(const DistillArgs& a, int64_t row, const FirstPlace& fp, Run r, float* red) {
+  const float w = fp.weight;
   if (w == 0.0f) return 0.0f;  // uniform over the block
   const T* z = static_cast<const T*>(a.logits) + row * a.V;
   const int64_t* id = a.ids + row * a.K;
   const float inv_tau = 1.0f / a.tau;
-  float tm = -INFINITY;
-  for (int64_t k = threadIdx.x; k < a.K; k += kDt)
+  float tm = -INFINITY, z0 = 0.0f;
+  if (fp.id >= 0 && fp.id < a.V) {
+    tm = fmaxf(tm, fp.teacher);
+    z0 = to_f32(z[fp.id]);
+  }
+  for (int64_t k = threadIdx.x + NT; k < a.K; k += NT)
     if (id[k] >= 0 && id[k] < a.V) tm = fmaxf(tm, teacher_at(a, row * a.K + k));
-  tm = block_max(tm, red);
+  tm = block_max<NT>(tm, red);
   if (tm == -INFINITY) return 0.0f;  // no used place
   float total = 0.f, s = 0.f;
-  for (int64_t k = threadIdx.x; k < a.K; k += kDt) {
-    const int64_t j = id[k];
+  for (int64_t k = threadIdx.x; k < a.K; k += NT) {
+    const bool ahead = k == threadIdx.x;
+    const int64_t j = ahead ? fp.id : id[k];
     if (j < 0 || j >= a.V) continue;
-    const float dt = (teacher_at(a, row * a.K + k) - tm) * inv_tau;
+    const float dt = ((ahead ? fp.teacher : teacher_at(a, row * a.K + k)) - tm) * inv_tau;
     const float e = exp2_hw(dt * kLog2e);
     if (e == 0.0f) continue;  // no mass there: its logits (infinite ones among them) do not count
     total += e;
-    s += e * (dt - (to_f32(z[j]) - r.m) * inv_tau);
+    s += e * (dt - ((ahead ? z0 : to_f32(z[j])) - r.m) * inv_tau);
   }
-  total = block_add(total, red);
-  s = block_add(s, red);
+  total = block_add<NT>(total, red);
+  s = block_add<NT>(s, red);
   // sum_k q_k (log q_k - log p_k), with log q = dt - log total, log p = (z - m)/tau - log s_student
   const float kl = s / total - logf(total) + logf(r.s);
   return a.tau * a.tau * w * kl;
@@ -174,22 +201,21 @@ __device__ float token_loss(const DistillArgs& a, int64_t row, Run r, float* red
 
 __device__ __forceinline__ float lse_of(Run r, float tau) { return r.m / tau + logf(r.s); }
 
-// A thread's part of a row's words [v0, v1).
-template <typename T>
+// A thread's part of a row's words [v0, v1), the block's NT threads side by side.
+template <typename T, int NT>
 __device__ __forceinline__ Run run_span(const T* z, int64_t v0, int64_t v1, float k) {
   constexpr int P = elem_traits<T>::per16;
   Run r = run_empty();
-  if (v0 >= v1) return r;
   const Span<T> sn(z, v0, v1);
   const int64_t j = v0 + threadIdx.x;
   if (j < sn.head) run_one(r, to_f32(z[j]), k);
   const u32x4* vz = reinterpret_cast<const u32x4*>(z + sn.head);
   constexpr int U = 4;  // vectors in flight per thread
   int64_t i = threadIdx.x;
-  for (; i + (U - 1) * kDt < sn.vecs; i += U * kDt) {
+  for (; i + (U - 1) * NT < sn.vecs; i += U * NT) {
     u32x4 raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = vz[i + u * kDt];
+    for (int u = 0; u < U; ++u) raw[u] = vz[i + u * NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float v[P];
@@ -197,10 +223,17 @@ __device__ __forceinline__ Run run_span(const T* z, int64_t v0, int64_t v1, floa
       run_many<P>(r, v, k);
     }
   }
-  for (; i < sn.vecs; i += kDt) {
-    float v[P];
-    unpack16<P>(vz[i], v);
-    run_many<P>(r, v, k);
+  if (i < sn.vecs) {  // up to U - 1 more, in flight together (the last of them read again where there are fewer)
+    u32x4 raw[U - 1];
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u) raw[u] = vz[i + u * NT < sn.vecs ? i + u * NT : i];
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u) {
+      if (i + u * NT >= sn.vecs) break;
+      float v[P];
+      unpack16<P>(raw[u], v);
+      run_many<P>(r, v, k);
+    }
   }
   const int64_t jt = sn.tail0 + threadIdx.x;
   if (jt < v1) run_one(r, to_f32(z[jt]), k);
@@ -209,44 +242,15 @@ __device__ __forceinline__ Run run_span(const T* z, int64_t v0, int64_t v1, floa
 
 }  // namespace
 
-// One block per (token, split).
-template <typename T>
-__global__ __launch_bounds__(kDt) void k_distill_stats(DistillArgs a) {
-  __shared__ float red[2 * kDt / 64];
-  const float k = kLog2e / a.tau;
-  const int64_t items = a.B * a.T * a.splits;
-  const int64_t len = (a.V + a.splits - 1) / a.splits;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t row = item / a.splits, sp = item - row * a.splits;
-    const int64_t v0 = sp * len, v1 = v0 + len < a.V ? v0 + len : a.V;
-    const T* z = static_cast<const T*>(a.logits) + row * a.V;
-    Run r = run_span(z, v0, v1, k);
-    r = block_join(r, k, red);
-    if (a.splits > 1) {
-      if (threadIdx.x == 0) a.part[item] = make_float2(r.m, r.s);
-    } else {
-      const float loss = token_loss<T>(a, row, r, red);
-      if (threadIdx.x == 0) {
-        a.lse[row] = lse_of(r, a.tau);
-        (a.T == 1 ? a.loss : a.row_loss)[row] = loss;
-      }
-    }
-  }
-}
-
-// The splits of a token joined in order, then its loss.
-template <typename T>
-__global__ __launch_bounds__(kDt) void k_distill_finish(DistillArgs a) {
-  __shared__ float red[2 * kDt / 64];
+// One block per token: its statistics, then its loss.
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void k_distill_loss(DistillArgs a) {
+  __shared__ float red[2 * NT / 64];
   const float k = kLog2e / a.tau;
   for (int64_t row = blockIdx.x; row < a.B * a.T; row += gridDim.x) {
-    Run r = run_empty();
-    for (int64_t i = threadIdx.x; i < a.splits; i += kDt) {
-      const float2 o = a.part[row * a.splits + i];
-      r = run_join(r, Run{o.x, o.y}, k);
-    }
-    r = block_join(r, k, red);
-    const float loss = token_loss<T>(a, row, r, red);
+    const FirstPlace fp = first_place(a, row);
+    const Run r = block_join<NT>(run_span<T, NT>(static_cast<const T*>(a.logits) + row * a.V, 0, a.V, k), k, red);
+    const float loss = token_loss<T, NT>(a, row, fp, r, red);
     if (threadIdx.x == 0) {
       a.lse[row] = lse_of(r, a.tau);
       (a.T == 1 ? a.loss : a.row_loss)[row] = loss;
@@ -260,7 +264,7 @@ __global__ __launch_bounds__(kDt) void k_distill_sum(const float* __restrict__ r
   for (int64_t b = blockIdx.x; b < B; b += gridDim.x) {
     float s = 0.f;
     for (int64_t t = threadIdx.x; t < Tn; t += kDt) s += row_loss[b * Tn + t];
-    s = block_add(s, red);
+    s = block_add<kDt>(s, red);
     if (threadIdx.x == 0) loss[b] = s;
   }
 }
@@ -295,7 +299,7 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
     if (f != 0.0f)
       for (int k = threadIdx.x; k < K; k += kDt)
         if (id[k] >= 0 && id[k] < a.V) tm = fmaxf(tm, teacher_at(a, row * a.K + k));
-    tm = block_max(tm, red);
+    tm = block_max<kDt>(tm, red);
     const bool any = f != 0.0f && tm != -INFINITY;
     float total = 0.f;
     if (any) {
@@ -311,14 +315,14 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
         total += e;
       }
     }
-    total = block_add(total, red);  // its barriers also publish ids and qs
+    total = block_add<kDt>(total, red);  // its barriers also publish ids and qs
     const float inv_total = any ? 1.0f / total : 0.0f;
     // log p_j = (z_j - m) / tau - shift. m = 0 and shift = lse, whose rounding costs p 2^-24 |lse|. Where that
     // would show (rows of a mask's value, down to the type's lowest, have no room for log V in lse) m and the
     // logarithm of the sum are formed again from the row.
     float shift = any ? a.lse[row] : 0.0f, m = 0.0f;
     if (!(fabsf(shift) < kFarLse)) {
-      const Run r = block_join(run_span(z, 0, a.V, kLog2e * inv_tau), kLog2e * inv_tau, red);
+      const Run r = block_join<kDt>(run_span<T, kDt>(z, 0, a.V, kLog2e * inv_tau), kLog2e * inv_tau, red);
       m = r.m;
       shift = logf(r.s);
     }
@@ -409,10 +413,10 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
   }
 }
 
-// Splits of a token's words: none from 512 tokens on (two blocks per CU stream
+// Splits of a token's words in the backward pass: none from 512 tokens on (two blocks per CU stream
 // HBM at its rate); below, as many as give about 1024 blocks, each of at
 // least 2048 words (8 per thread).
-int64_t distill_splits(int64_t rows, int64_t V) {
+static int64_t distill_splits(int64_t rows, int64_t V) {
   if (rows >= 512) return 1;
   const int64_t want = (1024 + rows - 1) / rows, most = (V + 2047) / 2048;
   return std::max<int64_t>(1, std::min(want, most));
@@ -420,24 +424,20 @@ int64_t distill_splits(int64_t rows, int64_t V) {
 
 hipError_t launch_distill_loss(hipStream_t st, int dtype, DistillArgs a) {
   const int64_t rows = a.B * a.T;
-  a.splits = distill_splits(rows, a.V);
-  const unsigned blocks = (unsigned)std::min<int64_t>(rows * a.splits, 1 << 20);
-  if (dtype == 1)
-    k_distill_stats<bf16s><<<blocks, kDt, 0, st>>>(a);
-  else
-    k_distill_stats<float><<<blocks, kDt, 0, st>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (a.splits > 1) {
-    const unsigned fb = (unsigned)rows;  // < 512
-    if (dtype == 1)
-      k_distill_finish<bf16s><<<fb, kDt, 0, st>>>(a);
-    else
-      k_distill_finish<float><<<fb, kDt, 0, st>>>(a);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (a.T == 1) return hipSuccess;
+  const unsigned blocks = (unsigned)std::min<int64_t>(rows, 1 << 20);
+  // Up to a token per CU 1024 threads for it, up to two 512 (a CU holds one workgroup of 1024: 300 tokens of
+  // 50257 bf16 take 15.3 us with 1024 threads, 10.2 with 512). Rows split over several workgroups with a second
+  // launch that joins them took longer: 4 tokens 12.0 us a call against 9.0, 300 tokens 14.1.
+  auto run = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    if (dtype == 1) k_distill_loss<bf16s, NT><<<blocks, NT, 0, st>>>(a);
+    else k_distill_loss<float, NT><<<blocks, NT, 0, st>>>(a);
+  };
+  if (rows <= 256) run(std::integral_constant<int, 1024>{});
+  else if (rows <= 512) run(std::integral_constant<int, 512>{});
+  else run(std::integral_constant<int, kDt>{});
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.T == 1) return e;
   k_distill_sum<<<(unsigned)std::min<int64_t>(a.B, 1 << 20), kDt, 0, st>>>(a.row_loss, a.B, a.T, a.loss);
   return hipGetLastError();
 }

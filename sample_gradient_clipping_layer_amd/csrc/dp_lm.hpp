@@ -61,12 +61,10 @@ struct DistillArgs {
   float* loss;        // [B]
   float* lse;         // [B][T]
   float* row_loss;    // workspace [B][T] (T > 1)
-  float2* part;       // workspace [B*T][splits] (splits > 1)
   const float* dloss; // [B] or null
   void* grad;         // backward: [B][T][V]
   int64_t splits;     // set by the launcher
 };
-int64_t distill_splits(int64_t rows, int64_t V);
 hipError_t launch_distill_loss(hipStream_t st, int dtype, DistillArgs a);
 hipError_t launch_distill_backward(hipStream_t st, int dtype, DistillArgs a);
 
