@@ -869,19 +869,31 @@ __global__ __launch_bounds__(256) void k_grouped_norm_packed(GNormArgs a) {
         const T* xt = X + (tok ? trow : 0) * K;
         const T* xu = X + (uok ? urow : 0) * K;
         const int64_t steps = (K + 2 * P - 1) / (2 * P);
+        // the next U steps' pieces are loaded ahead of this U's products
+        u32x4 nt[U], nu[U];
+        auto load = [&](int64_t s) {
+#pragma unroll
+          for (int i = 0; i < U; ++i) nt[i] = load_piece(xt, (2 * (s + i) + g) * P, K, tok);
+          if (u != t) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) nu[i] = load_piece(xu, (2 * (s + i) + g) * P, K, uok);
+          } else {
+#pragma unroll
+            for (int i = 0; i < U; ++i) nu[i] = nt[i];
+          }
+        };
+        load(wave * U);
         for (int64_t s = wave * U; s < steps; s += 4 * U) {
           u32x4 ft[U], fu[U];
 #pragma unroll
-          for (int i = 0; i < U; ++i) ft[i] = load_piece(xt, (2 * (s + i) + g) * P, K, tok);
-          if (u != t) {
-#pragma unroll
-            for (int i = 0; i < U; ++i) fu[i] = load_piece(xu, (2 * (s + i) + g) * P, K, uok);
-          } else {
-#pragma unroll
-            for (int i = 0; i < U; ++i) fu[i] = ft[i];
+          for (int i = 0; i < U; ++i) {
+            ft[i] = nt[i];
+            fu[i] = nu[i];
           }
+          if (s + 4 * U < steps) load(s + 4 * U);
 #pragma unroll
-          for (int i = 0; i < U; ++i) acc[m] = mma_step<T>(ft[i], fu[i], acc[m]);
+          for (int i = 0; i < U; ++i)
+            if (s + i < steps) acc[m] = mma_step<T>(ft[i], fu[i], acc[m]);
         }
       }
       __syncthreads();  // the previous pair's elements are read
