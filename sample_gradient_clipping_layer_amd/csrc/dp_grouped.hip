@@ -79,6 +79,7 @@ template <typename T, bool KCONT, int NF, int KB = 128>
 struct Opnd {
   static constexpr int SZ = sizeof(T);
   static constexpr int P = elem_traits<T>::per16;
+  static constexpr bool FEAT = !KCONT;               // features along the rows
   static constexpr int KC = KB / SZ;                 // K per chunk
   static constexpr int ROWB = KCONT ? KB : NF * SZ;  // LDS row bytes
   static constexpr int NROWS = KCONT ? NF : KC;
@@ -101,6 +102,7 @@ struct Win {
   int64_t ldb;   // bytes from row to row
   int64_t rows;  // valid rows
   int64_t cols;  // valid columns (elements)
+  int64_t over = 0;  // rows that may be read past their end: all but the matrix's last one
 };
 
 // Between a wave's LDS writes and its reads of what other lanes wrote (and
@@ -130,13 +132,15 @@ __device__ __forceinline__ u32x4 make_srd(const T* base, uint32_t bytes) {
 }
 
 // 16 bytes of elements [col, col + P) of a row of K, zero past K and where !ok;
-// rows of odd widths start at any element.
+// rows of odd widths start at any element. `over`: 16 bytes there may be read,
+// and what lies past K does no harm.
 template <typename T>
-__device__ __forceinline__ u32x4 load_piece(const T* __restrict__ row, int64_t col, int64_t K, bool ok) {
+__device__ __forceinline__ u32x4 load_piece(const T* __restrict__ row, int64_t col, int64_t K, bool ok,
+                                            bool over = false) {
   constexpr int P = elem_traits<T>::per16;
   u32x4 v = {0u, 0u, 0u, 0u};
   if (!ok || col >= K) return v;
-  if (col + P <= K) {
+  if (over || col + P <= K) {
     __builtin_memcpy(&v, row + col, 16);
     return v;
   }
@@ -178,13 +182,17 @@ struct Filler {
     for (int i = 0; i < LOADS; ++i)
       dma16_buf(srd, qp[i] < cols ? voff[i] : 0x80000000u, lds + (wave + NW * i) * 1024);
   }
-  // Through registers (any alignment): load, and after the LDS image's readers are done, store.
+  // Through registers (any alignment): load, and after the LDS image's readers are done, store. Features past
+  // the width only reach products that are not stored, so a row's last piece is read whole where the matrix goes
+  // on (element by element, with a wait for each, it held up every chunk of a tile at the edge).
   __device__ __forceinline__ void load(const Win<T>& w, u32x4 (&v)[LOADS], int wave, int lane) const {
+    // a piece that starts in a row ends in the next one at the latest when rows have 16 bytes
+    const int64_t over = O::FEAT && w.ldb >= 16 ? w.over : 0;
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const int r = ((wave + NW * i) * 1024 + 16 * lane) / O::ROWB;
       v[i] = load_piece(reinterpret_cast<const T*>(reinterpret_cast<const char*>(w.base) + (int64_t)r * w.ldb),
-                        qp[i], w.cols, r < w.rows);
+                        qp[i], w.cols, r < w.rows, r < over);
     }
   }
   __device__ __forceinline__ void store(const u32x4 (&v)[LOADS], unsigned char* lds, int wave, int lane) const {
@@ -362,7 +370,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_grouped_matmul(MatmulArgs a)
   rw.init(wn * WN, lane);
   auto xwin = [&](int64_t k0) { return Win<T>{X + k0, xb, mrows, klen - k0}; };
   auto wwin = [&](int64_t k0) {
-    return TRANS ? Win<T>{W + k0 * a.N, wb, klen - k0, a.N - n0} : Win<T>{W + k0, wb, a.N - n0, klen - k0};
+    return TRANS ? Win<T>{W + k0 * a.N, wb, klen - k0, a.N - n0, (a.E - e) * a.K - 1 - kb0 - k0} : Win<T>{W + k0, wb, a.N - n0, klen - k0};
   };
 
   f32x16 acc[NBN][NBM];
@@ -1176,7 +1184,7 @@ __device__ __forceinline__ Emit emit_at(const GSumArgs& a, int64_t e, int64_t sp
 template <bool RATIO>
 __global__ __launch_bounds__(512) void k_grouped_sum_big(GSumArgs a) {
   using T = bf16s;
-  constexpr int BM = 256, BN = 256, WGM = 4, WGN = 2, NW = 8, WM = 64, WN = 128, NBM = 2, NBN = 4, KB = 64, ST = 4;
+  constexpr int BM = 256, BN = 256, WGM = 4, NW = 8, WM = 64, WN = 128, NBM = 2, NBN = 4, KB = 64, ST = 4;
   using OA = Opnd<T, false, BM, KB>;
   using OG = Opnd<T, false, BN, KB>;
   using FA = Filler<OA, T, NW>;
@@ -1551,8 +1559,8 @@ __global__ __launch_bounds__(256) void k_grouped_sum(GSumArgs a) {
   zero_acc(acc);
   const T* A = static_cast<const T*>(a.A) + m0;
   const T* G = static_cast<const T*>(a.G) + n0;
-  auto awin = [&](int64_t row, int64_t rows) { return Win<T>{A + row * a.d, ab, rows, a.d - m0}; };
-  auto gwin = [&](int64_t row, int64_t rows) { return Win<T>{G + row * a.p, gb, rows, a.p - n0}; };
+  auto awin = [&](int64_t row, int64_t rows) { return Win<T>{A + row * a.d, ab, rows, a.d - m0, a.R - 1 - row}; };
+  auto gwin = [&](int64_t row, int64_t rows) { return Win<T>{G + row * a.p, gb, rows, a.p - n0, a.R - 1 - row}; };
 
   if constexpr (FOLD) {
     f32x16 tmp[NBM][NBN];
