@@ -9,8 +9,9 @@
 // A token without a used place, or with weight 0, has loss 0 and gradient 0
 // whatever its logits hold.
 //
-// Both directions are bound by HBM: the logits are read once (and the
-// gradient written once); a token's V words are streamed with a running
+// Both directions are bound by HBM (2048 x 32003 fp32 forward 44 us, 6.0 TB/s;
+// 4096 x 50257 bf16 backward 165 us, 5.0 TB/s): the logits are read once (and
+// the gradient written once); a token's V words are streamed with a running
 // maximum and sum per thread, joined across the block at the end. The
 // logarithm's argument is kept as (z - max) in raw logits, so that rows holding
 // the type's lowest value neither overflow nor give NaN. Where tokens are few,

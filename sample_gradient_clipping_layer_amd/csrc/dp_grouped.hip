@@ -316,6 +316,10 @@ __device__ __forceinline__ void chunk_mma(uint32_t sa, uint32_t sb, const RA& ra
 //
 // The weight is the MFMA's first operand, so an accumulator lane holds four
 // consecutive columns of one row of Y and stores them together.
+//
+// k_grouped_matmul: 128 x 128 tiles, and 32 x 128 ones for few rows, which are
+// bound by the experts' weights (8 rows over 8 experts of 1280 x 5120 bf16:
+// 16 us, 4.3 TB/s of the weights in use).
 struct MatmulArgs {
   const void *X, *W;
   void* Y;
@@ -494,6 +498,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_grouped_matmul(MatmulArgs a)
 //
 // Lane e of each wave holds expert e's row range and tile count, so a tile's
 // expert is found without memory, and the tiles are numbered without gaps.
+//
+// 32768 rows over 8 experts, 1280 -> 5120: 430 us, 1.0 PFLOP/s. The matrix
+// cores are busy 0.61 of the cycles, and the clock falls to 1.6 GHz. The
+// products and their loop alone take 264 us; the LDS reads, each added alone,
+// 110 more, the loads 95, the stores 50. 8192 rows over 16 experts, 5120 -> 1280: 130 us,
+// 0.83 PFLOP/s, 200 tiles on the 256 CUs.
 //
 // Each wave writes its 64 x 128 part of the tile through 4 KB of LDS of its
 // own (no barrier): 32 x 64 values at a time, 8-byte units swizzled by the
@@ -736,8 +746,10 @@ constexpr int norm_tile() {
 // Workgroup (tile t, j) takes the pairs (t, u), u - t = j, j + J, ...: a long
 // segment's pairs spread over J workgroups (one after another they were the
 // launch's critical path: 276 -> 181 us at 256 segments of 128 rows on
-// average, d + p = 6400; 151 with the deeper stages of the diagonal). A wave whose 64 x 64 part lies below the diagonal
-// or past the segment only takes part in the loads.
+// average, d + p = 6400; 151 us with the deeper stages of the diagonal, 2.8
+// TB/s of rows: a workgroup's chunks one after another still bound it). A wave
+// whose 64 x 64 part lies below the diagonal or past the segment only takes
+// part in the loads.
 template <typename T, bool DMA>
 __global__ __launch_bounds__(256, DMA ? 2 : 1) void k_grouped_norm(GNormArgs a) {
   constexpr int TS = norm_tile<T>(), WG = 2, NW = 4, WT = TS / 2, NB = WT / 32;
@@ -847,7 +859,9 @@ __global__ __launch_bounds__(256, DMA ? 2 : 1) void k_grouped_norm(GNormArgs a) 
 // the following tiles as far as the tile's last segment reaches. The rows go
 // from memory straight into fragments (a Gram of a tile with itself takes one
 // load per product), K dealt to the four waves and joined through LDS. Each
-// row's share of its segment's value goes to partial[row].
+// row's share of its segment's value goes to partial[row]. 16384 rows in 1024
+// segments of 16, d + p = 6400 bf16: 117 us a call, 1.8 TB/s; a wave's loads, in
+// turns of four, bound it.
 template <typename T>
 __global__ __launch_bounds__(256) void k_grouped_norm_packed(GNormArgs a) {
   constexpr int P = elem_traits<T>::per16, U = 4;
@@ -1181,6 +1195,14 @@ __device__ __forceinline__ Emit emit_at(const GSumArgs& a, int64_t e, int64_t sp
 // first, and its workgroups take the next item off the XCD's list as they
 // come free: uneven experts even out, and the workgroups share operand tiles
 // in their L2. (Which workgroup forms an item does not enter its result.)
+//
+// 32768 rows over 8 experts of 32 samples, 1280 x 5120: 570 to 700 us by the
+// factors (590 with all of them 1), 0.6 to 0.75 PFLOP/s; the matrix cores are
+// busy a third of the cycles. The rest is the loads (110 us, also from L2), the
+// rescale (90 us where every sample clips), the writing of the fp32 tiles
+// (70 us), a piece's unused rows (an eighth here) and a last round of items
+// that does not fill the GPU (splitting those over K gained nothing: the items
+// in flight share what the loads and the power allow).
 template <bool RATIO>
 __global__ __launch_bounds__(512) void k_grouped_sum_big(GSumArgs a) {
   using T = bf16s;
@@ -1732,7 +1754,7 @@ __global__ __launch_bounds__(256) void k_grouped_sum(GSumArgs a) {
 // The splits' sums added in order, noise and mean applied, for widths without
 // 16-byte vectors: a thread takes one column of a row quad, lanes side by side
 // (the layers' reduce gives a thread 4 x 4 elements, 16 loads of 4 bytes a
-// split: 20 us against 6 at six splits of 1665 x 517).
+// split: 20 us against 11 at six splits of 1665 x 517).
 __global__ __launch_bounds__(256) void k_grouped_reduce(GSumArgs a, NoiseArgs na) {
   const int64_t rows = a.E * a.d, n = (rows + 3) / 4 * a.p, stride = rows * a.p;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {

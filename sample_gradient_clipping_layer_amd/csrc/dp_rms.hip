@@ -6,7 +6,9 @@
 //              gain_rows[b] = sum_t dy[b][t] * u[b][t]
 //
 // Both are bound by HBM: each element is read once and written once, about
-// 10 fp32 operations in between. A row is held in the registers of one, four
+// 10 fp32 operations in between (32768 x 1280 bf16: forward 60 us, 5.6 TB/s;
+// backward 67 us, 5.0 TB/s, and 5 us for the join of the gains' partial sums;
+// a large copy reaches 5.1 TB/s). A row is held in the registers of one, four
 // or sixteen waves (8 to 32 elements per lane), so that one pass over memory
 // serves the row's reductions and its outputs. Rows of up to 2048 elements
 // take one wave, whose reductions are lane shuffles without a barrier.
@@ -32,8 +34,9 @@ __device__ __forceinline__ void put(bf16s& d, float v) { d.u = f32_to_bf16(v); }
 // The columns a lane holds: E elements as vectors of 16 bytes, the row's LPR
 // lanes side by side. Rows may start at any element (odd widths, views): the
 // hardware takes unaligned 16-byte accesses, and the row's last vector is
-// taken element by element when it is not whole (WHOLE: it always is). (Single-element accesses for
-// such rows took 16.6 us instead of 8 for a backward pass of 1001 x 1001 fp32.)
+// taken element by element when it is not whole (WHOLE: it always is).
+// Single-element accesses for such rows: 19.6 us a call instead of 11.6 for a
+// backward pass of 1001 rows of 1001 fp32.
 template <typename T, bool WHOLE, int E, int LPR>
 struct RowMap {
   static constexpr int P = elem_traits<T>::per16;

@@ -101,6 +101,9 @@ class PrivacyEngine:
                     raise ValueError("Conv2d padding must be numeric or 'valid'")
                 if not m.weight.requires_grad:
                     raise ValueError("a layer with a trainable bias needs a trainable weight (one norm covers both)")
+                if isinstance(m, (torch.nn.RMSNorm, RMSNorm, ExpertLinear)) and id(m.weight) in covered:
+                    raise ValueError("a norm's or an expert layer's weight is shared with another layer: its "
+                                     "per-sample gradients would have to be added before their norm")
                 self.layers.append(_Layer(m))
                 covered.update(id(p) for p in m.parameters())
         others = [n for n, p in model.named_parameters() if p.requires_grad and id(p) not in covered]

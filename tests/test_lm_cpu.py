@@ -152,6 +152,15 @@ def test_engine_covers_norms_and_experts():
         PrivacyEngine(RMSNorm(8), C=1.0, sigma=1.0).step(0)
 
 
+def test_engine_refuses_shared_norm_and_expert_weights():
+    for make in (lambda: RMSNorm(8), lambda: torch.nn.RMSNorm(8), lambda: ExpertLinear(2, 8, 8)):
+        a, b = make(), make()
+        b.weight = a.weight
+        with pytest.raises(ValueError):
+            PrivacyEngine(torch.nn.Sequential(a, b), C=1.0, sigma=1.0)
+        assert not getattr(a, "private", False)
+
+
 def test_route_orders_by_expert_then_sample():
     g = torch.Generator().manual_seed(0)
     ids = torch.randint(-1, 5, (3, 7, 2), generator=g)
