@@ -153,6 +153,67 @@ def test_few_rows_of_wide_experts(dtype, counts):
         assert (out[ends[-1]:] == 5.0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("E,B,lo,hi,d,p", [(3, 4, 0, 40, 72, 136), (3, 4, 60, 200, 33, 70), (16, 8, 0, 50, 1016, 1016),
+                                           (4, 3, 300, 500, 512, 640), (700, 9, 0, 2, 40, 24), (2, 3000, 0, 2, 24, 17)])
+def test_rows_ahead_of_and_behind_the_segments(dtype, E, B, lo, hi, d, p):
+    """Segments that start behind row 0 and end ahead of row R: the rows
+    outside are neither read (they hold NaN) nor written."""
+    dt = L.DT[dtype]
+    g = L.gen(E * B + d)
+    counts = _counts(g, E, B, lo, hi)
+    _, ends = L.segments_of(counts)
+    head, tail = 37, 130
+    n = ends[-1]
+    seg = (torch.tensor(ends) + head).cuda()
+    A, G = (torch.full((head + n + tail, w), float("nan"), dtype=dt, device="cuda") for w in (d, p))
+    a, gr = L.randn(g, n, d, scale=d ** -0.5, dtype=dt), L.randn(g, n, p, dtype=dt)
+    A[head:head + n], G[head:head + n] = a, gr
+    sq = torch.full((B,), float("nan"), device="cuda")
+    dpc.dp_grouped_norm(A, G, seg, sq)
+    L.check(sq, *L.grouped_norm(a, gr, ends, B), "sqnorm")
+    c = torch.rand(B, generator=g).cuda()
+    out = _sum(A, G, seg, c, (E, d, p))
+    L.check(out, *L.grouped_sum(a, gr, ends, c, 4.0), "sum")
+    W = L.randn(g, E, p, d, scale=d ** -0.5, dtype=dt)
+    for x, part, transpose, w in ((A, a, False, p), (G, gr, True, d)):
+        y = torch.full((head + n + tail, w), 5.0, dtype=dt, device="cuda")
+        dpc.dp_grouped_matmul(x, W, seg, y, transpose=transpose)
+        L.check(y[head:head + n], *L.grouped_matmul(part, W, ends, B, transpose), f"transpose={transpose}")
+        assert (y[:head] == 5.0).all() and (y[head + n:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_sample_of_many_rows(dtype):
+    """All rows in one segment, over many row tiles and workgroups."""
+    dt = L.DT[dtype]
+    g = L.gen(4)
+    seg, ends, A, G = _rows(3, [[6001]], 136, 72, dt)
+    sq = torch.empty(1, device="cuda")
+    dpc.dp_grouped_norm(A, G, seg, sq)
+    L.check(sq, *L.grouped_norm(A, G, ends, 1), "sqnorm")
+    c = torch.tensor([0.37], device="cuda")
+    L.check(_sum(A, G, seg, c, (1, 136, 72)), *L.grouped_sum(A, G, ends, c, 4.0), "sum")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,p", [(1, 1), (2, 3), (5, 1), (1, 130), (129, 2)])
+def test_rows_narrower_than_a_vector_end_with_their_tensor(dtype, d, p):
+    """Widths of a few elements, the tensors' last rows the last of the last
+    segment (nothing may be read past them)."""
+    dt = L.DT[dtype]
+    g = L.gen(d * 10 + p)
+    counts = [[70, 3], [0, 41]]
+    seg, ends, A, G = _rows(d, counts, d, p, dt)
+    c = torch.rand(2, generator=g).cuda()
+    L.check(_sum(A, G, seg, c, (2, d, p)), *L.grouped_sum(A, G, ends, c, 4.0), "sum")
+    W = L.randn(g, 2, p, d, dtype=dt)
+    for x, transpose, w in ((A, False, p), (G, True, d)):
+        y = torch.empty(ends[-1], w, dtype=dt, device="cuda")
+        dpc.dp_grouped_matmul(x, W, seg, y, transpose=transpose)
+        L.check(y, *L.grouped_matmul(x, W, ends, 2, transpose), f"transpose={transpose}")
+
+
 # ---- distillation
 
 
