@@ -50,6 +50,15 @@ class _Layer:
         self.segments = None  # ExpertLinear: its rows' (expert, sample) ranges
 
 
+def _torch_eps(m, dtype):
+    """The eps that a torch.nn.RMSNorm adds to rows of `dtype`. eps=None is the
+    machine epsilon of the type torch computes in, which is float32 for the
+    16-bit types too."""
+    if m.eps is not None:
+        return m.eps
+    return torch.finfo(torch.float64 if dtype == torch.float64 else torch.float32).eps
+
+
 _COVERED = (torch.nn.Linear, torch.nn.Conv2d, torch.nn.RMSNorm, RMSNorm, ExpertLinear)
 
 
@@ -169,9 +178,8 @@ class PrivacyEngine:
         else:
             dt = a.dtype if a.dtype in (torch.float32, torch.bfloat16) else torch.float32
             rows = torch.empty(a.shape[0], a.shape[-1], dtype=torch.float32, device=a.device)
-            eps = m.eps if m.eps is not None else torch.finfo(a.dtype).eps  # torch's default
-            dp_rms_norm_backward(g.to(dt).contiguous(), a.to(dt).contiguous(), m.weight.detach(), eps,
-                                 gain_rows=rows)
+            dp_rms_norm_backward(g.to(dt).contiguous(), a.to(dt).contiguous(), m.weight.detach(),
+                                 _torch_eps(m, a.dtype), gain_rows=rows)
         B = rows.shape[0]
         return torch.ones(B, 1, 1, dtype=torch.float32, device=rows.device), rows.view(B, 1, -1)
 

@@ -1,0 +1,55 @@
+"""The language-model layers and the loss as a user's module calls them, and
+the engine over them, where an argument, a type or an address is not the usual
+one."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import lm_util as L
+import sample_gradient_clipping_layer_amd as dpc
+from sample_gradient_clipping_layer_amd.engine import PrivacyEngine
+
+pytestmark = pytest.mark.gpu
+
+DT = {**L.DT, "f16": torch.float16}
+
+
+def _check_gain_step(engine, m, s, dy, eps, C):
+    """step() of a model that is one norm layer, from its rows s and output
+    gradients dy: norms and clipped mean in 64 bits."""
+    B, d = s.shape[0], s.shape[-1]
+    _, rows, _, br = L.rms_backward(dy, s, None, torch.ones(d, device="cuda"), eps)
+    norms = engine.step(0)
+    want = rows.norm(dim=1)
+    # a norm moves by the length of its rows' error at most; d products added, and a root
+    bn = br.norm(dim=1) + (d + 16) * L.U * want
+    L.check(norms, want, bn, "norms")
+    c = torch.clamp(C / want, max=1.0)
+    grad = (c[:, None] * rows).sum(0) / B
+    # c is off by the norm's relative error; then the rows' own, B products added, and the gradient's type
+    bound = (c[:, None] * (br + (bn / want)[:, None] * rows.abs() + (B + 16) * L.U * rows.abs())).sum(0) / B
+    half = torch.finfo(m.weight.dtype).eps / 2
+    L.check(m.weight.grad, grad, bound * (1 + half) + half * grad.abs() + torch.finfo(m.weight.dtype).tiny, "gradient")
+
+
+@pytest.mark.parametrize("dtype,weight_dtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f16", "f32")])
+def test_engine_takes_torchs_default_eps(dtype, weight_dtype):
+    """torch.nn.RMSNorm with eps=None over rows far below 1: torch adds
+    float32's epsilon whatever the rows' type (one type for both takes torch's
+    fused kernel, two do not)."""
+    dt, g = DT[dtype], L.gen(17)
+    B, T, d = 4, 6, 96
+    x = L.randn(g, B, T, d, scale=1e-2 if dt != torch.float32 else 1e-4).to(dt).requires_grad_()
+    t = L.randn(g, B, T, d, scale=0.1).to(dt)
+    m = torch.nn.RMSNorm(d, dtype=DT[weight_dtype]).cuda()
+    eps = torch.finfo(torch.float32).eps
+    y = m(x)
+    want = L.rms_forward(x.detach(), None, m.weight.detach(), eps)[0]
+    assert ((y.double() - want).abs() <= (torch.finfo(dt).eps / 2 + 64 * L.U) * want.abs() + 1e-30).all()
+    rows = L.rms_backward(t, x.detach(), None, m.weight.detach(), eps)[1]
+    C = float(rows.norm(dim=1).median())
+    engine = PrivacyEngine(m, C=C, sigma=0.0)
+    (m(x) * t).sum().backward()
+    _check_gain_step(engine, m, x.detach(), t, eps, C)
+    engine.detach()
