@@ -178,8 +178,11 @@ class PrivacyEngine:
         else:
             dt = a.dtype if a.dtype in (torch.float32, torch.bfloat16) else torch.float32
             rows = torch.empty(a.shape[0], a.shape[-1], dtype=torch.float32, device=a.device)
-            dp_rms_norm_backward(g.to(dt).contiguous(), a.to(dt).contiguous(), m.weight.detach(),
-                                 _torch_eps(m, a.dtype), gain_rows=rows)
+            gain = m.weight.detach()
+            if gain.dtype not in (torch.float32, torch.bfloat16):
+                gain = gain.float()  # it has no part in the rows, but the call reads it
+            dp_rms_norm_backward(g.to(dt).contiguous(), a.to(dt).contiguous(), gain, _torch_eps(m, a.dtype),
+                                 gain_rows=rows)
         B = rows.shape[0]
         return torch.ones(B, 1, 1, dtype=torch.float32, device=rows.device), rows.view(B, 1, -1)
 

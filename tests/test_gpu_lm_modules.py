@@ -53,3 +53,16 @@ def test_engine_takes_torchs_default_eps(dtype, weight_dtype):
     (m(x) * t).sum().backward()
     _check_gain_step(engine, m, x.detach(), t, eps, C)
     engine.detach()
+
+
+@pytest.mark.parametrize("weight_dtype", [torch.float16, torch.float64])
+def test_engine_takes_gains_of_other_types(weight_dtype):
+    """Gains of a type the library does not read: they enter it in float32."""
+    g = L.gen(18)
+    x = L.randn(g, 3, 5, 40).to(weight_dtype)
+    t = L.randn(g, 3, 5, 40, scale=0.1).to(weight_dtype)
+    m = torch.nn.RMSNorm(40, eps=1e-6, dtype=weight_dtype).cuda()
+    engine = PrivacyEngine(m, C=0.3, sigma=0.0)
+    (m(x) * t).sum().backward()
+    _check_gain_step(engine, m, x.float(), t.float(), 1e-6, 0.3)  # fp64 rows enter in fp32 too (values of fp32 here)
+    engine.detach()

@@ -45,3 +45,20 @@ def test_torch_norms_take_torchs_eps(monkeypatch, dtype, eps):
     steps = torch.finfo(dt).eps / 2 + 200 * torch.finfo(torch.float32).eps / 2
     assert ((rows[:, 0].double() - terms.sum(1)).abs() <= steps * terms.abs().sum(1)).all()
     engine.detach()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_torch_norms_of_any_floating_type(monkeypatch, dtype):
+    """A norm whose gain has the rows' own type, the types the engine takes of
+    linear layers among them."""
+    monkeypatch.setattr(eng, "dp_rms_norm_backward", _rms_rows)
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(1)
+    m = torch.nn.RMSNorm(16, eps=1e-6, dtype=dt)
+    engine = PrivacyEngine(m, C=1.0, sigma=0.0)
+    x = torch.randn(2, 3, 16, generator=g).to(dt)
+    m(x).sum().backward()
+    rows = engine._gain_operands(engine.layers[0])[1]
+    u = x.double() * torch.rsqrt((x.double() ** 2).mean(-1, keepdim=True) + 1e-6)
+    assert ((rows[:, 0].double() - u.sum(1)).abs() <= 8 * torch.finfo(torch.float32).eps * u.abs().sum(1)).all()
+    engine.detach()
