@@ -125,19 +125,20 @@ class PrivacyEngine:
         for L in self.layers:
             if isinstance(L.module, (RMSNorm, ExpertLinear)):
                 L.module.private = True  # their backward passes leave the weight's gradient to step()
-            self._handles.append(L.module.register_forward_hook(self._forward_hook(L)))
+            self._handles.append(L.module.register_forward_hook(self._forward_hook(L), with_kwargs=True))
             self._handles.append(L.module.register_full_backward_hook(self._backward_hook(L)))
         self.last_norms = None  # per-sample norms of the last step
 
     @staticmethod
     def _forward_hook(L):
-        def hook(module, inputs, output):
+        def hook(module, inputs, kwargs, output):  # arguments by position or by name
             if L.a is not None and L.g is None:
                 raise RuntimeError("a module ran twice in one forward pass")
-            L.a = inputs[0].detach()
+            a = inputs[0] if inputs else kwargs["input" if "input" in kwargs else "x"]
+            L.a = a.detach()
             L.g = None
             if isinstance(module, ExpertLinear):
-                L.segments = inputs[1]
+                L.segments = inputs[1] if len(inputs) > 1 else kwargs["segments"]
             elif isinstance(module, RMSNorm):
                 module.gain_rows = None
         return hook

@@ -7,7 +7,9 @@ import pytest
 import torch
 
 import sample_gradient_clipping_layer_amd.engine as eng
+import sample_gradient_clipping_layer_amd.layers as lay
 from sample_gradient_clipping_layer_amd.engine import PrivacyEngine
+from sample_gradient_clipping_layer_amd.layers import ExpertLinear, RMSNorm
 
 DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32, "f64": torch.float64}
 
@@ -61,4 +63,67 @@ def test_torch_norms_of_any_floating_type(monkeypatch, dtype):
     rows = engine._gain_operands(engine.layers[0])[1]
     u = x.double() * torch.rsqrt((x.double() ** 2).mean(-1, keepdim=True) + 1e-6)
     assert ((rows[:, 0].double() - u.sum(1)).abs() <= 8 * torch.finfo(torch.float32).eps * u.abs().sum(1)).all()
+    engine.detach()
+
+
+def _grouped_matmul(X, W, segments, out, transpose=False, workspace=None, stream=None):
+    E = W.shape[0]
+    B = (segments.numel() - 1) // E
+    for e in range(E):
+        i, j = int(segments[e * B]), int(segments[(e + 1) * B])
+        out[i:j] = X[i:j] @ (W[e] if transpose else W[e].T)
+
+
+def _rms_norm(x, gain, eps, out, residual=None, sum_out=None, stream=None):
+    s = x if residual is None else x + residual
+    out.copy_(s * torch.rsqrt((s * s).mean(-1, keepdim=True) + eps) * gain)
+    if sum_out is not None:
+        sum_out.copy_(s)
+
+
+def _rms_back(dy, s, gain, eps, dx=None, dsum=None, gain_rows=None, workspace=None, stream=None):
+    if gain_rows is not None:
+        _rms_rows(dy, s, gain, eps, gain_rows=gain_rows)
+    if dx is not None:
+        rstd = torch.rsqrt((s * s).mean(-1, keepdim=True) + eps)
+        u, h = s * rstd, dy * gain
+        dx.copy_(rstd * (h - u * (h * u).mean(-1, keepdim=True)) + (0 if dsum is None else dsum))
+
+
+@pytest.fixture
+def plain_calls(monkeypatch):
+    monkeypatch.setattr(eng, "dp_rms_norm_backward", _rms_rows)
+    monkeypatch.setattr(lay, "dp_rms_norm", _rms_norm)
+    monkeypatch.setattr(lay, "dp_rms_norm_backward", _rms_back)
+    monkeypatch.setattr(lay, "dp_grouped_matmul", _grouped_matmul)
+
+
+SEG = torch.tensor([0, 1, 3, 4, 6])  # 2 experts, 2 samples, 6 rows
+
+
+@pytest.mark.parametrize("call", [lambda m, x: m(x, SEG), lambda m, x: m(x, segments=SEG), lambda m, x: m(x=x, segments=SEG),
+                                  lambda m, x: m(segments=SEG, x=x)])
+def test_experts_called_by_keyword(plain_calls, call):
+    m = ExpertLinear(2, 3, 4)
+    engine = PrivacyEngine(m, C=1.0, sigma=0.0)
+    x = torch.arange(18.0).reshape(6, 3).requires_grad_()
+    g = torch.arange(24.0).reshape(6, 4)
+    (call(m, x) * g).sum().backward()
+    kept = engine.layers[0]
+    assert torch.equal(kept.a, x.detach()) and torch.equal(kept.segments, SEG) and torch.equal(kept.g, g)
+    engine.detach()
+
+
+@pytest.mark.parametrize("make,name", [(lambda: RMSNorm(3), "x"), (lambda: torch.nn.RMSNorm(3, eps=1e-6), "x"),
+                                       (lambda: torch.nn.Linear(3, 3), "input")])
+def test_layers_called_by_keyword(plain_calls, make, name):
+    m = make()
+    engine = PrivacyEngine(m, C=1.0, sigma=0.0)
+    x = torch.arange(6.0).reshape(2, 3)
+    kept = []
+    for call in (lambda: m(x), lambda: m(**{name: x})):
+        call().sum().backward()
+        L = engine.layers[0]
+        kept.append((L.a, L.g))
+    assert torch.equal(kept[0][0], kept[1][0]) and torch.equal(kept[0][1], kept[1][1])
     engine.detach()
