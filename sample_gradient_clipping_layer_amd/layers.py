@@ -110,7 +110,8 @@ class _ExpertLinear(torch.autograd.Function):
             E, p, d = weight.shape
             B = (segments.numel() - 1) // E
             out = torch.empty(E, d, p, dtype=torch.float32, device=x.device)
-            dp_grouped_clipped_sum_noise(x, g, segments, torch.ones(B, device=x.device), 1.0, 0.0, 1.0, 0, 0, 0, out)
+            dp_grouped_clipped_sum_noise(x, g, segments, torch.ones(B, dtype=torch.float32, device=x.device), 1.0,
+                                         0.0, 1.0, 0, 0, 0, out)
             dw = out.transpose(1, 2).to(weight.dtype).contiguous()
         return dx, dw, None, None
 

@@ -127,3 +127,27 @@ def test_layers_called_by_keyword(plain_calls, make, name):
         kept.append((L.a, L.g))
     assert torch.equal(kept[0][0], kept[1][0]) and torch.equal(kept[0][1], kept[1][1])
     engine.detach()
+
+
+@pytest.mark.parametrize("default", [torch.float32, torch.float64, torch.bfloat16])
+def test_expert_gradients_under_another_default_type(plain_calls, monkeypatch, default):
+    """Without an engine the weight's gradient is the clipped sum under factors
+    1, which the library takes in float32 whatever torch's default type is."""
+    def grouped_sum(A, G, segments, c, C, sigma, denom, seed, layer_id, step, out, workspace=None, stream=None):
+        assert c.dtype == torch.float32 and out.dtype == torch.float32 and (c == 1).all()
+        E, B = out.shape[0], c.numel()
+        for e in range(E):
+            i, j = int(segments[e * B]), int(segments[(e + 1) * B])
+            out[e] = A[i:j].T @ G[i:j] / denom
+
+    monkeypatch.setattr(lay, "dp_grouped_clipped_sum_noise", grouped_sum)
+    m = ExpertLinear(2, 3, 4, dtype=torch.float32)
+    x, g = torch.arange(18, dtype=torch.float32).reshape(6, 3), torch.arange(24, dtype=torch.float32).reshape(6, 4)
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        (m(x, SEG) * g).sum().backward()
+    finally:
+        torch.set_default_dtype(before)
+    want = torch.stack([g[0:3].T @ x[0:3], g[3:6].T @ x[3:6]])
+    assert torch.equal(m.weight.grad, want)
