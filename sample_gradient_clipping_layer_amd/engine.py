@@ -37,7 +37,7 @@ from . import (DP_BF16, DP_F32, MODE_EXPLICIT, MODE_GHOST, MODE_MIXED, MODE_TIME
                dp_clipped_sum_noise_layers, dp_conv_clipped_sum_noise, dp_conv_norm, dp_conv_workspace_bytes,
                dp_ghost_norm_clip_layers, dp_ghost_norm_layers, dp_grouped_clipped_sum_noise, dp_grouped_norm,
                dp_grouped_workspace_bytes, dp_layers_workspace_bytes, dp_rms_norm_backward, dp_unfold2d)
-from .layers import ExpertLinear, RMSNorm
+from .layers import ExpertLinear, RMSNorm, _aligned
 
 MODES = {"ghost-mixed": MODE_MIXED, "ghost": MODE_GHOST, "explicit": MODE_EXPLICIT, "time": MODE_TIME}
 
@@ -197,7 +197,7 @@ class PrivacyEngine:
         B = a.shape[0]
         dt = a.dtype if a.dtype in (torch.float32, torch.bfloat16) else torch.float32
         if isinstance(m, ExpertLinear):
-            A, G = a, g
+            return _aligned(a.to(dt)), _aligned(g.to(dt))
         elif isinstance(m, torch.nn.Linear):
             A = a.reshape(B, -1, a.shape[-1])
             G = g.reshape(B, -1, g.shape[-1])

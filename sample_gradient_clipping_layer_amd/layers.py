@@ -21,6 +21,14 @@ from . import (dp_clipped_sum_noise, dp_distill_loss, dp_distill_loss_backward,
                dp_grouped_clipped_sum_noise, dp_grouped_matmul, dp_rms_norm, dp_rms_norm_backward)
 
 
+def _aligned(t):
+    """t contiguous and at a 16-byte boundary, as the grouped and distillation
+    calls take it. A contiguous view keeps its offset (a slice of samples, the
+    part of a concatenation's gradient): one that starts elsewhere is copied."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, eps, module):
@@ -89,10 +97,10 @@ class RMSNorm(torch.nn.Module):
 class _ExpertLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, segments, module):
-        x = x.contiguous()
+        x = _aligned(x)
         # rows outside the segments belong to no expert: zeros
         out = torch.zeros(x.shape[0], weight.shape[1], dtype=x.dtype, device=x.device)
-        dp_grouped_matmul(x, weight, segments, out)
+        dp_grouped_matmul(x, _aligned(weight), segments, out)
         ctx.save_for_backward(x, weight, segments)
         ctx.module = module
         return out
@@ -101,11 +109,11 @@ class _ExpertLinear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, g):
         x, weight, segments = ctx.saved_tensors
-        g = g.contiguous()
+        g = _aligned(g)
         dx = dw = None
         if ctx.needs_input_grad[0]:
             dx = torch.zeros_like(x)
-            dp_grouped_matmul(g, weight, segments, dx, transpose=True)
+            dp_grouped_matmul(g, _aligned(weight), segments, dx, transpose=True)
         if ctx.needs_input_grad[1] and not ctx.module.private:
             E, p, d = weight.shape
             B = (segments.numel() - 1) // E
@@ -152,7 +160,7 @@ def route(expert_ids, experts: int):
 class _Distill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, teacher, tau, weight):
-        logits = logits.contiguous()
+        logits = _aligned(logits)
         B, T, _ = logits.shape
         loss = torch.empty(B, dtype=torch.float32, device=logits.device)
         lse = torch.empty(B, T, dtype=torch.float32, device=logits.device)

@@ -9,6 +9,7 @@ import torch
 import lm_util as L
 import sample_gradient_clipping_layer_amd as dpc
 from sample_gradient_clipping_layer_amd.engine import PrivacyEngine
+from sample_gradient_clipping_layer_amd.layers import ExpertLinear, RMSNorm, distillation_loss
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,76 @@ def test_engine_takes_gains_of_other_types(weight_dtype):
     (m(x) * t).sum().backward()
     _check_gain_step(engine, m, x.float(), t.float(), 1e-6, 0.3)  # fp64 rows enter in fp32 too (values of fp32 here)
     engine.detach()
+
+
+# ---- contiguous views that start off a 16-byte boundary
+
+
+def _off(t):
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    v = buf[1:].view(t.shape).copy_(t)
+    assert v.is_contiguous() and v.data_ptr() % 16
+    return v
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_expert_layer_over_offset_views(dtype):
+    """A microbatch's slice, the gradient that torch.cat hands to a part, and
+    weights of a flat buffer: the bits of the same values at an aligned start,
+    with and without an engine."""
+    dt, g = L.DT[dtype], L.gen(21)
+    d, p = 33, 35
+    seg = torch.tensor([0, 2, 5, 5, 9], device="cuda")
+    w, x = L.randn(g, 2, p, d, scale=d ** -0.5, dtype=dt), L.randn(g, 9, d, dtype=dt)
+    dy, head = L.randn(g, 9, p, dtype=dt), L.randn(g, 3, p, dtype=dt)
+    results = []
+    for place in (lambda t: t.clone(), _off):
+        for with_engine in (False, True):
+            m = ExpertLinear(2, d, p, device="cuda", dtype=dt)
+            m.weight = torch.nn.Parameter(place(w))
+            engine = PrivacyEngine(m, C=1.0, sigma=0.0) if with_engine else None
+            xx = place(x).requires_grad_()
+            # the part's gradient is a narrowed view of the concatenation's, 3 rows in
+            out = torch.cat([head, m(xx, segments=seg)])
+            out.backward(torch.cat([head, dy]) if place is _off else torch.cat([head, dy]).clone())
+            norms = engine.step(0) if with_engine else torch.zeros(2)
+            results.append((out.detach(), xx.grad, m.weight.grad, norms))
+            if with_engine:
+                engine.detach()
+    for a, b in ((results[0], results[2]), (results[1], results[3])):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distillation_loss_of_a_slice(dtype):
+    """Samples from the second on, of an odd number of logits each."""
+    dt, g = L.DT[dtype], L.gen(22)
+    B, T, V, K = 4, 3, 101, 5
+    z = L.randn(g, B, T, V, scale=3.0, dtype=dt)
+    ids, teacher = torch.randint(-1, V, (B, T, K), generator=g).cuda(), L.randn(g, B, T, K, dtype=dt)
+    assert z[1:].data_ptr() % 16
+    got = []
+    for part in (z[1:], z[1:].clone()):
+        part = part.detach().requires_grad_()
+        loss = distillation_loss(part, ids[1:], teacher[1:], 2.0)
+        loss.sum().backward()
+        got.append((loss.detach(), part.grad))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    want, _, bl, _ = L.distill_forward(z[1:], ids[1:], teacher[1:], 2.0, None)
+    L.check(got[0][0], want, bl, "loss")
+
+
+def test_norm_over_an_offset_view():
+    """RMSNorm takes rows at any element as they are."""
+    g = L.gen(23)
+    x, r = L.randn(g, 3, 7, 33, dtype=torch.bfloat16), L.randn(g, 3, 7, 33, dtype=torch.bfloat16)
+    got = []
+    for place in (lambda t: t.clone(), _off):
+        m = RMSNorm(33).cuda()
+        xx = place(x).requires_grad_()
+        y, s = m(xx, residual=place(r))
+        (y.float() * 0.5 + s.float()).sum().backward()
+        got.append((y.detach(), s.detach(), xx.grad, m.weight.grad))
+    for u, v in zip(*got):
+        assert torch.equal(u, v)

@@ -151,3 +151,46 @@ def test_expert_gradients_under_another_default_type(plain_calls, monkeypatch, d
         torch.set_default_dtype(before)
     want = torch.stack([g[0:3].T @ x[0:3], g[3:6].T @ x[3:6]])
     assert torch.equal(m.weight.grad, want)
+
+
+def _off(t):
+    """t's values in a contiguous view that starts one element off a 16-byte boundary."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    v = buf[1:].view(t.shape)
+    v.copy_(t)
+    assert v.is_contiguous() and v.data_ptr() % 16
+    return v
+
+
+def test_views_off_a_16_byte_boundary_reach_the_calls_aligned(plain_calls, monkeypatch):
+    """.contiguous() keeps a view's offset; the grouped and distillation calls
+    take 16-byte aligned tensors only."""
+    seen = []
+
+    def watch(name, f):
+        def call(*args, **kw):
+            big = args[:4] if name == "dp_grouped_matmul" else args[:2]
+            assert all(t.data_ptr() % (8 if t.dtype == torch.int64 else 16) == 0 for t in big), name
+            seen.append(name)
+            return f(*args, **kw)
+        return call
+
+    monkeypatch.setattr(lay, "dp_grouped_matmul", watch("dp_grouped_matmul", _grouped_matmul))
+    monkeypatch.setattr(lay, "dp_grouped_clipped_sum_noise", watch("sum", lambda *a, **k: a[10].zero_()))
+    monkeypatch.setattr(lay, "dp_distill_loss", lambda z, *a, **k: (seen.append("loss"), a[3].zero_(), a[4].zero_(),
+                                                                    [1 / (z.data_ptr() % 16 == 0)]))
+    monkeypatch.setattr(lay, "dp_distill_loss_backward", lambda z, ids, t, tau, lse, grad, **k: grad.zero_())
+    m = ExpertLinear(2, 3, 5)
+    m.weight = torch.nn.Parameter(_off(m.weight.detach()))  # parameters of a flat buffer
+    x, g = _off(torch.ones(6, 3)).requires_grad_(), _off(torch.ones(6, 5))
+    m(x, SEG).backward(g)
+    assert seen == ["dp_grouped_matmul", "dp_grouped_matmul", "sum"]
+    engine = PrivacyEngine(m, C=1.0, sigma=0.0)
+    m(x, SEG).backward(g)
+    A, G = engine._operands(engine.layers[0])
+    assert A.data_ptr() % 16 == 0 and G.data_ptr() % 16 == 0
+    assert torch.equal(A, x.detach()) and torch.equal(G, g)
+    engine.detach()
+    z = _off(torch.ones(2, 3, 5)).requires_grad_()
+    lay.distillation_loss(z, torch.zeros(2, 3, 1, dtype=torch.int64), torch.zeros(2, 3, 1)).sum().backward()
+    assert "loss" in seen and z.grad.shape == z.shape
