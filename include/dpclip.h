@@ -522,7 +522,9 @@ size_t dp_distill_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t 
  *
  *  X, W, Y, dtype  one number type, 16-byte aligned; fp32 accumulation, one
  *           rounding. Y overlaps neither X nor W.
- *  R, E, B, d, p  1 <= d, p <= 2^20; R and E*B below 2^31.
+ *  R, E, B, d, p  1 <= d, p <= 2^20; R at most 2^30, E*B at most 2^24. With n
+ *           columns of Y, (R / 128 + E) * ceil(n / 128) is at most 2^24 - 8 (a
+ *           grid of row tiles; some larger bf16 sizes are taken too).
  *  workspace  at least dp_grouped_workspace_bytes(...) bytes (may be NULL when
  *           that is 0).
  */
@@ -535,7 +537,8 @@ dp_status dp_grouped_matmul(void* stream, const void* X, const void* W, dp_dtype
  * sqnorm[b] (+)= sum_e || sum_{r in (e, b)} A_r G_r^T ||_F^2, by the ghost
  * identity of dp_ghost_norm on each (expert, sample) range.
  *
- *  A [R, d] rows that entered the experts, G [R, p] output gradients.
+ *  A [R, d] rows that entered the experts, G [R, p] output gradients;
+ *           R, E, B, d, p  1 <= d, p <= 2^20; R at most 2^30, E*B at most 2^24.
  *  sqnorm   [B] fp32, overwritten (accumulate == 0) or added to.
  */
 dp_status dp_grouped_norm(void* stream, const void* A, const void* G, dp_dtype dtype, const int64_t* segments,
@@ -549,9 +552,10 @@ dp_status dp_grouped_norm(void* stream, const void* A, const void* G, dp_dtype d
  *
  * as dp_clipped_sum_noise forms it for one layer; an expert without rows gets
  * the noise alone. The noise is that of a layer of E*d rows: z_e[m][n] is
- * element (e*d + m, n) of dp_clipped_sum_noise's z_w. ceil(E*d/4)*p < 2^32.
+ * element (e*d + m, n) of dp_clipped_sum_noise's z_w.
  *
- *  A, G, segments, R, E, B, d, p  as in dp_grouped_norm.
+ *  A, G, segments, R, E, B, d, p  as in dp_grouped_norm; also
+ *           ceil(E*d/4)*p < 2^32 and E * ceil(d/128) * ceil(p/128) < 2^23.
  *  c, C, sigma, denom, seed, layer_id, step  as in dp_clipped_sum_noise. The
  *           rows of a sample with factor 0 have to be finite: whether 0 * inf
  *           shows in out depends on the sizes.
@@ -562,8 +566,9 @@ dp_status dp_grouped_clipped_sum_noise(void* stream, const void* A, const void* 
                                        const float* c, float C, float sigma, float denom, uint64_t seed,
                                        uint32_t layer_id, uint32_t step, void* workspace, size_t ws_bytes,
                                        float* out);
-/* Workspace bytes that the dp_grouped_* calls need for these sizes (the
- * largest of the three). Returns 0 for invalid arguments. */
+/* Workspace bytes that the dp_grouped_* calls need for these sizes: the
+ * largest of the three, without a call that does not take them. Returns 0 for
+ * invalid arguments. */
 size_t dp_grouped_workspace_bytes(dp_dtype dtype, int64_t R, int64_t E, int64_t B, int64_t d, int64_t p);
 
 /* Workspace bytes that dp_ghost_norm and dp_clipped_sum_noise need for this

@@ -15,6 +15,8 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxElems = (int64_t)1 << 50;
 constexpr int64_t kMaxRowWidth = (int64_t)1 << 20;  // grouped products: a 256-row window's bytes fit 31 bits
+constexpr int64_t kMaxRows = (int64_t)1 << 30;      // rows, and rows rounded up to chunks, fit 31 bits
+constexpr int64_t kMaxRanges = (int64_t)1 << 24;    // (expert, sample) ranges
 
 bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
 bool finite(float x) { return isfinite(x) != 0; }
@@ -57,13 +59,14 @@ dp_status check_distill(int64_t B, int64_t T, int64_t V, int64_t K, float tau) {
 
 size_t distill_ws_bytes(int64_t B, int64_t T) { return T > 1 ? round256((size_t)B * (size_t)T * sizeof(float)) : 0; }
 
-dp_status check_grouped(dp_dtype dtype, const dpk::GroupedArgs& g) {
+dp_status check_grouped(dp_dtype dtype, const dpk::GroupedArgs& g, dpk::GroupedCall call) {
   if (g.R < 1 || g.E < 1 || g.B < 1 || g.d < 1 || g.p < 1) return DP_ERR_SHAPE;
-  if (g.R >= kMaxDim || g.E >= kMaxDim || g.B >= kMaxDim || g.E * g.B >= kMaxDim) return DP_ERR_SHAPE;
+  if (g.R > kMaxRows || g.E > kMaxRanges || g.B > kMaxRanges / g.E) return DP_ERR_SHAPE;
   if (g.d > kMaxRowWidth || g.p > kMaxRowWidth || g.E > kMaxElems / (g.d * g.p)) return DP_ERR_SHAPE;
-  if ((g.E * g.d + 3) / 4 >= ((int64_t)1 << 32) / g.p) return DP_ERR_SHAPE;  // noise group index fits 32 bits
   if (!dtype_ok(dtype)) return DP_ERR_DTYPE;
-  if (!dpk::grouped_fits(dtype, g)) return DP_ERR_SHAPE;
+  // noise group index fits 32 bits
+  if (call == dpk::GroupedCall::sum && (g.E * g.d + 3) / 4 >= ((int64_t)1 << 32) / g.p) return DP_ERR_SHAPE;
+  if (!dpk::grouped_fits(g, call, dtype)) return DP_ERR_SHAPE;
   return DP_OK;
 }
 
@@ -193,9 +196,14 @@ dp_status dp_distill_loss_backward(void* stream, const void* logits, const int64
 
 size_t dp_grouped_workspace_bytes(dp_dtype dtype, int64_t R, int64_t E, int64_t B, int64_t d, int64_t p) {
   const dpk::GroupedArgs g{nullptr, R, E, B, d, p};
-  if (check_grouped(dtype, g) != DP_OK) return 0;
-  return std::max({dpk::grouped_matmul_ws_bytes(dtype, g), dpk::grouped_norm_ws_bytes(dtype, g),
-                   dpk::grouped_sum_ws_bytes(dtype, g)});
+  using dpk::GroupedCall;
+  auto takes = [&](GroupedCall call) { return check_grouped(dtype, g, call) == DP_OK; };
+  size_t need = 0;
+  if (takes(GroupedCall::matmul) || takes(GroupedCall::matmul_transposed))
+    need = std::max(need, dpk::grouped_matmul_ws_bytes(dtype, g));
+  if (takes(GroupedCall::norm)) need = std::max(need, dpk::grouped_norm_ws_bytes(dtype, g));
+  if (takes(GroupedCall::sum)) need = std::max(need, dpk::grouped_sum_ws_bytes(dtype, g));
+  return need;
 }
 
 dp_status dp_grouped_matmul(void* stream, const void* X, const void* W, dp_dtype dtype, const int64_t* segments,
@@ -203,7 +211,7 @@ dp_status dp_grouped_matmul(void* stream, const void* X, const void* W, dp_dtype
                             size_t ws_bytes, void* Y) {
   if (!X || !W || !segments || !Y) return DP_ERR_NULL;
   const dpk::GroupedArgs g{segments, R, E, B, d, p};
-  dp_status s = check_grouped(dtype, g);
+  dp_status s = check_grouped(dtype, g, transpose ? dpk::GroupedCall::matmul_transposed : dpk::GroupedCall::matmul);
   if (s != DP_OK) return s;
   if (!aligned(X, 16) || !aligned(W, 16) || !aligned(Y, 16) || !aligned(segments, 8)) return DP_ERR_ALIGN;
   s = check_workspace(workspace, ws_bytes, dpk::grouped_matmul_ws_bytes(dtype, g));
@@ -219,7 +227,7 @@ dp_status dp_grouped_norm(void* stream, const void* A, const void* G, dp_dtype d
                           float* sqnorm, int32_t accumulate) {
   if (!A || !G || !segments || !sqnorm) return DP_ERR_NULL;
   const dpk::GroupedArgs g{segments, R, E, B, d, p};
-  dp_status s = check_grouped(dtype, g);
+  dp_status s = check_grouped(dtype, g, dpk::GroupedCall::norm);
   if (s != DP_OK) return s;
   if (!aligned(A, 16) || !aligned(G, 16) || !aligned(segments, 8) || !aligned(sqnorm, 4)) return DP_ERR_ALIGN;
   s = check_workspace(workspace, ws_bytes, dpk::grouped_norm_ws_bytes(dtype, g));
@@ -237,7 +245,7 @@ dp_status dp_grouped_clipped_sum_noise(void* stream, const void* A, const void* 
                                        float* out) {
   if (!A || !G || !segments || !c || !out) return DP_ERR_NULL;
   const dpk::GroupedArgs g{segments, R, E, B, d, p};
-  dp_status s = check_grouped(dtype, g);
+  dp_status s = check_grouped(dtype, g, dpk::GroupedCall::sum);
   if (s != DP_OK) return s;
   if (!aligned(A, 16) || !aligned(G, 16) || !aligned(segments, 8) || !aligned(c, 4) || !aligned(out, 4))
     return DP_ERR_ALIGN;

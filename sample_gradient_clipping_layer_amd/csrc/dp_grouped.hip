@@ -1801,6 +1801,11 @@ struct MatmulPlan {
   int bm;
   int64_t ks, kper;
 };
+// A grid of 256-thread workgroups, rounded up to the XCDs, has fewer than 2^32 threads.
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 8;
+int64_t matmul_items(int64_t bm, int64_t R, int64_t E, int64_t N, int64_t ks) {
+  return (R / bm + E) * ((N + 127) / 128) * ks;
+}
 MatmulPlan matmul_plan(int dtype, int64_t R, int64_t E, int64_t K, int64_t N) {
   const bool bf16 = dtype == 1, dma = dma_ok(dtype, {K, N});
   MatmulPlan best{128, 1, K};
@@ -1809,6 +1814,7 @@ MatmulPlan matmul_plan(int dtype, int64_t R, int64_t E, int64_t K, int64_t N) {
   const double k32 = std::ceil((double)K / 32);
   double best_us = 1e30;
   auto consider = [&](int bm, int bn, int64_t ks, int64_t kper, double chunk_us, double item_us, int per_cu) {
+    if (bm == 32 && matmul_items(bm, R, E, N, ks) > kMaxGrid) return;
     const double tiles = ((double)R / bm + 0.5 * (double)std::min(E, R)) * (double)((N + bn - 1) / bn) * (double)ks;
     // workgroups that share a CU share its matrix cores
     const double share = tiles <= 256 ? 1.0 / per_cu : 1.0;
@@ -1880,8 +1886,10 @@ struct NormPlan {
 };
 NormPlan norm_plan(int dtype, const GroupedArgs& g) {
   const int64_t avg = g.R / (g.E * g.B), ts = dtype == 1 ? norm_tile<bf16s>() : norm_tile<float>();
-  if (avg < 64) return NormPlan{true, 32, 1 + (avg + 15) / 16};
-  return NormPlan{false, ts, std::max<int64_t>(1, std::min<int64_t>(16, (3 * avg + ts - 1) / ts))};
+  // row tiles whose grid takes at least one workgroup each, else packed tiles, whose workgroups go over the items
+  const int64_t most = kMaxGrid / ((g.R / ts + g.E * g.B + 31) / 32 * 32);
+  if (avg < 64 || most < 1) return NormPlan{true, 32, 1 + (std::min<int64_t>(avg, 63) + 15) / 16};
+  return NormPlan{false, ts, std::max<int64_t>(1, std::min({(int64_t)16, most, (3 * avg + ts - 1) / ts}))};
 }
 int64_t piece_slots(const GroupedArgs& g) { return g.R / kPieceRows + g.E * g.B; }
 
@@ -1891,6 +1899,7 @@ struct SumPlan {
   bool big, pieces, dma, fused;
   int64_t mt, nt, ks;
 };
+constexpr int64_t kMaxSumItems = (int64_t)1 << 23;  // (expert, split, tile) items of a sum: an XCD's share is an int
 // The items of the XCD with the most of them.
 int64_t most_items(int64_t pairs, int64_t tiles) {
   int most = 0;
@@ -1916,7 +1925,8 @@ SumPlan sum_plan(int dtype, const GroupedArgs& g) {
     // 32-row chunks and a fixed part, as measured; then the traffic of the splits' sums and their reduce launch
     const double slots = big ? 256 : 512, item_us = big ? 20 : 6;
     const double chunk_us = big ? (pieces ? 1.1 : 1.7) : dtype == 1 ? (pieces ? 1.3 : 2.5) : dma ? 4.0 : 6.5;
-    for (int64_t ks = 1; ks <= 64 && (ks == 1 || ks * 2 <= chunks); ks = ks < 4 ? ks + 1 : ks * 3 / 2) {
+    for (int64_t ks = 1; ks <= 64 && (ks == 1 || (ks * 2 <= chunks && g.E * ks * s.mt * s.nt < kMaxSumItems));
+         ks = ks < 4 ? ks + 1 : ks * 3 / 2) {
       const double items = (double)(8 * most_items(g.E * ks, s.mt * s.nt));
       const double us = std::ceil(items / slots) * (std::ceil((double)chunks / ks) * chunk_us + item_us) +
                         (ks > 1 ? ks * out_us + 14.0 : 0.0);
@@ -2103,18 +2113,13 @@ hipError_t launch_grouped_sum(hipStream_t st, int dtype, const GroupedArgs& g, c
   return launch_split_reduce(st, a.ks, a.part, g.E * g.d, g.p, na, out);
 }
 
-bool grouped_fits(int dtype, const GroupedArgs& g) {
-  constexpr int64_t kMax = ((int64_t)1 << 32) / 512;
-  const int64_t cols = (std::max(g.d, g.p) + 127) / 128;
-  if ((g.R / 32 + g.E) * cols + 8 >= kMax) return false;
-  for (int tr = 0; tr < 2; ++tr) {
-    const MatmulPlan m = matmul_plan(dtype, g.R, g.E, tr ? g.p : g.d, tr ? g.d : g.p);
-    if ((g.R / m.bm + g.E) * cols * m.ks + 8 >= kMax) return false;
-  }
-  const NormPlan n = norm_plan(dtype, g);
-  if ((g.R / n.ts + g.E * g.B + 32) * n.J >= kMax || g.R / 32 + g.E * g.B + 8 >= kMax) return false;
-  const SumPlan s = sum_plan(dtype, g);
-  return g.E * s.ks * (s.mt * s.nt + 8) < kMax;
+bool grouped_fits(const GroupedArgs& g, GroupedCall call, int dtype) {
+  if (call == GroupedCall::norm) return true;  // the plan takes any size
+  if (call == GroupedCall::sum) return g.E * ((g.d + 127) / 128) * ((g.p + 127) / 128) < kMaxSumItems;
+  const bool tr = call == GroupedCall::matmul_transposed;
+  const int64_t N = tr ? g.d : g.p;
+  const MatmulPlan m = matmul_plan(dtype, g.R, g.E, tr ? g.p : g.d, N);
+  return m.bm == 256 || matmul_items(m.bm, g.R, g.E, N, m.ks) <= kMaxGrid;
 }
 
 }  // namespace dpk

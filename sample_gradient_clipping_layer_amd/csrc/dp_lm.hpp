@@ -82,6 +82,7 @@ size_t grouped_norm_ws_bytes(int dtype, const GroupedArgs& g);
 hipError_t launch_grouped_sum(hipStream_t st, int dtype, const GroupedArgs& g, const void* A, const void* G,
                               const float* c, void* ws, const NoiseArgs& na, float* out);
 size_t grouped_sum_ws_bytes(int dtype, const GroupedArgs& g);
-bool grouped_fits(int dtype, const GroupedArgs& g);
+enum class GroupedCall { matmul, matmul_transposed, norm, sum };
+bool grouped_fits(const GroupedArgs& g, GroupedCall call, int dtype);  // a launch of the call takes these sizes
 
 }  // namespace dpk
