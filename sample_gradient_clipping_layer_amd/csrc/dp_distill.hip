@@ -149,6 +149,10 @@ __device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t i) {
   return a.teacher_bf16 ? to_f32(static_cast<const bf16s*>(a.teacher)[i]) : static_cast<const float*>(a.teacher)[i];
 }
 
+// The maximum over the used places. A NaN counts as the largest: a maximum that
+// passed it over would leave a token whose teacher is all NaN without a place.
+__device__ __forceinline__ float teacher_max(float m, float t) { return fmaxf(m, t == t ? t : INFINITY); }
+
 // A token's weight and the place of its first K that this thread holds, read
 // ahead of the student's statistics.
 struct FirstPlace {
@@ -175,11 +179,11 @@ __device__ float token_loss(const DistillArgs& a, int64_t row, const FirstPlace&
   const float inv_tau = 1.0f / a.tau;
   float tm = -INFINITY, z0 = 0.0f;
   if (fp.id >= 0 && fp.id < a.V) {
-    tm = fmaxf(tm, fp.teacher);
+    tm = teacher_max(tm, fp.teacher);
     z0 = to_f32(z[fp.id]);
   }
   for (int64_t k = threadIdx.x + NT; k < a.K; k += NT)
-    if (id[k] >= 0 && id[k] < a.V) tm = fmaxf(tm, teacher_at(a, row * a.K + k));
+    if (id[k] >= 0 && id[k] < a.V) tm = teacher_max(tm, teacher_at(a, row * a.K + k));
   tm = block_max<NT>(tm, red);
   if (tm == -INFINITY) return 0.0f;  // no used place
   float total = 0.f, s = 0.f;
@@ -299,7 +303,7 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
     float tm = -INFINITY;
     if (f != 0.0f)
       for (int k = threadIdx.x; k < K; k += kDt)
-        if (id[k] >= 0 && id[k] < a.V) tm = fmaxf(tm, teacher_at(a, row * a.K + k));
+        if (id[k] >= 0 && id[k] < a.V) tm = teacher_max(tm, teacher_at(a, row * a.K + k));
     tm = block_max<kDt>(tm, red);
     const bool any = f != 0.0f && tm != -INFINITY;
     float total = 0.f;
