@@ -478,7 +478,7 @@ size_t dp_rms_norm_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t
  *  logits   [B, T, V], dtype, 16-byte aligned.
  *  ids      [B, T, K] int64; teacher [B, T, K], teacher_dtype (DP_F32 or
  *           DP_BF16). 1 <= K <= 2048.
- *  tau      temperature, finite, > 0.
+ *  tau      temperature, 2^-63 to 2^63.
  *  weight   [B, T] fp32, or NULL (1 everywhere).
  *  loss     [B] fp32.
  *  lse      [B, T] fp32: log sum_j exp(logits_j / tau), for the backward pass.

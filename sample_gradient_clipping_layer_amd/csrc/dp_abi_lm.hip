@@ -53,7 +53,7 @@ size_t rms_ws_bytes(int64_t B, int64_t T, int64_t d) {
 dp_status check_distill(int64_t B, int64_t T, int64_t V, int64_t K, float tau) {
   if (B < 1 || T < 1 || V < 1 || K < 1 || K > dpk::kDistillMaxTop) return DP_ERR_SHAPE;
   if (B >= kMaxDim || T >= kMaxDim || V >= kMaxDim || B * T > kMaxElems / V) return DP_ERR_SHAPE;
-  if (!finite(tau) || !(tau > 0.0f)) return DP_ERR_VALUE;
+  if (!(tau >= 0x1p-63f && tau <= 0x1p63f)) return DP_ERR_VALUE;  // 1 / tau and tau^2 inside fp32's range
   return DP_OK;
 }
 

@@ -1,6 +1,6 @@
-"""The sizes that the dp_grouped_* calls state as their limits, from both
-sides, without a GPU: a call of valid sizes gets as far as its misaligned
-pointer, one past a limit is refused for its shape."""
+"""The limits that the language-model calls state, from both sides, without a
+GPU: a call of valid sizes and values gets as far as its misaligned pointer,
+one past a limit is refused for its shape or value."""
 from __future__ import annotations
 
 import os
@@ -10,7 +10,7 @@ import pytest
 import sample_gradient_clipping_layer_amd as dpc
 
 FAKE = 0x100000  # aligned, never dereferenced
-SHAPE, ALIGN = dpc.DP_ERR_SHAPE, dpc.DP_ERR_ALIGN
+SHAPE, ALIGN, VALUE = dpc.DP_ERR_SHAPE, dpc.DP_ERR_ALIGN, dpc.DP_ERR_VALUE
 
 
 @pytest.fixture(scope="module")
@@ -90,3 +90,19 @@ def test_workspace_of_sizes_that_one_call_refuses(lib, dt):
     no_sum = lib.dp_grouped_workspace_bytes(dt, 1000, 1 << 23, 1, 1, 1)
     assert 4 * 1000 < no_sum  # the norm's
     assert lib.dp_grouped_workspace_bytes(dt, (1 << 30) + 1, 8, 4, 64, 64) == 0
+
+
+def test_temperatures(lib):
+    """From 2^-63 to 2^63: outside, the temperature's inverse or its square
+    leaves fp32's range (a loss of NaN at 1e-39 and of 0 at 1e-38)."""
+    def loss(tau):
+        return lib.dp_distill_loss(None, FAKE + 8, FAKE, FAKE, 1, 0, 2, 3, 50, 4, tau, None, None, 0, FAKE, FAKE)
+
+    def back(tau):
+        return lib.dp_distill_loss_backward(None, FAKE + 8, FAKE, FAKE, 1, 0, 2, 3, 50, 4, tau, None, None, FAKE, FAKE)
+
+    for f in (loss, back):
+        for tau in (2.0 ** -63, 1e-6, 1.0, 1e6, 2.0 ** 63):
+            assert f(tau) == ALIGN, tau
+        for tau in (1e-39, 1e-38, 2.0 ** -64, 2.0 ** 64, 3e38):
+            assert f(tau) == VALUE, tau
