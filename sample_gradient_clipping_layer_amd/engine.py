@@ -47,6 +47,7 @@ class _Layer:
         self.module = module
         self.a = None   # the module's input of the last forward pass
         self.g = None   # dL/d(output) of the last backward pass
+        self.passed = True  # that forward pass has had its backward pass
         self.segments = None  # ExpertLinear: its rows' (expert, sample) ranges
 
 
@@ -132,11 +133,12 @@ class PrivacyEngine:
     @staticmethod
     def _forward_hook(L):
         def hook(module, inputs, kwargs, output):  # arguments by position or by name
-            if L.a is not None and L.g is None:
+            if L.a is not None and not L.passed:
                 raise RuntimeError("a module ran twice in one forward pass")
             a = inputs[0] if inputs else kwargs["input" if "input" in kwargs else "x"]
             L.a = a.detach()
             L.g = None
+            L.passed = False
             if isinstance(module, ExpertLinear):
                 L.segments = inputs[1] if len(inputs) > 1 else kwargs["segments"]
             elif isinstance(module, RMSNorm):
@@ -148,6 +150,7 @@ class PrivacyEngine:
         def hook(module, grad_input, grad_output):
             g = grad_output[0]  # None: an RMSNorm of which only the sum was used
             L.g = None if g is None else g.detach()
+            L.passed = True
         return hook
 
     def detach(self):

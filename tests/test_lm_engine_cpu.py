@@ -194,3 +194,25 @@ def test_views_off_a_16_byte_boundary_reach_the_calls_aligned(plain_calls, monke
     z = _off(torch.ones(2, 3, 5)).requires_grad_()
     lay.distillation_loss(z, torch.zeros(2, 3, 1, dtype=torch.int64), torch.zeros(2, 3, 1)).sum().backward()
     assert "loss" in seen and z.grad.shape == z.shape
+
+
+@pytest.mark.parametrize("use", ["y", "s", "both"])
+def test_a_batch_left_out_does_not_count_as_a_second_run(plain_calls, use):
+    """Forward and backward without a step (a batch that is thrown away), then
+    the next batch, also where only the norm's sum enters the loss; a forward
+    pass without its backward is still told from it."""
+    m = RMSNorm(4)
+    engine = PrivacyEngine(m, C=1.0, sigma=0.0)
+    g = torch.Generator().manual_seed(2)
+    for _ in range(3):
+        x, r = torch.randn(2, 3, 4, generator=g).requires_grad_(), torch.randn(2, 3, 4, generator=g)
+        y, s = m(x, r)
+        (y if use == "y" else s if use == "s" else y + s).sum().backward()
+    rows = engine._gain_operands(engine.layers[0])[1]
+    v = (x + r).detach().double()
+    want = (v * torch.rsqrt((v * v).mean(-1, keepdim=True) + 1e-6)).sum(1) * (use != "s")
+    assert (rows[:, 0].double() - want).abs().max() < 1e-5
+    m(x, r)
+    with pytest.raises(RuntimeError, match="twice"):
+        m(x, r)
+    engine.detach()
