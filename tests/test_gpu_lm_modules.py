@@ -140,3 +140,94 @@ def test_norm_over_an_offset_view():
         got.append((y.detach(), s.detach(), xx.grad, m.weight.grad))
     for u, v in zip(*got):
         assert torch.equal(u, v)
+
+
+# ---- the norm's outputs over its inputs
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [96, 333, 1280, 4099, 20000])
+def test_norm_outputs_over_inputs(dtype, d):
+    """Every alias that the header allows: out and sum_out over x and residual
+    each way round, dx over dy and over dsum."""
+    dt, g = L.DT[dtype], L.gen(d)
+    rows = 9
+    x, r = L.randn(g, rows, d, dtype=dt), L.randn(g, rows, d, scale=2.0, dtype=dt)
+    gain = 1 + L.randn(g, d, scale=0.3)
+    out, s = torch.empty_like(x), torch.empty_like(x)
+    dpc.dp_rms_norm(x, gain, 1e-6, out, residual=r, sum_out=s)
+    for o, k in ((None, "x"), (None, "r"), ("x", None), ("r", None), ("x", "r"), ("r", "x")):
+        t = {"x": x.clone(), "r": r.clone(), None: torch.empty_like(x)}
+        o_t, s_t = (torch.empty_like(x) if o is None else t[o]), (torch.empty_like(x) if k is None else t[k])
+        dpc.dp_rms_norm(t["x"], gain, 1e-6, o_t, residual=t["r"], sum_out=s_t)
+        assert torch.equal(o_t, out) and torch.equal(s_t, s), (o, k)
+        for n in {"x", "r"} - {o, k}:
+            assert torch.equal(t[n], x if n == "x" else r)
+    dy, dsum = L.randn(g, 3, 3, d, scale=0.1, dtype=dt), L.randn(g, 3, 3, d, scale=0.2, dtype=dt)
+    s3 = s.view(3, 3, d)
+    dx, gr = torch.empty_like(s3), torch.empty(3, d, device="cuda")
+    dpc.dp_rms_norm_backward(dy, s3, gain, 1e-6, dx=dx, dsum=dsum, gain_rows=gr)
+    for over in ("dy", "dsum"):
+        t = {"dy": dy.clone(), "dsum": dsum.clone()}
+        gr2 = torch.empty_like(gr)
+        dpc.dp_rms_norm_backward(t["dy"], s3, gain, 1e-6, dx=t[over], dsum=t["dsum"], gain_rows=gr2)
+        assert torch.equal(t[over], dx) and torch.equal(gr2, gr), over
+
+
+# ---- a bf16 model's step from the operands it kept
+
+
+def test_bf16_model_against_gradients_of_its_own_operands():
+    """Norms and clipped gradients of every layer of a bf16 language model,
+    from its layers' inputs and output gradients in 64 bits; the norms' gains
+    from the sums that their forward passes gave, not from the library's rows."""
+    from test_gpu_lm_engine import B, E, _data, _Model
+    data = _data(6)
+    model = _Model(7, dtype=torch.bfloat16).cuda()
+    x, expert_ids, ids, teacher, weight = (t.cuda() for t in data)
+    sums = {}
+    for m in (model.norm, model.norm2):
+        m.register_forward_hook(lambda m, args, out: sums.__setitem__(m, (out[1] if isinstance(out, tuple) else args[0])
+                                                                      .detach().clone()))
+    engine = PrivacyEngine(model, C=0.7, sigma=0.0)
+    distillation_loss(model(x.bfloat16(), expert_ids), ids, teacher, 2.0, weight).sum().backward()
+    names = {id(p): n for n, p in model.named_parameters()}
+    per, err = {}, {}  # parameter -> per-sample gradients [B, ...] and their error bounds
+    for layer in engine.layers:
+        m, a, g = layer.module, layer.a.double(), layer.g.double()
+        if isinstance(m, RMSNorm):
+            _, rows, _, bound = L.rms_backward(layer.g, sums[m], None, m.weight.detach(), m.eps)
+            per[names[id(m.weight)]], err[names[id(m.weight)]] = rows, bound
+        elif isinstance(m, ExpertLinear):
+            ends = layer.segments.tolist()
+            full = torch.zeros(B, *m.weight.shape, dtype=torch.float64, device="cuda")
+            mag = torch.zeros_like(full)
+            for k in range(E * B):
+                i, j = ends[k], ends[k + 1]
+                full[k % B, k // B] = g[i:j].T @ a[i:j]
+                mag[k % B, k // B] = g[i:j].abs().T @ a[i:j].abs()
+            per[names[id(m.weight)]], err[names[id(m.weight)]] = full, 64 * L.U * mag
+        else:
+            gt = g.transpose(1, 2).contiguous()
+            per[names[id(m.weight)]] = torch.matmul(gt, a)
+            err[names[id(m.weight)]] = 64 * L.U * torch.matmul(gt.abs(), a.abs())
+            if m.bias is not None:
+                per[names[id(m.bias)]], err[names[id(m.bias)]] = g.sum(1), 64 * L.U * g.abs().sum(1)
+    assert set(per) == set(names.values())
+    want = torch.sqrt(sum((v ** 2).flatten(1).sum(1) for v in per.values()))
+    # a sample's norm moves by the length of its gradients' errors at most; the ghost sums add up to d + p = 64 products
+    # and 36 pairs of positions of each layer: 512 u of what they add, which the layers' magnitudes bound
+    mags = torch.sqrt(sum(((err[n] / (64 * L.U)) ** 2).flatten(1).sum(1) for n in per if "norm" not in n))
+    bn = torch.sqrt(sum((v ** 2).flatten(1).sum(1) for v in err.values())) + 512 * L.U * (mags ** 2 / want + want)
+    norms = engine.step(0)
+    L.check(norms, want, bn, "norms")
+    c = torch.clamp(0.7 / want, max=1.0)
+    assert (c < 1).any()
+    for n, p in model.named_parameters():
+        cc = c.view(B, *[1] * p.dim())
+        grad = (cc * per[n]).sum(0) / B
+        rel = (bn / want).view(B, *[1] * p.dim())
+        bound = (cc * (err[n] + (rel + (B + 16) * L.U) * (per[n].abs() + err[n] / (64 * L.U)))).sum(0) / B
+        half = L.half(p.dtype)
+        L.check(p.grad, grad, (1 + half) * bound + half * grad.abs() + 1e-37, n)
+    engine.detach()
