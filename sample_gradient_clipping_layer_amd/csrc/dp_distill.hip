@@ -340,7 +340,7 @@ __global__ __launch_bounds__(kDt) void k_distill_backward(DistillArgs a) {
       pv[u] = 0.f;
       if (any && k < K && ids[k] >= v0 && ids[k] < v1) pv[u] = to_f32(z[ids[k]]);
     }
-    if (K > 0) __syncthreads();
+    __syncthreads();  // every logit of a used word is read
     // ---- p_j f over the split
     auto p_of = [&](float zz) {
       return any ? f * exp2_hw(__builtin_fmaf(zz - m, inv_tau, -shift) * kLog2e) : 0.0f;

@@ -231,3 +231,54 @@ def test_bf16_model_against_gradients_of_its_own_operands():
         half = L.half(p.dtype)
         L.check(p.grad, grad, (1 + half) * bound + half * grad.abs() + 1e-37, n)
     engine.detach()
+
+
+# ---- norms beside convolutions
+
+
+@pytest.mark.parametrize("conv_input", ["library-unfold", "folded", "unfolded"])
+def test_norms_share_the_clipping_of_convolutions(conv_input):
+    """A convolution (by each of its routes), a norm over its channels and a
+    linear layer: one norm per sample over all three, against one backward pass
+    per example in 64 bits."""
+    torch.manual_seed(4)
+    B, C = 4, 8
+
+    class Net(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.conv = torch.nn.Conv2d(3, C, 3, padding=1)
+            self.norm = torch.nn.RMSNorm(C)
+            self.own = RMSNorm(C)
+            self.head = torch.nn.Linear(C, 5)
+
+        def forward(self, x):
+            h = self.norm(self.conv(x).flatten(2).transpose(1, 2))
+            if h.is_cuda:
+                y, s = self.own(torch.tanh(h), h)
+            else:
+                s = torch.tanh(h) + h
+                y = s * torch.rsqrt((s * s).mean(-1, keepdim=True) + self.own.eps) * self.own.weight
+            return self.head(y + s).square().mean((1, 2))
+
+    model = Net()
+    x = torch.randn(B, 3, 6, 5)
+    ref = Net().double()
+    ref.load_state_dict(model.state_dict())
+    ref.norm.eps = torch.finfo(torch.float32).eps
+    per = []
+    for i in range(B):
+        per.append(torch.autograd.grad(ref(x[i:i + 1].double()).sum(), list(ref.parameters())))
+    norms = torch.stack([torch.sqrt(sum((v ** 2).sum() for v in gs)) for gs in per])
+    bound = float(norms.median())
+    c = torch.clamp(bound / norms, max=1.0)
+    model.cuda()
+    engine = PrivacyEngine(model, C=bound, sigma=0.0, conv_input=conv_input)
+    model(x.cuda()).sum().backward()
+    got = engine.step(0)
+    # fp32 through the forward and backward pass, against 64 bits: the tolerances of the engine's other tests
+    assert torch.allclose(got.double().cpu(), norms, rtol=1e-4)
+    for k, p in enumerate(model.parameters()):
+        want = sum(c[i] * per[i][k] for i in range(B)) / B
+        assert (p.grad.double().cpu() - want).abs().max() <= 1e-3 * want.abs().max() + 1e-7, k
+    engine.detach()
