@@ -282,3 +282,55 @@ def test_norms_share_the_clipping_of_convolutions(conv_input):
         want = sum(c[i] * per[i][k] for i in range(B)) / B
         assert (p.grad.double().cpu() - want).abs().max() <= 1e-3 * want.abs().max() + 1e-7, k
     engine.detach()
+
+
+# ---- modules in a captured graph
+
+
+def test_modules_captured_and_replayed():
+    """Norm, experts and loss, forward and backward, captured once and replayed
+    over changed inputs and another routing: the eager bits, with eager work in
+    between."""
+    from sample_gradient_clipping_layer_amd.layers import route
+    g = L.gen(31)
+    B, T, D, H, E, V, K = 3, 5, 40, 72, 4, 61, 6
+    norm, up, head = RMSNorm(D).cuda(), ExpertLinear(E, D, H, device="cuda"), L.randn(g, H, V, scale=0.2)
+    params = [norm.weight, up.weight]
+    teacher = L.randn(g, B, T, K)
+
+    def fresh(seed):
+        h = L.gen(seed)
+        experts = torch.randint(-1, E, (B, T, 1), generator=h)
+        return L.randn(h, B, T, D), L.randn(h, B, T, D), experts.cuda(), torch.randint(-1, V, (B, T, K), generator=h).cuda()
+
+    x, r, experts, ids = fresh(0)
+
+    def work():
+        y, s = norm(x, residual=r)
+        order, seg = route(experts, E)
+        rows = up(y.reshape(-1, D)[order], seg)
+        back = torch.empty_like(order).scatter_(0, order, torch.arange(B * T, device="cuda"))
+        logits = torch.matmul(torch.tanh(rows[back]), head).view(B, T, V)
+        loss = distillation_loss(logits, ids, teacher, 1.5)
+        return [loss.detach(), s.detach(), *torch.autograd.grad(loss.sum() + s.square().sum() * 0.01, params)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for seed in (1, 2, 3, 0):
+        for static, new in zip((x, r, experts, ids), fresh(seed)):
+            static.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        want = work()
+        torch.cuda.synchronize()
+        for k, (u, v) in enumerate(zip(kept, want)):
+            assert torch.equal(u, v), k
