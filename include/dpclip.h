@@ -429,7 +429,9 @@ size_t dp_conv_workspace_bytes(const dp_conv2d* conv, dp_dtype dtype, int64_t B,
  *   s = x + residual      u = s / sqrt(mean(s^2) + eps)      out = u * gain
  *
  * in fp32, each output rounded once to dtype (out is formed from the sum
- * before its rounding to dtype). A row of zeros gives zeros when eps > 0.
+ * before its rounding to dtype). A row of zeros gives zeros when eps > 0. The
+ * sum of squares is an fp32 value too: rows whose elements pass about 1e18
+ * overflow it, and eps = 0 needs elements of 1e-18 or more.
  *
  *  x, residual  [rows, d], dtype; residual may be NULL (s = x).
  *  gain         [d], gain_dtype (DP_F32 or DP_BF16).
@@ -471,9 +473,9 @@ size_t dp_rms_norm_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t
  *
  * with p = softmax(logits[b][t] / tau) over the V words and q the softmax of
  * the token's used teacher logits / tau. Place k of a token is used when
- * 0 <= ids < V and its teacher logit is not -inf; places naming the same word
- * add up. A token without a used place, or with weight 0, adds 0 whatever its
- * logits hold.
+ * 0 <= ids < V and its teacher logit is not -inf (a NaN is used, and makes the
+ * loss NaN); places naming the same word are terms of their own. A token
+ * without a used place, or with weight 0, adds 0 whatever its logits hold.
  *
  *  logits   [B, T, V], dtype, 16-byte aligned.
  *  ids      [B, T, K] int64; teacher [B, T, K], teacher_dtype (DP_F32 or

@@ -1196,9 +1196,9 @@ __device__ __forceinline__ Emit emit_at(const GSumArgs& a, int64_t e, int64_t sp
 // come free: uneven experts even out, and the workgroups share operand tiles
 // in their L2. (Which workgroup forms an item does not enter its result.)
 //
-// 32768 rows over 8 experts of 32 samples, 1280 x 5120: 570 to 700 us by the
-// factors (590 with all of them 1), 0.6 to 0.75 PFLOP/s; the matrix cores are
-// busy a third of the cycles. The rest is the loads (110 us, also from L2), the
+// 32768 rows over 8 experts of 32 samples, 1280 x 5120: 550 to 615 us call
+// after call, whatever the factors (650 to 710 as single calls in a trace), 0.7
+// to 0.78 PFLOP/s; the matrix cores are busy a third of the cycles. The rest is the loads (110 us, also from L2), the
 // rescale (90 us where every sample clips), the writing of the fp32 tiles
 // (70 us), a piece's unused rows (an eighth here) and a last round of items
 // that does not fill the GPU (splitting those over K gained nothing: the items
@@ -1796,7 +1796,11 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 // splits' partial products and their joining launch. 256 x 256 tiles (bf16)
 // read the fewest operand bytes per product; 128 x 128 tiles run two to a CU;
 // tiles of 32 rows waste little on experts with few rows, and K can be split
-// for them, so that single tokens' weights are read by the whole GPU.
+// for them, so that single tokens' weights are read by the whole GPU. The wide
+// tile takes up to 64 experts, one a lane (32768 rows of 1280 x 1280: 188 us over
+// 64 experts, 193 us over 65 on 128 x 128 tiles). Widths without 16-byte vectors
+// have the 128 x 128 tile alone (8192 rows over 8 experts, 1281 x 5119: 290 us,
+// 117 at 1280 x 5120; 8 rows, 5119 x 517: 83 us, 15 at 5120 x 512).
 struct MatmulPlan {
   int bm;
   int64_t ks, kper;
@@ -1879,7 +1883,10 @@ hipError_t matmul_t(hipStream_t st, int dtype, MatmulArgs a) {
 }
 
 // The norm's kernel by the average rows per segment, and the workgroups per
-// row tile (enough for segments three times as long as the average).
+// row tile (enough for segments three times as long as the average). The sizes
+// of single segments are known on the device only: a routing that sends 16384
+// rows to one of 1024 segments takes the packed tiles (1280 + 1280 bf16: 5.6 ms,
+// 61 us dealt evenly; its pairs' products alone are 0.67 TFLOP).
 struct NormPlan {
   bool packed;
   int64_t ts, J;

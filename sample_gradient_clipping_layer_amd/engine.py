@@ -80,7 +80,8 @@ class PrivacyEngine:
     its per-sample gradient would go unclipped.
 
     mode: the per-layer path rule ('ghost-mixed', 'ghost', 'explicit',
-    'time'). conv_input: 'library-unfold' (the default: the library writes
+    'time') of the linear and convolution layers; expert layers have the ghost
+    norm alone. conv_input: 'library-unfold' (the default: the library writes
     each Conv2d input's unfolding, and the layers share the multi-layer
     calls), 'folded' (the library takes each Conv2d input as it is and forms
     the unfolded rows in its kernels, one call per Conv2d layer; no unfolded

@@ -185,9 +185,9 @@ def distillation_loss(logits, ids, teacher, temperature: float = 1.0, weight=Non
         loss[b] = tau^2 * sum_t weight[b, t] * KL(q || p)
 
     p = softmax(logits / tau) over the vocabulary, q the softmax of the
-    token's used teacher logits / tau. logits [B, T, V]; ids [B, T, K] int64,
-    -1 where a place is unused; teacher [B, T, K]; weight [B, T] float32 or
-    None. Gradients flow to logits only. ``distillation_loss(...).sum()
+    token's used teacher logits / tau (a word named twice is two terms of the
+    sum). logits [B, T, V]; ids [B, T, K] int64, -1 where a place is unused;
+    teacher [B, T, K]; weight [B, T] float32 or None. Gradients flow to logits only. ``distillation_loss(...).sum()
     .backward()`` is what PrivacyEngine's backward pass asks for."""
     return _Distill.apply(logits, ids.contiguous(), teacher.detach().contiguous(), float(temperature),
                           None if weight is None else weight.detach().float().contiguous())
