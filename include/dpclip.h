@@ -430,8 +430,8 @@ size_t dp_conv_workspace_bytes(const dp_conv2d* conv, dp_dtype dtype, int64_t B,
  *
  * in fp32, each output rounded once to dtype (out is formed from the sum
  * before its rounding to dtype). A row of zeros gives zeros when eps > 0. The
- * sum of squares is an fp32 value too: rows whose elements pass about 1e18
- * overflow it, and eps = 0 needs elements of 1e-18 or more.
+ * sum of squares is an fp32 value too: elements up to 1e17 do not overflow it,
+ * and eps = 0 needs an element of 1e-18 or more in the row.
  *
  *  x, residual  [rows, d], dtype; residual may be NULL (s = x).
  *  gain         [d], gain_dtype (DP_F32 or DP_BF16).

@@ -99,3 +99,28 @@ def test_eight_million_experts():
     grads, mags = _range_grads(A, G, counts)
     cc = c.double()
     L.check(out, cc * grads, 8 * L.U * cc * mags + 1e-37, "sum")
+
+
+def test_the_most_rows_and_ranges():
+    """2^30 rows in 2^24 ranges of 64: row tiles would need more workgroups
+    than a grid has, so the norms go over packed tiles."""
+    B, n, dt = 1 << 24, 64, torch.bfloat16
+    R = B * n
+    seg = torch.arange(B + 1, device="cuda") * n
+    g = _cuda_gen(1)
+    A, G = (torch.randn(R, 1, generator=g, device="cuda", dtype=dt) for _ in range(2))
+    sq = torch.empty(B, device="cuda")
+    dpc.dp_grouped_norm(A, G, seg, sq)
+    for i in range(0, B, B // 8):  # a part of the samples at a time
+        rows = slice(i * n, (i + B // 8) * n)
+        prod = (A[rows].double() * G[rows].double()).view(-1, n)
+        L.check(sq[i:i + B // 8], prod.sum(1) ** 2, prod.abs().sum(1) ** 2 * 514 * L.U + 1e-37, "sqnorm")
+    c = torch.zeros(B, device="cuda")
+    c[-3:] = torch.tensor([0.3, 1.0, 0.7])
+    out = torch.empty(1, 1, 1, device="cuda")
+    dpc.dp_grouped_clipped_sum_noise(A, G, seg, c, 1.0, 0.0, 1.0, 0, 0, 0, out)
+    terms = (A[-3 * n:].double() * G[-3 * n:].double()).view(3, n) * c[-3:, None].double()
+    L.check(out.view(()), terms.sum(), (3 * n + 64) * L.U * terms.abs().sum(), "sum")
+    y = torch.empty_like(A)
+    dpc.dp_grouped_matmul(A, torch.full((1, 1, 1), 1.5, device="cuda", dtype=dt), seg, y)
+    assert torch.equal(y, A * 1.5)  # one product, exact in fp32, rounded once
