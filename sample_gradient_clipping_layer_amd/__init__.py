@@ -825,7 +825,8 @@ def _grouped_layer(A, G, segments, vec, name, stream):
 def dp_grouped_norm(A, G, segments, sqnorm, accumulate: bool = False, workspace=None, stream=None):
     """Per-sample squared gradient norms of an expert layer over all its
     experts into sqnorm [B], from its rows A [R, d] and output gradients
-    G [R, p], sorted by (expert, sample) as segments [E*B + 1] says."""
+    G [R, p], sorted by (expert, sample) as segments [E*B + 1] says (B is
+    sqnorm's length; E follows from both)."""
     st, dt, R, E, B, d, p = _grouped_layer(A, G, segments, sqnorm, "sqnorm", stream)
     ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_grouped_workspace_bytes(dt, R, E, B, d, p), A.device, stream)
     _check("dp_grouped_norm", lib().dp_grouped_norm(
