@@ -15,7 +15,7 @@ Operators and their directions (``case["op"]``):
                     entropy and its top alternatives (and what the gradient
                     takes: the largest logit and the log of the sum beside it)
   logprob-backward  the gradient of the first two over the whole vocabulary
-  balance-forward   a router's balance loss per sample, and its rows per expert
+  balance-forward   a router's balance loss per sample, its rows per expert and its tokens
   balance-backward  its gradient
 """
 import math
@@ -223,12 +223,14 @@ def prepare(case, seed):
         s["loss"] = torch.empty(B, device="cuda", dtype=torch.float32)
         if op == "balance-forward":
             s["counts"] = torch.empty(B, E, device="cuda", dtype=torch.int64)
+            s["tokens"] = torch.empty(B, device="cuda", dtype=torch.int64)
             if own:
                 s["ws"] = _scratch(_library().dp_balance_workspace_bytes(_code(dt), B, T, E))
         else:
             s["counts"] = torch.zeros(B, E + 1, device="cuda", dtype=torch.int64).scatter_add_(
                 1, torch.where(used, ids, torch.full_like(ids, E)).view(B, -1),
                 torch.ones(B, T * top, device="cuda", dtype=torch.int64))[:, :E].contiguous()
+            s["tokens"] = used[..., 0].sum(1)
             s["dloss"] = 0.01 * (0.5 + torch.rand(B, generator=g, device="cuda"))
             s["grad"] = torch.empty_like(s["logits"])
     return s
@@ -262,8 +264,8 @@ def _run_own(s):
         dpc.dp_embedding_norm(s["G"], s["ids"], s["order"], s["starts"], s["sq"], scale=case["scale"],
                               workspace=s["ws"])
         dpc.dp_clip_factors(s["sq"], s["C"], s["c"])
-        dpc.dp_embedding_clipped_sum_noise(s["G"], s["order"], s["starts"], s["c"], s["C"], 0.0, float(case["B"]), 0,
-                                           0, 0, s["out"], scale=case["scale"], workspace=s["ws"])
+        dpc.dp_embedding_clipped_sum_noise(s["G"], s["ids"], s["order"], s["starts"], s["c"], s["C"], 0.0,
+                                           float(case["B"]), 0, 0, 0, s["out"], scale=case["scale"], workspace=s["ws"])
         return s["sq"], s["c"], s["out"]
     if op == "ln-forward":
         dpc.dp_layer_norm(s["x"], s["gain"], s["bias"], EPS, s["out"], residual=s["residual"], sum_out=s["sum"])
@@ -282,9 +284,9 @@ def _run_own(s):
                                       entropy=s["entropy"], dentropy=s["dentropy"])
         return s["grad"]
     if op == "balance-forward":
-        dpc.dp_balance_loss(s["logits"], s["ids"], s["loss"], s["counts"], workspace=s["ws"])
-        return s["loss"], s["counts"]
-    dpc.dp_balance_loss_backward(s["logits"], s["ids"], s["counts"], s["grad"], dloss=s["dloss"])
+        dpc.dp_balance_loss(s["logits"], s["ids"], s["loss"], s["counts"], s["tokens"], workspace=s["ws"])
+        return s["loss"], s["counts"], s["tokens"]
+    dpc.dp_balance_loss_backward(s["logits"], s["ids"], s["counts"], s["tokens"], s["grad"], dloss=s["dloss"])
     return s["grad"]
 
 
@@ -361,7 +363,7 @@ def _run_plain(s):
         counts = counts.scatter_add_(1, place, torch.ones_like(place))[:, :E]
         mean = (p * used[..., None]).sum(1) / tokens
         share = counts.float() / counts.sum(1, keepdim=True).float()
-        return E * (share * mean).sum(1), counts
+        return E * (share * mean).sum(1), counts, used.sum(1)
     # a share more for all experts changes nothing: where they are nearly even only the differences are left
     above = s["counts"] - s["counts"].amin(1, keepdim=True)
     share = above.float() / s["counts"].sum(1, keepdim=True).float()
@@ -448,7 +450,7 @@ def exact(case, seed):
     if op == "balance-forward":
         share = counts.to(f64) / rows
         loss = [E * torch.dot(share[b], p[b][used[b]].mean(0)) for b in range(B)]
-        return torch.stack(loss), counts
+        return torch.stack(loss), counts, torch.tensor([used[b].nonzero().numel() for b in range(B)], device="cuda")
     # differences to the rarest expert: the gradient does not change with a share that all experts have more
     a = (counts - counts.amin(1, keepdim=True)).to(f64) / rows * (E * s["dloss"].to(f64) / used.sum(1))[:, None]
     inner = torch.matmul(p, a[..., None])
