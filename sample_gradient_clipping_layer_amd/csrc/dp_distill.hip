@@ -21,6 +21,7 @@
 // nothing is atomic.
 #include "dp_common.hpp"
 #include "dp_lm.hpp"
+#include "dp_vocab.hpp"
 
 #include <float.h>
 
@@ -29,12 +30,7 @@ namespace dpk {
 namespace {
 
 constexpr int kDt = 256;  // threads per block
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFarLse = 1024.0f;  // from here on the backward forms a row's statistics again
-
-// 2^x by the hardware's instruction: within one step, results below 2^-126
-// flushed to 0 (they are terms of sums of order 1, or probabilities).
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // (m, s): s = sum of 2^((z - m) k) over the values seen, k = log2(e)/tau. The
 // initial maximum is finite, so that no difference of infinities arises.
@@ -90,60 +86,6 @@ __device__ __forceinline__ Run block_join(Run r, float k, float* red) {
   for (int w = 0; w < NT / 64; ++w) s += red[2 * w + 1] * exp2_hw((red[2 * w] - m) * k);
   return Run{m, s};
 }
-template <int NT>
-__device__ __forceinline__ float block_max(float v, float* red) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int w = 1; w < NT / 64; ++w) v = fmaxf(v, red[w]);
-  return v;
-}
-template <int NT>
-__device__ __forceinline__ float block_add(float v, float* red) {
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int w = 1; w < NT / 64; ++w) v += red[w];
-  return v;
-}
-
-template <int P>
-__device__ __forceinline__ void unpack16(u32x4 raw, float* v) {
-  if constexpr (P == 8) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(raw[e] << 16);
-      v[2 * e + 1] = __uint_as_float(raw[e] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(raw[e]);
-  }
-}
-
-// Elements [v0, v1) of a row as single elements up to the first 16-byte
-// boundary, 16-byte vectors, and single elements after the last: rows of odd
-// V start anywhere.
-template <typename T>
-struct Span {
-  int64_t head, vecs, tail0;  // [v0, head) single, head + P*i vectors, [tail0, v1) single
-  __device__ __forceinline__ Span(const T* row, int64_t v0, int64_t v1) {
-    constexpr int P = elem_traits<T>::per16;
-    const int64_t mis = (int64_t)((reinterpret_cast<uintptr_t>(row + v0) & 15) / sizeof(T));
-    head = v0 + (mis ? P - mis : 0);
-    if (head > v1) head = v1;
-    vecs = (v1 - head) / P;
-    tail0 = head + vecs * P;
-  }
-};
-
 // Teacher logit i, fp32 or bf16.
 __device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t i) {
   return a.teacher_bf16 ? to_f32(static_cast<const bf16s*>(a.teacher)[i]) : static_cast<const float*>(a.teacher)[i];
