@@ -467,6 +467,193 @@ dp_status dp_rms_norm_backward(void* stream, const void* dy, const void* s, cons
 size_t dp_rms_norm_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t d);
 
 /*
+ * Layer norm with the residual's addition, over the last dimension:
+ *
+ *   s = x + residual    u = (s - mean(s)) / sqrt(var(s) + eps)    out = u * gain + bias
+ *
+ * with the variance of d values (not d - 1), in fp32, each output rounded once
+ * to dtype (out is formed from the sum before its rounding to dtype). A row of
+ * one value gives the bias when eps > 0.
+ *
+ *  x, residual  [rows, d], dtype; residual may be NULL (s = x).
+ *  gain, bias   [d], gain_dtype (DP_F32 or DP_BF16); bias may be NULL (0).
+ *  d            1 <= d <= 32768.
+ *  eps          finite, >= 0; with 0 a row of one value gives NaN.
+ *  out          [rows, d], dtype; may be x or residual.
+ *  sum_out      [rows, d], dtype: s (what the backward pass reads); may be
+ *               NULL, x or residual, not out.
+ * Tensors aligned to their element. Elements up to 1e17 do not overflow the
+ * sum of squares.
+ */
+dp_status dp_layer_norm(void* stream, const void* x, const void* residual, const void* gain, const void* bias,
+                        dp_dtype dtype, dp_dtype gain_dtype, int64_t rows, int64_t d, float eps, void* out,
+                        void* sum_out);
+
+/*
+ * Its backward pass, with the gain's and the bias's gradient of every sample
+ * (each the linear layer A = 1 [B, 1, 1], G = rows [B, 1, d] of dp_ghost_norm
+ * and dp_clipped_sum_noise):
+ *
+ *   h = dy * gain    dx = dsum + (h - mean(h) - u * mean(h * u)) / sqrt(var(s) + eps)
+ *   gain_rows[b] = sum_t dy[b][t] * u[b][t]    bias_rows[b] = sum_t dy[b][t]
+ *
+ *  dy, s, dsum  [B, T, d], dtype. s: the forward's sum; dsum: the gradient
+ *               that reaches s past the norm (the residual stream), or NULL.
+ *  dx           [B, T, d], dtype, or NULL: the gradient of x and of residual;
+ *               may be dy or dsum.
+ *  gain_rows, bias_rows  [B, d] fp32, or NULL; of dx and these one is required.
+ *  workspace    at least dp_layer_norm_workspace_bytes(...) bytes when
+ *               gain_rows or bias_rows is not NULL.
+ */
+dp_status dp_layer_norm_backward(void* stream, const void* dy, const void* s, const void* dsum, const void* gain,
+                                 dp_dtype dtype, dp_dtype gain_dtype, int64_t B, int64_t T, int64_t d, float eps,
+                                 void* workspace, size_t ws_bytes, void* dx, float* gain_rows, float* bias_rows);
+size_t dp_layer_norm_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t d);
+
+/*
+ * Rows of a table of V words: out[n] = scale * weight[ids[n]], rounded once to
+ * dtype. An id outside [0, V) is a dropped token: its row is 0.
+ *
+ *  ids      [N] int64.
+ *  weight   [V, d], weight_dtype; out [N, d], dtype. Aligned to their element.
+ *  N, V     below 2^31; 1 <= d <= 2^20.
+ */
+dp_status dp_embedding(void* stream, const int64_t* ids, const void* weight, dp_dtype dtype, dp_dtype weight_dtype,
+                       int64_t N, int64_t V, int64_t d, float scale, void* out);
+
+/*
+ * The tokens in the order of their words, for the table's gradient: order [N]
+ * int64 holds the tokens sorted by word, those of one word ascending, dropped
+ * ones last; the places of word w are [starts[w], starts[w + 1]) (starts:
+ * [V + 1] int64, starts[V] the number of tokens that are not dropped).
+ *
+ *  workspace  at least dp_embedding_order_workspace_bytes(N, V) bytes.
+ */
+dp_status dp_embedding_order(void* stream, const int64_t* ids, int64_t N, int64_t V, void* workspace, size_t ws_bytes,
+                             int64_t* order, int64_t* starts);
+size_t dp_embedding_order_workspace_bytes(int64_t N, int64_t V);
+
+/*
+ * Per-sample squared gradient norms of the table, from the output gradients G
+ * [B, T, d] of dp_embedding on ids [B, T]:
+ *
+ *   sqnorm[b] (+)= scale^2 * sum_w || sum_{t: ids[b][t] = w} G[b][t] ||^2
+ *
+ *  G        [B, T, d], dtype, aligned to its element; B*T below 2^31.
+ *  ids, order  as dp_embedding_order took and left them (N = B*T). With other
+ *           contents the result means nothing; nothing outside is accessed.
+ *  sqnorm   [B] fp32, overwritten (accumulate == 0) or added to.
+ *  workspace  at least dp_embedding_workspace_bytes(...) bytes.
+ */
+dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const int64_t* ids, const int64_t* order,
+                            int64_t B, int64_t T, int64_t V, int64_t d, float scale, void* workspace, size_t ws_bytes,
+                            float* sqnorm, int32_t accumulate);
+
+/*
+ * Clipped, noised mean gradient of the whole table:
+ *
+ *   out[w] = (scale * sum_b c[b] * sum_{t: ids[b][t] = w} G[b][t] + (sigma*C) * z[w]) * (1/denom)
+ *
+ * as dp_clipped_sum_noise forms it for a layer of V rows; a word without a
+ * token gets the noise alone.
+ *
+ *  G, ids, order, B, T, V, d, workspace  as in dp_embedding_norm; starts as
+ *           dp_embedding_order left it; also ceil(V/4)*d < 2^32.
+ *  c, C, sigma, denom, seed, layer_id, step  as in dp_clipped_sum_noise.
+ *  out      [V, d] fp32 (the layout of a torch Embedding's weight).
+ */
+dp_status dp_embedding_clipped_sum_noise(void* stream, const void* G, dp_dtype dtype, const int64_t* ids,
+                                         const int64_t* order, const int64_t* starts, int64_t B, int64_t T, int64_t V,
+                                         int64_t d, float scale, const float* c, float C, float sigma, float denom,
+                                         uint64_t seed, uint32_t layer_id, uint32_t step, void* workspace,
+                                         size_t ws_bytes, float* out);
+/* Workspace bytes that dp_embedding_norm and dp_embedding_clipped_sum_noise
+ * need (the larger of the two). Returns 0 for invalid arguments. */
+size_t dp_embedding_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t V, int64_t d);
+
+/*
+ * Log probabilities of given tokens under softmax(logits / tau), the entropy
+ * of that distribution and its top alternatives, a row of V logits each:
+ *
+ *   logp = log p_target       entropy = -sum_j p_j log p_j
+ *   top_ids, top_logp: the K most probable words, largest first (of equal
+ *   logits the lower word first), and their log probabilities
+ *
+ * A target outside [0, V) has logp 0. A row whose logits are all -inf has no
+ * distribution: logp and top_logp are -inf, the entropy is 0 (its top words
+ * are the first K). A row with a NaN or +inf gives NaN in logp, entropy and
+ * top_logp (a NaN comes first among its top words).
+ *
+ *  logits   [rows, V], dtype, 16-byte aligned; targets [rows] int64.
+ *  rows, V  below 2^31.
+ *  tau      temperature, 2^-63 to 2^63.
+ *  K        0 (no top alternatives) to 256, at most V.
+ *  logp     [rows] fp32.
+ *  stats    [rows, 2] fp32, for the backward pass: the largest logit m and
+ *           log sum_j exp((logits_j - m) / tau).
+ *  entropy  [rows] fp32, or NULL.
+ *  top_ids  [rows, K] int64, top_logp [rows, K] fp32; NULL when K is 0.
+ */
+dp_status dp_token_logprob(void* stream, const void* logits, const int64_t* targets, dp_dtype dtype, int64_t rows,
+                           int64_t V, float tau, int64_t K, float* logp, float* stats, float* entropy,
+                           int64_t* top_ids, float* top_logp);
+
+/*
+ * Their gradient, the output gradient G of the layer that made the logits:
+ *
+ *   grad_j = (dlogp * (1[j = target] - p_j) - dentropy * p_j * (log p_j + entropy)) / tau
+ *
+ * A row whose dlogp (0 for a target outside [0, V)) and dentropy are 0 gets 0
+ * whatever its logits hold, and so does one without a distribution.
+ *
+ *  stats, entropy  as dp_token_logprob left them (entropy: when dentropy is set).
+ *  dlogp, dentropy [rows] fp32, one of them may be NULL (0).
+ *  grad     [rows, V], dtype, 16-byte aligned; may be logits, and overlaps
+ *           nothing else.
+ */
+dp_status dp_token_logprob_backward(void* stream, const void* logits, const int64_t* targets, dp_dtype dtype,
+                                    int64_t rows, int64_t V, float tau, const float* stats, const float* dlogp,
+                                    const float* entropy, const float* dentropy, void* grad);
+
+/*
+ * A router's balance loss, one value per sample, with its rows per expert:
+ *
+ *   loss[b] = E * sum_e f_e * P_e
+ *   f_e = counts[b][e] / sum_e' counts[b][e']    P_e = mean of softmax(logits[b][t])_e over the used tokens t
+ *
+ * counts[b][e] is the number of places of sample b that name expert e. A place
+ * is used when its id lies in [0, E), a token when one of its places is; a
+ * sample without a used token has loss 0. (Even routing gives 1.) Tokens that
+ * are not used count for nothing, whatever their logits hold.
+ *
+ *  logits   [B, T, E], dtype, aligned to its element; 1 <= E <= 1024.
+ *  ids      [B, T, top] int64, as route() and the expert layers take them;
+ *           1 <= top <= 1024; T*top below 2^31.
+ *  loss     [B] fp32; counts [B, E] int64; tokens [B] int64: the used tokens.
+ *  workspace  at least dp_balance_workspace_bytes(...) bytes (may be NULL when
+ *           that is 0).
+ */
+dp_status dp_balance_loss(void* stream, const void* logits, const int64_t* ids, dp_dtype dtype, int64_t B, int64_t T,
+                          int64_t E, int64_t top, void* workspace, size_t ws_bytes, float* loss, int64_t* counts,
+                          int64_t* tokens);
+size_t dp_balance_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t E);
+
+/*
+ * Its gradient (the counts are constants, as the routing is a choice):
+ *
+ *   grad[b][t][e] = p_e * (a_e - sum_e' p_e' a_e')    a_e = dloss[b] * E * f_e / tokens[b]
+ *
+ * and 0 for a token that is not used.
+ *
+ *  counts, tokens  as dp_balance_loss left them.
+ *  dloss    [B] fp32, or NULL (1 everywhere).
+ *  grad     [B, T, E], dtype, aligned to its element; may be logits.
+ */
+dp_status dp_balance_loss_backward(void* stream, const void* logits, const int64_t* ids, dp_dtype dtype, int64_t B,
+                                   int64_t T, int64_t E, int64_t top, const int64_t* counts, const int64_t* tokens,
+                                   const float* dloss, void* grad);
+
+/*
  * Distillation loss from a teacher's top logits, one value per sample:
  *
  *   loss[b] = tau^2 * sum_t weight[b][t] * sum_k q_k (log q_k - log p_{ids_k})

@@ -38,6 +38,21 @@ The functions mirror the C ABI in ``include/dpclip.h``:
     dp_rms_norm(x, gain, eps, out, residual=None, sum_out=None)
     dp_rms_norm_backward(dy, s, gain, eps, dx=None, dsum=None, gain_rows=None, workspace=None)
     dp_rms_norm_workspace_bytes(dtype, B, T, d) -> int
+    dp_layer_norm(x, gain, bias, eps, out, residual=None, sum_out=None)
+    dp_layer_norm_backward(dy, s, gain, eps, dx=None, dsum=None, gain_rows=None, bias_rows=None, workspace=None)
+    dp_layer_norm_workspace_bytes(dtype, B, T, d) -> int
+    dp_embedding(ids, weight, out, scale=1.0)
+    dp_embedding_order(ids, V, order, starts, workspace=None)
+    dp_embedding_order_workspace_bytes(N, V) -> int
+    dp_embedding_norm(G, ids, order, starts, sqnorm, scale=1.0, accumulate=False, workspace=None)
+    dp_embedding_clipped_sum_noise(G, ids, order, starts, c, C, sigma, denom, seed, layer_id, step, out, scale=1.0,
+                                   workspace=None)
+    dp_embedding_workspace_bytes(dtype, B, T, V, d) -> int
+    dp_token_logprob(logits, targets, tau, logp, stats, entropy=None, top_ids=None, top_logp=None)
+    dp_token_logprob_backward(logits, targets, tau, stats, grad, dlogp=None, entropy=None, dentropy=None)
+    dp_balance_loss(logits, ids, loss, counts, tokens, workspace=None)
+    dp_balance_loss_backward(logits, ids, counts, tokens, grad, dloss=None)
+    dp_balance_workspace_bytes(dtype, B, T, E) -> int
     dp_distill_loss(logits, ids, teacher, tau, loss, lse, weight=None, workspace=None)
     dp_distill_loss_backward(logits, ids, teacher, tau, lse, grad, weight=None, dloss=None)
     dp_distill_workspace_bytes(dtype, B, T, V, K) -> int
@@ -76,6 +91,11 @@ EXPORTS = ("dp_ghost_norm", "dp_ghost_norm_layers", "dp_ghost_norm_clip_layers",
            "dp_workspace_bytes", "dp_choose_path", "dp_status_string", "dp_abi_version",
            "dp_conv_norm", "dp_conv_clipped_sum_noise", "dp_conv_workspace_bytes", "dp_unfold2d",
            "dp_rms_norm", "dp_rms_norm_backward", "dp_rms_norm_workspace_bytes",
+           "dp_layer_norm", "dp_layer_norm_backward", "dp_layer_norm_workspace_bytes",
+           "dp_embedding", "dp_embedding_order", "dp_embedding_order_workspace_bytes", "dp_embedding_norm",
+           "dp_embedding_clipped_sum_noise", "dp_embedding_workspace_bytes",
+           "dp_token_logprob", "dp_token_logprob_backward",
+           "dp_balance_loss", "dp_balance_loss_backward", "dp_balance_workspace_bytes",
            "dp_distill_loss", "dp_distill_loss_backward", "dp_distill_workspace_bytes",
            "dp_grouped_matmul", "dp_grouped_norm", "dp_grouped_clipped_sum_noise", "dp_grouped_workspace_bytes")
 
@@ -179,6 +199,35 @@ def _declare(lib):
     lib.dp_rms_norm_backward.restype = c_i32
     lib.dp_rms_norm_workspace_bytes.argtypes = [c_i32, c_i64, c_i64, c_i64]
     lib.dp_rms_norm_workspace_bytes.restype = sz
+    lib.dp_layer_norm.argtypes = [vp, vp, vp, vp, vp, c_i32, c_i32, c_i64, c_i64, f, vp, vp]
+    lib.dp_layer_norm.restype = c_i32
+    lib.dp_layer_norm_backward.argtypes = [vp, vp, vp, vp, vp, c_i32, c_i32, c_i64, c_i64, c_i64, f, vp, sz, vp, fp, fp]
+    lib.dp_layer_norm_backward.restype = c_i32
+    lib.dp_layer_norm_workspace_bytes.argtypes = [c_i32, c_i64, c_i64, c_i64]
+    lib.dp_layer_norm_workspace_bytes.restype = sz
+    lib.dp_embedding.argtypes = [vp, vp, vp, c_i32, c_i32, c_i64, c_i64, c_i64, f, vp]
+    lib.dp_embedding.restype = c_i32
+    lib.dp_embedding_order.argtypes = [vp, vp, c_i64, c_i64, vp, sz, vp, vp]
+    lib.dp_embedding_order.restype = c_i32
+    lib.dp_embedding_order_workspace_bytes.argtypes = [c_i64, c_i64]
+    lib.dp_embedding_order_workspace_bytes.restype = sz
+    lib.dp_embedding_norm.argtypes = [vp, vp, c_i32, vp, vp, c_i64, c_i64, c_i64, c_i64, f, vp, sz, fp, c_i32]
+    lib.dp_embedding_norm.restype = c_i32
+    lib.dp_embedding_clipped_sum_noise.argtypes = [vp, vp, c_i32, vp, vp, vp, c_i64, c_i64, c_i64, c_i64, f, fp, f, f, f,
+                                                   c_u64, c_u32, c_u32, vp, sz, fp]
+    lib.dp_embedding_clipped_sum_noise.restype = c_i32
+    lib.dp_embedding_workspace_bytes.argtypes = [c_i32, c_i64, c_i64, c_i64, c_i64]
+    lib.dp_embedding_workspace_bytes.restype = sz
+    lib.dp_token_logprob.argtypes = [vp, vp, vp, c_i32, c_i64, c_i64, f, c_i64, fp, fp, fp, vp, fp]
+    lib.dp_token_logprob.restype = c_i32
+    lib.dp_token_logprob_backward.argtypes = [vp, vp, vp, c_i32, c_i64, c_i64, f, fp, fp, fp, fp, vp]
+    lib.dp_token_logprob_backward.restype = c_i32
+    lib.dp_balance_loss.argtypes = [vp, vp, vp, c_i32, c_i64, c_i64, c_i64, c_i64, vp, sz, fp, vp, vp]
+    lib.dp_balance_loss.restype = c_i32
+    lib.dp_balance_loss_backward.argtypes = [vp, vp, vp, c_i32, c_i64, c_i64, c_i64, c_i64, vp, vp, fp, vp]
+    lib.dp_balance_loss_backward.restype = c_i32
+    lib.dp_balance_workspace_bytes.argtypes = [c_i32, c_i64, c_i64, c_i64]
+    lib.dp_balance_workspace_bytes.restype = sz
     lib.dp_distill_loss.argtypes = [vp, vp, vp, vp, c_i32, c_i32, c_i64, c_i64, c_i64, c_i64, f, fp, vp, sz, fp, fp]
     lib.dp_distill_loss.restype = c_i32
     lib.dp_distill_loss_backward.argtypes = [vp, vp, vp, vp, c_i32, c_i32, c_i64, c_i64, c_i64, c_i64, f, fp, fp,
@@ -729,6 +778,215 @@ def dp_rms_norm_backward(dy, s, gain, eps: float, dx=None, dsum=None, gain_rows=
     _check("dp_rms_norm_backward", lib().dp_rms_norm_backward(
         st, dy.data_ptr(), s.data_ptr(), _addr(dsum), gain.data_ptr(), code, _dtype_code(gain), B, T, d, eps, ws, nbytes,
         _addr(dx), _addr(gain_rows)))
+
+
+def dp_layer_norm_workspace_bytes(dtype: int, B: int, T: int, d: int) -> int:
+    return int(lib().dp_layer_norm_workspace_bytes(dtype, B, T, d))
+
+
+def dp_layer_norm(x, gain, bias, eps: float, out, residual=None, sum_out=None, stream=None):
+    """out = (s - mean(s)) / sqrt(var(s) + eps) * gain + bias over the last
+    dimension, s = x (+ residual); s itself into sum_out. gain and bias (or
+    None) are both float32 or both bfloat16."""
+    import torch
+    if x.dim() < 1 or x.numel() < 1:
+        raise ValueError("x must have at least one element")
+    dt = _act_dtypes(x, "x")
+    d = x.shape[-1]
+    st = _lm_tensors(stream, ("x", x, dt, None), ("residual", residual, dt, x.shape), ("out", out, dt, x.shape),
+                     ("sum_out", sum_out, dt, x.shape), ("gain", gain, (torch.float32, torch.bfloat16), (d,)),
+                     ("bias", bias, (gain.dtype,), (d,)))
+    if sum_out is not None and sum_out.data_ptr() == out.data_ptr():
+        raise ValueError("sum_out and out must be different tensors")
+    _check("dp_layer_norm", lib().dp_layer_norm(st, x.data_ptr(), _addr(residual), gain.data_ptr(), _addr(bias),
+                                                _dtype_code(x), _dtype_code(gain), x.numel() // d, d, eps,
+                                                out.data_ptr(), _addr(sum_out)))
+
+
+def dp_layer_norm_backward(dy, s, gain, eps: float, dx=None, dsum=None, gain_rows=None, bias_rows=None, workspace=None,
+                           stream=None):
+    """Backward pass of dp_layer_norm from s [B, T, d] (or [B, d]): dx (the
+    gradient of x and of residual, dsum joined in), gain_rows and bias_rows
+    [B, d], the gain's and the bias's gradient of every sample; each may be None."""
+    import torch
+    if s.dim() < 2 or s.numel() < 1:
+        raise ValueError("s [B, ..., d] with at least one element expected")
+    dt = _act_dtypes(s, "s")
+    B, d = s.shape[0], s.shape[-1]
+    T = s.numel() // (B * d)
+    f32 = (torch.float32,)
+    st = _lm_tensors(stream, ("s", s, dt, None), ("dy", dy, dt, s.shape), ("dsum", dsum, dt, s.shape),
+                     ("dx", dx, dt, s.shape), ("gain", gain, (torch.float32, torch.bfloat16), (d,)),
+                     ("gain_rows", gain_rows, f32, (B, d)), ("bias_rows", bias_rows, f32, (B, d)))
+    if dx is None and gain_rows is None and bias_rows is None:
+        raise ValueError("dx, gain_rows or bias_rows is required")
+    code = _dtype_code(s)
+    ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_layer_norm_workspace_bytes(code, B, T, d)
+                                      if gain_rows is not None or bias_rows is not None else 0, s.device, stream)
+    _check("dp_layer_norm_backward", lib().dp_layer_norm_backward(
+        st, dy.data_ptr(), s.data_ptr(), _addr(dsum), gain.data_ptr(), code, _dtype_code(gain), B, T, d, eps, ws, nbytes,
+        _addr(dx), _addr(gain_rows), _addr(bias_rows)))
+
+
+def dp_embedding(ids, weight, out, scale: float = 1.0, stream=None):
+    """out[..., :] = scale * weight[ids] for ids [...] int64 and weight [V, d]
+    (float32 or bfloat16, as out is); 0 for an id outside [0, V)."""
+    import torch
+    if weight.dim() != 2 or ids.numel() < 1:
+        raise ValueError(f"weight [V, d] and at least one id expected, got {tuple(weight.shape)} and {tuple(ids.shape)}")
+    V, d = weight.shape
+    dt = _act_dtypes(out, "out")
+    st = _lm_tensors(stream, ("ids", ids, (torch.int64,), None), ("out", out, dt, (*ids.shape, d)),
+                     ("weight", weight, (torch.float32, torch.bfloat16), None))
+    _check("dp_embedding", lib().dp_embedding(st, ids.data_ptr(), weight.data_ptr(), _dtype_code(out),
+                                              _dtype_code(weight), ids.numel(), V, d, scale, out.data_ptr()))
+
+
+def dp_embedding_order_workspace_bytes(N: int, V: int) -> int:
+    return int(lib().dp_embedding_order_workspace_bytes(N, V))
+
+
+def dp_embedding_order(ids, V: int, order, starts, workspace=None, stream=None):
+    """The tokens sorted by word: order [ids.numel()] and starts [V + 1] (word
+    w's places are starts[w] .. starts[w + 1]), all int64; dropped tokens last."""
+    import torch
+    i64, N = (torch.int64,), ids.numel()
+    if N < 1:
+        raise ValueError("ids must have at least one element")
+    st = _lm_tensors(stream, ("ids", ids, i64, None), ("order", order, i64, (N,)), ("starts", starts, i64, (V + 1,)))
+    ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_embedding_order_workspace_bytes(N, V), ids.device, stream)
+    _check("dp_embedding_order", lib().dp_embedding_order(st, ids.data_ptr(), N, V, ws, nbytes, order.data_ptr(),
+                                                          starts.data_ptr()))
+
+
+def dp_embedding_workspace_bytes(dtype: int, B: int, T: int, V: int, d: int) -> int:
+    return int(lib().dp_embedding_workspace_bytes(dtype, B, T, V, d))
+
+
+def _embedding_grad(G, ids, order, starts, vec, name, stream, *more):
+    """Checks of a table's output gradients, ids and order, and of the [B] vector `vec`."""
+    import torch
+    if G.dim() < 2 or G.numel() < 1 or ids.shape != G.shape[:-1]:
+        raise ValueError(f"G [B, ..., d] and ids [B, ...] expected, got {tuple(G.shape)} and {tuple(ids.shape)}")
+    dt, i64, N = _act_dtypes(G, "G"), (torch.int64,), ids.numel()
+    B, d, V = G.shape[0], G.shape[-1], starts.numel() - 1
+    st = _lm_tensors(stream, ("G", G, dt, None), ("ids", ids, i64, None), ("order", order, i64, (N,)),
+                     ("starts", starts, i64, (V + 1,)), (name, vec, (torch.float32,), (B,)),
+                     *((n, t, (torch.float32,), (V, d)) for n, t in more))
+    return st, _dtype_code(G), B, N // B, V, d
+
+
+def dp_embedding_norm(G, ids, order, starts, sqnorm, scale: float = 1.0, accumulate: bool = False, workspace=None,
+                      stream=None):
+    """Per-sample squared gradient norms [B] of a table from its output
+    gradients G [B, ..., d] on ids [B, ...]; order and starts as
+    dp_embedding_order left them."""
+    st, dt, B, T, V, d = _embedding_grad(G, ids, order, starts, sqnorm, "sqnorm", stream)
+    ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_embedding_workspace_bytes(dt, B, T, V, d), G.device, stream)
+    _check("dp_embedding_norm", lib().dp_embedding_norm(
+        st, G.data_ptr(), dt, ids.data_ptr(), order.data_ptr(), B, T, V, d, scale, ws, nbytes, sqnorm.data_ptr(),
+        1 if accumulate else 0))
+
+
+def dp_embedding_clipped_sum_noise(G, ids, order, starts, c, C: float, sigma: float, denom: float, seed: int,
+                                   layer_id: int, step: int, out, scale: float = 1.0, workspace=None, stream=None):
+    """Clipped noised mean gradient of a whole table into out [V, d]."""
+    st, dt, B, T, V, d = _embedding_grad(G, ids, order, starts, c, "c", stream, ("out", out))
+    ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_embedding_workspace_bytes(dt, B, T, V, d), G.device, stream)
+    _check("dp_embedding_clipped_sum_noise", lib().dp_embedding_clipped_sum_noise(
+        st, G.data_ptr(), dt, ids.data_ptr(), order.data_ptr(), starts.data_ptr(), B, T, V, d, scale, c.data_ptr(), C,
+        sigma, denom, int(seed) & 0xFFFFFFFFFFFFFFFF, int(layer_id) & 0xFFFFFFFF, int(step) & 0xFFFFFFFF, ws, nbytes,
+        out.data_ptr()))
+
+
+def _logprob(logits, targets, stream, *more):
+    import torch
+    if logits.dim() < 1 or logits.numel() < 1 or targets.shape != logits.shape[:-1]:
+        raise ValueError(f"logits [..., V] and targets [...] expected, got {tuple(logits.shape)} and "
+                         f"{tuple(targets.shape)}")
+    dt, f32 = _act_dtypes(logits, "logits"), (torch.float32,)
+    shape = targets.shape
+    st = _lm_tensors(stream, ("logits", logits, dt, None), ("targets", targets, (torch.int64,), None),
+                     *((n, t, dt, logits.shape) if k < 0 else (n, t, f32, (*shape, k) if k else shape)
+                       for n, t, k in more))
+    V = logits.shape[-1]
+    return st, _dtype_code(logits), logits.numel() // V, V
+
+
+def dp_token_logprob(logits, targets, tau: float, logp, stats, entropy=None, top_ids=None, top_logp=None, stream=None):
+    """Log probabilities logp [...] of targets [...] (int64; outside [0, V): 0)
+    under softmax(logits [..., V] / tau); stats [..., 2] is kept for the
+    backward pass. Also, when given, the distribution's entropy [...] and its K
+    most probable words: top_ids [..., K] int64 and top_logp [..., K]."""
+    import torch
+    if (top_ids is None) != (top_logp is None):
+        raise ValueError("top_ids and top_logp go together")
+    K = 0 if top_ids is None else top_ids.shape[-1] if top_ids.dim() else 0
+    more = [("logp", logp, 0), ("stats", stats, 2), ("entropy", entropy, 0)]
+    if top_ids is not None:
+        if K < 1:
+            raise ValueError("top_ids must have at least one place per token")
+        more.append(("top_logp", top_logp, K))
+    st, dt, rows, V = _logprob(logits, targets, stream, *more)
+    if top_ids is not None:
+        _lm_tensors(stream, ("top_ids", top_ids, (torch.int64,), (*targets.shape, K)))
+    _check("dp_token_logprob", lib().dp_token_logprob(
+        st, logits.data_ptr(), targets.data_ptr(), dt, rows, V, tau, K, logp.data_ptr(), stats.data_ptr(),
+        _addr(entropy), _addr(top_ids), _addr(top_logp)))
+
+
+def dp_token_logprob_backward(logits, targets, tau: float, stats, grad, dlogp=None, entropy=None, dentropy=None,
+                              stream=None):
+    """Gradient of sum(dlogp * logp) + sum(dentropy * entropy) (either may be
+    None) with respect to the logits into grad [..., V], which may be logits
+    itself. entropy, as dp_token_logprob left it, goes with dentropy."""
+    if dlogp is None and dentropy is None:
+        raise ValueError("dlogp or dentropy is required")
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs the entropy")
+    st, dt, rows, V = _logprob(logits, targets, stream, ("stats", stats, 2), ("dlogp", dlogp, 0),
+                               ("entropy", entropy, 0), ("dentropy", dentropy, 0), ("grad", grad, -1))
+    _check("dp_token_logprob_backward", lib().dp_token_logprob_backward(
+        st, logits.data_ptr(), targets.data_ptr(), dt, rows, V, tau, stats.data_ptr(), _addr(dlogp), _addr(entropy),
+        _addr(dentropy), grad.data_ptr()))
+
+
+def dp_balance_workspace_bytes(dtype: int, B: int, T: int, E: int) -> int:
+    return int(lib().dp_balance_workspace_bytes(dtype, B, T, E))
+
+
+def _balance(logits, ids, counts, tokens, stream, *more):
+    import torch
+    if logits.dim() != 3 or ids.dim() != 3 or ids.shape[:2] != logits.shape[:2] or ids.numel() < 1:
+        raise ValueError(f"logits [B, T, E] and ids [B, T, top] expected, got {tuple(logits.shape)} and "
+                         f"{tuple(ids.shape)}")
+    dt, i64 = _act_dtypes(logits, "logits"), (torch.int64,)
+    B, T, E = logits.shape
+    st = _lm_tensors(stream, ("logits", logits, dt, None), ("ids", ids, i64, None), ("counts", counts, i64, (B, E)),
+                     ("tokens", tokens, i64, (B,)),
+                     *((n, t, dt, logits.shape) if n == "grad" else (n, t, (torch.float32,), (B,)) for n, t in more))
+    return st, _dtype_code(logits), B, T, E, ids.shape[2]
+
+
+def dp_balance_loss(logits, ids, loss, counts, tokens, workspace=None, stream=None):
+    """A router's balance loss [B] from its logits [B, T, E] and the experts
+    chosen, ids [B, T, top] int64 (an id outside [0, E) drops that place); also
+    the places that name each expert, counts [B, E], and the tokens with a used
+    place, tokens [B], both int64."""
+    st, dt, B, T, E, top = _balance(logits, ids, counts, tokens, stream, ("loss", loss))
+    ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_balance_workspace_bytes(dt, B, T, E), logits.device, stream)
+    _check("dp_balance_loss", lib().dp_balance_loss(
+        st, logits.data_ptr(), ids.data_ptr(), dt, B, T, E, top, ws, nbytes, loss.data_ptr(), counts.data_ptr(),
+        tokens.data_ptr()))
+
+
+def dp_balance_loss_backward(logits, ids, counts, tokens, grad, dloss=None, stream=None):
+    """Gradient of sum_b dloss[b] * loss[b] (dloss None: of the sum) with
+    respect to the logits into grad [B, T, E], which may be logits itself."""
+    st, dt, B, T, E, top = _balance(logits, ids, counts, tokens, stream, ("grad", grad), ("dloss", dloss))
+    _check("dp_balance_loss_backward", lib().dp_balance_loss_backward(
+        st, logits.data_ptr(), ids.data_ptr(), dt, B, T, E, top, counts.data_ptr(), tokens.data_ptr(), _addr(dloss),
+        grad.data_ptr()))
 
 
 def dp_distill_workspace_bytes(dtype: int, B: int, T: int, V: int, K: int) -> int:

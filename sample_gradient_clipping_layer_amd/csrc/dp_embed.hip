@@ -1,0 +1,739 @@
+// A table of words: the lookup of scaled rows, the order of tokens by word,
+// and the clipping of the table's gradient.
+//
+//   lookup:  out[n] = scale * W[ids[n]]  (0 for an id outside [0, V): a dropped token)
+//   order:   the tokens n sorted by word, tokens of one word ascending, dropped
+//            ones last; word w's places are [starts[w], starts[w + 1])
+//   norm:    sqnorm[b] = scale^2 * sum_w || sum_{t: ids[b][t] = w} G[b][t] ||^2
+//   sum:     out[w] = (scale * sum_{n of w} c[sample of n] * G[n] + (sigma C) z_w) / denom, every word of the table
+//
+// A per-sample gradient of the table has at most T rows that are not 0, so
+// nothing of its size [B][V][d] is ever formed: in the order, the tokens of
+// one (word, sample) are a run of neighbouring places, and the tokens of one
+// word a run of those. All passes are bound by HBM; each reads G once.
+//
+// A run may be long (a frequent word, a batch padded with one word). Sums over
+// long runs take the sums of tiles: a first launch adds up every tile of 16
+// neighbouring places (and of 16 such tiles, and so on) that lies within one
+// run, and what reads a run takes whole tiles from there. Sums are formed in
+// fp32 in an order that the sizes and the ids alone decide; nothing is atomic
+// but the counts of the sort, which are whole numbers.
+//
+// The sort is by digits of the word, least significant first, each digit in a
+// launch of its own: a workgroup ranks the tokens of its tile by digit (within
+// a wave by ballots, in order), and finds where its share of every digit goes
+// from the counts that all workgroups left. Places and starts are checked
+// where they are read: whatever they hold, accesses stay inside the tensors.
+#include "dp_common.hpp"
+#include "dp_lm.hpp"
+#include "dp_noise.hpp"
+#include "dp_rows.hpp"
+
+namespace dpk {
+
+// ---- lookup
+
+// One thread per 16 bytes of out, tokens side by side; four in flight per thread.
+template <typename T, typename WT, bool WHOLE>
+__global__ __launch_bounds__(256) void k_embedding(EmbedArgs a, int vpr, FastDiv by_vpr, int tokens) {
+  constexpr int P = elem_traits<T>::per16, U = 4;
+  const int d = (int)a.d;
+  for (int64_t n0 = (int64_t)blockIdx.x * tokens; n0 < a.N; n0 += (int64_t)gridDim.x * tokens) {
+    const int here = (int)(a.N - n0 < tokens ? a.N - n0 : tokens);
+    const uint32_t work = (uint32_t)here * (uint32_t)vpr;
+    for (uint32_t i0 = threadIdx.x; i0 < work; i0 += U * 256) {
+      int64_t id[U], n[U];
+      int c[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t i = i0 + u * 256 < work ? i0 + u * 256 : i0;
+        const uint32_t t = fast_div(i, by_vpr);
+        n[u] = n0 + t;
+        c[u] = (int)(i - t * (uint32_t)vpr) * P;
+        id[u] = a.ids[n[u]];
+      }
+      float v[U][P];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[u][e] = 0.f;
+        if (id[u] < 0 || id[u] >= a.V) continue;
+        const WT* w = static_cast<const WT*>(a.weight) + id[u] * a.d + c[u];
+        if (WHOLE || c[u] + P <= d) {
+          WT raw[P];
+          __builtin_memcpy(raw, w, sizeof(raw));
+#pragma unroll
+          for (int e = 0; e < P; ++e) v[u][e] = to_f32(raw[e]) * a.scale;
+        } else {
+#pragma unroll
+          for (int e = 0; e < P - 1; ++e)
+            if (c[u] + e < d) v[u][e] = to_f32(w[e]) * a.scale;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i0 + u * 256 >= work) break;
+        T* o = static_cast<T*>(a.out) + n[u] * a.d + c[u];
+        if (WHOLE || c[u] + P <= d) {
+          u32x4 raw;
+          if constexpr (P == 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) raw[e] = pack_bf16(v[u][2 * e], v[u][2 * e + 1]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) raw[e] = __float_as_uint(v[u][e]);
+          }
+          __builtin_memcpy(o, &raw, 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < P - 1; ++e)
+            if (c[u] + e < d) put(o[e], v[u][e]);
+        }
+      }
+    }
+  }
+}
+
+// ---- order
+
+namespace {
+
+constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
+constexpr int kSortMaxDigits = 512;
+
+// How the sort of N ids over V words goes: digits per pass, ids per workgroup.
+struct SortPlan {
+  int passes, bits;
+  int rounds, log_tile;  // ids per thread and, as a power of two, per workgroup
+  int64_t blocks;
+  __host__ __device__ int digits() const { return 1 << bits; }
+  __host__ __device__ int64_t tile() const { return (int64_t)1 << log_tile; }
+};
+
+SortPlan sort_plan(int64_t N, int64_t V) {
+  int bits = 1;
+  while (((int64_t)1 << bits) <= V) ++bits;  // keys 0 .. V (V: dropped)
+  SortPlan p;
+  p.passes = (bits + 8) / 9;
+  p.bits = (bits + p.passes - 1) / p.passes;
+  // tiles of 1024 ids; from 128 workgroups on larger ones, whose ids are read in more rounds
+  p.rounds = 4;
+  p.log_tile = 10;
+  while (p.rounds < 64 && (N + p.tile() - 1) / p.tile() > 128) {
+    p.rounds *= 2;
+    ++p.log_tile;
+  }
+  p.blocks = (N + p.tile() - 1) / p.tile();
+  return p;
+}
+
+__device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V) { return id < 0 || id >= V ? (uint32_t)V : (uint32_t)id; }
+
+}  // namespace
+
+// The first digit's counts of every workgroup's tile; clears the counts of the later passes.
+__global__ __launch_bounds__(kSortThreads) void k_order_count(const int64_t* __restrict__ ids, int64_t N, int64_t V,
+                                                              SortPlan p, uint32_t* __restrict__ counts) {
+  __shared__ uint32_t bins[kSortMaxDigits];
+  const int D = p.digits();
+  for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < (int64_t)(p.passes - 1) * p.blocks * D;
+       i += (int64_t)gridDim.x * kSortThreads)
+    counts[p.blocks * D + i] = 0;
+  for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
+    for (int k = threadIdx.x; k < D; k += kSortThreads) bins[k] = 0;
+    __syncthreads();
+    const int64_t i0 = b * p.tile();
+    for (int r = 0; r < p.rounds; ++r) {
+      const int64_t i = i0 + r * kSortThreads + threadIdx.x;
+      if (i < N) atomicAdd(&bins[key_of(ids[i], V) & (D - 1)], 1u);
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < D; k += kSortThreads) counts[b * D + k] = bins[k];
+    __syncthreads();
+  }
+}
+
+// Exclusive sums down the workgroups, per digit, in place, and each digit's total behind them (many workgroups).
+__global__ __launch_bounds__(64) void k_order_scan(SortPlan p, uint32_t* __restrict__ counts, uint32_t* __restrict__ totals) {
+  const int D = p.digits();
+  const int k = blockIdx.x * 64 + threadIdx.x;
+  if (k >= D) return;
+  uint32_t sum = 0;
+#pragma unroll 8
+  for (int64_t b = 0; b < p.blocks; ++b) {
+    const uint32_t c = counts[b * D + k];
+    counts[b * D + k] = sum;
+    sum += c;
+  }
+  totals[k] = sum;
+}
+
+// One digit's pass: the tokens of a workgroup's tile to their places by that
+// digit, in order. ids_in: the first pass reads the ids themselves; else keys
+// and tokens of the pass before. The next digit is counted on the way, where
+// the tokens go. totals: the counts are sums already (k_order_scan).
+__global__ __launch_bounds__(kSortThreads) void k_order_scatter(const int64_t* __restrict__ ids_in,
+                                                                const uint32_t* __restrict__ keys_in,
+                                                                const uint32_t* __restrict__ toks_in, int64_t N,
+                                                                int64_t V, SortPlan p, int pass,
+                                                                const uint32_t* __restrict__ counts,
+                                                                const uint32_t* __restrict__ totals,
+                                                                uint32_t* __restrict__ next_counts,
+                                                                uint32_t* __restrict__ keys_out,
+                                                                uint32_t* __restrict__ toks_out,
+                                                                int64_t* __restrict__ order) {
+  __shared__ uint32_t seen[kSortWaves][kSortMaxDigits];  // of a wave so far; then where its tokens of a digit go
+  __shared__ uint32_t base[kSortMaxDigits];
+  __shared__ uint32_t scan[kSortThreads];
+  const int D = p.digits(), shift = pass * p.bits;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t b = blockIdx.x;
+  const int64_t w0 = b * p.tile() + (int64_t)wave * 64 * p.rounds;  // this wave's ids, `rounds` times 64 of them
+  for (int k = threadIdx.x; k < kSortWaves * D; k += kSortThreads) seen[k / D][k % D] = 0;
+  // ---- the counts of the digit in earlier workgroups and in all
+  const int per = (D + kSortThreads - 1) / kSortThreads;  // 1 or 2 digits per thread
+  uint32_t before[2] = {0, 0}, total[2] = {0, 0};
+  for (int u = 0; u < per; ++u) {
+    const int k = threadIdx.x * per + u;
+    if (k >= D) break;
+    if (totals) {
+      before[u] = counts[b * D + k];
+      total[u] = totals[k];
+    } else {
+#pragma unroll 8
+      for (int64_t j = 0; j < p.blocks; ++j) {
+        const uint32_t c = counts[j * D + k];
+        total[u] += c;
+        before[u] += j < b ? c : 0u;
+      }
+    }
+  }
+  // ---- exclusive sum over the digits
+  uint32_t mine = total[0] + total[1], run = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t o = __shfl_up(run, off, kWave);
+    if (lane >= off) run += o;
+  }
+  if (lane == 63) scan[wave] = run;
+  __syncthreads();
+  uint32_t at = run - mine;
+  for (int w = 0; w < wave; ++w) at += scan[w];
+  for (int u = 0; u < per; ++u) {
+    const int k = threadIdx.x * per + u;
+    if (k >= D) break;
+    base[k] = at + before[u];
+    at += total[u];
+  }
+  // ---- ranks within the wave, in order: the lanes before this one with its digit, and those of earlier rounds
+  const uint64_t below = lane == 0 ? 0 : (~0ull >> (64 - lane));
+  for (int r = 0; r < p.rounds; ++r) {
+    const int64_t i = w0 + r * 64 + lane;
+    const uint32_t key = i >= N ? 0u : ids_in ? key_of(ids_in[i], V) : keys_in[i];
+    const uint32_t digit = (key >> shift) & (D - 1);
+    uint64_t same = __ballot(i < N);
+    for (int q = 0; q < p.bits; ++q) {
+      const uint64_t has = __ballot((digit >> q) & 1);
+      same &= ((digit >> q) & 1) ? has : ~has;
+    }
+    if (i < N && (same & below) == 0) seen[wave][digit] += (uint32_t)__popcll(same);
+  }
+  __syncthreads();
+  // ---- where each wave's tokens of a digit start
+  for (int k = threadIdx.x; k < D; k += kSortThreads) {
+    uint32_t s = base[k];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = seen[w][k];
+      seen[w][k] = s;
+      s += c;
+    }
+  }
+  __syncthreads();
+  const int next_shift = shift + p.bits;
+  for (int r = 0; r < p.rounds; ++r) {
+    const int64_t i = w0 + r * 64 + lane;
+    const uint32_t key = i >= N ? 0u : ids_in ? key_of(ids_in[i], V) : keys_in[i];
+    const uint32_t digit = (key >> shift) & (D - 1);
+    uint64_t same = __ballot(i < N);
+    for (int q = 0; q < p.bits; ++q) {
+      const uint64_t has = __ballot((digit >> q) & 1);
+      same &= ((digit >> q) & 1) ? has : ~has;
+    }
+    uint32_t to = 0;
+    if (i < N) to = seen[wave][digit] + (uint32_t)__popcll(same & below);
+    __builtin_amdgcn_wave_barrier();  // every lane has read its digit's place before one moves it on
+    if (i < N) {
+      if ((same & below) == 0) seen[wave][digit] = to + (uint32_t)__popcll(same);
+      keys_out[to] = key;
+      if (order) order[to] = toks_in ? toks_in[i] : i;
+      else toks_out[to] = toks_in ? toks_in[i] : (uint32_t)i;
+      if (next_counts) atomicAdd(&next_counts[(int64_t)(to >> p.log_tile) * D + ((key >> next_shift) & (D - 1))], 1u);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// starts[w] = how many keys are smaller than w, by bisection.
+__global__ __launch_bounds__(256) void k_order_starts(const uint32_t* __restrict__ keys, int64_t N, int64_t V,
+                                                      int64_t* __restrict__ starts) {
+  for (int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x; w <= V; w += (int64_t)gridDim.x * 256) {
+    int64_t lo = 0, hi = N;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (keys[mid] < (uint32_t)w) lo = mid + 1;
+      else hi = mid;
+    }
+    starts[w] = lo;
+  }
+}
+
+// ---- sums over runs of places
+
+namespace {
+
+constexpr int kTile = kEmbedTile;
+
+// The token of a place, or -1 if it is none or the place's entry is no token.
+__device__ __forceinline__ int64_t token_at(const EmbedGradArgs& a, int64_t i) {
+  const int64_t n = a.order[i];
+  return n >= 0 && n < a.N ? n : -1;
+}
+
+__device__ __forceinline__ uint32_t sample_of(const EmbedGradArgs& a, int64_t n) { return fast_div((uint32_t)n, a.by_t); }
+
+// What a run of places shares: the word, and for the norm the sample too. Dropped tokens have none.
+template <bool NORM>
+__device__ __forceinline__ int64_t run_of(const EmbedGradArgs& a, int64_t n) {
+  if (n < 0) return -1;
+  const int64_t id = a.ids[n];
+  if (id < 0 || id >= a.V) return -1;
+  return NORM ? id * a.B + sample_of(a, n) : id;
+}
+
+// 16 bytes' worth of columns of one row, in fp32.
+template <typename T, bool WHOLE>
+struct Cols {
+  static constexpr int P = elem_traits<T>::per16;
+  static __device__ __forceinline__ u32x4 fetch(const T* row, int c, int d) {
+    u32x4 raw{0u, 0u, 0u, 0u};
+    if (WHOLE ? c < d : c + P <= d) {
+      __builtin_memcpy(&raw, row + c, 16);
+    } else if (!WHOLE && c < d) {
+#pragma unroll
+      for (int e = 0; e < P - 1; ++e)
+        if (c + e < d) {
+          const uint32_t bits = raw_bits(row[c + e]);
+          if constexpr (P == 8) raw[e >> 1] |= bits << (16 * (e & 1));
+          else raw[e] = bits;
+        }
+    }
+    return raw;
+  }
+  static __device__ __forceinline__ void add(float* acc, u32x4 raw, float f) {
+    if constexpr (P == 8) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[2 * e] = __builtin_fmaf(f, __uint_as_float(raw[e] << 16), acc[2 * e]);
+        acc[2 * e + 1] = __builtin_fmaf(f, __uint_as_float(raw[e] & 0xFFFF0000u), acc[2 * e + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, __uint_as_float(raw[e]), acc[e]);
+    }
+  }
+  // a row of the tiles' sums, fp32
+  static __device__ __forceinline__ void add_sums(float* acc, const float* row, int c, int d) {
+    if (WHOLE ? c < d : c + P <= d) {
+      float v[P];
+      __builtin_memcpy(v, row + c, sizeof(v));
+#pragma unroll
+      for (int e = 0; e < P; ++e) acc[e] += v[e];
+    } else if (!WHOLE && c < d) {
+#pragma unroll
+      for (int e = 0; e < P - 1; ++e)
+        if (c + e < d) acc[e] += row[c + e];
+    }
+  }
+  static __device__ __forceinline__ void put_sums(float* row, const float* acc, int c, int d) {
+    if (WHOLE ? c < d : c + P <= d) {
+      __builtin_memcpy(row + c, acc, 4 * P);
+    } else if (!WHOLE && c < d) {
+#pragma unroll
+      for (int e = 0; e < P - 1; ++e)
+        if (c + e < d) row[c + e] = acc[e];
+    }
+  }
+};
+
+// acc += the rows of places [s, e), weighted by their samples' factors (c != null). Places of one run.
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void add_rows(const EmbedGradArgs& a, float* acc, int64_t s, int64_t e, int col) {
+  using C = Cols<T, WHOLE>;
+  constexpr int U = 4;  // rows in flight
+  const int d = (int)a.d;
+  for (; s < e; s += U) {
+    int64_t n[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) n[u] = s + u < e ? token_at(a, s + u) : -1;
+    u32x4 raw[U];
+    float f[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      raw[u] = u32x4{0u, 0u, 0u, 0u};
+      f[u] = 0.f;
+      if (n[u] >= 0) {
+        raw[u] = C::fetch(static_cast<const T*>(a.G) + n[u] * a.d, col, d);
+        f[u] = a.c ? a.c[sample_of(a, n[u])] : 1.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (n[u] >= 0) C::add(acc, raw[u], f[u]);
+  }
+}
+
+// The same with whole tiles taken from their sums: the ends by places, then
+// by tiles of 16, of 256 and so on, up to the highest level there is.
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void add_run(const EmbedGradArgs& a, float* acc, int64_t s, int64_t e, int col) {
+  using C = Cols<T, WHOLE>;
+  if (a.levels == 0 || e - s < kTile) {
+    add_rows<T, WHOLE>(a, acc, s, e, col);
+    return;
+  }
+  const int64_t up = (s + kTile - 1) / kTile * kTile, down = e / kTile * kTile;
+  if (up >= down) {
+    add_rows<T, WHOLE>(a, acc, s, e, col);
+    return;
+  }
+  add_rows<T, WHOLE>(a, acc, s, up, col);
+  add_rows<T, WHOLE>(a, acc, down, e, col);
+  int64_t lo = up / kTile, hi = down / kTile;
+  for (int l = 0; lo < hi; ++l) {
+    const float* sums = a.sums + a.level_at[l] * a.d;
+    const bool top = l + 1 == a.levels;
+    int64_t in_lo = top ? hi : (lo + kTile - 1) / kTile * kTile, in_hi = top ? hi : hi / kTile * kTile;
+    if (in_lo >= in_hi) in_lo = in_hi = hi;
+#pragma unroll 4
+    for (int64_t i = lo; i < in_lo; ++i) C::add_sums(acc, sums + i * a.d, col, (int)a.d);
+#pragma unroll 4
+    for (int64_t i = in_hi; i < hi; ++i) C::add_sums(acc, sums + i * a.d, col, (int)a.d);
+    lo = in_lo / kTile;
+    hi = in_hi / kTile;
+    if (in_lo >= in_hi) break;
+  }
+}
+
+}  // namespace
+
+// Sums of the tiles of level `l` (of 16^(l+1) places) that lie within one run,
+// a wave for each tile and 64 x 16 bytes' worth of columns.
+template <typename T, bool WHOLE, bool NORM>
+__global__ __launch_bounds__(256) void k_embed_tiles(EmbedGradArgs a, int l, int64_t span, int64_t tiles, int col_waves) {
+  using C = Cols<T, WHOLE>;
+  const int64_t items = tiles * col_waves;
+  const int lane = threadIdx.x & 63;
+  for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < items; item += (int64_t)gridDim.x * 4) {
+    const int64_t tile = item / col_waves;
+    const int col = ((int)(item - tile * col_waves) * 64 + lane) * C::P;
+    const int64_t i0 = tile * span;
+    const int64_t r = run_of<NORM>(a, token_at(a, i0));
+    if (r < 0 || r != run_of<NORM>(a, token_at(a, i0 + span - 1))) continue;
+    float acc[C::P];
+#pragma unroll
+    for (int e = 0; e < C::P; ++e) acc[e] = 0.f;
+    if (l == 0) {
+      add_rows<T, WHOLE>(a, acc, i0, i0 + kTile, col);
+    } else {
+      const float* sums = a.sums + (a.level_at[l - 1] + tile * kTile) * a.d;
+#pragma unroll 4
+      for (int k = 0; k < kTile; ++k) C::add_sums(acc, sums + k * a.d, col, (int)a.d);
+    }
+    C::put_sums(a.sums + (a.level_at[l] + tile) * a.d, acc, col, (int)a.d);
+  }
+}
+
+// Squared norms of the runs that start in a wave's 8 places, each written at
+// the token of the run's first place, 0 at its other tokens'.
+template <typename T, bool WHOLE>
+__global__ __launch_bounds__(256) void k_embed_norm(EmbedGradArgs a) {
+  using C = Cols<T, WHOLE>;
+  constexpr int R = kEmbedNormPlaces;
+  const int lane = threadIdx.x & 63;
+  const int64_t waves = (a.N + R - 1) / R;
+  for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < waves; w += (int64_t)gridDim.x * 4) {
+    const int64_t i0 = w * R;
+    const int m = (int)(a.N - i0 < R ? a.N - i0 : R);  // this wave's places
+    // lane k <= m holds place i0 - 1 + k; further lanes the places behind, to see where the last run ends
+    const int64_t i = i0 - 1 + lane;
+    int64_t n = -1, run = -1;
+    if (i >= 0 && i < a.N) {
+      n = token_at(a, i);
+      run = run_of<true>(a, n);
+    }
+    const int64_t prev = __shfl_up(run, 1, kWave);
+    const uint64_t heads = __ballot(lane > 0 && run >= 0 && run != prev);
+    const uint64_t goes_on = __ballot(lane > 0 && run >= 0 && run == prev);  // same run as the place before
+    for (int k = 0; k < m; ++k) {
+      const int at = k + 1;  // the lane of this place
+      float sq = 0.f;
+      if ((heads >> at) & 1) {
+        // places of the run behind its first, as far as the lanes see
+        const uint64_t rest = goes_on >> at >> 1;
+        int len = 1 + (~rest ? __builtin_ctzll(~rest) : 64);
+        int64_t end = i0 + k + len;
+        if (at + len >= 64) {  // on past the last lane
+          const int64_t mine = __shfl(run, at, kWave);
+          while (end < a.N) {
+            const int64_t j = end + lane;
+            const uint64_t ends = __ballot(j >= a.N || run_of<true>(a, token_at(a, j < a.N ? j : a.N - 1)) != mine);
+            if (ends) {
+              end += __builtin_ctzll(ends);
+              break;
+            }
+            end += 64;
+          }
+        }
+        for (int c0 = 0; c0 < (int)a.d; c0 += 64 * C::P) {
+          float acc[C::P];
+#pragma unroll
+          for (int e = 0; e < C::P; ++e) acc[e] = 0.f;
+          add_run<T, WHOLE>(a, acc, i0 + k, end, c0 + lane * C::P);
+#pragma unroll
+          for (int e = 0; e < C::P; ++e) sq = __builtin_fmaf(acc[e], acc[e], sq);
+        }
+        sq = wave_sum(sq);
+      }
+      const int64_t tok = __shfl(n, at, kWave);
+      if (lane == 0 && tok >= 0) a.token_sq[tok] = sq;
+    }
+  }
+}
+
+// sqnorm[b] (+)= scale^2 * the sum of its tokens' values.
+__global__ __launch_bounds__(256) void k_embed_norm_finish(EmbedGradArgs a) {
+  __shared__ float red[4];
+  for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
+    float s = 0.f;
+    for (int64_t t = threadIdx.x; t < a.T; t += 256) s += a.token_sq[b * a.T + t];
+    s = block_sum<256>(s, red);
+    if (threadIdx.x == 0) {
+      s *= a.scale * a.scale;
+      a.sqnorm[b] = a.accumulate ? a.sqnorm[b] + s : s;
+    }
+    __syncthreads();
+  }
+}
+
+// The clipped, noised mean of 4 neighbouring words (whose noise shares its
+// blocks) and 64 x 4 columns, by a wave.
+template <typename T, bool WHOLE>
+__global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, NoiseArgs na, float* __restrict__ out, int col_waves) {
+  using C = Cols<T, WHOLE>;
+  constexpr int P = C::P;
+  const int lane = threadIdx.x & 63;
+  const int d = (int)a.d;
+  const int64_t groups = (a.V + 3) / 4, items = groups * col_waves;
+  for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < items; item += (int64_t)gridDim.x * 4) {
+    const int64_t g = item / col_waves;
+    const int col = ((int)(item - g * col_waves) * 64 + lane) * P;
+    int64_t st = 0;
+    if (lane < 5 && 4 * g + lane <= a.V) {
+      st = a.starts[4 * g + lane];
+      st = st < 0 ? 0 : st > a.N ? a.N : st;
+    }
+    float acc[4][P];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) acc[k][e] = 0.f;
+      const int64_t s = __shfl(st, k, kWave), e = __shfl(st, k + 1, kWave);
+      if (4 * g + k < a.V && s < e) {
+        add_run<T, WHOLE>(a, acc[k], s, e, col);
+#pragma unroll
+        for (int q = 0; q < P; ++q) acc[k][q] *= a.scale;
+      }
+    }
+    if (na.sc != 0.0f) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const f32x4 z = normals4((uint32_t)g * (uint32_t)d + (uint32_t)(col + e), 2 * na.layer, na.step, 0, na.k0, na.k1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k][e] = noised_mean_spec(acc[k][e], na.sc, z[k], na.inv_denom);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < P; ++e) acc[k][e] *= na.inv_denom;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (4 * g + k < a.V) C::put_sums(out + (4 * g + k) * a.d, acc[k], col, d);
+  }
+}
+
+namespace {
+
+constexpr int64_t kEmbedBlocks = 1 << 20;
+unsigned grid_of(int64_t blocks) { return (unsigned)std::max<int64_t>(1, std::min(blocks, kEmbedBlocks)); }
+
+template <typename T>
+int col_waves_of(int64_t d) {
+  constexpr int per = 64 * elem_traits<T>::per16;
+  return (int)((d + per - 1) / per);
+}
+
+// The tiles' sums, level by level.
+template <typename T, bool WHOLE, bool NORM>
+hipError_t launch_tiles(hipStream_t st, const EmbedGradArgs& a) {
+  const int cw = col_waves_of<T>(a.d);
+  int64_t span = kTile;
+  for (int l = 0; l < a.levels; ++l, span *= kTile) {
+    const int64_t tiles = a.N / span;
+    k_embed_tiles<T, WHOLE, NORM><<<grid_of((tiles * cw + 3) / 4), 256, 0, st>>>(a, l, span, tiles, cw);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <typename T, bool WHOLE>
+hipError_t launch_norm(hipStream_t st, const EmbedGradArgs& a) {
+  hipError_t e = launch_tiles<T, WHOLE, true>(st, a);
+  if (e != hipSuccess) return e;
+  const int64_t waves = (a.N + kEmbedNormPlaces - 1) / kEmbedNormPlaces;
+  k_embed_norm<T, WHOLE><<<grid_of((waves + 3) / 4), 256, 0, st>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_embed_norm_finish<<<grid_of(a.B), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, bool WHOLE>
+hipError_t launch_sum(hipStream_t st, const EmbedGradArgs& a, const NoiseArgs& na, float* out) {
+  const hipError_t e = launch_tiles<T, WHOLE, false>(st, a);
+  if (e != hipSuccess) return e;
+  const int cw = col_waves_of<T>(a.d);
+  k_embed_sum<T, WHOLE><<<grid_of(((a.V + 3) / 4 * cw + 3) / 4), 256, 0, st>>>(a, na, out, cw);
+  return hipGetLastError();
+}
+
+// Levels of tiles for runs of up to `longest` places: none up to 32, else as many as leave a run at most 128
+// tiles of the highest.
+int levels_for(int64_t N, int64_t longest) {
+  int levels = 0;
+  int64_t n = N;
+  while (levels < kEmbedMaxLevels && longest > (levels ? 128 : 32) && n >= kTile) {
+    ++levels;
+    longest /= kTile;
+    n /= kTile;
+  }
+  return levels;
+}
+
+void set_levels(EmbedGradArgs& a, int64_t longest) {
+  a.levels = levels_for(a.N, longest);
+  int64_t rows = 0, n = a.N;
+  for (int l = 0; l < a.levels; ++l) {
+    n /= kTile;
+    a.level_at[l] = rows;
+    rows += n;
+  }
+}
+
+int64_t level_rows(int64_t N, int levels) {
+  int64_t rows = 0;
+  for (int l = 0; l < levels; ++l) {
+    N /= kTile;
+    rows += N;
+  }
+  return rows;
+}
+
+}  // namespace
+
+hipError_t launch_embedding(hipStream_t st, int dtype, int weight_dtype, const EmbedArgs& a) {
+  const int P = dtype == 1 ? 8 : 4;
+  const int vpr = (int)((a.d + P - 1) / P);
+  const int tokens = std::max(1, 1024 / vpr);  // four vectors a thread, or one token
+  const FastDiv by = make_fastdiv((uint32_t)vpr);
+  const bool whole = a.d % P == 0;
+  auto run = [&](auto t, auto w, auto wh) {
+    k_embedding<decltype(t), decltype(w), decltype(wh)::value>
+        <<<grid_of((a.N + tokens - 1) / tokens), 256, 0, st>>>(a, vpr, by, tokens);
+    return hipGetLastError();
+  };
+  auto pick = [&](auto t, auto w) { return whole ? run(t, w, std::true_type{}) : run(t, w, std::false_type{}); };
+  if (dtype == 1) return weight_dtype == 1 ? pick(bf16s{}, bf16s{}) : pick(bf16s{}, float{});
+  return weight_dtype == 1 ? pick(float{}, bf16s{}) : pick(float{}, float{});
+}
+
+// Workspace: the counts of every pass, the digits' totals, two lists of keys and of tokens.
+size_t embed_order_ws_bytes(int64_t N, int64_t V) {
+  const SortPlan p = sort_plan(N, V);
+  const int64_t words = (p.passes * p.blocks + 1) * p.digits() + 4 * ((N + 3) / 4 * 4);
+  return ((size_t)words * 4 + 255) / 256 * 256;
+}
+
+hipError_t launch_embed_order(hipStream_t st, const int64_t* ids, int64_t N, int64_t V, void* ws, int64_t* order,
+                              int64_t* starts) {
+  const SortPlan p = sort_plan(N, V);
+  const int64_t D = p.digits(), list = (N + 3) / 4 * 4;
+  uint32_t* counts = static_cast<uint32_t*>(ws);
+  uint32_t* totals = counts + p.passes * p.blocks * D;
+  uint32_t* lists = totals + D;  // keys, tokens, keys, tokens
+  const bool summed = p.blocks > 128;
+  k_order_count<<<(unsigned)std::min<int64_t>(p.blocks, 1 << 20), kSortThreads, 0, st>>>(ids, N, V, p, counts);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    uint32_t* c = counts + pass * p.blocks * D;
+    if (summed) {
+      k_order_scan<<<(unsigned)((D + 63) / 64), 64, 0, st>>>(p, c, totals);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    uint32_t* in = lists + ((pass + 1) & 1) * 2 * list;
+    uint32_t* out = lists + (pass & 1) * 2 * list;
+    const bool last = pass + 1 == p.passes;
+    k_order_scatter<<<(unsigned)p.blocks, kSortThreads, 0, st>>>(
+        pass == 0 ? ids : nullptr, pass == 0 ? nullptr : in, pass == 0 ? nullptr : in + list, N, V, p, pass, c,
+        summed ? totals : nullptr, last ? nullptr : c + p.blocks * D, out, out + list, last ? order : nullptr);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (last) {
+      k_order_starts<<<grid_of((V + 256) / 256), 256, 0, st>>>(out, N, V, starts);
+      e = hipGetLastError();
+    }
+  }
+  return e;
+}
+
+// A token's squared norm each, then the tiles' sums; the norm's runs are within a sample, the sum's are not.
+size_t embed_ws_bytes(int64_t B, int64_t T, int64_t d) {
+  const int64_t N = B * T;
+  const size_t norm = (size_t)((N + 63) / 64 * 64) * 4 + (size_t)level_rows(N, levels_for(N, T)) * (size_t)d * 4;
+  const size_t sum = (size_t)level_rows(N, levels_for(N, N)) * (size_t)d * 4;
+  return (std::max(norm, sum) + 255) / 256 * 256;
+}
+
+hipError_t launch_embed_norm(hipStream_t st, int dtype, EmbedGradArgs a, void* ws) {
+  set_levels(a, a.T);
+  a.token_sq = static_cast<float*>(ws);
+  a.sums = a.token_sq + (a.N + 63) / 64 * 64;
+  const bool whole = a.d % (dtype == 1 ? 8 : 4) == 0;
+  if (dtype == 1) return whole ? launch_norm<bf16s, true>(st, a) : launch_norm<bf16s, false>(st, a);
+  return whole ? launch_norm<float, true>(st, a) : launch_norm<float, false>(st, a);
+}
+
+hipError_t launch_embed_sum(hipStream_t st, int dtype, EmbedGradArgs a, void* ws, const NoiseArgs& na, float* out) {
+  set_levels(a, a.N);
+  a.sums = static_cast<float*>(ws);
+  const bool whole = a.d % (dtype == 1 ? 8 : 4) == 0;
+  if (dtype == 1) return whole ? launch_sum<bf16s, true>(st, a, na, out) : launch_sum<bf16s, false>(st, a, na, out);
+  return whole ? launch_sum<float, true>(st, a, na, out) : launch_sum<float, false>(st, a, na, out);
+}
+
+}  // namespace dpk

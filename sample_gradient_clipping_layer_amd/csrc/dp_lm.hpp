@@ -48,6 +48,105 @@ int64_t rms_chunks(int64_t B, int64_t T);
 hipError_t launch_rms_norm(hipStream_t st, int dtype, const RmsArgs& a);
 hipError_t launch_rms_norm_backward(hipStream_t st, int dtype, RmsBackArgs a);
 
+// ---- layer norm
+struct LayerNormArgs {
+  const void *x, *residual;  // residual may be null
+  const void *gain, *bias;   // one type; bias may be null
+  int gain_bf16;
+  float eps;
+  int64_t rows, d;
+  void *out, *sum_out;  // sum_out may be null
+};
+struct LayerNormBackArgs {
+  const void *dy, *s, *dsum;  // dsum may be null
+  const void* gain;
+  int gain_bf16;
+  float eps;
+  int64_t B, T, d;
+  void* dx;                        // may be null
+  float *gain_rows, *bias_rows;    // [B][d], may be null
+  float* partial;                  // [2][B][chunks][d] when chunks > 1
+  // set by the launcher
+  int64_t chunks, chunk_rows;
+  int own_groups;
+};
+hipError_t launch_layer_norm(hipStream_t st, int dtype, const LayerNormArgs& a);
+hipError_t launch_layer_norm_backward(hipStream_t st, int dtype, LayerNormBackArgs a);
+
+// ---- table of words
+constexpr int kEmbedTile = 16;         // places (or tiles) of a tile
+constexpr int kEmbedMaxLevels = 8;
+constexpr int kEmbedNormPlaces = 8;    // places whose runs a wave sums
+struct EmbedArgs {
+  const int64_t* ids;  // [N]
+  const void* weight;  // [V][d]
+  int64_t N, V, d;
+  float scale;
+  void* out;  // [N][d]
+};
+struct EmbedGradArgs {
+  const void* G;         // [N][d]
+  const int64_t* ids;    // [N]
+  const int64_t* order;  // [N]
+  const int64_t* starts; // [V + 1] (sum)
+  const float* c;        // [B] (sum), null: 1
+  int64_t N, B, T, V, d; // N = B T
+  FastDiv by_t;
+  float scale;
+  float* sqnorm;  // [B] (norm)
+  int accumulate;
+  // set by the launcher
+  float* token_sq;  // [N] (norm)
+  float* sums;      // tiles' sums, [rows of all levels][d]
+  int levels;
+  int64_t level_at[kEmbedMaxLevels];  // first row of a level in sums
+};
+size_t embed_order_ws_bytes(int64_t N, int64_t V);
+size_t embed_ws_bytes(int64_t B, int64_t T, int64_t d);
+hipError_t launch_embedding(hipStream_t st, int dtype, int weight_dtype, const EmbedArgs& a);
+hipError_t launch_embed_order(hipStream_t st, const int64_t* ids, int64_t N, int64_t V, void* ws, int64_t* order,
+                              int64_t* starts);
+hipError_t launch_embed_norm(hipStream_t st, int dtype, EmbedGradArgs a, void* ws);
+hipError_t launch_embed_sum(hipStream_t st, int dtype, EmbedGradArgs a, void* ws, const NoiseArgs& na, float* out);
+
+// ---- log probabilities of given tokens
+constexpr int64_t kLogprobMaxTop = 256;
+struct LogprobArgs {
+  const void* logits;      // [rows][V]
+  const int64_t* targets;  // [rows]
+  float tau;
+  int64_t rows, V, K;
+  float *logp, *entropy;   // [rows]; entropy may be null
+  float* stats;            // [rows][2]
+  int64_t* top_ids;        // [rows][K], null when K == 0
+  float* top_logp;
+  // backward
+  const float *dlogp, *dentropy;  // [rows], either may be null
+  void* grad;              // [rows][V]
+  int64_t splits;          // set by the launcher
+};
+hipError_t launch_token_logprob(hipStream_t st, int dtype, const LogprobArgs& a);
+hipError_t launch_token_logprob_backward(hipStream_t st, int dtype, LogprobArgs a);
+
+// ---- balance loss
+constexpr int64_t kBalanceMaxExperts = 1024;
+struct BalanceArgs {
+  const void* logits;   // [B][T][E]
+  const int64_t* ids;   // [B][T][top]
+  int64_t B, T, E, top;
+  float* loss;          // [B]
+  int64_t *counts, *tokens;  // [B][E], [B]
+  const float* dloss;   // [B] or null
+  void* grad;           // [B][T][E]
+  // set by the launcher
+  int64_t chunks, chunk_rows;
+  float* part_sums;     // [B][chunks][E] sums of probabilities (chunks > 1)
+  uint32_t* part_counts;  // [B][chunks][E + 1] used places per expert, used tokens
+};
+size_t balance_ws_bytes(int64_t B, int64_t T, int64_t E);
+hipError_t launch_balance_loss(hipStream_t st, int dtype, BalanceArgs a, void* ws);
+hipError_t launch_balance_backward(hipStream_t st, int dtype, BalanceArgs a);
+
 // ---- distillation loss
 constexpr int64_t kDistillMaxTop = 2048;
 struct DistillArgs {

@@ -1,0 +1,484 @@
+// Log probabilities of given tokens, with the entropy of the distribution and
+// its top alternatives, and the gradient of the first two.
+//
+// With x_j = (z_j - m) / tau, m the largest logit, s = sum_j exp(x_j):
+//   logp = x_y - log s           (0 for a target outside [0, V))
+//   H = log s - sum_j exp(x_j) x_j / s     (every term of the sum has one sign)
+//   top: the K largest logits, equal ones by ascending word, as log probabilities
+//   dz_j = (dlogp (1[j = y] - p_j) - dH p_j (log p_j + H)) / tau
+//
+// Both directions are bound by HBM: the logits are read once (and the gradient
+// written once). A token's words are streamed by one workgroup with a running
+// maximum, sum and weighted sum per thread, joined at the end.
+//
+// The top words come out of the same pass. Each thread knows its largest
+// logit; the K-th largest of these (of 256 groups of threads) is a floor that
+// at least K words reach, and in a row without a pattern hardly more. Only the
+// threads whose own largest reaches it read their words again, collect those
+// that do, and the collected ones are put in order by counting the larger ones.
+// Where too many reach the floor (rows of few different values, words of a
+// mask's value) or fewer than K (rows with NaN, masks that leave almost
+// nothing) the K-th largest is found from counts of the leading digits instead,
+// in further passes over the row.
+//
+// A row whose logits are all -inf has no distribution: logp and the top words'
+// are -inf, H is 0 and the gradient 0. A row with a NaN or +inf gives NaN.
+#include "dp_common.hpp"
+#include "dp_lm.hpp"
+#include "dp_vocab.hpp"
+
+#include <float.h>
+
+namespace dpk {
+
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+// A distance from the maximum, in powers of two, beyond which 2^-x is 0: it stands for larger ones (and infinite
+// ones) in the products 2^-x x.
+constexpr float kFar = 256.0f;
+
+// s = sum of 2^-x and u = sum of 2^-x x over the values seen, x = (m - z) k >= 0, k = log2(e) / tau. The initial
+// maximum is finite, so that no difference of infinities arises.
+struct Stat {
+  float m, s, u;
+};
+__device__ __forceinline__ Stat stat_empty() { return Stat{-FLT_MAX, 0.f, 0.f}; }
+
+// r as seen from the maximum m >= r.m
+template <bool ENT>
+__device__ __forceinline__ void stat_move(Stat& r, float m, float k) {
+  const float x = (m - r.m) * k, f = exp2_hw(-x);
+  if constexpr (ENT) r.u = f * __builtin_fmaf(fminf(x, kFar), r.s, r.u);
+  r.s *= f;
+  r.m = m;
+}
+template <bool ENT>
+__device__ __forceinline__ Stat stat_join(Stat a, Stat b, float k) {
+  const float m = fmaxf(a.m, b.m);
+  stat_move<ENT>(a, m, k);
+  stat_move<ENT>(b, m, k);
+  return Stat{m, a.s + b.s, a.u + b.u};
+}
+template <bool ENT, int P>
+__device__ __forceinline__ void stat_add(Stat& r, const float* z, float k) {
+  float m = r.m;
+#pragma unroll
+  for (int e = 0; e < P; ++e) m = fmaxf(m, z[e]);
+  stat_move<ENT>(r, m, k);
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    const float x = (m - z[e]) * k, t = exp2_hw(-x);
+    r.s += t;
+    if constexpr (ENT) r.u = __builtin_fmaf(t, fminf(x, kFar), r.u);
+  }
+}
+
+// f(word, P values) over a thread's part of a row: single elements to the first 16-byte boundary, 16-byte vectors,
+// single elements at the end. U vectors in flight.
+template <typename T, int NT, int U, typename F1, typename FP>
+__device__ __forceinline__ void thread_words(const T* z, int64_t V, F1 one, FP many) {
+  constexpr int P = elem_traits<T>::per16;
+  const Span<T> sn(z, 0, V);
+  const int64_t j = threadIdx.x;
+  if (j < sn.head) one(j, to_f32(z[j]));
+  const u32x4* vz = reinterpret_cast<const u32x4*>(z + sn.head);
+  for (int64_t i = threadIdx.x; i < sn.vecs; i += U * NT) {
+    u32x4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = vz[i + u * NT < sn.vecs ? i + u * NT : i];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u * NT >= sn.vecs) break;
+      float v[P];
+      unpack16<P>(raw[u], v);
+      many(sn.head + (i + u * NT) * P, v);
+    }
+  }
+  const int64_t jt = sn.tail0 + threadIdx.x;
+  if (jt < V) one(jt, to_f32(z[jt]));
+}
+
+// Joined over the block; the same value in every thread. Contains barriers.
+template <bool ENT, int NT>
+__device__ __forceinline__ Stat block_stat(Stat r, float k, float* red) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    Stat o{__shfl_xor(r.m, off, kWave), __shfl_xor(r.s, off, kWave), 0.f};
+    if constexpr (ENT) o.u = __shfl_xor(r.u, off, kWave);
+    r = stat_join<ENT>(r, o, k);
+  }
+  if constexpr (NT == 64) return r;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+    red[3 * (threadIdx.x >> 6)] = r.m;
+    red[3 * (threadIdx.x >> 6) + 1] = r.s;
+    red[3 * (threadIdx.x >> 6) + 2] = r.u;
+  }
+  __syncthreads();
+  constexpr int NW = NT / 64;
+  const int w = threadIdx.x & (NW - 1);  // each wave joins them all, over its lanes
+  Stat t{red[3 * w], red[3 * w + 1], red[3 * w + 2]};
+#pragma unroll
+  for (int off = NW / 2; off > 0; off >>= 1)
+    t = stat_join<ENT>(t, Stat{__shfl_xor(t.m, off, kWave), __shfl_xor(t.s, off, kWave), __shfl_xor(t.u, off, kWave)}, k);
+  return t;
+}
+
+// A logit and its word as one number: larger logits first, among equal ones (0 and -0 are) the lower word; NaN above
+// all.
+__device__ __forceinline__ uint32_t key_of(float z) {
+  const uint32_t b = __float_as_uint(z + 0.0f);
+  return z != z ? 0xFFFFFFFFu : b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float((key >> 31) ? key ^ 0x80000000u : ~key);
+}
+__device__ __forceinline__ uint64_t place_of(float z, int64_t word) {
+  return ((uint64_t)key_of(z) << 32) | (uint32_t)~(uint32_t)word;
+}
+
+// LDS of the selection: 256 groups' maxima or digit counts, and the collected words.
+template <int NT>
+struct TopLds {
+  static constexpr int groups = NT < 256 ? NT : 256;
+  static constexpr int cap = NT == 64 ? 512 : 1024;
+  union {
+    __attribute__((aligned(16))) float best[groups];
+    uint32_t bins[256];
+  };
+  uint64_t found[cap];
+  float floor;
+  uint32_t count, digit, above, at;
+};
+
+// The words whose place is at least `least`.
+template <typename T, int NT>
+__device__ __forceinline__ void collect(const T* z, int64_t V, uint64_t least, TopLds<NT>& l) {
+  constexpr int P = elem_traits<T>::per16;
+  auto one = [&](int64_t j, float v) {
+    const uint64_t p = place_of(v, j);
+    if (p >= least) {
+      const uint32_t at = atomicAdd(&l.count, 1u);
+      if (at < (uint32_t)TopLds<NT>::cap) l.found[at] = p;
+    }
+  };
+  thread_words<T, NT, 4>(z, V, one, [&](int64_t j, const float* v) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) one(j + e, v[e]);
+  });
+}
+
+// A place that K words of the row reach, and at most `cap`: digits of 8 bits from the top, each from the counts of
+// the words that share the digits so far.
+template <typename T, int NT>
+__device__ uint64_t least_place(const T* z, int64_t V, int64_t K, TopLds<NT>& l) {
+  constexpr int P = elem_traits<T>::per16;
+  uint64_t prefix = 0;
+  uint32_t want = (uint32_t)K, above = 0;
+  for (int shift = 56; ; shift -= 8) {
+    if (shift < 32 && shift >= 8 && V <= ((int64_t)1 << shift)) {  // a digit of 255 in every word
+      prefix = (prefix << 8) | 255;
+      continue;
+    }
+    for (int k = threadIdx.x; k < 256; k += NT) l.bins[k] = 0;
+    __syncthreads();
+    auto one = [&](int64_t j, float v) {
+      const uint64_t p = place_of(v, j);
+      if (shift < 56 && (p >> (shift + 8)) != prefix) return;
+      const uint32_t digit = (uint32_t)(p >> shift) & 255u;
+      // rows of one value: one add for the wave
+      const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)digit);
+      const uint64_t same = __ballot(digit == first), here = __ballot(true);
+      if (same == here) {
+        if ((here & ((1ull << (threadIdx.x & 63)) - 1)) == 0) atomicAdd(&l.bins[digit], (uint32_t)__popcll(here));
+      } else {
+        atomicAdd(&l.bins[digit], 1u);
+      }
+    };
+    thread_words<T, NT, 4>(z, V, one, [&](int64_t j, const float* v) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) one(j + e, v[e]);
+    });
+    __syncthreads();
+    if (threadIdx.x < 64) {  // four digits a lane, from 255 down
+      uint32_t c[4], sum = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum += c[u] = l.bins[255 - 4 * threadIdx.x - u];
+      uint32_t run = sum;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t o = __shfl_up(run, off, kWave);
+        if ((int)threadIdx.x >= off) run += o;
+      }
+      uint32_t before = run - sum;
+      if (before < want && run >= want) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (before < want && before + c[u] >= want) {
+            l.digit = 255 - 4 * threadIdx.x - u;
+            l.above = before;
+            l.at = c[u];
+          }
+          before += c[u];
+        }
+      }
+    }
+    __syncthreads();
+    prefix = (prefix << 8) | l.digit;
+    above += l.above;
+    want -= l.above;
+    const uint32_t at = l.at;
+    __syncthreads();  // read before the next digit's
+    if (shift == 0 || above + at <= (uint32_t)TopLds<NT>::cap) return prefix << shift;
+  }
+}
+
+// The row's K top words into top_ids and top_logp. mine: the largest logit that this thread has seen.
+template <typename T, int NT>
+__device__ void top_words(const LogprobArgs& a, int64_t row, const T* z, float mine, Stat r, TopLds<NT>& l) {
+  constexpr int P = elem_traits<T>::per16, G = TopLds<NT>::groups, S = NT / G;  // S threads to a group
+  const int K = (int)a.K;
+  if (threadIdx.x == 0) {
+    l.count = 0;
+    l.floor = INFINITY;
+  }
+  const bool plain = r.s == r.s;  // no NaN, no +inf
+  float best = mine;
+#pragma unroll
+  for (int off = 1; off < S; off <<= 1) best = fmaxf(best, __shfl_xor(best, off, kWave));
+  if (threadIdx.x % S == 0) l.best[threadIdx.x / S] = best;
+  __syncthreads();
+  {
+    // how many groups are ahead of this one: larger, or equal and before it
+    const int g = threadIdx.x / S, part = threadIdx.x % S;
+    int ahead = 0;
+#pragma unroll 4
+    for (int i = part * (G / S); i < (part + 1) * (G / S); i += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(l.best + i);
+      ahead += (o.x > best || (o.x == best && i < g)) + (o.y > best || (o.y == best && i + 1 < g)) +
+               (o.z > best || (o.z == best && i + 2 < g)) + (o.w > best || (o.w == best && i + 3 < g));
+    }
+#pragma unroll
+    for (int off = 1; off < S; off <<= 1) ahead += __shfl_xor(ahead, off, kWave);
+    if (part == 0 && ahead == K - 1) l.floor = best;
+  }
+  __syncthreads();
+  const float floor = l.floor;
+  if (plain && mine >= floor) {
+    auto one = [&](int64_t j, float v) {
+      if (v >= floor) {
+        const uint32_t at = atomicAdd(&l.count, 1u);
+        if (at < (uint32_t)TopLds<NT>::cap) l.found[at] = place_of(v, j);
+      }
+    };
+    thread_words<T, NT, 4>(z, a.V, one, [&](int64_t j, const float* v) {
+      float m = v[0];
+#pragma unroll
+      for (int e = 1; e < P; ++e) m = fmaxf(m, v[e]);
+      if (m >= floor) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) one(j + e, v[e]);
+      }
+    });
+  }
+  __syncthreads();
+  uint32_t n = l.count;
+  __syncthreads();
+  if (n < (uint32_t)K || n > (uint32_t)TopLds<NT>::cap) {  // uniform
+    const uint64_t least = least_place<T, NT>(z, a.V, K, l);
+    if (threadIdx.x == 0) l.count = 0;
+    __syncthreads();
+    collect<T, NT>(z, a.V, least, l);
+    __syncthreads();
+    n = l.count < (uint32_t)TopLds<NT>::cap ? l.count : (uint32_t)TopLds<NT>::cap;
+  }
+  const float inv_tau = 1.0f / a.tau, log_s = logf(r.s);
+  for (uint32_t i = threadIdx.x; i < n; i += NT) {
+    const uint64_t p = l.found[i];
+    uint32_t rank = 0;
+#pragma unroll 4
+    for (uint32_t j = 0; j < n; ++j) rank += l.found[j] > p;
+    if (rank < (uint32_t)K) {
+      const float v = key_value((uint32_t)(p >> 32));
+      a.top_ids[row * K + rank] = (int64_t)(uint32_t)~(uint32_t)p;
+      a.top_logp[row * K + rank] = r.s == 0.0f ? -INFINITY : __builtin_fmaf(v - r.m, inv_tau, -log_s);
+    }
+  }
+  __syncthreads();  // found and best are reused by the next row
+}
+
+}  // namespace
+
+// One workgroup per token.
+template <typename T, int NT, bool ENT, bool TOP>
+__global__ __launch_bounds__(NT) void k_token_logprob(LogprobArgs a) {
+  constexpr int P = elem_traits<T>::per16;
+  __shared__ float red[3 * NT / 64];
+  const float k = kLog2e / a.tau;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* z = static_cast<const T*>(a.logits) + row * a.V;
+    const int64_t y = a.targets[row];
+    const bool given = y >= 0 && y < a.V;
+    const float zy = given ? to_f32(z[y]) : 0.0f;
+    Stat r = stat_empty();
+    thread_words<T, NT, 4>(z, a.V, [&](int64_t, float v) { stat_add<ENT, 1>(r, &v, k); },
+                           [&](int64_t, const float* v) { stat_add<ENT, P>(r, v, k); });
+    const float mine = r.m;
+    r = block_stat<ENT, NT>(r, k, red);
+    if (threadIdx.x == 0) {
+      const bool none = r.s == 0.0f;  // every logit is -inf
+      const float log_s = none ? 0.0f : logf(r.s);
+      a.logp[row] = !given ? 0.0f : none ? -INFINITY : (zy - r.m) / a.tau - log_s;
+      a.stats[2 * row] = none ? -INFINITY : r.m;
+      a.stats[2 * row + 1] = log_s;
+      if (ENT) a.entropy[row] = none ? 0.0f : log_s + kLn2 * (r.u / r.s);
+    }
+    if constexpr (TOP) {
+      __shared__ TopLds<NT> lds;
+      top_words<T, NT>(a, row, z, mine, r, lds);
+    }
+  }
+}
+
+// One workgroup per (token, split of its words).
+template <typename T, int NT, bool ENT>
+__global__ __launch_bounds__(NT) void k_token_logprob_backward(LogprobArgs a) {
+  constexpr int P = elem_traits<T>::per16;
+  const float inv_tau = 1.0f / a.tau;
+  const int64_t items = a.rows * a.splits, len = (a.V + a.splits - 1) / a.splits;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t row = item / a.splits, sp = item - row * a.splits;
+    const int64_t v0 = sp * len, v1 = v0 + len < a.V ? v0 + len : a.V;
+    if (v0 >= v1) continue;  // uniform
+    const T* z = static_cast<const T*>(a.logits) + row * a.V;
+    T* g = static_cast<T*>(a.grad) + row * a.V;
+    const int64_t y = a.targets[row];
+    const float dl = a.dlogp && y >= 0 && y < a.V ? a.dlogp[row] * inv_tau : 0.0f;
+    const float dh = ENT ? a.dentropy[row] * inv_tau : 0.0f;
+    const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
+    const float h = ENT ? a.entropy[row] : 0.0f;
+    // nothing to pass on, or a row without a distribution: 0 whatever the logits hold
+    const bool on = (dl != 0.0f || dh != 0.0f) && m != -INFINITY;
+    auto grad_of = [&](float zz) {
+      const float lp = __builtin_fmaf(zz - m, inv_tau, -log_s);
+      const float p = exp2_hw(lp * kLog2e);
+      // beyond exp(-200) p is 0: its logarithm may be -inf
+      return ENT ? -p * __builtin_fmaf(dh, fmaxf(lp, -200.0f) + h, dl) : -p * dl;
+    };
+    const Span<T> sn(z, v0, v1);
+    auto put1 = [&](int64_t j) {
+      const float v = on ? grad_of(to_f32(z[j])) + (j == y ? dl : 0.0f) : 0.0f;
+      if constexpr (P == 8) g[j].u = f32_to_bf16(v);
+      else g[j] = v;
+    };
+    {
+      const int64_t j = v0 + threadIdx.x, jt = sn.tail0 + threadIdx.x;
+      if (j < sn.head) put1(j);
+      if (jt < v1) put1(jt);
+    }
+    const u32x4* vz = reinterpret_cast<const u32x4*>(z + sn.head);
+    // grad and logits share their misalignment (checked on the host), so these are aligned too
+    u32x4* vg = reinterpret_cast<u32x4*>(g + sn.head);
+    if (!on) {
+      for (int64_t i = threadIdx.x; i < sn.vecs; i += NT) vg[i] = u32x4{0u, 0u, 0u, 0u};
+      continue;
+    }
+    const int64_t yv = y >= sn.head && y < sn.tail0 ? (y - sn.head) / P : -1;  // the target's vector and place in it
+    const int ye = (int)(y - sn.head - yv * P);
+    auto vec = [&](u32x4 raw, int64_t i) {
+      float v[P];
+      unpack16<P>(raw, v);
+#pragma unroll
+      for (int e = 0; e < P; ++e) v[e] = grad_of(v[e]);
+      if (i == yv) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[e] += e == ye ? dl : 0.0f;
+      }
+      u32x4 o;
+      if constexpr (P == 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(v[e]);
+      }
+      return o;
+    };
+    // eight vectors in flight per thread, past the caches both ways
+    constexpr int U = 8;
+    int64_t i = threadIdx.x;
+    for (; i + (U - 1) * NT < sn.vecs; i += U * NT) {
+      u32x4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = __builtin_nontemporal_load(vz + i + u * NT);
+#pragma unroll
+      for (int u = 0; u < U; ++u) __builtin_nontemporal_store(vec(raw[u], i + u * NT), vg + i + u * NT);
+    }
+    for (; i < sn.vecs; i += NT) vg[i] = vec(vz[i], i);
+  }
+}
+
+namespace {
+
+unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>(n, 1 << 20); }
+
+template <typename T, int NT>
+hipError_t launch_fwd(hipStream_t st, const LogprobArgs& a) {
+  const unsigned blocks = grid_of(a.rows);
+  if (a.entropy) {
+    if (a.K) k_token_logprob<T, NT, true, true><<<blocks, NT, 0, st>>>(a);
+    else k_token_logprob<T, NT, true, false><<<blocks, NT, 0, st>>>(a);
+  } else {
+    if (a.K) k_token_logprob<T, NT, false, true><<<blocks, NT, 0, st>>>(a);
+    else k_token_logprob<T, NT, false, false><<<blocks, NT, 0, st>>>(a);
+  }
+  return hipGetLastError();
+}
+
+template <typename T, int NT>
+hipError_t launch_bwd(hipStream_t st, const LogprobArgs& a) {
+  const unsigned blocks = grid_of(a.rows * a.splits);
+  if (a.dentropy) k_token_logprob_backward<T, NT, true><<<blocks, NT, 0, st>>>(a);
+  else k_token_logprob_backward<T, NT, false><<<blocks, NT, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+// Threads for a token's words. Few tokens: as many as a workgroup may have, so
+// that a row is few loads of each. Many tokens of a small vocabulary: a wave
+// each (which takes up to 32 top words).
+int logprob_threads(int64_t rows, int64_t V, int64_t K) {
+  if (K <= 32 && (V <= 256 || (rows > 512 && V <= 4096))) return 64;
+  if (rows > 512 || V <= 2048) return 256;
+  return rows > 256 || V <= 4096 ? 512 : 1024;
+}
+
+}  // namespace
+
+hipError_t launch_token_logprob(hipStream_t st, int dtype, const LogprobArgs& a) {
+  auto run = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    return dtype == 1 ? launch_fwd<bf16s, NT>(st, a) : launch_fwd<float, NT>(st, a);
+  };
+  switch (logprob_threads(a.rows, a.V, a.K)) {
+    case 64: return run(std::integral_constant<int, 64>{});
+    case 256: return run(std::integral_constant<int, 256>{});
+    case 512: return run(std::integral_constant<int, 512>{});
+    default: return run(std::integral_constant<int, 1024>{});
+  }
+}
+
+hipError_t launch_token_logprob_backward(hipStream_t st, int dtype, LogprobArgs a) {
+  // Splits of a token's words: none from 512 tokens on; below, as many as give about 1024 workgroups, each of at
+  // least 2048 words.
+  a.splits = 1;
+  if (a.rows < 512) {
+    const int64_t want = (1024 + a.rows - 1) / a.rows, most = (a.V + 2047) / 2048;
+    a.splits = std::max<int64_t>(1, std::min(want, most));
+  }
+  if (a.splits == 1 && a.V <= 4096)
+    return dtype == 1 ? launch_bwd<bf16s, 64>(st, a) : launch_bwd<float, 64>(st, a);
+  return dtype == 1 ? launch_bwd<bf16s, 256>(st, a) : launch_bwd<float, 256>(st, a);
+}
+
+}  // namespace dpk
