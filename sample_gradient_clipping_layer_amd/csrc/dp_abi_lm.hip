@@ -246,7 +246,7 @@ dp_status dp_embedding_order(void* stream, const int64_t* ids, int64_t N, int64_
 }
 
 size_t dp_embedding_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t V, int64_t d) {
-  return dtype_ok(dtype) && check_embedding(B, T, V, d) == DP_OK ? dpk::embed_ws_bytes(B, T, d) : 0;
+  return dtype_ok(dtype) && check_embedding(B, T, V, d) == DP_OK ? dpk::embed_ws_bytes(dtype, B, T, d) : 0;
 }
 
 dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const int64_t* ids, const int64_t* order,
@@ -259,7 +259,7 @@ dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const i
   if (!finite(scale)) return DP_ERR_VALUE;
   if (!aligned(G, elem_bytes(dtype)) || !aligned(ids, 8) || !aligned(order, 8) || !aligned(sqnorm, 4))
     return DP_ERR_ALIGN;
-  s = check_workspace(workspace, ws_bytes, dpk::embed_ws_bytes(B, T, d));
+  s = check_workspace(workspace, ws_bytes, dpk::embed_ws_bytes(dtype, B, T, d));
   if (s != DP_OK) return s;
   s = device_ready();
   if (s != DP_OK) return s;
@@ -294,7 +294,7 @@ dp_status dp_embedding_clipped_sum_noise(void* stream, const void* G, dp_dtype d
   if (!aligned(G, elem_bytes(dtype)) || !aligned(ids, 8) || !aligned(order, 8) || !aligned(starts, 8) ||
       !aligned(c, 4) || !aligned(out, 4))
     return DP_ERR_ALIGN;
-  s = check_workspace(workspace, ws_bytes, dpk::embed_ws_bytes(B, T, d));
+  s = check_workspace(workspace, ws_bytes, dpk::embed_ws_bytes(dtype, B, T, d));
   if (s != DP_OK) return s;
   s = device_ready();
   if (s != DP_OK) return s;

@@ -98,8 +98,9 @@ __global__ __launch_bounds__(256) void k_embedding(EmbedArgs a, int vpr, FastDiv
 
 namespace {
 
-constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortMaxDigits = 512;
+constexpr int kSortDirect = 64;  // workgroups whose counts each workgroup adds up by itself
 
 // How the sort of N ids over V words goes: digits per pass, ids per workgroup.
 struct SortPlan {
@@ -116,10 +117,10 @@ SortPlan sort_plan(int64_t N, int64_t V) {
   SortPlan p;
   p.passes = (bits + 8) / 9;
   p.bits = (bits + p.passes - 1) / p.passes;
-  // tiles of 1024 ids; from 128 workgroups on larger ones, whose ids are read in more rounds
-  p.rounds = 4;
+  // a token a thread; more from 128 workgroups on, up to 16
+  p.rounds = 1;
   p.log_tile = 10;
-  while (p.rounds < 64 && (N + p.tile() - 1) / p.tile() > 128) {
+  while (p.rounds < 16 && (N + p.tile() - 1) / p.tile() > 128) {
     p.rounds *= 2;
     ++p.log_tile;
   }
@@ -129,6 +130,15 @@ SortPlan sort_plan(int64_t N, int64_t V) {
 
 __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V) { return id < 0 || id >= V ? (uint32_t)V : (uint32_t)id; }
 
+// The lanes of `among` whose value's bits [0, bits) are this lane's.
+__device__ __forceinline__ uint64_t same_bits(uint64_t among, uint32_t value, int bits) {
+  for (int q = 0; q < bits; ++q) {
+    const uint64_t has = __ballot((value >> q) & 1);
+    among &= ((value >> q) & 1) ? has : ~has;
+  }
+  return among;
+}
+
 }  // namespace
 
 // The first digit's counts of every workgroup's tile; clears the counts of the later passes.
@@ -136,21 +146,18 @@ __global__ __launch_bounds__(kSortThreads) void k_order_count(const int64_t* __r
                                                               SortPlan p, uint32_t* __restrict__ counts) {
   __shared__ uint32_t bins[kSortMaxDigits];
   const int D = p.digits();
-  for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < (int64_t)(p.passes - 1) * p.blocks * D;
-       i += (int64_t)gridDim.x * kSortThreads)
+  const int64_t b = blockIdx.x;
+  for (int64_t i = b * kSortThreads + threadIdx.x; i < (int64_t)(p.passes - 1) * p.blocks * D; i += p.blocks * kSortThreads)
     counts[p.blocks * D + i] = 0;
-  for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
-    for (int k = threadIdx.x; k < D; k += kSortThreads) bins[k] = 0;
-    __syncthreads();
-    const int64_t i0 = b * p.tile();
-    for (int r = 0; r < p.rounds; ++r) {
-      const int64_t i = i0 + r * kSortThreads + threadIdx.x;
-      if (i < N) atomicAdd(&bins[key_of(ids[i], V) & (D - 1)], 1u);
-    }
-    __syncthreads();
-    for (int k = threadIdx.x; k < D; k += kSortThreads) counts[b * D + k] = bins[k];
-    __syncthreads();
+  for (int k = threadIdx.x; k < D; k += kSortThreads) bins[k] = 0;
+  __syncthreads();
+  const int64_t i0 = b * p.tile();
+  for (int r = 0; r < p.rounds; ++r) {
+    const int64_t i = i0 + r * kSortThreads + threadIdx.x;
+    if (i < N) atomicAdd(&bins[key_of(ids[i], V) & (D - 1)], 1u);
   }
+  __syncthreads();
+  for (int k = threadIdx.x; k < D; k += kSortThreads) counts[b * D + k] = bins[k];
 }
 
 // Exclusive sums down the workgroups, per digit, in place, and each digit's total behind them (many workgroups).
@@ -171,7 +178,9 @@ __global__ __launch_bounds__(64) void k_order_scan(SortPlan p, uint32_t* __restr
 // One digit's pass: the tokens of a workgroup's tile to their places by that
 // digit, in order. ids_in: the first pass reads the ids themselves; else keys
 // and tokens of the pass before. The next digit is counted on the way, where
-// the tokens go. totals: the counts are sums already (k_order_scan).
+// the tokens go (one add for the tokens of one word in a wave: a frequent
+// word's go to one count, and adds to one address wait for each other, 10 us
+// at 32768 tokens). totals: the counts are sums already (k_order_scan).
 __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const int64_t* __restrict__ ids_in,
                                                                 const uint32_t* __restrict__ keys_in,
                                                                 const uint32_t* __restrict__ toks_in, int64_t N,
@@ -183,108 +192,129 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const int64_t* _
                                                                 uint32_t* __restrict__ toks_out,
                                                                 int64_t* __restrict__ order) {
   __shared__ uint32_t seen[kSortWaves][kSortMaxDigits];  // of a wave so far; then where its tokens of a digit go
-  __shared__ uint32_t base[kSortMaxDigits];
-  __shared__ uint32_t scan[kSortThreads];
+  __shared__ uint32_t base[kSortMaxDigits], all[kSortMaxDigits];
+  __shared__ uint32_t scan[kSortWaves];
   const int D = p.digits(), shift = pass * p.bits;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t b = blockIdx.x;
   const int64_t w0 = b * p.tile() + (int64_t)wave * 64 * p.rounds;  // this wave's ids, `rounds` times 64 of them
+  auto key_at = [&](int64_t i) { return i >= N ? 0u : ids_in ? key_of(ids_in[i], V) : keys_in[i]; };
+  const uint32_t first_key = key_at(w0 + lane);  // on its way while the counts are added up
   for (int k = threadIdx.x; k < kSortWaves * D; k += kSortThreads) seen[k / D][k % D] = 0;
-  // ---- the counts of the digit in earlier workgroups and in all
-  const int per = (D + kSortThreads - 1) / kSortThreads;  // 1 or 2 digits per thread
-  uint32_t before[2] = {0, 0}, total[2] = {0, 0};
-  for (int u = 0; u < per; ++u) {
-    const int k = threadIdx.x * per + u;
-    if (k >= D) break;
-    if (totals) {
-      before[u] = counts[b * D + k];
-      total[u] = totals[k];
-    } else {
-#pragma unroll 8
-      for (int64_t j = 0; j < p.blocks; ++j) {
-        const uint32_t c = counts[j * D + k];
-        total[u] += c;
-        before[u] += j < b ? c : 0u;
-      }
+  for (int k = threadIdx.x; k < D; k += kSortThreads) base[k] = all[k] = 0;
+  __syncthreads();
+  // ---- the counts of the digit in earlier workgroups and in all, several threads to a digit
+  if (totals) {
+    for (int k = threadIdx.x; k < D; k += kSortThreads) {
+      base[k] = counts[b * D + k];
+      all[k] = totals[k];
     }
+  } else {
+    const int parts = kSortThreads / D, k = threadIdx.x & (D - 1), part = threadIdx.x / D;
+    uint32_t before = 0, total = 0;
+#pragma unroll 8
+    for (int64_t j = part; j < p.blocks; j += parts) {
+      const uint32_t c = counts[j * D + k];
+      total += c;
+      before += j < b ? c : 0u;
+    }
+    if (total) atomicAdd(&all[k], total);
+    if (before) atomicAdd(&base[k], before);
   }
+  __syncthreads();
   // ---- exclusive sum over the digits
-  uint32_t mine = total[0] + total[1], run = mine;
+  uint32_t mine = (int)threadIdx.x < D ? all[threadIdx.x] : 0, run = mine;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const uint32_t o = __shfl_up(run, off, kWave);
     if (lane >= off) run += o;
   }
   if (lane == 63) scan[wave] = run;
-  __syncthreads();
-  uint32_t at = run - mine;
-  for (int w = 0; w < wave; ++w) at += scan[w];
-  for (int u = 0; u < per; ++u) {
-    const int k = threadIdx.x * per + u;
-    if (k >= D) break;
-    base[k] = at + before[u];
-    at += total[u];
-  }
   // ---- ranks within the wave, in order: the lanes before this one with its digit, and those of earlier rounds
   const uint64_t below = lane == 0 ? 0 : (~0ull >> (64 - lane));
   for (int r = 0; r < p.rounds; ++r) {
     const int64_t i = w0 + r * 64 + lane;
-    const uint32_t key = i >= N ? 0u : ids_in ? key_of(ids_in[i], V) : keys_in[i];
-    const uint32_t digit = (key >> shift) & (D - 1);
-    uint64_t same = __ballot(i < N);
-    for (int q = 0; q < p.bits; ++q) {
-      const uint64_t has = __ballot((digit >> q) & 1);
-      same &= ((digit >> q) & 1) ? has : ~has;
-    }
+    const uint32_t digit = ((r == 0 ? first_key : key_at(i)) >> shift) & (D - 1);
+    const uint64_t same = same_bits(__ballot(i < N), digit, p.bits);
     if (i < N && (same & below) == 0) seen[wave][digit] += (uint32_t)__popcll(same);
   }
   __syncthreads();
   // ---- where each wave's tokens of a digit start
-  for (int k = threadIdx.x; k < D; k += kSortThreads) {
-    uint32_t s = base[k];
+  if ((int)threadIdx.x < D) {
+    uint32_t s = base[threadIdx.x] + run - mine;
+    for (int w = 0; w < wave; ++w) s += scan[w];
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = seen[w][k];
-      seen[w][k] = s;
+      const uint32_t c = seen[w][threadIdx.x];
+      seen[w][threadIdx.x] = s;
       s += c;
     }
   }
   __syncthreads();
-  const int next_shift = shift + p.bits;
   for (int r = 0; r < p.rounds; ++r) {
     const int64_t i = w0 + r * 64 + lane;
-    const uint32_t key = i >= N ? 0u : ids_in ? key_of(ids_in[i], V) : keys_in[i];
+    const bool in = i < N;
+    const uint32_t key = r == 0 ? first_key : key_at(i), tok = in && toks_in ? toks_in[i] : (uint32_t)i;
     const uint32_t digit = (key >> shift) & (D - 1);
-    uint64_t same = __ballot(i < N);
-    for (int q = 0; q < p.bits; ++q) {
-      const uint64_t has = __ballot((digit >> q) & 1);
-      same &= ((digit >> q) & 1) ? has : ~has;
-    }
+    const uint64_t same = same_bits(__ballot(in), digit, p.bits);
     uint32_t to = 0;
-    if (i < N) to = seen[wave][digit] + (uint32_t)__popcll(same & below);
+    if (in) to = seen[wave][digit] + (uint32_t)__popcll(same & below);
     __builtin_amdgcn_wave_barrier();  // every lane has read its digit's place before one moves it on
-    if (i < N) {
-      if ((same & below) == 0) seen[wave][digit] = to + (uint32_t)__popcll(same);
-      keys_out[to] = key;
-      if (order) order[to] = toks_in ? toks_in[i] : i;
-      else toks_out[to] = toks_in ? toks_in[i] : (uint32_t)i;
-      if (next_counts) atomicAdd(&next_counts[(int64_t)(to >> p.log_tile) * D + ((key >> next_shift) & (D - 1))], 1u);
-    }
+    if (in && (same & below) == 0) seen[wave][digit] = to + (uint32_t)__popcll(same);
     __builtin_amdgcn_wave_barrier();
+    if (in) {
+      keys_out[to] = key;
+      if (order) order[to] = tok;
+      else toks_out[to] = tok;
+    }
+    if (next_counts) {
+      const uint32_t next = (key >> (shift + p.bits)) & (D - 1);
+      // neighbours by this digit share their tile but where one ends
+      const uint32_t tile = to >> p.log_tile;
+      uint64_t twins = same_bits(same, next, p.bits);
+      const uint32_t first_tile = __shfl(tile, in ? __builtin_ctzll(twins) : lane, kWave);
+      twins &= __ballot(tile == first_tile);
+      if (in && (tile != first_tile || (twins & below) == 0))
+        atomicAdd(&next_counts[(int64_t)tile * D + next], tile != first_tile ? 1u : (uint32_t)__popcll(twins));
+    }
   }
 }
 
-// starts[w] = how many keys are smaller than w, by bisection.
+// starts[w] = how many keys are smaller than w. A workgroup's 256 words lie
+// close together in the keys: each of its waves finds where the first one's
+// and the last one's are, 64 keys a step, and a word is then looked up in the
+// few between them, held in LDS where they fit.
 __global__ __launch_bounds__(256) void k_order_starts(const uint32_t* __restrict__ keys, int64_t N, int64_t V,
                                                       int64_t* __restrict__ starts) {
-  for (int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x; w <= V; w += (int64_t)gridDim.x * 256) {
-    int64_t lo = 0, hi = N;
+  constexpr int kHeld = 2048;
+  __shared__ uint32_t held[kHeld];
+  const int lane = threadIdx.x & 63;
+  auto below = [&](int64_t word, int64_t lo, int64_t hi) {  // the first place in [lo, hi) with a key >= word, or hi
     while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (keys[mid] < (uint32_t)w) lo = mid + 1;
-      else hi = mid;
+      const int64_t step = (hi - lo + 63) / 64, at = lo + (lane + 1) * step - 1;
+      const uint64_t less = __ballot(at < hi && keys[at < hi ? at : hi - 1] < (uint32_t)word);
+      lo += __popcll(less) * step;  // the pivots ascend: the first so many are smaller
+      hi = lo + step - 1 < hi ? lo + step - 1 : hi;
     }
-    starts[w] = lo;
+    return lo;
+  };
+  for (int64_t w0 = (int64_t)blockIdx.x * 256; w0 <= V; w0 += (int64_t)gridDim.x * 256) {
+    const int64_t last = w0 + 255 < V ? w0 + 255 : V;
+    const int64_t lo = below(w0, 0, N), hi = below(last, lo, N);
+    const bool fits = hi - lo <= kHeld;
+    __syncthreads();
+    if (fits)
+      for (int64_t i = threadIdx.x; i < hi - lo; i += 256) held[i] = keys[lo + i];
+    __syncthreads();
+    const int64_t w = w0 + threadIdx.x;
+    if (w > last) continue;
+    int64_t s = lo, e = hi;
+    while (s < e) {
+      const int64_t mid = (s + e) >> 1;
+      if ((fits ? held[mid - lo] : keys[mid]) < (uint32_t)w) s = mid + 1;
+      else e = mid;
+    }
+    starts[w] = s;
   }
 }
 
@@ -366,30 +396,45 @@ struct Cols {
   }
 };
 
-// acc += the rows of places [s, e), weighted by their samples' factors (c != null). Places of one run.
+__device__ __forceinline__ int lane_int(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ float lane_float(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+
+// The tokens of places [s, min(s + 64, e)) and their samples' factors (1 without), a place a lane; -1 for none.
+struct Places {
+  int tok;
+  float f;
+};
+__device__ __forceinline__ Places places_at(const EmbedGradArgs& a, int64_t s, int64_t e) {
+  const int64_t i = s + (threadIdx.x & 63);
+  Places p{-1, 0.f};
+  if (i < e) {
+    p.tok = (int)token_at(a, i);
+    if (p.tok >= 0) p.f = a.c ? a.c[sample_of(a, p.tok)] : 1.0f;
+  }
+  return p;
+}
+
+// acc += the rows of places [s, e), weighted by their samples' factors (a.c != null), by a wave. Places of one run.
 template <typename T, bool WHOLE>
 __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, float* acc, int64_t s, int64_t e, int col) {
   using C = Cols<T, WHOLE>;
-  constexpr int U = 4;  // rows in flight
-  const int d = (int)a.d;
-  for (; s < e; s += U) {
-    int64_t n[U];
+  constexpr int U = 8;  // rows in flight
+  for (; s < e; s += 64) {
+    const Places p = places_at(a, s, e);
+    const int m = (int)(e - s < 64 ? e - s : 64);
+    for (int r = 0; r < m; r += U) {
+      u32x4 raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) n[u] = s + u < e ? token_at(a, s + u) : -1;
-    u32x4 raw[U];
-    float f[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      raw[u] = u32x4{0u, 0u, 0u, 0u};
-      f[u] = 0.f;
-      if (n[u] >= 0) {
-        raw[u] = C::fetch(static_cast<const T*>(a.G) + n[u] * a.d, col, d);
-        f[u] = a.c ? a.c[sample_of(a, n[u])] : 1.0f;
+      for (int u = 0; u < U; ++u) {
+        const int n = lane_int(p.tok, r + u);  // lanes past the last place hold none
+        raw[u] = u32x4{0u, 0u, 0u, 0u};
+        if (n >= 0) raw[u] = C::fetch(static_cast<const T*>(a.G) + n * a.d, col, (int)a.d);
       }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (n[u] >= 0) C::add(acc, raw[u], f[u]);
+      for (int u = 0; u < U; ++u) C::add(acc, raw[u], lane_float(p.f, r + u));
+    }
   }
 }
 
@@ -427,96 +472,164 @@ __device__ __forceinline__ void add_run(const EmbedGradArgs& a, float* acc, int6
 
 }  // namespace
 
-// Sums of the tiles of level `l` (of 16^(l+1) places) that lie within one run,
-// a wave for each tile and 64 x 16 bytes' worth of columns.
+// Sums of the tiles of level l (of `span` = 16^(l+1) places) that lie within
+// one run and, where `both`, of those of level l + 1 above them: a workgroup
+// for 16 tiles and 64 x 16 bytes' worth of columns, a wave for each tile.
 template <typename T, bool WHOLE, bool NORM>
-__global__ __launch_bounds__(256) void k_embed_tiles(EmbedGradArgs a, int l, int64_t span, int64_t tiles, int col_waves) {
+__global__ __launch_bounds__(1024) void k_embed_tiles(EmbedGradArgs a, int l, int64_t span, int64_t tiles, int col_waves,
+                                                      int both) {
   using C = Cols<T, WHOLE>;
-  const int64_t items = tiles * col_waves;
-  const int lane = threadIdx.x & 63;
-  for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < items; item += (int64_t)gridDim.x * 4) {
-    const int64_t tile = item / col_waves;
-    const int col = ((int)(item - tile * col_waves) * 64 + lane) * C::P;
-    const int64_t i0 = tile * span;
-    const int64_t r = run_of<NORM>(a, token_at(a, i0));
-    if (r < 0 || r != run_of<NORM>(a, token_at(a, i0 + span - 1))) continue;
-    float acc[C::P];
-#pragma unroll
-    for (int e = 0; e < C::P; ++e) acc[e] = 0.f;
-    if (l == 0) {
-      add_rows<T, WHOLE>(a, acc, i0, i0 + kTile, col);
-    } else {
-      const float* sums = a.sums + (a.level_at[l - 1] + tile * kTile) * a.d;
-#pragma unroll 4
-      for (int k = 0; k < kTile; ++k) C::add_sums(acc, sums + k * a.d, col, (int)a.d);
+  constexpr int P = C::P;
+  __shared__ float part[kTile][64 * P];
+  __shared__ int64_t ends[2];  // the runs of the first and the last place of the 16 tiles
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t items = (tiles + kTile - 1) / kTile * col_waves;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t group = item / col_waves, tile = group * kTile + wave;
+    const int col = ((int)(item - group * col_waves) * 64 + lane) * P;
+    int64_t first = -1, last = -2;
+    if (tile < tiles) {
+      const int64_t i = tile * span + (lane == 1 ? span - 1 : 0);
+      const int64_t r = lane < 2 ? run_of<NORM>(a, token_at(a, i)) : -1;
+      first = __shfl(r, 0, kWave);
+      last = __shfl(r, 1, kWave);
     }
-    C::put_sums(a.sums + (a.level_at[l] + tile) * a.d, acc, col, (int)a.d);
+    if (lane == 0 && wave == 0) ends[0] = first;
+    if (lane == 0 && wave == kTile - 1) ends[1] = last;
+    float acc[P];
+#pragma unroll
+    for (int e = 0; e < P; ++e) acc[e] = 0.f;
+    if (first >= 0 && first == last) {
+      if (l == 0) {
+        add_rows<T, WHOLE>(a, acc, tile * kTile, tile * kTile + kTile, col);
+      } else {
+        const float* sums = a.sums + (a.level_at[l - 1] + tile * kTile) * a.d;
+#pragma unroll 8
+        for (int k = 0; k < kTile; ++k) C::add_sums(acc, sums + k * a.d, col, (int)a.d);
+      }
+      C::put_sums(a.sums + (a.level_at[l] + tile) * a.d, acc, col, (int)a.d);
+    }
+    if (!both) continue;
+    __syncthreads();
+    const bool whole = ends[0] >= 0 && ends[0] == ends[1];
+    if (whole) {  // the same in every wave
+#pragma unroll
+      for (int e = 0; e < P; ++e) part[wave][e * 64 + lane] = acc[e];
+    }
+    __syncthreads();
+    if (whole && wave == 0) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) acc[e] = 0.f;
+#pragma unroll 4
+      for (int w = 0; w < kTile; ++w)
+#pragma unroll
+        for (int e = 0; e < P; ++e) acc[e] += part[w][e * 64 + lane];
+      C::put_sums(a.sums + (a.level_at[l + 1] + group) * a.d, acc, col, (int)a.d);
+    }
+    __syncthreads();  // part and ends are written again
   }
 }
 
-// Squared norms of the runs that start in a wave's 8 places, each written at
-// the token of the run's first place, 0 at its other tokens'.
+// Squared norms of the runs that start in a wave's 8 places, over its part of
+// the columns, each written at the token of the run's last of these places, 0
+// at the other tokens. The rows of all 8 places are read together; what
+// follows of the last run behind them is added from its tiles.
 template <typename T, bool WHOLE>
-__global__ __launch_bounds__(256) void k_embed_norm(EmbedGradArgs a) {
+__global__ __launch_bounds__(256) void k_embed_norm(EmbedGradArgs a, int col_groups) {
   using C = Cols<T, WHOLE>;
-  constexpr int R = kEmbedNormPlaces;
+  constexpr int R = kEmbedNormPlaces, P = C::P;
   const int lane = threadIdx.x & 63;
-  const int64_t waves = (a.N + R - 1) / R;
-  for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < waves; w += (int64_t)gridDim.x * 4) {
+  const int64_t items = (a.N + R - 1) / R * col_groups;
+  for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < items; item += (int64_t)gridDim.x * 4) {
+    const int64_t w = item / col_groups;
+    const int cg = (int)(item - w * col_groups);
     const int64_t i0 = w * R;
     const int m = (int)(a.N - i0 < R ? a.N - i0 : R);  // this wave's places
-    // lane k <= m holds place i0 - 1 + k; further lanes the places behind, to see where the last run ends
+    // lane k + 1 holds place i0 + k; lane 0 the one before, further lanes those behind
     const int64_t i = i0 - 1 + lane;
-    int64_t n = -1, run = -1;
+    int n = -1;
+    int64_t run = -1;
     if (i >= 0 && i < a.N) {
-      n = token_at(a, i);
+      n = (int)token_at(a, i);
       run = run_of<true>(a, n);
     }
     const int64_t prev = __shfl_up(run, 1, kWave);
     const uint64_t heads = __ballot(lane > 0 && run >= 0 && run != prev);
     const uint64_t goes_on = __ballot(lane > 0 && run >= 0 && run == prev);  // same run as the place before
-    for (int k = 0; k < m; ++k) {
-      const int at = k + 1;  // the lane of this place
-      float sq = 0.f;
-      if ((heads >> at) & 1) {
-        // places of the run behind its first, as far as the lanes see
-        const uint64_t rest = goes_on >> at >> 1;
-        int len = 1 + (~rest ? __builtin_ctzll(~rest) : 64);
-        int64_t end = i0 + k + len;
-        if (at + len >= 64) {  // on past the last lane
-          const int64_t mine = __shfl(run, at, kWave);
-          while (end < a.N) {
-            const int64_t j = end + lane;
-            const uint64_t ends = __ballot(j >= a.N || run_of<true>(a, token_at(a, j < a.N ? j : a.N - 1)) != mine);
-            if (ends) {
-              end += __builtin_ctzll(ends);
-              break;
-            }
-            end += 64;
+    // the places of runs that start here, and the last place of each of them
+    uint32_t mine = 0, lasts = 0;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const bool in = k < m && (((heads >> (k + 1)) & 1) || (k > 0 && ((goes_on >> (k + 1)) & 1) && ((mine >> (k - 1)) & 1)));
+      mine |= (uint32_t)in << k;
+      const bool more = k + 1 < R && k + 1 < m && ((goes_on >> (k + 2)) & 1);
+      lasts |= (uint32_t)(in && !more) << k;
+    }
+    // the last run's places behind these
+    int64_t end = i0 + m;
+    if (((mine >> (m - 1)) & 1) && ((goes_on >> (m + 1)) & 1)) {
+      const uint64_t rest = ~(goes_on >> (m + 1));
+      end += __builtin_ctzll(rest);  // bits past the lanes are ones: at most to lane 63
+      if (end == i0 + 63) {          // on past the last lane
+        const int64_t same = __shfl(run, m, kWave);
+        while (end < a.N) {
+          const int64_t j = end + lane;
+          const uint64_t stops = __ballot(j >= a.N || run_of<true>(a, token_at(a, j < a.N ? j : a.N - 1)) != same);
+          if (stops) {
+            end += __builtin_ctzll(stops);
+            break;
+          }
+          end += 64;
+        }
+      }
+    }
+    float sq[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) sq[k] = 0.f;
+    if (mine) {
+      for (int c0 = cg * 64 * P; c0 < (int)a.d; c0 += col_groups * 64 * P) {
+        const int col = c0 + lane * P;
+        u32x4 raw[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          raw[k] = u32x4{0u, 0u, 0u, 0u};
+          if ((mine >> k) & 1) raw[k] = C::fetch(static_cast<const T*>(a.G) + lane_int(n, k + 1) * a.d, col, (int)a.d);
+        }
+        float acc[P];
+#pragma unroll
+        for (int e = 0; e < P; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          if (!((mine >> k) & 1)) continue;  // uniform
+          C::add(acc, raw[k], 1.0f);
+          if (!((lasts >> k) & 1)) continue;
+          if (k == m - 1 && end > i0 + m) add_run<T, WHOLE>(a, acc, i0 + m, end, col);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            sq[k] = __builtin_fmaf(acc[e], acc[e], sq[k]);
+            acc[e] = 0.f;
           }
         }
-        for (int c0 = 0; c0 < (int)a.d; c0 += 64 * C::P) {
-          float acc[C::P];
-#pragma unroll
-          for (int e = 0; e < C::P; ++e) acc[e] = 0.f;
-          add_run<T, WHOLE>(a, acc, i0 + k, end, c0 + lane * C::P);
-#pragma unroll
-          for (int e = 0; e < C::P; ++e) sq = __builtin_fmaf(acc[e], acc[e], sq);
-        }
-        sq = wave_sum(sq);
       }
-      const int64_t tok = __shfl(n, at, kWave);
-      if (lane == 0 && tok >= 0) a.token_sq[tok] = sq;
     }
+    float out = 0.f;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const float s = (lasts >> k) & 1 ? wave_sum(sq[k]) : 0.f;
+      if (lane == k + 1) out = s;
+    }
+    if (lane >= 1 && lane <= m && n >= 0) a.token_sq[cg * a.N + n] = out;
   }
 }
 
 // sqnorm[b] (+)= scale^2 * the sum of its tokens' values.
-__global__ __launch_bounds__(256) void k_embed_norm_finish(EmbedGradArgs a) {
+__global__ __launch_bounds__(256) void k_embed_norm_finish(EmbedGradArgs a, int col_groups) {
   __shared__ float red[4];
   for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
     float s = 0.f;
-    for (int64_t t = threadIdx.x; t < a.T; t += 256) s += a.token_sq[b * a.T + t];
+    for (int g = 0; g < col_groups; ++g)
+#pragma unroll 4
+      for (int64_t t = threadIdx.x; t < a.T; t += 256) s += a.token_sq[g * a.N + b * a.T + t];
     s = block_sum<256>(s, red);
     if (threadIdx.x == 0) {
       s *= a.scale * a.scale;
@@ -527,7 +640,7 @@ __global__ __launch_bounds__(256) void k_embed_norm_finish(EmbedGradArgs a) {
 }
 
 // The clipped, noised mean of 4 neighbouring words (whose noise shares its
-// blocks) and 64 x 4 columns, by a wave.
+// blocks) and 64 x 16 bytes' worth of columns, by a wave.
 template <typename T, bool WHOLE>
 __global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, NoiseArgs na, float* __restrict__ out, int col_waves) {
   using C = Cols<T, WHOLE>;
@@ -539,22 +652,51 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, NoiseArgs na
     const int64_t g = item / col_waves;
     const int col = ((int)(item - g * col_waves) * 64 + lane) * P;
     int64_t st = 0;
-    if (lane < 5 && 4 * g + lane <= a.V) {
-      st = a.starts[4 * g + lane];
+    if (lane < 5) {  // words past the table have no places
+      st = a.starts[4 * g + lane <= a.V ? 4 * g + lane : a.V];
       st = st < 0 ? 0 : st > a.N ? a.N : st;
     }
     float acc[4][P];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int e = 0; e < P; ++e) acc[k][e] = 0.f;
-      const int64_t s = __shfl(st, k, kWave), e = __shfl(st, k + 1, kWave);
-      if (4 * g + k < a.V && s < e) {
-        add_run<T, WHOLE>(a, acc[k], s, e, col);
+    int64_t at[5];  // where the words' places start
 #pragma unroll
-        for (int q = 0; q < P; ++q) acc[k][q] *= a.scale;
+    for (int k = 0; k < 5; ++k) at[k] = __shfl(st, k, kWave);
+    bool few = at[0] <= at[1] && at[1] <= at[2] && at[2] <= at[3] && at[3] <= at[4] && at[4] - at[0] <= 64;
+    if (few) {  // the rows of all four words, read together
+      constexpr int U = 8;
+      const int m = (int)(at[4] - at[0]);
+      Places p{-1, 0.f};
+      if (m > 0) p = places_at(a, at[0], at[4]);
+      const int e1 = (int)(at[1] - at[0]), e2 = (int)(at[2] - at[0]), e3 = (int)(at[3] - at[0]);
+      for (int r = 0; r < m; r += U) {
+        u32x4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int n = lane_int(p.tok, r + u);
+          raw[u] = u32x4{0u, 0u, 0u, 0u};
+          if (n >= 0) raw[u] = C::fetch(static_cast<const T*>(a.G) + n * a.d, col, d);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float f = lane_float(p.f, r + u);
+          if (r + u < e1) C::add(acc[0], raw[u], f);
+          else if (r + u < e2) C::add(acc[1], raw[u], f);
+          else if (r + u < e3) C::add(acc[2], raw[u], f);
+          else C::add(acc[3], raw[u], f);
+        }
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (4 * g + k < a.V && at[k] < at[k + 1]) add_run<T, WHOLE>(a, acc[k], at[k], at[k + 1], col);
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int e = 0; e < P; ++e) acc[k][e] *= a.scale;
     if (na.sc != 0.0f) {
 #pragma unroll
       for (int e = 0; e < P; ++e) {
@@ -590,24 +732,32 @@ template <typename T, bool WHOLE, bool NORM>
 hipError_t launch_tiles(hipStream_t st, const EmbedGradArgs& a) {
   const int cw = col_waves_of<T>(a.d);
   int64_t span = kTile;
-  for (int l = 0; l < a.levels; ++l, span *= kTile) {
+  for (int l = 0; l < a.levels; l += 2, span *= kTile * kTile) {
     const int64_t tiles = a.N / span;
-    k_embed_tiles<T, WHOLE, NORM><<<grid_of((tiles * cw + 3) / 4), 256, 0, st>>>(a, l, span, tiles, cw);
+    k_embed_tiles<T, WHOLE, NORM><<<grid_of((tiles + kTile - 1) / kTile * cw), 1024, 0, st>>>(a, l, span, tiles, cw,
+                                                                                              l + 1 < a.levels);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
+// Parts of the columns that waves of k_embed_norm share out: as many as give about 8192 waves.
+int64_t norm_col_groups(int64_t N, int64_t d, int col_waves) {
+  const int64_t waves = (N + kEmbedNormPlaces - 1) / kEmbedNormPlaces;
+  return std::max<int64_t>(1, std::min<int64_t>(col_waves, 8192 / waves));
+}
+
 template <typename T, bool WHOLE>
 hipError_t launch_norm(hipStream_t st, const EmbedGradArgs& a) {
   hipError_t e = launch_tiles<T, WHOLE, true>(st, a);
   if (e != hipSuccess) return e;
-  const int64_t waves = (a.N + kEmbedNormPlaces - 1) / kEmbedNormPlaces;
-  k_embed_norm<T, WHOLE><<<grid_of((waves + 3) / 4), 256, 0, st>>>(a);
+  const int64_t groups = norm_col_groups(a.N, a.d, col_waves_of<T>(a.d));
+  const int64_t waves = (a.N + kEmbedNormPlaces - 1) / kEmbedNormPlaces * groups;
+  k_embed_norm<T, WHOLE><<<grid_of((waves + 3) / 4), 256, 0, st>>>(a, (int)groups);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_embed_norm_finish<<<grid_of(a.B), 256, 0, st>>>(a);
+  k_embed_norm_finish<<<grid_of(a.B), 256, 0, st>>>(a, (int)groups);
   return hipGetLastError();
 }
 
@@ -652,6 +802,12 @@ int64_t level_rows(int64_t N, int levels) {
   return rows;
 }
 
+// Floats of the tokens' squared norms, a list for each part of the columns.
+int64_t token_floats(int dtype, int64_t N, int64_t d) {
+  const int cw = dtype == 1 ? col_waves_of<bf16s>(d) : col_waves_of<float>(d);
+  return (N * norm_col_groups(N, d, cw) + 63) / 64 * 64;
+}
+
 }  // namespace
 
 hipError_t launch_embedding(hipStream_t st, int dtype, int weight_dtype, const EmbedArgs& a) {
@@ -684,8 +840,8 @@ hipError_t launch_embed_order(hipStream_t st, const int64_t* ids, int64_t N, int
   uint32_t* counts = static_cast<uint32_t*>(ws);
   uint32_t* totals = counts + p.passes * p.blocks * D;
   uint32_t* lists = totals + D;  // keys, tokens, keys, tokens
-  const bool summed = p.blocks > 128;
-  k_order_count<<<(unsigned)std::min<int64_t>(p.blocks, 1 << 20), kSortThreads, 0, st>>>(ids, N, V, p, counts);
+  const bool summed = p.blocks > kSortDirect;
+  k_order_count<<<(unsigned)p.blocks, kSortThreads, 0, st>>>(ids, N, V, p, counts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   for (int pass = 0; pass < p.passes; ++pass) {
@@ -711,10 +867,10 @@ hipError_t launch_embed_order(hipStream_t st, const int64_t* ids, int64_t N, int
   return e;
 }
 
-// A token's squared norm each, then the tiles' sums; the norm's runs are within a sample, the sum's are not.
-size_t embed_ws_bytes(int64_t B, int64_t T, int64_t d) {
+// The tokens' squared norms, then the tiles' sums; the norm's runs are within a sample, the sum's are not.
+size_t embed_ws_bytes(int dtype, int64_t B, int64_t T, int64_t d) {
   const int64_t N = B * T;
-  const size_t norm = (size_t)((N + 63) / 64 * 64) * 4 + (size_t)level_rows(N, levels_for(N, T)) * (size_t)d * 4;
+  const size_t norm = (size_t)token_floats(dtype, N, d) * 4 + (size_t)level_rows(N, levels_for(N, T)) * (size_t)d * 4;
   const size_t sum = (size_t)level_rows(N, levels_for(N, N)) * (size_t)d * 4;
   return (std::max(norm, sum) + 255) / 256 * 256;
 }
@@ -722,7 +878,7 @@ size_t embed_ws_bytes(int64_t B, int64_t T, int64_t d) {
 hipError_t launch_embed_norm(hipStream_t st, int dtype, EmbedGradArgs a, void* ws) {
   set_levels(a, a.T);
   a.token_sq = static_cast<float*>(ws);
-  a.sums = a.token_sq + (a.N + 63) / 64 * 64;
+  a.sums = a.token_sq + token_floats(dtype, a.N, a.d);
   const bool whole = a.d % (dtype == 1 ? 8 : 4) == 0;
   if (dtype == 1) return whole ? launch_norm<bf16s, true>(st, a) : launch_norm<bf16s, false>(st, a);
   return whole ? launch_norm<float, true>(st, a) : launch_norm<float, false>(st, a);

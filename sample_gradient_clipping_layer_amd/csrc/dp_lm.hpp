@@ -96,13 +96,13 @@ struct EmbedGradArgs {
   float* sqnorm;  // [B] (norm)
   int accumulate;
   // set by the launcher
-  float* token_sq;  // [N] (norm)
+  float* token_sq;  // [parts of the columns][N] (norm)
   float* sums;      // tiles' sums, [rows of all levels][d]
   int levels;
   int64_t level_at[kEmbedMaxLevels];  // first row of a level in sums
 };
 size_t embed_order_ws_bytes(int64_t N, int64_t V);
-size_t embed_ws_bytes(int64_t B, int64_t T, int64_t d);
+size_t embed_ws_bytes(int dtype, int64_t B, int64_t T, int64_t d);
 hipError_t launch_embedding(hipStream_t st, int dtype, int weight_dtype, const EmbedArgs& a);
 hipError_t launch_embed_order(hipStream_t st, const int64_t* ids, int64_t N, int64_t V, void* ws, int64_t* order,
                               int64_t* starts);

@@ -99,30 +99,37 @@ __device__ __forceinline__ void thread_words(const T* z, int64_t V, F1 one, FP m
   if (jt < V) one(jt, to_f32(z[jt]));
 }
 
+// A wave's first lane's, in every lane. (The lanes of a butterfly of fused multiply-adds do not all end with the same
+// bits.)
+__device__ __forceinline__ float first_lane(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v)));
+}
+
 // Joined over the block; the same value in every thread. Contains barriers.
 template <bool ENT, int NT>
 __device__ __forceinline__ Stat block_stat(Stat r, float k, float* red) {
+  auto join = [&](Stat& t, int off) {
+    Stat o{__shfl_xor(t.m, off, kWave), __shfl_xor(t.s, off, kWave), 0.f};
+    if constexpr (ENT) o.u = __shfl_xor(t.u, off, kWave);
+    t = stat_join<ENT>(t, o, k);
+  };
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    Stat o{__shfl_xor(r.m, off, kWave), __shfl_xor(r.s, off, kWave), 0.f};
-    if constexpr (ENT) o.u = __shfl_xor(r.u, off, kWave);
-    r = stat_join<ENT>(r, o, k);
-  }
-  if constexpr (NT == 64) return r;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) {
-    red[3 * (threadIdx.x >> 6)] = r.m;
-    red[3 * (threadIdx.x >> 6) + 1] = r.s;
-    red[3 * (threadIdx.x >> 6) + 2] = r.u;
-  }
-  __syncthreads();
-  constexpr int NW = NT / 64;
-  const int w = threadIdx.x & (NW - 1);  // each wave joins them all, over its lanes
-  Stat t{red[3 * w], red[3 * w + 1], red[3 * w + 2]};
+  for (int off = 32; off > 0; off >>= 1) join(r, off);
+  if constexpr (NT > 64) {
+    constexpr int NW = NT / 64;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+      red[3 * (threadIdx.x >> 6)] = r.m;
+      red[3 * (threadIdx.x >> 6) + 1] = r.s;
+      red[3 * (threadIdx.x >> 6) + 2] = r.u;
+    }
+    __syncthreads();
+    const int w = threadIdx.x & (NW - 1);  // each wave joins them all, over its lanes
+    r = Stat{red[3 * w], red[3 * w + 1], red[3 * w + 2]};
 #pragma unroll
-  for (int off = NW / 2; off > 0; off >>= 1)
-    t = stat_join<ENT>(t, Stat{__shfl_xor(t.m, off, kWave), __shfl_xor(t.s, off, kWave), __shfl_xor(t.u, off, kWave)}, k);
-  return t;
+    for (int off = NW / 2; off > 0; off >>= 1) join(r, off);
+  }
+  return Stat{first_lane(r.m), first_lane(r.s), first_lane(r.u)};
 }
 
 // A logit and its word as one number: larger logits first, among equal ones (0 and -0 are) the lower word; NaN above
