@@ -289,18 +289,27 @@ __global__ __launch_bounds__(256) void k_order_starts(const uint32_t* __restrict
   constexpr int kHeld = 2048;
   __shared__ uint32_t held[kHeld];
   const int lane = threadIdx.x & 63;
-  auto below = [&](int64_t word, int64_t lo, int64_t hi) {  // the first place in [lo, hi) with a key >= word, or hi
-    while (lo < hi) {
-      const int64_t step = (hi - lo + 63) / 64, at = lo + (lane + 1) * step - 1;
-      const uint64_t less = __ballot(at < hi && keys[at < hi ? at : hi - 1] < (uint32_t)word);
-      lo += __popcll(less) * step;  // the pivots ascend: the first so many are smaller
-      hi = lo + step - 1 < hi ? lo + step - 1 : hi;
-    }
-    return lo;
-  };
   for (int64_t w0 = (int64_t)blockIdx.x * 256; w0 <= V; w0 += (int64_t)gridDim.x * 256) {
     const int64_t last = w0 + 255 < V ? w0 + 255 : V;
-    const int64_t lo = below(w0, 0, N), hi = below(last, lo, N);
+    // [s[q], e[q]]: where the first place with a key of w0 (q = 0) or `last` (q = 1) or more lies
+    int64_t s[2] = {0, 0}, e[2] = {N, N};
+    while (s[0] < e[0] || s[1] < e[1]) {
+      int64_t step[2], at[2];
+      uint32_t key[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        step[q] = (e[q] - s[q] + 63) / 64;
+        at[q] = s[q] + (lane + 1) * step[q] - 1;
+        key[q] = at[q] < e[q] ? keys[at[q]] : ~0u;
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint64_t less = __ballot(at[q] < e[q] && key[q] < (uint32_t)(q ? last : w0));
+        s[q] += __popcll(less) * step[q];  // the pivots ascend: the first so many are smaller
+        if (step[q]) e[q] = s[q] + step[q] - 1 < e[q] ? s[q] + step[q] - 1 : e[q];
+      }
+    }
+    const int64_t lo = s[0], hi = s[1];
     const bool fits = hi - lo <= kHeld;
     __syncthreads();
     if (fits)
@@ -308,13 +317,13 @@ __global__ __launch_bounds__(256) void k_order_starts(const uint32_t* __restrict
     __syncthreads();
     const int64_t w = w0 + threadIdx.x;
     if (w > last) continue;
-    int64_t s = lo, e = hi;
-    while (s < e) {
-      const int64_t mid = (s + e) >> 1;
-      if ((fits ? held[mid - lo] : keys[mid]) < (uint32_t)w) s = mid + 1;
-      else e = mid;
+    int64_t from = lo, to = hi;
+    while (from < to) {
+      const int64_t mid = (from + to) >> 1;
+      if ((fits ? held[mid - lo] : keys[mid]) < (uint32_t)w) from = mid + 1;
+      else to = mid;
     }
-    starts[w] = s;
+    starts[w] = from;
   }
 }
 
@@ -323,6 +332,9 @@ __global__ __launch_bounds__(256) void k_order_starts(const uint32_t* __restrict
 namespace {
 
 constexpr int kTile = kEmbedTile;
+
+// This wave's number in its workgroup, in a scalar register: what follows from it is the wave's, not a lane's.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
 
 // The token of a place, or -1 if it is none or the place's entry is no token.
 __device__ __forceinline__ int64_t token_at(const EmbedGradArgs& a, int64_t i) {
@@ -341,57 +353,75 @@ __device__ __forceinline__ int64_t run_of(const EmbedGradArgs& a, int64_t n) {
   return NORM ? id * a.B + sample_of(a, n) : id;
 }
 
-// 16 bytes' worth of columns of one row, in fp32.
-template <typename T, bool WHOLE>
+// What is read in place of a row that is not there, so that loads of several rows need no branches between them.
+__device__ const uint32_t kZeros[8] = {};
+
+// The P columns that a lane holds of a row of d: those from `c` on, or, where fewer are left, the row's last P (the
+// first `skip` of them are its neighbour's too). So every access is one whole vector, aligned or not: a row's end read
+// element by element has to be put together before the next row's loads are issued (8 rows of 333 fp32: 11 us instead
+// of 3). TINY: rows of fewer than P columns, element by element.
+template <typename T, int P, bool TINY>
 struct Cols {
-  static constexpr int P = elem_traits<T>::per16;
-  static __device__ __forceinline__ u32x4 fetch(const T* row, int c, int d) {
-    u32x4 raw{0u, 0u, 0u, 0u};
-    if (WHOLE ? c < d : c + P <= d) {
-      __builtin_memcpy(&raw, row + c, 16);
-    } else if (!WHOLE && c < d) {
+  static constexpr int bytes = P * (int)sizeof(T);
+  typedef uint32_t Raw __attribute__((ext_vector_type(bytes / 4)));
+  int at, skip, d;
+  bool on;
+  __device__ __forceinline__ Cols(int c, int64_t width) : d((int)width) {
+    on = c < d;
+    at = TINY || c + P <= d ? c : d - P;
+    skip = c - at;
+  }
+  // row n of X, zeros for n < 0
+  __device__ __forceinline__ Raw fetch(const void* X, int n) const {
+    const T* row = static_cast<const T*>(X) + (int64_t)(n < 0 ? 0 : n) * d;
+    Raw raw;
+    if (TINY) {
+#pragma unroll
+      for (int w = 0; w < bytes / 4; ++w) raw[w] = 0u;
 #pragma unroll
       for (int e = 0; e < P - 1; ++e)
-        if (c + e < d) {
-          const uint32_t bits = raw_bits(row[c + e]);
-          if constexpr (P == 8) raw[e >> 1] |= bits << (16 * (e & 1));
+        if (at + e < d && n >= 0) {
+          const uint32_t bits = raw_bits(row[at + e]);
+          if constexpr (sizeof(T) == 2) raw[e >> 1] |= bits << (16 * (e & 1));
           else raw[e] = bits;
         }
+    } else {
+      __builtin_memcpy(&raw, on && n >= 0 ? row + at : reinterpret_cast<const T*>(kZeros), bytes);
     }
     return raw;
   }
-  static __device__ __forceinline__ void add(float* acc, u32x4 raw, float f) {
-    if constexpr (P == 8) {
+  static __device__ __forceinline__ void add(float* acc, Raw raw, float f) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[2 * e] = __builtin_fmaf(f, __uint_as_float(raw[e] << 16), acc[2 * e]);
-        acc[2 * e + 1] = __builtin_fmaf(f, __uint_as_float(raw[e] & 0xFFFF0000u), acc[2 * e + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, __uint_as_float(raw[e]), acc[e]);
+    for (int e = 0; e < P; ++e) {
+      float v;
+      if constexpr (sizeof(T) == 2) v = __uint_as_float(e & 1 ? raw[e >> 1] & 0xFFFF0000u : raw[e >> 1] << 16);
+      else v = __uint_as_float(raw[e]);
+      acc[e] = __builtin_fmaf(f, v, acc[e]);
     }
   }
   // a row of the tiles' sums, fp32
-  static __device__ __forceinline__ void add_sums(float* acc, const float* row, int c, int d) {
-    if (WHOLE ? c < d : c + P <= d) {
-      float v[P];
-      __builtin_memcpy(v, row + c, sizeof(v));
+  __device__ __forceinline__ void add_sums(float* acc, const float* row) const {
+    float v[P];
 #pragma unroll
-      for (int e = 0; e < P; ++e) acc[e] += v[e];
-    } else if (!WHOLE && c < d) {
+    for (int e = 0; e < P; ++e) v[e] = 0.f;
+    if (TINY) {
 #pragma unroll
       for (int e = 0; e < P - 1; ++e)
-        if (c + e < d) acc[e] += row[c + e];
+        if (at + e < d) v[e] = row[at + e];
+    } else if (on) {
+      __builtin_memcpy(v, row + at, sizeof(v));
     }
+#pragma unroll
+    for (int e = 0; e < P; ++e) acc[e] += v[e];
   }
-  static __device__ __forceinline__ void put_sums(float* row, const float* acc, int c, int d) {
-    if (WHOLE ? c < d : c + P <= d) {
-      __builtin_memcpy(row + c, acc, 4 * P);
-    } else if (!WHOLE && c < d) {
+  // a row's columns that two lanes hold are stored by both, with the same value
+  __device__ __forceinline__ void put_sums(float* row, const float* acc) const {
+    if (TINY) {
 #pragma unroll
       for (int e = 0; e < P - 1; ++e)
-        if (c + e < d) row[c + e] = acc[e];
+        if (at + e < d) row[at + e] = acc[e];
+    } else if (on) {
+      __builtin_memcpy(row + at, acc, 4 * P);
     }
   }
 };
@@ -399,6 +429,10 @@ struct Cols {
 __device__ __forceinline__ int lane_int(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 __device__ __forceinline__ float lane_float(float v, int lane) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+
+__device__ __forceinline__ int64_t lane_int64(int64_t v, int lane) {
+  return (int64_t)(((uint64_t)(uint32_t)lane_int((int)(v >> 32), lane) << 32) | (uint32_t)lane_int((int)v, lane));
 }
 
 // The tokens of places [s, min(s + 64, e)) and their samples' factors (1 without), a place a lane; -1 for none.
@@ -416,57 +450,51 @@ __device__ __forceinline__ Places places_at(const EmbedGradArgs& a, int64_t s, i
   return p;
 }
 
+// acc += the rows of lanes [r0, r0 + U) of p; lanes past the last place hold none.
+template <int U, typename C>
+__device__ __forceinline__ void add_places(const EmbedGradArgs& a, const C& cols, float* acc, const Places& p, int r0) {
+  typename C::Raw raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) raw[u] = cols.fetch(a.G, lane_int(p.tok, r0 + u));
+#pragma unroll
+  for (int u = 0; u < U; ++u) C::add(acc, raw[u], lane_float(p.f, r0 + u));
+}
+
 // acc += the rows of places [s, e), weighted by their samples' factors (a.c != null), by a wave. Places of one run.
-template <typename T, bool WHOLE>
-__device__ __forceinline__ void add_rows(const EmbedGradArgs& a, float* acc, int64_t s, int64_t e, int col) {
-  using C = Cols<T, WHOLE>;
-  constexpr int U = 8;  // rows in flight
+template <typename C>
+__device__ __forceinline__ void add_rows(const EmbedGradArgs& a, const C& cols, float* acc, int64_t s, int64_t e) {
   for (; s < e; s += 64) {
     const Places p = places_at(a, s, e);
     const int m = (int)(e - s < 64 ? e - s : 64);
-    for (int r = 0; r < m; r += U) {
-      u32x4 raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int n = lane_int(p.tok, r + u);  // lanes past the last place hold none
-        raw[u] = u32x4{0u, 0u, 0u, 0u};
-        if (n >= 0) raw[u] = C::fetch(static_cast<const T*>(a.G) + n * a.d, col, (int)a.d);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) C::add(acc, raw[u], lane_float(p.f, r + u));
-    }
+#pragma unroll 1
+    for (int r = 0; r < m; r += 8) add_places<8>(a, cols, acc, p, r);
   }
 }
 
 // The same with whole tiles taken from their sums: the ends by places, then
 // by tiles of 16, of 256 and so on, up to the highest level there is.
-template <typename T, bool WHOLE>
-__device__ __forceinline__ void add_run(const EmbedGradArgs& a, float* acc, int64_t s, int64_t e, int col) {
-  using C = Cols<T, WHOLE>;
-  if (a.levels == 0 || e - s < kTile) {
-    add_rows<T, WHOLE>(a, acc, s, e, col);
-    return;
-  }
+template <typename C>
+__device__ __forceinline__ void add_run(const EmbedGradArgs& a, const C& cols, float* acc, int64_t s, int64_t e) {
   const int64_t up = (s + kTile - 1) / kTile * kTile, down = e / kTile * kTile;
-  if (up >= down) {
-    add_rows<T, WHOLE>(a, acc, s, e, col);
+  if (a.levels == 0 || up >= down) {
+    add_rows(a, cols, acc, s, e);
     return;
   }
-  add_rows<T, WHOLE>(a, acc, s, up, col);
-  add_rows<T, WHOLE>(a, acc, down, e, col);
+  add_rows(a, cols, acc, s, up);
+  add_rows(a, cols, acc, down, e);
   int64_t lo = up / kTile, hi = down / kTile;
   for (int l = 0; lo < hi; ++l) {
     const float* sums = a.sums + a.level_at[l] * a.d;
-    const bool top = l + 1 == a.levels;
-    int64_t in_lo = top ? hi : (lo + kTile - 1) / kTile * kTile, in_hi = top ? hi : hi / kTile * kTile;
-    if (in_lo >= in_hi) in_lo = in_hi = hi;
+    // the tiles of the next level inside [lo, hi): [in_lo, in_hi) of this one
+    int64_t in_lo = (lo + kTile - 1) / kTile * kTile, in_hi = hi / kTile * kTile;
+    if (l + 1 == a.levels || in_lo >= in_hi) in_lo = in_hi = hi;
 #pragma unroll 4
-    for (int64_t i = lo; i < in_lo; ++i) C::add_sums(acc, sums + i * a.d, col, (int)a.d);
+    for (int64_t i = lo; i < in_lo; ++i) cols.add_sums(acc, sums + i * a.d);
 #pragma unroll 4
-    for (int64_t i = in_hi; i < hi; ++i) C::add_sums(acc, sums + i * a.d, col, (int)a.d);
+    for (int64_t i = in_hi; i < hi; ++i) cols.add_sums(acc, sums + i * a.d);
+    if (in_lo >= in_hi) break;
     lo = in_lo / kTile;
     hi = in_hi / kTile;
-    if (in_lo >= in_hi) break;
   }
 }
 
@@ -475,24 +503,32 @@ __device__ __forceinline__ void add_run(const EmbedGradArgs& a, float* acc, int6
 // Sums of the tiles of level l (of `span` = 16^(l+1) places) that lie within
 // one run and, where `both`, of those of level l + 1 above them: a workgroup
 // for 16 tiles and 64 x 16 bytes' worth of columns, a wave for each tile.
-template <typename T, bool WHOLE, bool NORM>
+template <typename T, bool TINY, bool NORM>
 __global__ __launch_bounds__(1024) void k_embed_tiles(EmbedGradArgs a, int l, int64_t span, int64_t tiles, int col_waves,
                                                       int both) {
-  using C = Cols<T, WHOLE>;
-  constexpr int P = C::P;
+  constexpr int P = elem_traits<T>::per16;
+  using C = Cols<T, P, TINY>;
   __shared__ float part[kTile][64 * P];
   __shared__ int64_t ends[2];  // the runs of the first and the last place of the 16 tiles
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
   const int64_t items = (tiles + kTile - 1) / kTile * col_waves;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t group = item / col_waves, tile = group * kTile + wave;
-    const int col = ((int)(item - group * col_waves) * 64 + lane) * P;
+    const C cols(((int)(item - group * col_waves) * 64 + lane) * P, a.d);
     int64_t first = -1, last = -2;
+    Places p{-1, 0.f};
     if (tile < tiles) {
-      const int64_t i = tile * span + (lane == 1 ? span - 1 : 0);
-      const int64_t r = lane < 2 ? run_of<NORM>(a, token_at(a, i)) : -1;
-      first = __shfl(r, 0, kWave);
-      last = __shfl(r, 1, kWave);
+      const int64_t i0 = tile * span;
+      int64_t r = -1;
+      if (l == 0) {  // every place: its row is read if they are one run
+        p = places_at(a, i0, i0 + kTile);
+        if (lane < kTile) r = run_of<NORM>(a, p.tok);
+        last = lane_int64(r, kTile - 1);
+      } else {
+        if (lane < 2) r = run_of<NORM>(a, token_at(a, lane == 0 ? i0 : i0 + span - 1));
+        last = lane_int64(r, 1);
+      }
+      first = lane_int64(r, 0);
     }
     if (lane == 0 && wave == 0) ends[0] = first;
     if (lane == 0 && wave == kTile - 1) ends[1] = last;
@@ -501,13 +537,13 @@ __global__ __launch_bounds__(1024) void k_embed_tiles(EmbedGradArgs a, int l, in
     for (int e = 0; e < P; ++e) acc[e] = 0.f;
     if (first >= 0 && first == last) {
       if (l == 0) {
-        add_rows<T, WHOLE>(a, acc, tile * kTile, tile * kTile + kTile, col);
+        add_places<kTile>(a, cols, acc, p, 0);
       } else {
         const float* sums = a.sums + (a.level_at[l - 1] + tile * kTile) * a.d;
-#pragma unroll 8
-        for (int k = 0; k < kTile; ++k) C::add_sums(acc, sums + k * a.d, col, (int)a.d);
+#pragma unroll 4
+        for (int k = 0; k < kTile; ++k) cols.add_sums(acc, sums + k * a.d);
       }
-      C::put_sums(a.sums + (a.level_at[l] + tile) * a.d, acc, col, (int)a.d);
+      cols.put_sums(a.sums + (a.level_at[l] + tile) * a.d, acc);
     }
     if (!both) continue;
     __syncthreads();
@@ -524,7 +560,7 @@ __global__ __launch_bounds__(1024) void k_embed_tiles(EmbedGradArgs a, int l, in
       for (int w = 0; w < kTile; ++w)
 #pragma unroll
         for (int e = 0; e < P; ++e) acc[e] += part[w][e * 64 + lane];
-      C::put_sums(a.sums + (a.level_at[l + 1] + group) * a.d, acc, col, (int)a.d);
+      cols.put_sums(a.sums + (a.level_at[l + 1] + group) * a.d, acc);
     }
     __syncthreads();  // part and ends are written again
   }
@@ -534,13 +570,13 @@ __global__ __launch_bounds__(1024) void k_embed_tiles(EmbedGradArgs a, int l, in
 // the columns, each written at the token of the run's last of these places, 0
 // at the other tokens. The rows of all 8 places are read together; what
 // follows of the last run behind them is added from its tiles.
-template <typename T, bool WHOLE>
-__global__ __launch_bounds__(256) void k_embed_norm(EmbedGradArgs a, int col_groups) {
-  using C = Cols<T, WHOLE>;
-  constexpr int R = kEmbedNormPlaces, P = C::P;
+template <typename T, bool TINY>
+__global__ __launch_bounds__(256, 4) void k_embed_norm(EmbedGradArgs a, int col_groups) {
+  constexpr int R = kEmbedNormPlaces, P = elem_traits<T>::per16;
+  using C = Cols<T, P, TINY>;
   const int lane = threadIdx.x & 63;
   const int64_t items = (a.N + R - 1) / R * col_groups;
-  for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < items; item += (int64_t)gridDim.x * 4) {
+  for (int64_t item = (int64_t)blockIdx.x * 4 + wave_id(); item < items; item += (int64_t)gridDim.x * 4) {
     const int64_t w = item / col_groups;
     const int cg = (int)(item - w * col_groups);
     const int64_t i0 = w * R;
@@ -571,7 +607,7 @@ __global__ __launch_bounds__(256) void k_embed_norm(EmbedGradArgs a, int col_gro
       const uint64_t rest = ~(goes_on >> (m + 1));
       end += __builtin_ctzll(rest);  // bits past the lanes are ones: at most to lane 63
       if (end == i0 + 63) {          // on past the last lane
-        const int64_t same = __shfl(run, m, kWave);
+        const int64_t same = lane_int64(run, m);
         while (end < a.N) {
           const int64_t j = end + lane;
           const uint64_t stops = __ballot(j >= a.N || run_of<true>(a, token_at(a, j < a.N ? j : a.N - 1)) != same);
@@ -583,41 +619,46 @@ __global__ __launch_bounds__(256) void k_embed_norm(EmbedGradArgs a, int col_gro
         }
       }
     }
-    float sq[R];
+    const bool tail = end > i0 + m;
+    if (tail) lasts &= ~(1u << (m - 1));  // that run ends behind these places
+    float sq[R], sq_tail = 0.f;
 #pragma unroll
     for (int k = 0; k < R; ++k) sq[k] = 0.f;
     if (mine) {
       for (int c0 = cg * 64 * P; c0 < (int)a.d; c0 += col_groups * 64 * P) {
-        const int col = c0 + lane * P;
-        u32x4 raw[R];
+        const C cols(c0 + lane * P, a.d);
+        typename C::Raw raw[R];
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-          raw[k] = u32x4{0u, 0u, 0u, 0u};
-          if ((mine >> k) & 1) raw[k] = C::fetch(static_cast<const T*>(a.G) + lane_int(n, k + 1) * a.d, col, (int)a.d);
-        }
+        for (int k = 0; k < R; ++k) raw[k] = cols.fetch(a.G, (mine >> k) & 1 ? lane_int(n, k + 1) : -1);
         float acc[P];
 #pragma unroll
         for (int e = 0; e < P; ++e) acc[e] = 0.f;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-          if (!((mine >> k) & 1)) continue;  // uniform
           C::add(acc, raw[k], 1.0f);
-          if (!((lasts >> k) & 1)) continue;
-          if (k == m - 1 && end > i0 + m) add_run<T, WHOLE>(a, acc, i0 + m, end, col);
+          if ((lasts >> k) & 1) {
 #pragma unroll
-          for (int e = 0; e < P; ++e) {
-            sq[k] = __builtin_fmaf(acc[e], acc[e], sq[k]);
-            acc[e] = 0.f;
+            for (int e = 0; e < P; ++e) {
+              sq[k] = __builtin_fmaf(acc[e], e < cols.skip ? 0.f : acc[e], sq[k]);
+              acc[e] = 0.f;
+            }
           }
+        }
+        if (tail) {
+          add_run(a, cols, acc, i0 + m, end);
+#pragma unroll
+          for (int e = 0; e < P; ++e) sq_tail = __builtin_fmaf(acc[e], e < cols.skip ? 0.f : acc[e], sq_tail);
         }
       }
     }
+    sq_tail = wave_sum(sq_tail);
     float out = 0.f;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       const float s = (lasts >> k) & 1 ? wave_sum(sq[k]) : 0.f;
       if (lane == k + 1) out = s;
     }
+    if (tail && lane == m) out = sq_tail;
     if (lane >= 1 && lane <= m && n >= 0) a.token_sq[cg * a.N + n] = out;
   }
 }
@@ -640,17 +681,17 @@ __global__ __launch_bounds__(256) void k_embed_norm_finish(EmbedGradArgs a, int 
 }
 
 // The clipped, noised mean of 4 neighbouring words (whose noise shares its
-// blocks) and 64 x 16 bytes' worth of columns, by a wave.
-template <typename T, bool WHOLE>
-__global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, NoiseArgs na, float* __restrict__ out, int col_waves) {
-  using C = Cols<T, WHOLE>;
-  constexpr int P = C::P;
+// blocks) and 256 columns, by a wave: four columns a lane, so that 32 sums leave room for 8 rows in flight beside 16
+// waves a CU (with eight columns: 152 registers and 85 us instead of 62 for 32768 tokens of 1280 bf16).
+template <typename T, bool TINY>
+__global__ __launch_bounds__(256, 5) void k_embed_sum(EmbedGradArgs a, NoiseArgs na, float* __restrict__ out, int col_waves) {
+  constexpr int P = 4;
+  using C = Cols<T, P, TINY>;
   const int lane = threadIdx.x & 63;
-  const int d = (int)a.d;
   const int64_t groups = (a.V + 3) / 4, items = groups * col_waves;
-  for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < items; item += (int64_t)gridDim.x * 4) {
+  for (int64_t item = (int64_t)blockIdx.x * 4 + wave_id(); item < items; item += (int64_t)gridDim.x * 4) {
     const int64_t g = item / col_waves;
-    const int col = ((int)(item - g * col_waves) * 64 + lane) * P;
+    const C cols(((int)(item - g * col_waves) * 64 + lane) * P, a.d);
     int64_t st = 0;
     if (lane < 5) {  // words past the table have no places
       st = a.starts[4 * g + lane <= a.V ? 4 * g + lane : a.V];
@@ -663,7 +704,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, NoiseArgs na
       for (int e = 0; e < P; ++e) acc[k][e] = 0.f;
     int64_t at[5];  // where the words' places start
 #pragma unroll
-    for (int k = 0; k < 5; ++k) at[k] = __shfl(st, k, kWave);
+    for (int k = 0; k < 5; ++k) at[k] = lane_int64(st, k);
     bool few = at[0] <= at[1] && at[1] <= at[2] && at[2] <= at[3] && at[3] <= at[4] && at[4] - at[0] <= 64;
     if (few) {  // the rows of all four words, read together
       constexpr int U = 8;
@@ -671,14 +712,11 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, NoiseArgs na
       Places p{-1, 0.f};
       if (m > 0) p = places_at(a, at[0], at[4]);
       const int e1 = (int)(at[1] - at[0]), e2 = (int)(at[2] - at[0]), e3 = (int)(at[3] - at[0]);
+#pragma unroll 1
       for (int r = 0; r < m; r += U) {
-        u32x4 raw[U];
+        typename C::Raw raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int n = lane_int(p.tok, r + u);
-          raw[u] = u32x4{0u, 0u, 0u, 0u};
-          if (n >= 0) raw[u] = C::fetch(static_cast<const T*>(a.G) + n * a.d, col, d);
-        }
+        for (int u = 0; u < U; ++u) raw[u] = cols.fetch(a.G, lane_int(p.tok, r + u));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float f = lane_float(p.f, r + u);
@@ -691,7 +729,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, NoiseArgs na
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (4 * g + k < a.V && at[k] < at[k + 1]) add_run<T, WHOLE>(a, acc[k], at[k], at[k + 1], col);
+        if (4 * g + k < a.V && at[k] < at[k + 1]) add_run(a, cols, acc[k], at[k], at[k + 1]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -700,7 +738,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, NoiseArgs na
     if (na.sc != 0.0f) {
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const f32x4 z = normals4((uint32_t)g * (uint32_t)d + (uint32_t)(col + e), 2 * na.layer, na.step, 0, na.k0, na.k1);
+        const f32x4 z = normals4((uint32_t)g * (uint32_t)a.d + (uint32_t)(cols.at + e), 2 * na.layer, na.step, 0, na.k0, na.k1);
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[k][e] = noised_mean_spec(acc[k][e], na.sc, z[k], na.inv_denom);
       }
@@ -712,7 +750,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedGradArgs a, NoiseArgs na
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (4 * g + k < a.V) C::put_sums(out + (4 * g + k) * a.d, acc[k], col, d);
+      if (4 * g + k < a.V) cols.put_sums(out + (4 * g + k) * a.d, acc[k]);
   }
 }
 
@@ -728,13 +766,13 @@ int col_waves_of(int64_t d) {
 }
 
 // The tiles' sums, level by level.
-template <typename T, bool WHOLE, bool NORM>
+template <typename T, bool TINY, bool NORM>
 hipError_t launch_tiles(hipStream_t st, const EmbedGradArgs& a) {
   const int cw = col_waves_of<T>(a.d);
   int64_t span = kTile;
   for (int l = 0; l < a.levels; l += 2, span *= kTile * kTile) {
     const int64_t tiles = a.N / span;
-    k_embed_tiles<T, WHOLE, NORM><<<grid_of((tiles + kTile - 1) / kTile * cw), 1024, 0, st>>>(a, l, span, tiles, cw,
+    k_embed_tiles<T, TINY, NORM><<<grid_of((tiles + kTile - 1) / kTile * cw), 1024, 0, st>>>(a, l, span, tiles, cw,
                                                                                               l + 1 < a.levels);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -748,25 +786,27 @@ int64_t norm_col_groups(int64_t N, int64_t d, int col_waves) {
   return std::max<int64_t>(1, std::min<int64_t>(col_waves, 8192 / waves));
 }
 
-template <typename T, bool WHOLE>
+template <typename T, bool TINY>
 hipError_t launch_norm(hipStream_t st, const EmbedGradArgs& a) {
-  hipError_t e = launch_tiles<T, WHOLE, true>(st, a);
+  hipError_t e = launch_tiles<T, TINY, true>(st, a);
   if (e != hipSuccess) return e;
   const int64_t groups = norm_col_groups(a.N, a.d, col_waves_of<T>(a.d));
   const int64_t waves = (a.N + kEmbedNormPlaces - 1) / kEmbedNormPlaces * groups;
-  k_embed_norm<T, WHOLE><<<grid_of((waves + 3) / 4), 256, 0, st>>>(a, (int)groups);
+  k_embed_norm<T, TINY><<<grid_of((waves + 3) / 4), 256, 0, st>>>(a, (int)groups);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   k_embed_norm_finish<<<grid_of(a.B), 256, 0, st>>>(a, (int)groups);
   return hipGetLastError();
 }
 
-template <typename T, bool WHOLE>
+template <typename T, bool TINY>
 hipError_t launch_sum(hipStream_t st, const EmbedGradArgs& a, const NoiseArgs& na, float* out) {
-  const hipError_t e = launch_tiles<T, WHOLE, false>(st, a);
+  const hipError_t e = launch_tiles<T, TINY, false>(st, a);
   if (e != hipSuccess) return e;
-  const int cw = col_waves_of<T>(a.d);
-  k_embed_sum<T, WHOLE><<<grid_of(((a.V + 3) / 4 * cw + 3) / 4), 256, 0, st>>>(a, na, out, cw);
+  const int cw = (int)((a.d + 255) / 256);
+  const unsigned grid = grid_of(((a.V + 3) / 4 * cw + 3) / 4);
+  if (TINY && a.d < 4) k_embed_sum<T, true><<<grid, 256, 0, st>>>(a, na, out, cw);  // four columns a lane
+  else k_embed_sum<T, false><<<grid, 256, 0, st>>>(a, na, out, cw);
   return hipGetLastError();
 }
 
@@ -879,17 +919,15 @@ hipError_t launch_embed_norm(hipStream_t st, int dtype, EmbedGradArgs a, void* w
   set_levels(a, a.T);
   a.token_sq = static_cast<float*>(ws);
   a.sums = a.token_sq + token_floats(dtype, a.N, a.d);
-  const bool whole = a.d % (dtype == 1 ? 8 : 4) == 0;
-  if (dtype == 1) return whole ? launch_norm<bf16s, true>(st, a) : launch_norm<bf16s, false>(st, a);
-  return whole ? launch_norm<float, true>(st, a) : launch_norm<float, false>(st, a);
+  if (dtype == 1) return a.d < 8 ? launch_norm<bf16s, true>(st, a) : launch_norm<bf16s, false>(st, a);
+  return a.d < 4 ? launch_norm<float, true>(st, a) : launch_norm<float, false>(st, a);
 }
 
 hipError_t launch_embed_sum(hipStream_t st, int dtype, EmbedGradArgs a, void* ws, const NoiseArgs& na, float* out) {
   set_levels(a, a.N);
   a.sums = static_cast<float*>(ws);
-  const bool whole = a.d % (dtype == 1 ? 8 : 4) == 0;
-  if (dtype == 1) return whole ? launch_sum<bf16s, true>(st, a, na, out) : launch_sum<bf16s, false>(st, a, na, out);
-  return whole ? launch_sum<float, true>(st, a, na, out) : launch_sum<float, false>(st, a, na, out);
+  if (dtype == 1) return a.d < 8 ? launch_sum<bf16s, true>(st, a, na, out) : launch_sum<bf16s, false>(st, a, na, out);
+  return a.d < 4 ? launch_sum<float, true>(st, a, na, out) : launch_sum<float, false>(st, a, na, out);
 }
 
 }  // namespace dpk

@@ -11,15 +11,17 @@
 // written once). A token's words are streamed by one workgroup with a running
 // maximum, sum and weighted sum per thread, joined at the end.
 //
-// The top words come out of the same pass. Each thread knows its largest
-// logit; the K-th largest of these (of 256 groups of threads) is a floor that
-// at least K words reach, and in a row without a pattern hardly more. Only the
-// threads whose own largest reaches it read their words again, collect those
-// that do, and the collected ones are put in order by counting the larger ones.
-// Where too many reach the floor (rows of few different values, words of a
-// mask's value) or fewer than K (rows with NaN, masks that leave almost
-// nothing) the K-th largest is found from counts of the leading digits instead,
-// in further passes over the row.
+// The top words come out of the same pass, which leaves the largest logit of
+// every 16-byte vector of the row (from 2048 vectors on, of every 8
+// neighbouring ones, a cache line). With those dealt to 256 groups, the K-th
+// largest of the groups' is a floor that at least K words reach, and in a row
+// without a pattern hardly more (K = 64: 74 on average). One wave finds it by
+// bisection of its bits, counting with ballots; the vectors or lines that reach
+// it are read once more, by all threads, the words that reach it are collected,
+// and put in order by counting the larger ones. Where too many reach the floor
+// (rows of few different values, words of a mask's value) or fewer than K (rows
+// with NaN, masks that leave almost nothing) the K-th largest is found from
+// counts of the leading digits instead, in further passes over the row.
 //
 // A row whose logits are all -inf has no distribution: logp and the top words'
 // are -inf, H is 0 and the gradient 0. A row with a NaN or +inf gives NaN.
@@ -60,22 +62,37 @@ __device__ __forceinline__ Stat stat_join(Stat a, Stat b, float k) {
   stat_move<ENT>(b, m, k);
   return Stat{m, a.s + b.s, a.u + b.u};
 }
+// top: the largest of the P values
 template <bool ENT, int P>
-__device__ __forceinline__ void stat_add(Stat& r, const float* z, float k) {
-  float m = r.m;
-#pragma unroll
-  for (int e = 0; e < P; ++e) m = fmaxf(m, z[e]);
-  stat_move<ENT>(r, m, k);
+__device__ __forceinline__ void stat_add(Stat& r, const float* z, float top, float k) {
+  stat_move<ENT>(r, fmaxf(r.m, top), k);
 #pragma unroll
   for (int e = 0; e < P; ++e) {
-    const float x = (m - z[e]) * k, t = exp2_hw(-x);
+    const float x = (r.m - z[e]) * k, t = exp2_hw(-x);
     r.s += t;
     if constexpr (ENT) r.u = __builtin_fmaf(t, fminf(x, kFar), r.u);
   }
 }
+template <int P>
+__device__ __forceinline__ float largest(const float* z) {
+  float m = z[0];
+#pragma unroll
+  for (int e = 1; e < P; ++e) m = fmaxf(m, z[e]);
+  return m;
+}
+// The largest of eight neighbouring lanes' values, in each of them (a lane that is switched off does not count).
+__device__ __forceinline__ float largest_of_8(float v) {
+  const auto other = [](float x, auto ctrl) {
+    const int i = (int)__float_as_uint(x);
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(i, i, decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  v = fmaxf(v, other(v, std::integral_constant<int, 0xB1>{}));   // the neighbour
+  v = fmaxf(v, other(v, std::integral_constant<int, 0x4E>{}));   // two lanes on
+  return fmaxf(v, other(v, std::integral_constant<int, 0x141>{}));  // the mirrored lane of the eight
+}
 
-// f(word, P values) over a thread's part of a row: single elements to the first 16-byte boundary, 16-byte vectors,
-// single elements at the end. U vectors in flight.
+// one(word, value) and many(word, P values, vector) over a thread's part of a row: single elements to the first
+// 16-byte boundary, 16-byte vectors, single elements at the end. U vectors in flight.
 template <typename T, int NT, int U, typename F1, typename FP>
 __device__ __forceinline__ void thread_words(const T* z, int64_t V, F1 one, FP many) {
   constexpr int P = elem_traits<T>::per16;
@@ -92,7 +109,7 @@ __device__ __forceinline__ void thread_words(const T* z, int64_t V, F1 one, FP m
       if (i + u * NT >= sn.vecs) break;
       float v[P];
       unpack16<P>(raw[u], v);
-      many(sn.head + (i + u * NT) * P, v);
+      many(sn.head + (i + u * NT) * P, v, i + u * NT);
     }
   }
   const int64_t jt = sn.tail0 + threadIdx.x;
@@ -145,18 +162,29 @@ __device__ __forceinline__ uint64_t place_of(float z, int64_t word) {
   return ((uint64_t)key_of(z) << 32) | (uint32_t)~(uint32_t)word;
 }
 
-// LDS of the selection: 256 groups' maxima or digit counts, and the collected words.
+constexpr int kGroups = 256, kParts = 2048;
+
+// LDS of the selection: the largest logit of every part of the row (a vector, or 8) or the collected words, the groups'
+// largest keys or digit counts, the parts that reach the floor.
 template <int NT>
 struct TopLds {
-  static constexpr int groups = NT < 256 ? NT : 256;
-  static constexpr int cap = NT == 64 ? 512 : 1024;
+  static constexpr int parts = NT == 64 ? 1024 : kParts, cap = NT == 64 ? 512 : 1024;
+  union {  // the words are collected once the parts have been looked through
+    float part[parts];
+    uint64_t found[cap];
+  };
   union {
-    __attribute__((aligned(16))) float best[groups];
+    __attribute__((aligned(16))) uint32_t best[kGroups];
     uint32_t bins[256];
   };
-  uint64_t found[cap];
-  float floor;
-  uint32_t count, digit, above, at;
+  uint16_t reach[cap];
+  uint32_t floor, reaches, count, digit, above, at;
+};
+
+template <>
+struct TopLds<0> {  // no top words
+  static constexpr int parts = 1;
+  float part[1];
 };
 
 // The words whose place is at least `least`.
@@ -170,7 +198,7 @@ __device__ __forceinline__ void collect(const T* z, int64_t V, uint64_t least, T
       if (at < (uint32_t)TopLds<NT>::cap) l.found[at] = p;
     }
   };
-  thread_words<T, NT, 4>(z, V, one, [&](int64_t j, const float* v) {
+  thread_words<T, NT, 1>(z, V, one, [&](int64_t j, const float* v, int64_t) {
 #pragma unroll
     for (int e = 0; e < P; ++e) one(j + e, v[e]);
   });
@@ -203,7 +231,7 @@ __device__ uint64_t least_place(const T* z, int64_t V, int64_t K, TopLds<NT>& l)
         atomicAdd(&l.bins[digit], 1u);
       }
     };
-    thread_words<T, NT, 4>(z, V, one, [&](int64_t j, const float* v) {
+    thread_words<T, NT, 1>(z, V, one, [&](int64_t j, const float* v, int64_t) {
 #pragma unroll
       for (int e = 0; e < P; ++e) one(j + e, v[e]);
     });
@@ -241,58 +269,94 @@ __device__ uint64_t least_place(const T* z, int64_t V, int64_t K, TopLds<NT>& l)
   }
 }
 
-// The row's K top words into top_ids and top_logp. mine: the largest logit that this thread has seen.
+// The K-th largest of the groups' largest keys, its low bits 0 (the 16 that bf16 does not have, or 12), by one wave,
+// four groups a lane.
 template <typename T, int NT>
-__device__ void top_words(const LogprobArgs& a, int64_t row, const T* z, float mine, Stat r, TopLds<NT>& l) {
-  constexpr int P = elem_traits<T>::per16, G = TopLds<NT>::groups, S = NT / G;  // S threads to a group
+__device__ __forceinline__ uint32_t find_floor(int K, const TopLds<NT>& l) {
+  constexpr int last = elem_traits<T>::per16 == 8 ? 16 : 12;
+  const u32x4 best = *reinterpret_cast<const u32x4*>(l.best + 4 * threadIdx.x);
+  uint32_t floor = 0;
+  for (int bit = 31; bit >= last; --bit) {
+    const uint32_t t = floor | (1u << bit);
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) n += __popcll(__ballot(best[u] >= t));
+    if (n >= K) floor = t;
+  }
+  return floor;
+}
+
+// The row's K top words into top_ids and top_logp, from the parts' largest logits in l.part. by8: parts of 8 vectors.
+template <typename T, int NT>
+__device__ __forceinline__ void top_words(const LogprobArgs& a, int64_t row, const T* z, bool by8, Stat r, TopLds<NT>& l) {
+  constexpr int P = elem_traits<T>::per16;
   const int K = (int)a.K;
-  if (threadIdx.x == 0) {
-    l.count = 0;
-    l.floor = INFINITY;
+  const Span<T> sn(z, 0, a.V);
+  const int64_t parts64 = by8 ? (sn.vecs + 7) / 8 : sn.vecs;
+  const int parts = (int)(parts64 < TopLds<NT>::parts ? parts64 : TopLds<NT>::parts);
+  __syncthreads();  // l.part is whole
+  for (int g = threadIdx.x; g < kGroups; g += NT) {
+    float m = -FLT_MAX;
+    for (int p = g; p < parts; p += kGroups) m = fmaxf(m, l.part[p]);
+    l.best[g] = key_of(m);
   }
-  const bool plain = r.s == r.s;  // no NaN, no +inf
-  float best = mine;
-#pragma unroll
-  for (int off = 1; off < S; off <<= 1) best = fmaxf(best, __shfl_xor(best, off, kWave));
-  if (threadIdx.x % S == 0) l.best[threadIdx.x / S] = best;
+  if (threadIdx.x == 0) l.count = l.reaches = 0;
   __syncthreads();
-  {
-    // how many groups are ahead of this one: larger, or equal and before it
-    const int g = threadIdx.x / S, part = threadIdx.x % S;
-    int ahead = 0;
-#pragma unroll 4
-    for (int i = part * (G / S); i < (part + 1) * (G / S); i += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(l.best + i);
-      ahead += (o.x > best || (o.x == best && i < g)) + (o.y > best || (o.y == best && i + 1 < g)) +
-               (o.z > best || (o.z == best && i + 2 < g)) + (o.w > best || (o.w == best && i + 3 < g));
+  if (threadIdx.x < 64) {
+    const uint32_t f = find_floor<T, NT>(K, l);
+    if (threadIdx.x == 0) l.floor = f;
+  }
+  __syncthreads();
+  const uint32_t floor = l.floor;
+  for (int p = threadIdx.x; p < parts; p += NT)
+    if (key_of(l.part[p]) >= floor) {
+      const uint32_t at = atomicAdd(&l.reaches, 1u);
+      if (at < (uint32_t)TopLds<NT>::cap) l.reach[at] = (uint16_t)p;
     }
-#pragma unroll
-    for (int off = 1; off < S; off <<= 1) ahead += __shfl_xor(ahead, off, kWave);
-    if (part == 0 && ahead == K - 1) l.floor = best;
-  }
   __syncthreads();
-  const float floor = l.floor;
-  if (plain && mine >= floor) {
+  const uint32_t reaches = l.reaches;
+  if (r.s == r.s && reaches <= (uint32_t)TopLds<NT>::cap) {  // no NaN, no +inf
     auto one = [&](int64_t j, float v) {
-      if (v >= floor) {
+      if (key_of(v) >= floor) {
         const uint32_t at = atomicAdd(&l.count, 1u);
         if (at < (uint32_t)TopLds<NT>::cap) l.found[at] = place_of(v, j);
       }
     };
-    thread_words<T, NT, 4>(z, a.V, one, [&](int64_t j, const float* v) {
-      float m = v[0];
+    const int64_t j = threadIdx.x, jt = sn.tail0 + threadIdx.x;
+    if (j < sn.head) one(j, to_f32(z[j]));
+    if (jt < a.V) one(jt, to_f32(z[jt]));
+    const u32x4* vz = reinterpret_cast<const u32x4*>(z + sn.head);
+    // a part number stands for all that share it: parts, 2 * parts ... on (rows of very many words)
+    const int shift = by8 ? 3 : 0;
+    const uint32_t work = reaches << shift;
+    constexpr int U = 2;
+    for (int64_t first = 0; first < sn.vecs; first += (int64_t)TopLds<NT>::parts << shift) {
+      for (uint32_t i0 = threadIdx.x; i0 < work; i0 += U * NT) {
+        u32x4 raw[U];
+        int64_t at[U];
 #pragma unroll
-      for (int e = 1; e < P; ++e) m = fmaxf(m, v[e]);
-      if (m >= floor) {
+        for (int u = 0; u < U; ++u) {
+          const uint32_t i = i0 + u * NT;
+          at[u] = i < work ? first + ((int64_t)l.reach[i >> shift] << shift) + (i & ((1u << shift) - 1)) : sn.vecs;
+          raw[u] = u32x4{0u, 0u, 0u, 0u};
+          if (at[u] < sn.vecs) raw[u] = vz[at[u]];
+        }
 #pragma unroll
-        for (int e = 0; e < P; ++e) one(j + e, v[e]);
+        for (int u = 0; u < U; ++u) {
+          if (at[u] >= sn.vecs) continue;
+          float v[P];
+          unpack16<P>(raw[u], v);
+          if (key_of(largest<P>(v)) < floor) continue;
+#pragma unroll
+          for (int e = 0; e < P; ++e) one(sn.head + at[u] * P + e, v[e]);
+        }
       }
-    });
+    }
   }
   __syncthreads();
   uint32_t n = l.count;
-  __syncthreads();
   if (n < (uint32_t)K || n > (uint32_t)TopLds<NT>::cap) {  // uniform
+    __syncthreads();  // count is read before it is cleared
     const uint64_t least = least_place<T, NT>(z, a.V, K, l);
     if (threadIdx.x == 0) l.count = 0;
     __syncthreads();
@@ -312,16 +376,17 @@ __device__ void top_words(const LogprobArgs& a, int64_t row, const T* z, float m
       a.top_logp[row * K + rank] = r.s == 0.0f ? -INFINITY : __builtin_fmaf(v - r.m, inv_tau, -log_s);
     }
   }
-  __syncthreads();  // found and best are reused by the next row
+  __syncthreads();  // found and the parts are written again by the next row
 }
 
 }  // namespace
 
 // One workgroup per token.
 template <typename T, int NT, bool ENT, bool TOP>
-__global__ __launch_bounds__(NT) void k_token_logprob(LogprobArgs a) {
+__global__ __launch_bounds__(NT, 8) void k_token_logprob(LogprobArgs a) {
   constexpr int P = elem_traits<T>::per16;
   __shared__ float red[3 * NT / 64];
+  __shared__ TopLds<TOP ? NT : 0> lds;
   const float k = kLog2e / a.tau;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* z = static_cast<const T*>(a.logits) + row * a.V;
@@ -329,9 +394,24 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LogprobArgs a) {
     const bool given = y >= 0 && y < a.V;
     const float zy = given ? to_f32(z[y]) : 0.0f;
     Stat r = stat_empty();
-    thread_words<T, NT, 4>(z, a.V, [&](int64_t, float v) { stat_add<ENT, 1>(r, &v, k); },
-                           [&](int64_t, const float* v) { stat_add<ENT, P>(r, v, k); });
-    const float mine = r.m;
+    // whether a part of the row is 8 vectors, and the vectors that a part number stands for again behind them
+    const bool by8 = TOP && a.V / P > TopLds<NT>::parts;
+    constexpr int kSpan = TopLds<NT>::parts * 8;
+    thread_words<T, NT, 4>(
+        z, a.V, [&](int64_t, float v) { stat_add<ENT, 1>(r, &v, v, k); },
+        [&](int64_t, const float* v, int64_t i) {
+          const float top = largest<P>(v);
+          if (TOP) {
+            if (by8) {
+              const float m = largest_of_8(top);
+              float& part = lds.part[((uint32_t)i & (kSpan - 1)) >> 3];
+              if ((i & 7) == 0) part = i < kSpan ? m : fmaxf(part, m);
+            } else {
+              lds.part[i] = top;
+            }
+          }
+          stat_add<ENT, P>(r, v, top, k);
+        });
     r = block_stat<ENT, NT>(r, k, red);
     if (threadIdx.x == 0) {
       const bool none = r.s == 0.0f;  // every logit is -inf
@@ -341,10 +421,7 @@ __global__ __launch_bounds__(NT) void k_token_logprob(LogprobArgs a) {
       a.stats[2 * row + 1] = log_s;
       if (ENT) a.entropy[row] = none ? 0.0f : log_s + kLn2 * (r.u / r.s);
     }
-    if constexpr (TOP) {
-      __shared__ TopLds<NT> lds;
-      top_words<T, NT>(a, row, z, mine, r, lds);
-    }
+    if constexpr (TOP) top_words<T, NT>(a, row, z, by8, r, lds);
   }
 }
 
@@ -453,9 +530,9 @@ hipError_t launch_bwd(hipStream_t st, const LogprobArgs& a) {
 
 // Threads for a token's words. Few tokens: as many as a workgroup may have, so
 // that a row is few loads of each. Many tokens of a small vocabulary: a wave
-// each (which takes up to 32 top words).
+// each.
 int logprob_threads(int64_t rows, int64_t V, int64_t K) {
-  if (K <= 32 && (V <= 256 || (rows > 512 && V <= 4096))) return 64;
+  if (V <= 256 || (rows > 512 && V <= 4096)) return 64;
   if (rows > 512 || V <= 2048) return 256;
   return rows > 256 || V <= 4096 ? 512 : 1024;
 }
