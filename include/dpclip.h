@@ -523,8 +523,8 @@ dp_status dp_embedding(void* stream, const int64_t* ids, const void* weight, dp_
 
 /*
  * The tokens in the order of their words, for the table's gradient: order [N]
- * int64 holds the tokens sorted by word, those of one word ascending, dropped
- * ones last; the places of word w are [starts[w], starts[w + 1]) (starts:
+ * int64 holds word * 2^32 + token of every token, ascending, with word V for a
+ * dropped one; the places of word w are [starts[w], starts[w + 1]) (starts:
  * [V + 1] int64, starts[V] the number of tokens that are not dropped).
  *
  *  workspace  at least dp_embedding_order_workspace_bytes(N, V) bytes.
@@ -540,13 +540,12 @@ size_t dp_embedding_order_workspace_bytes(int64_t N, int64_t V);
  *   sqnorm[b] (+)= scale^2 * sum_w || sum_{t: ids[b][t] = w} G[b][t] ||^2
  *
  *  G        [B, T, d], dtype, aligned to its element; B*T below 2^31.
- *  ids, order  as dp_embedding_order took and left them (N = B*T). With other
+ *  order    as dp_embedding_order left it for ids (N = B*T). With other
  *           contents the result means nothing; nothing outside is accessed.
  *  sqnorm   [B] fp32, overwritten (accumulate == 0) or added to.
  *  workspace  at least dp_embedding_workspace_bytes(...) bytes.
  */
-dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const int64_t* ids, const int64_t* order,
-                            int64_t B, int64_t T, int64_t V, int64_t d, float scale, void* workspace, size_t ws_bytes,
+dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const int64_t* order, int64_t B, int64_t T, int64_t V, int64_t d, float scale, void* workspace, size_t ws_bytes,
                             float* sqnorm, int32_t accumulate);
 
 /*
@@ -557,13 +556,14 @@ dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const i
  * as dp_clipped_sum_noise forms it for a layer of V rows; a word without a
  * token gets the noise alone.
  *
- *  G, ids, order, B, T, V, d, workspace  as in dp_embedding_norm; starts as
+ *  G, order, B, T, V, d, workspace  as in dp_embedding_norm; starts as
  *           dp_embedding_order left it; also ceil(V/4)*d < 2^32.
- *  c, C, sigma, denom, seed, layer_id, step  as in dp_clipped_sum_noise.
+ *  c, C, sigma, denom, seed, layer_id, step  as in dp_clipped_sum_noise. The
+ *           rows of a sample with factor 0 have to be finite (0 * inf is NaN).
  *  out      [V, d] fp32 (the layout of a torch Embedding's weight).
  */
-dp_status dp_embedding_clipped_sum_noise(void* stream, const void* G, dp_dtype dtype, const int64_t* ids,
-                                         const int64_t* order, const int64_t* starts, int64_t B, int64_t T, int64_t V,
+dp_status dp_embedding_clipped_sum_noise(void* stream, const void* G, dp_dtype dtype, const int64_t* order,
+                                         const int64_t* starts, int64_t B, int64_t T, int64_t V,
                                          int64_t d, float scale, const float* c, float C, float sigma, float denom,
                                          uint64_t seed, uint32_t layer_id, uint32_t step, void* workspace,
                                          size_t ws_bytes, float* out);

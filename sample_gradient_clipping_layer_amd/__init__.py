@@ -211,9 +211,9 @@ def _declare(lib):
     lib.dp_embedding_order.restype = c_i32
     lib.dp_embedding_order_workspace_bytes.argtypes = [c_i64, c_i64]
     lib.dp_embedding_order_workspace_bytes.restype = sz
-    lib.dp_embedding_norm.argtypes = [vp, vp, c_i32, vp, vp, c_i64, c_i64, c_i64, c_i64, f, vp, sz, fp, c_i32]
+    lib.dp_embedding_norm.argtypes = [vp, vp, c_i32, vp, c_i64, c_i64, c_i64, c_i64, f, vp, sz, fp, c_i32]
     lib.dp_embedding_norm.restype = c_i32
-    lib.dp_embedding_clipped_sum_noise.argtypes = [vp, vp, c_i32, vp, vp, vp, c_i64, c_i64, c_i64, c_i64, f, fp, f, f, f,
+    lib.dp_embedding_clipped_sum_noise.argtypes = [vp, vp, c_i32, vp, vp, c_i64, c_i64, c_i64, c_i64, f, fp, f, f, f,
                                                    c_u64, c_u32, c_u32, vp, sz, fp]
     lib.dp_embedding_clipped_sum_noise.restype = c_i32
     lib.dp_embedding_workspace_bytes.argtypes = [c_i32, c_i64, c_i64, c_i64, c_i64]
@@ -847,8 +847,9 @@ def dp_embedding_order_workspace_bytes(N: int, V: int) -> int:
 
 
 def dp_embedding_order(ids, V: int, order, starts, workspace=None, stream=None):
-    """The tokens sorted by word: order [ids.numel()] and starts [V + 1] (word
-    w's places are starts[w] .. starts[w + 1]), all int64; dropped tokens last."""
+    """The tokens sorted by word: order [ids.numel()], word * 2**32 + token
+    ascending (word V for a dropped one), and starts [V + 1] (word w's places
+    are starts[w] .. starts[w + 1]), all int64."""
     import torch
     i64, N = (torch.int64,), ids.numel()
     if N < 1:
@@ -884,7 +885,7 @@ def dp_embedding_norm(G, ids, order, starts, sqnorm, scale: float = 1.0, accumul
     st, dt, B, T, V, d = _embedding_grad(G, ids, order, starts, sqnorm, "sqnorm", stream)
     ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_embedding_workspace_bytes(dt, B, T, V, d), G.device, stream)
     _check("dp_embedding_norm", lib().dp_embedding_norm(
-        st, G.data_ptr(), dt, ids.data_ptr(), order.data_ptr(), B, T, V, d, scale, ws, nbytes, sqnorm.data_ptr(),
+        st, G.data_ptr(), dt, order.data_ptr(), B, T, V, d, scale, ws, nbytes, sqnorm.data_ptr(),
         1 if accumulate else 0))
 
 
@@ -894,7 +895,7 @@ def dp_embedding_clipped_sum_noise(G, ids, order, starts, c, C: float, sigma: fl
     st, dt, B, T, V, d = _embedding_grad(G, ids, order, starts, c, "c", stream, ("out", out))
     ws, nbytes, _held = _lm_workspace(workspace, lambda: dp_embedding_workspace_bytes(dt, B, T, V, d), G.device, stream)
     _check("dp_embedding_clipped_sum_noise", lib().dp_embedding_clipped_sum_noise(
-        st, G.data_ptr(), dt, ids.data_ptr(), order.data_ptr(), starts.data_ptr(), B, T, V, d, scale, c.data_ptr(), C,
+        st, G.data_ptr(), dt, order.data_ptr(), starts.data_ptr(), B, T, V, d, scale, c.data_ptr(), C,
         sigma, denom, int(seed) & 0xFFFFFFFFFFFFFFFF, int(layer_id) & 0xFFFFFFFF, int(step) & 0xFFFFFFFF, ws, nbytes,
         out.data_ptr()))
 

@@ -249,15 +249,14 @@ size_t dp_embedding_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_
   return dtype_ok(dtype) && check_embedding(B, T, V, d) == DP_OK ? dpk::embed_ws_bytes(dtype, B, T, d) : 0;
 }
 
-dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const int64_t* ids, const int64_t* order,
-                            int64_t B, int64_t T, int64_t V, int64_t d, float scale, void* workspace, size_t ws_bytes,
+dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const int64_t* order, int64_t B, int64_t T, int64_t V, int64_t d, float scale, void* workspace, size_t ws_bytes,
                             float* sqnorm, int32_t accumulate) {
-  if (!G || !ids || !order || !sqnorm) return DP_ERR_NULL;
+  if (!G || !order || !sqnorm) return DP_ERR_NULL;
   dp_status s = check_embedding(B, T, V, d);
   if (s != DP_OK) return s;
   if (!dtype_ok(dtype)) return DP_ERR_DTYPE;
   if (!finite(scale)) return DP_ERR_VALUE;
-  if (!aligned(G, elem_bytes(dtype)) || !aligned(ids, 8) || !aligned(order, 8) || !aligned(sqnorm, 4))
+  if (!aligned(G, elem_bytes(dtype)) || !aligned(order, 8) || !aligned(sqnorm, 4))
     return DP_ERR_ALIGN;
   s = check_workspace(workspace, ws_bytes, dpk::embed_ws_bytes(dtype, B, T, d));
   if (s != DP_OK) return s;
@@ -265,7 +264,6 @@ dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const i
   if (s != DP_OK) return s;
   dpk::EmbedGradArgs a{};
   a.G = G;
-  a.ids = ids;
   a.order = order;
   a.N = B * T;
   a.B = B;
@@ -279,19 +277,19 @@ dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const i
   return hip_status(dpk::launch_embed_norm(static_cast<hipStream_t>(stream), dtype, a, workspace));
 }
 
-dp_status dp_embedding_clipped_sum_noise(void* stream, const void* G, dp_dtype dtype, const int64_t* ids,
-                                         const int64_t* order, const int64_t* starts, int64_t B, int64_t T, int64_t V,
+dp_status dp_embedding_clipped_sum_noise(void* stream, const void* G, dp_dtype dtype, const int64_t* order,
+                                         const int64_t* starts, int64_t B, int64_t T, int64_t V,
                                          int64_t d, float scale, const float* c, float C, float sigma, float denom,
                                          uint64_t seed, uint32_t layer_id, uint32_t step, void* workspace,
                                          size_t ws_bytes, float* out) {
-  if (!G || !ids || !order || !starts || !c || !out) return DP_ERR_NULL;
+  if (!G || !order || !starts || !c || !out) return DP_ERR_NULL;
   dp_status s = check_embedding(B, T, V, d);
   if (s != DP_OK) return s;
   if ((V + 3) / 4 >= ((int64_t)1 << 32) / d) return DP_ERR_SHAPE;  // noise group index fits 32 bits
   if (!dtype_ok(dtype)) return DP_ERR_DTYPE;
   if (!finite(scale) || !finite(C) || !(C > 0.0f) || !finite(sigma) || sigma < 0.0f || !finite(denom) || !(denom > 0.0f))
     return DP_ERR_VALUE;
-  if (!aligned(G, elem_bytes(dtype)) || !aligned(ids, 8) || !aligned(order, 8) || !aligned(starts, 8) ||
+  if (!aligned(G, elem_bytes(dtype)) || !aligned(order, 8) || !aligned(starts, 8) ||
       !aligned(c, 4) || !aligned(out, 4))
     return DP_ERR_ALIGN;
   s = check_workspace(workspace, ws_bytes, dpk::embed_ws_bytes(dtype, B, T, d));
@@ -300,7 +298,6 @@ dp_status dp_embedding_clipped_sum_noise(void* stream, const void* G, dp_dtype d
   if (s != DP_OK) return s;
   dpk::EmbedGradArgs a{};
   a.G = G;
-  a.ids = ids;
   a.order = order;
   a.starts = starts;
   a.c = c;

@@ -2,8 +2,8 @@
 // and the clipping of the table's gradient.
 //
 //   lookup:  out[n] = scale * W[ids[n]]  (0 for an id outside [0, V): a dropped token)
-//   order:   the tokens n sorted by word, tokens of one word ascending, dropped
-//            ones last; word w's places are [starts[w], starts[w + 1])
+//   order:   word 2^32 + token of every token, ascending, dropped ones (word V) last; the places of word w are
+//            [starts[w], starts[w + 1])
 //   norm:    sqnorm[b] = scale^2 * sum_w || sum_{t: ids[b][t] = w} G[b][t] ||^2
 //   sum:     out[w] = (scale * sum_{n of w} c[sample of n] * G[n] + (sigma C) z_w) / denom, every word of the table
 //
@@ -17,13 +17,15 @@
 // neighbouring places (and of 16 such tiles, and so on) that lies within one
 // run, and what reads a run takes whole tiles from there. Sums are formed in
 // fp32 in an order that the sizes and the ids alone decide; nothing is atomic
-// but the counts of the sort, which are whole numbers.
+// but the counts of the sort, which are whole numbers. A place holds its word
+// beside its token, so that finding a run's ends takes no second load.
 //
 // The sort is by digits of the word, least significant first, each digit in a
 // launch of its own: a workgroup ranks the tokens of its tile by digit (within
 // a wave by ballots, in order), and finds where its share of every digit goes
-// from the counts that all workgroups left. Places and starts are checked
-// where they are read: whatever they hold, accesses stay inside the tensors.
+// from the counts that all workgroups left. Up to 4096 tokens are sorted by one
+// workgroup in one launch. Places and starts are checked where they are read:
+// whatever they hold, accesses stay inside the tensors.
 #include "dp_common.hpp"
 #include "dp_lm.hpp"
 #include "dp_noise.hpp"
@@ -100,6 +102,7 @@ namespace {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortMaxDigits = 512;
+constexpr int kSortSmall = 4096;  // tokens that one workgroup sorts in one launch
 constexpr int kSortDirect = 64;  // workgroups whose counts each workgroup adds up by itself
 
 // How the sort of N ids over V words goes: digits per pass, ids per workgroup.
@@ -129,6 +132,10 @@ SortPlan sort_plan(int64_t N, int64_t V) {
 }
 
 __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V) { return id < 0 || id >= V ? (uint32_t)V : (uint32_t)id; }
+
+__device__ __forceinline__ int64_t place_of(uint32_t word, uint32_t tok) {
+  return (int64_t)(((uint64_t)word << 32) | tok);
+}
 
 // The lanes of `among` whose value's bits [0, bits) are this lane's.
 __device__ __forceinline__ uint64_t same_bits(uint64_t among, uint32_t value, int bits) {
@@ -264,7 +271,7 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const int64_t* _
     __builtin_amdgcn_wave_barrier();
     if (in) {
       keys_out[to] = key;
-      if (order) order[to] = tok;
+      if (order) order[to] = place_of(key, tok);
       else toks_out[to] = tok;
     }
     if (next_counts) {
@@ -277,6 +284,85 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const int64_t* _
       if (in && (tile != first_tile || (twins & below) == 0))
         atomicAdd(&next_counts[(int64_t)tile * D + next], tile != first_tile ? 1u : (uint32_t)__popcll(twins));
     }
+  }
+}
+
+// All digits of up to 4096 tokens by one workgroup, the tokens in LDS between
+// the passes; the keys in order are left for the starts.
+__global__ __launch_bounds__(kSortThreads) void k_order_small(const int64_t* __restrict__ ids, int N, int64_t V, SortPlan p,
+                                                              uint32_t* __restrict__ keys_out,
+                                                              int64_t* __restrict__ order) {
+  __shared__ uint32_t keys[2][kSortSmall];
+  __shared__ uint16_t toks[2][kSortSmall];
+  __shared__ uint32_t seen[kSortWaves][kSortMaxDigits];
+  __shared__ uint32_t scan[kSortWaves];
+  const int D = p.digits();
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int rounds = (N + kSortThreads - 1) / kSortThreads, w0 = wave * 64 * rounds;
+  const uint64_t below = lane == 0 ? 0 : (~0ull >> (64 - lane));
+  for (int i = threadIdx.x; i < N; i += kSortThreads) {
+    keys[0][i] = key_of(ids[i], V);
+    toks[0][i] = (uint16_t)i;
+  }
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const uint32_t* key = keys[pass & 1];
+    const uint16_t* tok = toks[pass & 1];
+    const int shift = pass * p.bits;
+    for (int k = threadIdx.x; k < kSortWaves * D; k += kSortThreads) seen[k / D][k % D] = 0;
+    __syncthreads();
+    for (int r = 0; r < rounds; ++r) {
+      const int i = w0 + r * 64 + lane;
+      const uint32_t digit = ((i < N ? key[i] : 0u) >> shift) & (D - 1);
+      const uint64_t same = same_bits(__ballot(i < N), digit, p.bits);
+      if (i < N && (same & below) == 0) seen[wave][digit] += (uint32_t)__popcll(same);
+    }
+    __syncthreads();
+    uint32_t mine = 0;
+    if ((int)threadIdx.x < D) {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) mine += seen[w][threadIdx.x];
+    }
+    uint32_t run = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const uint32_t o = __shfl_up(run, off, kWave);
+      if (lane >= off) run += o;
+    }
+    if (lane == 63) scan[wave] = run;
+    __syncthreads();
+    if ((int)threadIdx.x < D) {
+      uint32_t s = run - mine;
+      for (int w = 0; w < wave; ++w) s += scan[w];
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        const uint32_t c = seen[w][threadIdx.x];
+        seen[w][threadIdx.x] = s;
+        s += c;
+      }
+    }
+    __syncthreads();
+    const bool last = pass + 1 == p.passes;
+    for (int r = 0; r < rounds; ++r) {
+      const int i = w0 + r * 64 + lane;
+      const bool in = i < N;
+      const uint32_t k = in ? key[i] : 0u, digit = (k >> shift) & (D - 1);
+      const uint64_t same = same_bits(__ballot(in), digit, p.bits);
+      uint32_t to = 0;
+      if (in) to = seen[wave][digit] + (uint32_t)__popcll(same & below);
+      __builtin_amdgcn_wave_barrier();  // every lane has read its digit's place before one moves it on
+      if (in && (same & below) == 0) seen[wave][digit] = to + (uint32_t)__popcll(same);
+      __builtin_amdgcn_wave_barrier();
+      if (in) {
+        if (last) {
+          keys_out[to] = k;
+          order[to] = place_of(k, tok[i]);
+        } else {
+          keys[(pass + 1) & 1][to] = k;
+          toks[(pass + 1) & 1][to] = tok[i];
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -336,21 +422,23 @@ constexpr int kTile = kEmbedTile;
 // This wave's number in its workgroup, in a scalar register: what follows from it is the wave's, not a lane's.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
 
-// The token of a place, or -1 if it is none or the place's entry is no token.
-__device__ __forceinline__ int64_t token_at(const EmbedGradArgs& a, int64_t i) {
-  const int64_t n = a.order[i];
-  return n >= 0 && n < a.N ? n : -1;
-}
+__device__ __forceinline__ uint32_t sample_of(const EmbedGradArgs& a, int tok) { return fast_div((uint32_t)tok, a.by_t); }
 
-__device__ __forceinline__ uint32_t sample_of(const EmbedGradArgs& a, int64_t n) { return fast_div((uint32_t)n, a.by_t); }
-
-// What a run of places shares: the word, and for the norm the sample too. Dropped tokens have none.
+// A place's token, -1 if it holds none, and what its run shares: the word, and for the norm the sample too; -1 for a
+// dropped token.
+struct Place {
+  int tok;
+  int64_t run;
+};
 template <bool NORM>
-__device__ __forceinline__ int64_t run_of(const EmbedGradArgs& a, int64_t n) {
-  if (n < 0) return -1;
-  const int64_t id = a.ids[n];
-  if (id < 0 || id >= a.V) return -1;
-  return NORM ? id * a.B + sample_of(a, n) : id;
+__device__ __forceinline__ Place place_at(const EmbedGradArgs& a, int64_t i) {
+  const int64_t o = a.order[i], word = o >> 32, tok = o & 0xFFFFFFFF;
+  Place p{-1, -1};
+  if (tok < a.N) {
+    p.tok = (int)tok;
+    if (word >= 0 && word < a.V) p.run = NORM ? word * a.B + sample_of(a, p.tok) : word;
+  }
+  return p;
 }
 
 // What is read in place of a row that is not there, so that loads of several rows need no branches between them.
@@ -414,6 +502,14 @@ struct Cols {
 #pragma unroll
     for (int e = 0; e < P; ++e) acc[e] += v[e];
   }
+  // past the caches; rows at 16-byte boundaries of a multiple of P columns
+  __device__ __forceinline__ void stream_sums(float* row, const float* acc) const {
+#pragma unroll
+    for (int q = 0; q < P / 4; ++q) {
+      const f32x4 v{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+      if (on) __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(row + at + 4 * q));
+    }
+  }
   // a row's columns that two lanes hold are stored by both, with the same value
   __device__ __forceinline__ void put_sums(float* row, const float* acc) const {
     if (TINY) {
@@ -435,17 +531,21 @@ __device__ __forceinline__ int64_t lane_int64(int64_t v, int lane) {
   return (int64_t)(((uint64_t)(uint32_t)lane_int((int)(v >> 32), lane) << 32) | (uint32_t)lane_int((int)v, lane));
 }
 
-// The tokens of places [s, min(s + 64, e)) and their samples' factors (1 without), a place a lane; -1 for none.
+// The places [s, min(s + 64, e)), a lane each: their tokens (-1 for none) and their samples' factors (1 without).
 struct Places {
   int tok;
   float f;
+  int64_t run;
 };
+template <bool NORM>
 __device__ __forceinline__ Places places_at(const EmbedGradArgs& a, int64_t s, int64_t e) {
   const int64_t i = s + (threadIdx.x & 63);
-  Places p{-1, 0.f};
+  Places p{-1, 0.f, -1};
   if (i < e) {
-    p.tok = (int)token_at(a, i);
-    if (p.tok >= 0) p.f = a.c ? a.c[sample_of(a, p.tok)] : 1.0f;
+    const Place q = place_at<NORM>(a, i);
+    p.tok = q.tok;
+    p.run = q.run;
+    if (p.tok >= 0) p.f = NORM ? 1.0f : a.c[sample_of(a, p.tok)];
   }
   return p;
 }
@@ -460,11 +560,11 @@ __device__ __forceinline__ void add_places(const EmbedGradArgs& a, const C& cols
   for (int u = 0; u < U; ++u) C::add(acc, raw[u], lane_float(p.f, r0 + u));
 }
 
-// acc += the rows of places [s, e), weighted by their samples' factors (a.c != null), by a wave. Places of one run.
-template <typename C>
+// acc += the rows of places [s, e) (the sum: times their samples' factors), by a wave. Places of one run.
+template <bool NORM, typename C>
 __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, const C& cols, float* acc, int64_t s, int64_t e) {
   for (; s < e; s += 64) {
-    const Places p = places_at(a, s, e);
+    const Places p = places_at<NORM>(a, s, e);
     const int m = (int)(e - s < 64 ? e - s : 64);
 #pragma unroll 1
     for (int r = 0; r < m; r += 8) add_places<8>(a, cols, acc, p, r);
@@ -473,15 +573,15 @@ __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, const C& cols, 
 
 // The same with whole tiles taken from their sums: the ends by places, then
 // by tiles of 16, of 256 and so on, up to the highest level there is.
-template <typename C>
+template <bool NORM, typename C>
 __device__ __forceinline__ void add_run(const EmbedGradArgs& a, const C& cols, float* acc, int64_t s, int64_t e) {
   const int64_t up = (s + kTile - 1) / kTile * kTile, down = e / kTile * kTile;
   if (a.levels == 0 || up >= down) {
-    add_rows(a, cols, acc, s, e);
+    add_rows<NORM>(a, cols, acc, s, e);
     return;
   }
-  add_rows(a, cols, acc, s, up);
-  add_rows(a, cols, acc, down, e);
+  add_rows<NORM>(a, cols, acc, s, up);
+  add_rows<NORM>(a, cols, acc, down, e);
   int64_t lo = up / kTile, hi = down / kTile;
   for (int l = 0; lo < hi; ++l) {
     const float* sums = a.sums + a.level_at[l] * a.d;
@@ -516,16 +616,16 @@ __global__ __launch_bounds__(1024) void k_embed_tiles(EmbedGradArgs a, int l, in
     const int64_t group = item / col_waves, tile = group * kTile + wave;
     const C cols(((int)(item - group * col_waves) * 64 + lane) * P, a.d);
     int64_t first = -1, last = -2;
-    Places p{-1, 0.f};
+    Places p{-1, 0.f, -1};
     if (tile < tiles) {
       const int64_t i0 = tile * span;
       int64_t r = -1;
       if (l == 0) {  // every place: its row is read if they are one run
-        p = places_at(a, i0, i0 + kTile);
-        if (lane < kTile) r = run_of<NORM>(a, p.tok);
+        p = places_at<NORM>(a, i0, i0 + kTile);
+        r = p.run;
         last = lane_int64(r, kTile - 1);
       } else {
-        if (lane < 2) r = run_of<NORM>(a, token_at(a, lane == 0 ? i0 : i0 + span - 1));
+        if (lane < 2) r = place_at<NORM>(a, lane == 0 ? i0 : i0 + span - 1).run;
         last = lane_int64(r, 1);
       }
       first = lane_int64(r, 0);
@@ -583,12 +683,10 @@ __global__ __launch_bounds__(256, 4) void k_embed_norm(EmbedGradArgs a, int col_
     const int m = (int)(a.N - i0 < R ? a.N - i0 : R);  // this wave's places
     // lane k + 1 holds place i0 + k; lane 0 the one before, further lanes those behind
     const int64_t i = i0 - 1 + lane;
-    int n = -1;
-    int64_t run = -1;
-    if (i >= 0 && i < a.N) {
-      n = (int)token_at(a, i);
-      run = run_of<true>(a, n);
-    }
+    Place here{-1, -1};
+    if (i >= 0 && i < a.N) here = place_at<true>(a, i);
+    const int n = here.tok;
+    const int64_t run = here.run;
     const int64_t prev = __shfl_up(run, 1, kWave);
     const uint64_t heads = __ballot(lane > 0 && run >= 0 && run != prev);
     const uint64_t goes_on = __ballot(lane > 0 && run >= 0 && run == prev);  // same run as the place before
@@ -610,7 +708,7 @@ __global__ __launch_bounds__(256, 4) void k_embed_norm(EmbedGradArgs a, int col_
         const int64_t same = lane_int64(run, m);
         while (end < a.N) {
           const int64_t j = end + lane;
-          const uint64_t stops = __ballot(j >= a.N || run_of<true>(a, token_at(a, j < a.N ? j : a.N - 1)) != same);
+          const uint64_t stops = __ballot(j >= a.N || place_at<true>(a, j < a.N ? j : a.N - 1).run != same);
           if (stops) {
             end += __builtin_ctzll(stops);
             break;
@@ -645,7 +743,7 @@ __global__ __launch_bounds__(256, 4) void k_embed_norm(EmbedGradArgs a, int col_
           }
         }
         if (tail) {
-          add_run(a, cols, acc, i0 + m, end);
+          add_run<true>(a, cols, acc, i0 + m, end);
 #pragma unroll
           for (int e = 0; e < P; ++e) sq_tail = __builtin_fmaf(acc[e], e < cols.skip ? 0.f : acc[e], sq_tail);
         }
@@ -688,6 +786,7 @@ __global__ __launch_bounds__(256, 5) void k_embed_sum(EmbedGradArgs a, NoiseArgs
   constexpr int P = 4;
   using C = Cols<T, P, TINY>;
   const int lane = threadIdx.x & 63;
+  const bool stream = !TINY && a.d % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
   const int64_t groups = (a.V + 3) / 4, items = groups * col_waves;
   for (int64_t item = (int64_t)blockIdx.x * 4 + wave_id(); item < items; item += (int64_t)gridDim.x * 4) {
     const int64_t g = item / col_waves;
@@ -707,10 +806,10 @@ __global__ __launch_bounds__(256, 5) void k_embed_sum(EmbedGradArgs a, NoiseArgs
     for (int k = 0; k < 5; ++k) at[k] = lane_int64(st, k);
     bool few = at[0] <= at[1] && at[1] <= at[2] && at[2] <= at[3] && at[3] <= at[4] && at[4] - at[0] <= 64;
     if (few) {  // the rows of all four words, read together
-      constexpr int U = 8;
+      constexpr int U = 4;
       const int m = (int)(at[4] - at[0]);
-      Places p{-1, 0.f};
-      if (m > 0) p = places_at(a, at[0], at[4]);
+      Places p{-1, 0.f, -1};
+      if (m > 0) p = places_at<false>(a, at[0], at[4]);
       const int e1 = (int)(at[1] - at[0]), e2 = (int)(at[2] - at[0]), e3 = (int)(at[3] - at[0]);
 #pragma unroll 1
       for (int r = 0; r < m; r += U) {
@@ -729,7 +828,7 @@ __global__ __launch_bounds__(256, 5) void k_embed_sum(EmbedGradArgs a, NoiseArgs
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (4 * g + k < a.V && at[k] < at[k + 1]) add_run(a, cols, acc[k], at[k], at[k + 1]);
+        if (4 * g + k < a.V && at[k] < at[k + 1]) add_run<false>(a, cols, acc[k], at[k], at[k + 1]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -749,8 +848,11 @@ __global__ __launch_bounds__(256, 5) void k_embed_sum(EmbedGradArgs a, NoiseArgs
         for (int e = 0; e < P; ++e) acc[k][e] *= na.inv_denom;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (4 * g + k < a.V) cols.put_sums(out + (4 * g + k) * a.d, acc[k]);
+    for (int k = 0; k < 4; ++k) {
+      if (4 * g + k >= a.V) break;
+      if (stream) cols.stream_sums(out + (4 * g + k) * a.d, acc[k]);
+      else cols.put_sums(out + (4 * g + k) * a.d, acc[k]);
+    }
   }
 }
 
@@ -810,12 +912,12 @@ hipError_t launch_sum(hipStream_t st, const EmbedGradArgs& a, const NoiseArgs& n
   return hipGetLastError();
 }
 
-// Levels of tiles for runs of up to `longest` places: none up to 32, else as many as leave a run at most 128
+// Levels of tiles for runs of up to `longest` places: none up to 64, else as many as leave a run at most 128
 // tiles of the highest.
 int levels_for(int64_t N, int64_t longest) {
   int levels = 0;
   int64_t n = N;
-  while (levels < kEmbedMaxLevels && longest > (levels ? 128 : 32) && n >= kTile) {
+  while (levels < kEmbedMaxLevels && longest > (levels ? 128 : 64) && n >= kTile) {
     ++levels;
     longest /= kTile;
     n /= kTile;
@@ -881,6 +983,15 @@ hipError_t launch_embed_order(hipStream_t st, const int64_t* ids, int64_t N, int
   uint32_t* totals = counts + p.passes * p.blocks * D;
   uint32_t* lists = totals + D;  // keys, tokens, keys, tokens
   const bool summed = p.blocks > kSortDirect;
+  auto find_starts = [&](const uint32_t* keys) {
+    k_order_starts<<<grid_of((V + 256) / 256), 256, 0, st>>>(keys, N, V, starts);
+    return hipGetLastError();
+  };
+  if (N <= kSortSmall) {
+    k_order_small<<<1, kSortThreads, 0, st>>>(ids, (int)N, V, p, lists, order);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? find_starts(lists) : e;
+  }
   k_order_count<<<(unsigned)p.blocks, kSortThreads, 0, st>>>(ids, N, V, p, counts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -899,10 +1010,7 @@ hipError_t launch_embed_order(hipStream_t st, const int64_t* ids, int64_t N, int
         summed ? totals : nullptr, last ? nullptr : c + p.blocks * D, out, out + list, last ? order : nullptr);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (last) {
-      k_order_starts<<<grid_of((V + 256) / 256), 256, 0, st>>>(out, N, V, starts);
-      e = hipGetLastError();
-    }
+    if (last) e = find_starts(out);
   }
   return e;
 }

@@ -86,10 +86,9 @@ struct EmbedArgs {
 };
 struct EmbedGradArgs {
   const void* G;         // [N][d]
-  const int64_t* ids;    // [N]
   const int64_t* order;  // [N]
   const int64_t* starts; // [V + 1] (sum)
-  const float* c;        // [B] (sum), null: 1
+  const float* c;        // [B] (sum)
   int64_t N, B, T, V, d; // N = B T
   FastDiv by_t;
   float scale;

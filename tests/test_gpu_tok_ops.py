@@ -173,7 +173,8 @@ def test_embedding_beside_its_neighbours():
 
 
 # one digit, two, three; one workgroup to many; a full tile and one token more; more workgroups than are summed at once
-ORDERS = [(1, 1, 1), (1, 1, 5), (3, 7, 2), (1, 1024, 300), (1, 1025, 511), (5, 700, 512), (32, 1024, 50257),
+ORDERS = [(1, 1, 1), (1, 1, 5), (3, 7, 2), (1, 1024, 300), (1, 1025, 511), (5, 700, 512), (2, 2048, 40000),
+          (1, 4097, 40000), (32, 1024, 50257),
           (3, 333, 262143), (2, 50, 262144), (2, 9, 1 << 24), (140, 1000, 600), (9, 20000, 70000)]
 
 

@@ -77,25 +77,25 @@ def test_embedding_refusals(lib):
 
 
 def test_embedding_gradient_refusals(lib):
-    def norm(G=FAKE, dt=1, ids=FAKE, o=FAKE, B=2, T=30, V=10, d=8, scale=1.0, ws=FAKE, n=WS, sq=FAKE):
-        return lib.dp_embedding_norm(None, G, dt, ids, o, B, T, V, d, scale, ws, n, sq, 0)
+    def norm(G=FAKE, dt=1, o=FAKE, B=2, T=30, V=10, d=8, scale=1.0, ws=FAKE, n=WS, sq=FAKE):
+        return lib.dp_embedding_norm(None, G, dt, o, B, T, V, d, scale, ws, n, sq, 0)
 
-    def csum(G=FAKE, dt=1, ids=FAKE, o=FAKE, st=FAKE, B=2, T=30, V=10, d=8, scale=1.0, c=FAKE, C=1.0, sigma=1.0,
+    def csum(G=FAKE, dt=1, o=FAKE, st=FAKE, B=2, T=30, V=10, d=8, scale=1.0, c=FAKE, C=1.0, sigma=1.0,
              denom=1.0, ws=FAKE, n=WS, out=FAKE):
-        return lib.dp_embedding_clipped_sum_noise(None, G, dt, ids, o, st, B, T, V, d, scale, c, C, sigma, denom, 0, 0, 0,
-                                                  ws, n, out)
+        return lib.dp_embedding_clipped_sum_noise(None, G, dt, o, st, B, T, V, d, scale, c, C, sigma, denom, 0, 0, 0, ws,
+                                                  n, out)
 
     need = lib.dp_embedding_workspace_bytes(1, 2, 30, 10, 8)
     assert need > 0 and lib.dp_embedding_workspace_bytes(3, 2, 30, 10, 8) == 0
     for f in (norm, csum):
-        assert f(G=None) == f(ids=None) == f(o=None) == f(ws=None) == NULL
+        assert f(G=None) == f(o=None) == f(ws=None) == NULL
         for bad in (dict(B=0), dict(T=0), dict(V=0), dict(d=0), dict(d=(1 << 20) + 1), dict(B=1 << 31), dict(T=1 << 31),
                     dict(B=1 << 16, T=1 << 15), dict(V=1 << 31)):
             assert f(**bad) == SHAPE, bad
         assert f(dt=2) == DTYPE
         assert f(scale=NAN) == VALUE
         assert f(n=need - 1) == WORK
-        assert f(G=FAKE + 1) == f(ids=FAKE + 4) == f(o=FAKE + 4) == f(ws=FAKE + 8) == ALIGN
+        assert f(G=FAKE + 1) == f(o=FAKE + 4) == f(ws=FAKE + 8) == ALIGN
     assert norm(sq=None) == csum(st=None) == csum(c=None) == csum(out=None) == NULL
     assert norm(sq=FAKE + 2) == csum(st=FAKE + 4) == csum(c=FAKE + 2) == csum(out=FAKE + 2) == ALIGN
     assert csum(C=0.0) == csum(sigma=-1.0) == csum(denom=0.0) == csum(C=NAN) == csum(denom=INF) == VALUE

@@ -65,7 +65,7 @@ def order(ids, V):
     """(order, starts) of ids as host lists' tensors."""
     key = torch.where((ids < 0) | (ids >= V), torch.full_like(ids, V), ids).reshape(-1).cpu()
     key, places = torch.sort(key, stable=True)
-    return places, torch.searchsorted(key, torch.arange(V + 1))
+    return (key << 32) + places, torch.searchsorted(key, torch.arange(V + 1))
 
 
 def embedding_norm(G, ids, V, scale):
