@@ -51,7 +51,10 @@ size_t rms_ws_bytes(int64_t B, int64_t T, int64_t d) {
   return chunks > 1 ? round256((size_t)B * (size_t)chunks * (size_t)d * sizeof(float)) : 0;
 }
 
-size_t layer_norm_ws_bytes(int64_t B, int64_t T, int64_t d) { return 2 * rms_ws_bytes(B, T, d); }
+size_t layer_norm_ws_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t d) {
+  const int64_t chunks = dpk::layer_norm_chunks(dtype, B, T, d);
+  return chunks > 1 ? round256((size_t)B * (size_t)chunks * (size_t)d * 2 * sizeof(float)) : 0;
+}
 
 dp_status check_embedding(int64_t N, int64_t V, int64_t d) {
   if (N < 1 || V < 1 || d < 1 || d > kMaxRowWidth) return DP_ERR_SHAPE;
@@ -159,7 +162,7 @@ dp_status dp_rms_norm_backward(void* stream, const void* dy, const void* s, cons
 
 size_t dp_layer_norm_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t d) {
   if (!dtype_ok(dtype) || check_rms(B, T, d) != DP_OK) return 0;
-  return layer_norm_ws_bytes(B, T, d);
+  return layer_norm_ws_bytes(dtype, B, T, d);
 }
 
 dp_status dp_layer_norm(void* stream, const void* x, const void* residual, const void* gain, const void* bias,
@@ -192,7 +195,7 @@ dp_status dp_layer_norm_backward(void* stream, const void* dy, const void* s, co
   if (!aligned(dy, eb) || !aligned(s, eb) || !aligned(dsum, eb) || !aligned(dx, eb) ||
       !aligned(gain, elem_bytes(gain_dtype)) || !aligned(gain_rows, 4) || !aligned(bias_rows, 4))
     return DP_ERR_ALIGN;
-  st = check_workspace(workspace, ws_bytes, gain_rows || bias_rows ? layer_norm_ws_bytes(B, T, d) : 0);
+  st = check_workspace(workspace, ws_bytes, gain_rows || bias_rows ? layer_norm_ws_bytes(dtype, B, T, d) : 0);
   if (st != DP_OK) return st;
   st = device_ready();
   if (st != DP_OK) return st;

@@ -26,6 +26,7 @@
 // from the counts that all workgroups left. Up to 4096 tokens are sorted by one
 // workgroup in one launch. Places and starts are checked where they are read:
 // whatever they hold, accesses stay inside the tensors.
+#include "dp_cols.hpp"
 #include "dp_common.hpp"
 #include "dp_lm.hpp"
 #include "dp_noise.hpp"
@@ -441,87 +442,6 @@ __device__ __forceinline__ Place place_at(const EmbedGradArgs& a, int64_t i) {
   return p;
 }
 
-// What is read in place of a row that is not there, so that loads of several rows need no branches between them.
-__device__ const uint32_t kZeros[8] = {};
-
-// The P columns that a lane holds of a row of d: those from `c` on, or, where fewer are left, the row's last P (the
-// first `skip` of them are its neighbour's too). So every access is one whole vector, aligned or not: a row's end read
-// element by element has to be put together before the next row's loads are issued (8 rows of 333 fp32: 11 us instead
-// of 3). TINY: rows of fewer than P columns, element by element.
-template <typename T, int P, bool TINY>
-struct Cols {
-  static constexpr int bytes = P * (int)sizeof(T);
-  typedef uint32_t Raw __attribute__((ext_vector_type(bytes / 4)));
-  int at, skip, d;
-  bool on;
-  __device__ __forceinline__ Cols(int c, int64_t width) : d((int)width) {
-    on = c < d;
-    at = TINY || c + P <= d ? c : d - P;
-    skip = c - at;
-  }
-  // row n of X, zeros for n < 0
-  __device__ __forceinline__ Raw fetch(const void* X, int n) const {
-    const T* row = static_cast<const T*>(X) + (int64_t)(n < 0 ? 0 : n) * d;
-    Raw raw;
-    if (TINY) {
-#pragma unroll
-      for (int w = 0; w < bytes / 4; ++w) raw[w] = 0u;
-#pragma unroll
-      for (int e = 0; e < P - 1; ++e)
-        if (at + e < d && n >= 0) {
-          const uint32_t bits = raw_bits(row[at + e]);
-          if constexpr (sizeof(T) == 2) raw[e >> 1] |= bits << (16 * (e & 1));
-          else raw[e] = bits;
-        }
-    } else {
-      __builtin_memcpy(&raw, on && n >= 0 ? row + at : reinterpret_cast<const T*>(kZeros), bytes);
-    }
-    return raw;
-  }
-  static __device__ __forceinline__ void add(float* acc, Raw raw, float f) {
-#pragma unroll
-    for (int e = 0; e < P; ++e) {
-      float v;
-      if constexpr (sizeof(T) == 2) v = __uint_as_float(e & 1 ? raw[e >> 1] & 0xFFFF0000u : raw[e >> 1] << 16);
-      else v = __uint_as_float(raw[e]);
-      acc[e] = __builtin_fmaf(f, v, acc[e]);
-    }
-  }
-  // a row of the tiles' sums, fp32
-  __device__ __forceinline__ void add_sums(float* acc, const float* row) const {
-    float v[P];
-#pragma unroll
-    for (int e = 0; e < P; ++e) v[e] = 0.f;
-    if (TINY) {
-#pragma unroll
-      for (int e = 0; e < P - 1; ++e)
-        if (at + e < d) v[e] = row[at + e];
-    } else if (on) {
-      __builtin_memcpy(v, row + at, sizeof(v));
-    }
-#pragma unroll
-    for (int e = 0; e < P; ++e) acc[e] += v[e];
-  }
-  // past the caches; rows at 16-byte boundaries of a multiple of P columns
-  __device__ __forceinline__ void stream_sums(float* row, const float* acc) const {
-#pragma unroll
-    for (int q = 0; q < P / 4; ++q) {
-      const f32x4 v{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-      if (on) __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(row + at + 4 * q));
-    }
-  }
-  // a row's columns that two lanes hold are stored by both, with the same value
-  __device__ __forceinline__ void put_sums(float* row, const float* acc) const {
-    if (TINY) {
-#pragma unroll
-      for (int e = 0; e < P - 1; ++e)
-        if (at + e < d) row[at + e] = acc[e];
-    } else if (on) {
-      __builtin_memcpy(row + at, acc, 4 * P);
-    }
-  }
-};
-
 __device__ __forceinline__ int lane_int(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 __device__ __forceinline__ float lane_float(float v, int lane) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
@@ -531,15 +451,14 @@ __device__ __forceinline__ int64_t lane_int64(int64_t v, int lane) {
   return (int64_t)(((uint64_t)(uint32_t)lane_int((int)(v >> 32), lane) << 32) | (uint32_t)lane_int((int)v, lane));
 }
 
-// The places [s, min(s + 64, e)), a lane each: their tokens (-1 for none) and their samples' factors (1 without).
+// Place i if it lies below e: its token (-1 for none), its sample's factor (1 in the norm) and its run.
 struct Places {
   int tok;
   float f;
   int64_t run;
 };
 template <bool NORM>
-__device__ __forceinline__ Places places_at(const EmbedGradArgs& a, int64_t s, int64_t e) {
-  const int64_t i = s + (threadIdx.x & 63);
+__device__ __forceinline__ Places places_at(const EmbedGradArgs& a, int64_t i, int64_t e) {
   Places p{-1, 0.f, -1};
   if (i < e) {
     const Place q = place_at<NORM>(a, i);
@@ -564,15 +483,32 @@ __device__ __forceinline__ void add_places(const EmbedGradArgs& a, const C& cols
 template <bool NORM, typename C>
 __device__ __forceinline__ void add_rows(const EmbedGradArgs& a, const C& cols, float* acc, int64_t s, int64_t e) {
   for (; s < e; s += 64) {
-    const Places p = places_at<NORM>(a, s, e);
+    const Places p = places_at<NORM>(a, s + (threadIdx.x & 63), e);
     const int m = (int)(e - s < 64 ? e - s : 64);
 #pragma unroll 1
-    for (int r = 0; r < m; r += 8) add_places<8>(a, cols, acc, p, r);
+    for (int r = 0; r < m; r += 16) add_places<16>(a, cols, acc, p, r);
   }
 }
 
-// The same with whole tiles taken from their sums: the ends by places, then
-// by tiles of 16, of 256 and so on, up to the highest level there is.
+// acc += rows [lo, hi) of sums, eight in flight.
+template <typename C>
+__device__ __forceinline__ void add_sums(const C& cols, float* acc, const float* sums, int64_t lo, int64_t hi) {
+  constexpr int U = 8, N = C::columns;
+#pragma unroll 1
+  for (int64_t i = lo; i < hi; i += U) {
+    float v[U][N];
+#pragma unroll
+    for (int u = 0; u < U; ++u) cols.fetch_sums(sums, i + u < hi ? i + u : -1, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[e] += v[u][e];
+  }
+}
+
+// The same with whole tiles taken from their sums: the ends by places (both
+// together, in the lanes of one load), then by tiles of 16, of 256 and so on, up
+// to the highest level there is.
 template <bool NORM, typename C>
 __device__ __forceinline__ void add_run(const EmbedGradArgs& a, const C& cols, float* acc, int64_t s, int64_t e) {
   const int64_t up = (s + kTile - 1) / kTile * kTile, down = e / kTile * kTile;
@@ -580,18 +516,19 @@ __device__ __forceinline__ void add_run(const EmbedGradArgs& a, const C& cols, f
     add_rows<NORM>(a, cols, acc, s, e);
     return;
   }
-  add_rows<NORM>(a, cols, acc, s, up);
-  add_rows<NORM>(a, cols, acc, down, e);
+  const int lane = threadIdx.x & 63;
+  const Places p = places_at<NORM>(a, lane < kTile ? s + lane : down + lane - kTile,
+                                   lane < kTile ? up : lane < 2 * kTile ? e : 0);
+  if (s < up) add_places<kTile>(a, cols, acc, p, 0);
+  if (down < e) add_places<kTile>(a, cols, acc, p, kTile);
   int64_t lo = up / kTile, hi = down / kTile;
   for (int l = 0; lo < hi; ++l) {
     const float* sums = a.sums + a.level_at[l] * a.d;
     // the tiles of the next level inside [lo, hi): [in_lo, in_hi) of this one
     int64_t in_lo = (lo + kTile - 1) / kTile * kTile, in_hi = hi / kTile * kTile;
     if (l + 1 == a.levels || in_lo >= in_hi) in_lo = in_hi = hi;
-#pragma unroll 4
-    for (int64_t i = lo; i < in_lo; ++i) cols.add_sums(acc, sums + i * a.d);
-#pragma unroll 4
-    for (int64_t i = in_hi; i < hi; ++i) cols.add_sums(acc, sums + i * a.d);
+    add_sums(cols, acc, sums, lo, in_lo);
+    add_sums(cols, acc, sums, in_hi, hi);
     if (in_lo >= in_hi) break;
     lo = in_lo / kTile;
     hi = in_hi / kTile;
@@ -621,7 +558,7 @@ __global__ __launch_bounds__(1024) void k_embed_tiles(EmbedGradArgs a, int l, in
       const int64_t i0 = tile * span;
       int64_t r = -1;
       if (l == 0) {  // every place: its row is read if they are one run
-        p = places_at<NORM>(a, i0, i0 + kTile);
+        p = places_at<NORM>(a, i0 + lane, i0 + kTile);
         r = p.run;
         last = lane_int64(r, kTile - 1);
       } else {
@@ -639,9 +576,7 @@ __global__ __launch_bounds__(1024) void k_embed_tiles(EmbedGradArgs a, int l, in
       if (l == 0) {
         add_places<kTile>(a, cols, acc, p, 0);
       } else {
-        const float* sums = a.sums + (a.level_at[l - 1] + tile * kTile) * a.d;
-#pragma unroll 4
-        for (int k = 0; k < kTile; ++k) cols.add_sums(acc, sums + k * a.d);
+        add_sums(cols, acc, a.sums + a.level_at[l - 1] * a.d, tile * kTile, tile * kTile + kTile);
       }
       cols.put_sums(a.sums + (a.level_at[l] + tile) * a.d, acc);
     }
@@ -782,7 +717,7 @@ __global__ __launch_bounds__(256) void k_embed_norm_finish(EmbedGradArgs a, int 
 // blocks) and 256 columns, by a wave: four columns a lane, so that 32 sums leave room for 8 rows in flight beside 16
 // waves a CU (with eight columns: 152 registers and 85 us instead of 62 for 32768 tokens of 1280 bf16).
 template <typename T, bool TINY>
-__global__ __launch_bounds__(256, 5) void k_embed_sum(EmbedGradArgs a, NoiseArgs na, float* __restrict__ out, int col_waves) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) void k_embed_sum(EmbedGradArgs a, NoiseArgs na, float* __restrict__ out, int col_waves) {
   constexpr int P = 4;
   using C = Cols<T, P, TINY>;
   const int lane = threadIdx.x & 63;
@@ -809,7 +744,7 @@ __global__ __launch_bounds__(256, 5) void k_embed_sum(EmbedGradArgs a, NoiseArgs
       constexpr int U = 4;
       const int m = (int)(at[4] - at[0]);
       Places p{-1, 0.f, -1};
-      if (m > 0) p = places_at<false>(a, at[0], at[4]);
+      if (m > 0) p = places_at<false>(a, at[0] + lane, at[4]);
       const int e1 = (int)(at[1] - at[0]), e2 = (int)(at[2] - at[0]), e3 = (int)(at[3] - at[0]);
 #pragma unroll 1
       for (int r = 0; r < m; r += U) {

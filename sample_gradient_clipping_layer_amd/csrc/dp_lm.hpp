@@ -70,6 +70,7 @@ struct LayerNormBackArgs {
   int64_t chunks, chunk_rows;
   int own_groups;
 };
+int64_t layer_norm_chunks(int dtype, int64_t B, int64_t T, int64_t d);
 hipError_t launch_layer_norm(hipStream_t st, int dtype, const LayerNormArgs& a);
 hipError_t launch_layer_norm_backward(hipStream_t st, int dtype, LayerNormBackArgs a);
 

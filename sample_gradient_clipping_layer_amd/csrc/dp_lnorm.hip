@@ -29,6 +29,56 @@ __device__ __forceinline__ float mul_rounded(float a, float b) {
   return a * b;
 }
 
+__device__ __forceinline__ float sub_rounded(float a, float b) {
+#pragma clang fp contract(off)
+  return a - b;
+}
+
+// The P values of a vector of a row. `again`: unpacked anew, so that the compiler does not keep them in fp32 from the
+// last time (bf16: half the registers).
+template <int P>
+__device__ __forceinline__ void unpack_vec(u32x4& raw, float* v, bool again) {
+  if constexpr (P == 8) {
+    if (again) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t x = raw[w];
+        asm volatile("" : "+v"(x));
+        raw[w] = x;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(raw[e] << 16);
+      v[2 * e + 1] = __uint_as_float(raw[e] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(raw[e]);
+  }
+}
+
+// Vector j of a row's lane from fp32, as RowMap::store does it.
+template <typename T, typename M, bool WHOLE>
+__device__ __forceinline__ void store_vec(T* __restrict__ row, int d, int lane, int j, const float* v) {
+  const int c = M::col(j, lane);
+  if (WHOLE ? c < d : c + M::P <= d) {
+    u32x4 raw;
+    if constexpr (M::P == 8) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) raw[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) raw[e] = __float_as_uint(v[e]);
+    }
+    __builtin_memcpy(row + c, &raw, 16);
+  } else if (!WHOLE && c < d) {
+#pragma unroll
+    for (int e = 0; e < M::P - 1; ++e)
+      if (c + e < d) put(row[c + e], v[e]);
+  }
+}
+
 // v - mean over the row's columns, 0 past its end; the sums of squares and of the values are added to q and r.
 template <typename M, bool WHOLE, int E>
 __device__ __forceinline__ void centre(float* v, float mean, int d, int lane, float& q, float& r) {
@@ -52,7 +102,7 @@ __global__ __launch_bounds__(row_threads<WPR>()) void k_layer_norm(LayerNormArgs
   constexpr int NW = row_threads<WPR>() / 64, GROUPS = NW / WPR, LPR = 64 * WPR;
   using M = RowMap<T, WHOLE, E, LPR>;
   __shared__ float red1[32], red2[64];
-  const int wave = threadIdx.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));  // scalar: so are a row's addresses
   const int group = WPR == 1 ? wave : 0;
   const int lane = WPR == 1 ? (threadIdx.x & 63) : threadIdx.x;
   int phase1 = 0, phase2 = 0;
@@ -96,21 +146,61 @@ __global__ __launch_bounds__(row_threads<WPR>()) void k_layer_norm(LayerNormArgs
   }
 }
 
+// Waves per SIMD that the backward pass asks for.
+template <typename T, int E, int WPR>
+constexpr int backward_waves() {
+  return WPR >= 8 ? WPR / 4 : E * sizeof(T) <= 32 ? 4 : E * sizeof(T) <= 48 ? 3 : 2;
+}
+
 // Work items: (sample, chunk of its rows); with `own_groups` every group of
 // a block takes a sample of its own (chunks == 1).
 template <typename T, bool WHOLE, int E, int WPR>
-__global__ __launch_bounds__(row_threads<WPR>()) void k_layer_norm_backward(LayerNormBackArgs a) {
+__global__ __launch_bounds__(row_threads<WPR>(), (backward_waves<T, E, WPR>())) void k_layer_norm_backward(LayerNormBackArgs a) {
   constexpr int NW = row_threads<WPR>() / 64, GROUPS = NW / WPR, LPR = 64 * WPR;
   using M = RowMap<T, WHOLE, E, LPR>;
   __shared__ float red1[64], red2[96];
   __shared__ float part[GROUPS > 1 ? (GROUPS - 1) * E * 64 : 1];
-  const int wave = threadIdx.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));  // scalar: so are a row's addresses
   const int group = WPR == 1 ? wave : 0;
   const int lane = WPR == 1 ? (threadIdx.x & 63) : threadIdx.x;
   int phase1 = 0, phase2 = 0;
-  float g[E];
-  // 1024-thread blocks have 128 registers a lane: the gain is read again for every row there (from L2)
-  if constexpr (WPR < 16) M::load_gain(a.gain, a.gain_bf16, (int)a.d, lane, g);
+  // Registers for rows in flight are what is short, with the two sums of every column: the gain is held in LDS (read
+  // again from L2 by 1024-thread blocks), a row as it was loaded, unpacked a vector at a time in each of its three
+  // passes. (32 x 1024 tokens of 1600 bf16: 140 us with the row and the gain in fp32 over the reductions, 97 so. The
+  // next row loaded meanwhile takes the registers that a further wave would: 107.)
+  constexpr bool HELD = WPR < 16;
+  constexpr int P = M::P, N = M::N;
+  __shared__ __attribute__((aligned(16))) float held[HELD ? E * LPR : 4];
+  if constexpr (HELD) {
+    if (group == 0) {
+      float g[E];
+      M::load_gain(a.gain, a.gain_bf16, (int)a.d, lane, g);
+#pragma unroll
+      for (int q = 0; q < E / 4; ++q)
+        *reinterpret_cast<f32x4*>(held + (q * LPR + lane) * 4) = f32x4{g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]};
+    }
+    __syncthreads();
+  }
+  auto gain = [&](int j, float* g) {
+    if constexpr (HELD) {
+      int at = lane;
+      asm volatile("" : "+v"(at));  // read where it is used, not kept in registers over the rows
+#pragma unroll
+      for (int q = 0; q < P / 4; ++q) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(held + ((j * (P / 4) + q) * LPR + at) * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[4 * q + e] = v[e];
+      }
+    } else {
+      const int c = M::col(j, lane);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        const int at = c + e < a.d ? c + e : 0;
+        g[e] = a.gain_bf16 ? to_f32(static_cast<const bf16s*>(a.gain)[at]) : static_cast<const float*>(a.gain)[at];
+      }
+    }
+  };
+  const int d = (int)a.d;
   const float inv_d = 1.0f / (float)a.d;
   const int64_t per_block = a.own_groups ? GROUPS : 1;
   const int64_t items = a.B * a.chunks;
@@ -123,52 +213,79 @@ __global__ __launch_bounds__(row_threads<WPR>()) void k_layer_norm_backward(Laye
     float acc_g[E], acc_b[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc_g[e] = acc_b[e] = 0.f;
-    for (int64_t t = t0 + (a.own_groups ? 0 : group); t < t1; t += (a.own_groups ? 1 : GROUPS)) {
+    typename M::Raw rs, rh, ro;
+    auto fetch = [&](int64_t t) {
       const int64_t off = (b * a.T + t) * a.d;
-      typename M::Raw rs, rh, ro;
-      M::fetch(static_cast<const T*>(a.s) + off, (int)a.d, lane, rs);
-      M::fetch(static_cast<const T*>(a.dy) + off, (int)a.d, lane, rh);
-      if (WPR < 16 && a.dsum) M::fetch(static_cast<const T*>(a.dsum) + off, (int)a.d, lane, ro);
-      if constexpr (WPR == 16) M::load_gain(a.gain, a.gain_bf16, (int)a.d, lane, g);
-      float s[E], h[E];
-      M::unpack(rs, s);
-      M::unpack(rh, h);
+      M::fetch(static_cast<const T*>(a.s) + off, d, lane, rs);
+      M::fetch(static_cast<const T*>(a.dy) + off, d, lane, rh);
+      if (a.dsum) M::fetch(static_cast<const T*>(a.dsum) + off, d, lane, ro);
+    };
+    const int64_t step = a.own_groups ? 1 : GROUPS, first = t0 + (a.own_groups ? 0 : group);
+    for (int64_t t = first; t < t1; t += step) {
+      fetch(t);
       float sums[2] = {0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        sums[0] += s[e];
-        sums[1] = __builtin_fmaf(h[e], g[e], sums[1]);
+      for (int j = 0; j < N; ++j) {
+        float s[P], h[P], g[P];
+        gain(j, g);
+        unpack_vec<P>(rs[j], s, false);
+        unpack_vec<P>(rh[j], h, false);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          sums[0] += s[e];
+          sums[1] = __builtin_fmaf(h[e], g[e], sums[1]);
+        }
       }
       row_sums<WPR, 2>(sums, red1, wave, phase1);
+      const float mean = mul_rounded(sums[0], inv_d), mean_h = sums[1] * inv_d;
       float qrh[3] = {0.f, 0.f, 0.f};
-      centre<M, WHOLE, E>(s, mul_rounded(sums[0], inv_d), (int)a.d, lane, qrh[0], qrh[1]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) qrh[2] = __builtin_fmaf(h[e] * g[e], s[e], qrh[2]);
+      for (int j = 0; j < N; ++j) {
+        float s[P], h[P], g[P];
+        gain(j, g);
+        unpack_vec<P>(rs[j], s, true);
+        unpack_vec<P>(rh[j], h, true);
+        const int c = M::col(j, lane);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const float o = (WHOLE ? c : c + e) < d ? sub_rounded(s[e], mean) : 0.f;
+          qrh[0] = __builtin_fmaf(o, o, qrh[0]);
+          qrh[1] += o;
+          qrh[2] = __builtin_fmaf(h[e] * g[e], o, qrh[2]);
+        }
+      }
       row_sums<WPR, 3>(qrh, red2, wave, phase2);
       const float rest = mul_rounded(qrh[1], inv_d);  // what the rounded mean left
       const float var = fmaxf(__builtin_fmaf(qrh[0], inv_d, -rest * rest), 0.f);
       const float rstd = 1.0f / sqrtf(var + a.eps);
-      const float mean_h = sums[1] * inv_d;
-      if (a.dx) {
-        // mean(h u) * rstd, for u = (s - rest) * rstd
-        const float along = __builtin_fmaf(-rest, mean_h, qrh[2] * inv_d) * rstd * rstd;
-        float o[E];
-        if (a.dsum) {
-          if (WPR == 16) M::fetch(static_cast<const T*>(a.dsum) + off, (int)a.d, lane, ro);
-          M::unpack(ro, o);
-        } else {
+      // mean(h u) * rstd, for u = (s - rest) * rstd
+      const float along = __builtin_fmaf(-rest, mean_h, qrh[2] * inv_d) * rstd * rstd;
+      T* out = static_cast<T*>(a.dx) + (b * a.T + t) * a.d;
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = 0.f;
+      for (int j = 0; j < N; ++j) {
+        float s[P], h[P];
+        unpack_vec<P>(rs[j], s, true);
+        unpack_vec<P>(rh[j], h, true);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          s[e] = sub_rounded(s[e], mean) - rest;  // past the row's end dy is 0
+          acc_g[j * P + e] = __builtin_fmaf(h[e], s[e] * rstd, acc_g[j * P + e]);
+          acc_b[j * P + e] += h[e];
         }
+        if (a.dx) {
+          float o[P], g[P];
+          gain(j, g);
+          if (a.dsum) {
+            unpack_vec<P>(ro[j], o, false);
+          } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          o[e] = __builtin_fmaf(rstd, __builtin_fmaf(h[e], g[e], -mean_h) - (s[e] - rest) * along, o[e]);
-        M::store(static_cast<T*>(a.dx) + off, (int)a.d, lane, o);
-      }
+            for (int e = 0; e < P; ++e) o[e] = 0.f;
+          }
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        acc_g[e] = __builtin_fmaf(h[e], (s[e] - rest) * rstd, acc_g[e]);
-        acc_b[e] += h[e];
+          for (int e = 0; e < P; ++e)
+            o[e] = __builtin_fmaf(rstd, __builtin_fmaf(h[e], g[e], -mean_h) - s[e] * along, o[e]);
+          store_vec<T, M, WHOLE>(out, d, lane, j, o);
+        }
       }
     }
     if (!a.gain_rows && !a.bias_rows) continue;
@@ -225,6 +342,18 @@ hipError_t row_dispatch_backward(int64_t d, F f) {
 
 constexpr int64_t kLnBlocks = 256 * 8;  // blocks that fill the 256 CUs; more rows than that are looped over
 
+// Workgroups of the backward pass that the 256 CUs hold at once.
+template <typename T>
+int64_t backward_resident(int64_t d) {
+  int64_t n = 0;
+  (void)row_dispatch_backward(d, [&](auto e, auto w) {
+    constexpr int E = decltype(e)::value, WPR = decltype(w)::value;
+    n = (int64_t)256 * backward_waves<T, E, WPR>() * 256 / row_threads<WPR>();
+    return hipSuccess;
+  });
+  return n;
+}
+
 template <typename T, bool WHOLE>
 hipError_t launch_fwd(hipStream_t st, const LayerNormArgs& a) {
   return row_dispatch(a.d, [&](auto e, auto w) {
@@ -249,6 +378,13 @@ hipError_t launch_bwd(hipStream_t st, const LayerNormBackArgs& a) {
 
 }  // namespace
 
+// How a sample's rows are spread over workgroups: as far as all of them are held at once (32 samples of 1024 tokens of
+// 1280 bf16: 768 are held; 83 us by 1024 workgroups), each of at least four rows (one per wave).
+int64_t layer_norm_chunks(int dtype, int64_t B, int64_t T, int64_t d) {
+  const int64_t held = dtype == 1 ? backward_resident<bf16s>(d) : backward_resident<float>(d);
+  return std::max<int64_t>(1, std::min(held / B, (T + 3) / 4));
+}
+
 hipError_t launch_layer_norm(hipStream_t st, int dtype, const LayerNormArgs& a) {
   const bool whole = a.d % (dtype == 1 ? 8 : 4) == 0;
   if (dtype == 1) return whole ? launch_fwd<bf16s, true>(st, a) : launch_fwd<bf16s, false>(st, a);
@@ -257,7 +393,7 @@ hipError_t launch_layer_norm(hipStream_t st, int dtype, const LayerNormArgs& a) 
 
 hipError_t launch_layer_norm_backward(hipStream_t st, int dtype, LayerNormBackArgs a) {
   const bool rows = a.gain_rows || a.bias_rows;
-  a.chunks = rows ? rms_chunks(a.B, a.T) : rms_chunks(1, a.B * a.T);
+  a.chunks = rows ? layer_norm_chunks(dtype, a.B, a.T, a.d) : layer_norm_chunks(dtype, 1, a.B * a.T, a.d);
   if (!rows) {  // no per-sample sums: the rows are one run
     a.T = a.B * a.T;
     a.B = 1;
