@@ -9,6 +9,8 @@ import pytest
 import torch
 
 import sample_gradient_clipping_layer_amd as dpc
+from sample_gradient_clipping_layer_amd.engine import PrivacyEngine
+from sample_gradient_clipping_layer_amd.layers import Embedding, LayerNorm, RMSNorm, replace_layer_norms, token_loss
 
 FAKE = 0x100000  # aligned, never dereferenced
 WS = 1 << 40
@@ -123,13 +125,13 @@ def test_token_logprob_refusals(lib):
 
 
 def test_balance_refusals(lib):
-    def call(z=FAKE, ids=FAKE, dt=1, B=2, T=100, E=8, top=2, ws=FAKE, n=WS, loss=FAKE, c=FAKE, t=FAKE):
+    def call(z=FAKE, ids=FAKE, dt=1, B=2, T=5000, E=8, top=2, ws=FAKE, n=WS, loss=FAKE, c=FAKE, t=FAKE):
         return lib.dp_balance_loss(None, z, ids, dt, B, T, E, top, ws, n, loss, c, t)
 
     def back(z=FAKE, ids=FAKE, dt=1, B=2, T=100, E=8, top=2, c=FAKE, t=FAKE, dl=None, g=FAKE):
         return lib.dp_balance_loss_backward(None, z, ids, dt, B, T, E, top, c, t, dl, g)
 
-    need = lib.dp_balance_workspace_bytes(1, 2, 100, 8)
+    need = lib.dp_balance_workspace_bytes(1, 2, 5000, 8)
     assert need > 0 and lib.dp_balance_workspace_bytes(1, 2, 8, 8) == 0 and lib.dp_balance_workspace_bytes(1, 0, 8, 8) == 0
     for f in (call, back):
         assert f(z=None) == f(ids=None) == f(c=None) == f(t=None) == NULL
@@ -182,3 +184,78 @@ def test_binding_refuses_host_and_misshapen_tensors():
         dpc.dp_token_logprob_backward(z, ids, 1.0, torch.zeros(2, 3, 2), z.clone(), dentropy=torch.zeros(2, 3))
     with pytest.raises(ValueError):
         dpc.dp_balance_loss(z, ids, torch.zeros(2), torch.zeros(2, 7, dtype=torch.int64), torch.zeros(2, dtype=torch.int64))
+
+
+def test_engine_covers_tables_and_layer_norms():
+    model = torch.nn.Sequential(Embedding(10, 8), LayerNorm(8), torch.nn.Embedding(10, 8, padding_idx=3),
+                                LayerNorm(8, bias=False), torch.nn.Linear(8, 2))
+    e = PrivacyEngine(model, C=1.0, sigma=1.0)
+    assert len(e.layers) == 5 and model[0].private and model[1].private and model[3].private
+    e.detach()
+    assert not model[0].private and not model[1].private
+    with pytest.raises(RuntimeError):
+        e.step(0)
+    frozen = Embedding(10, 8)
+    frozen.weight.requires_grad_(False)
+    e = PrivacyEngine(torch.nn.Sequential(frozen, torch.nn.Linear(8, 2)), C=1.0, sigma=1.0)
+    assert len(e.layers) == 1 and not frozen.private
+    e.detach()
+
+
+def test_engine_refuses_what_it_cannot_clip():
+    for m in (torch.nn.Embedding(4, 4, max_norm=1.0), torch.nn.Embedding(4, 4, scale_grad_by_freq=True),
+              torch.nn.Embedding(4, 4, sparse=True), torch.nn.LayerNorm(4), torch.nn.LayerNorm((2, 4))):
+        with pytest.raises(ValueError):
+            PrivacyEngine(torch.nn.Sequential(torch.nn.Linear(4, 4), m), C=1.0, sigma=1.0)
+    frozen = LayerNorm(4)
+    frozen.weight.requires_grad_(False)  # its bias alone is trainable
+    with pytest.raises(ValueError):
+        PrivacyEngine(frozen, C=1.0, sigma=1.0)
+
+
+@pytest.mark.parametrize("make", [lambda: (Embedding(6, 6), torch.nn.Linear(6, 6, bias=False)),
+                                  lambda: (torch.nn.Linear(6, 6, bias=False), Embedding(6, 6)),
+                                  lambda: (torch.nn.Embedding(6, 6), torch.nn.Linear(6, 6)),
+                                  lambda: (Embedding(6, 6), torch.nn.Embedding(6, 6)),
+                                  lambda: (LayerNorm(6), LayerNorm(6)), lambda: (LayerNorm(6), RMSNorm(6))])
+def test_engine_refuses_shared_tables_and_norms(make):
+    """A table tied to the head among them: the two gradients of a sample would
+    have to be added before their norm."""
+    a, b = make()
+    b.weight = a.weight
+    with pytest.raises(ValueError):
+        PrivacyEngine(torch.nn.Sequential(a, b), C=1.0, sigma=1.0)
+    assert not getattr(a, "private", False) and not getattr(b, "private", False)
+
+
+def test_replace_layer_norms():
+    class Block(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.ln = torch.nn.LayerNorm(8, eps=3e-4)
+            self.again = self.ln
+            self.parts = torch.nn.ModuleList([torch.nn.LayerNorm(8, bias=False), torch.nn.Linear(8, 8)])
+            self.plain = torch.nn.LayerNorm(8, elementwise_affine=False)
+            self.nothing = None
+
+    m = Block()
+    before, params = list(m.state_dict()), dict(m.named_parameters())
+    assert replace_layer_norms(m) is m
+    assert list(m.state_dict()) == before
+    assert all(p is params[n] for n, p in m.named_parameters())
+    assert isinstance(m.ln, LayerNorm) and m.ln is m.again and m.ln.eps == 3e-4
+    assert isinstance(m.parts[0], LayerNorm) and m.parts[0].bias is None
+    assert type(m.plain) is torch.nn.LayerNorm
+    assert isinstance(replace_layer_norms(torch.nn.LayerNorm(4)), LayerNorm)
+    with pytest.raises(ValueError):
+        LayerNorm.from_torch(torch.nn.LayerNorm((2, 4)))
+
+
+def test_layers_refuse_host_tensors():
+    ids = torch.zeros(2, 3, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        Embedding(4, 8)(ids)
+    with pytest.raises(ValueError):
+        LayerNorm(8)(torch.zeros(2, 8))
+    with pytest.raises(ValueError):
+        token_loss(torch.zeros(2, 3, 5), ids)
