@@ -173,21 +173,22 @@ __global__ __launch_bounds__(NT) void k_balance_sums(BalanceArgs a) {
   }
 }
 
-// A sample's chunks, added in order, by one workgroup: its waves take parts of the chunks.
-__global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a) {
-  constexpr int NT = 1024, WAVES = NT / 64;
-  __shared__ float part[WAVES][64];
-  __shared__ uint64_t partc[WAVES][64];
-  __shared__ float red[WAVES];
-  __shared__ uint64_t redc[WAVES];
+// A sample's chunks, added in order, by one workgroup: its waves take parts of the chunks, the first wave the rest.
+__global__ __launch_bounds__(512) void k_balance_finish(BalanceArgs a) {
+  constexpr int WAVES = 8;
+  __shared__ float part[2][WAVES][64];
+  __shared__ uint32_t partc[2][WAVES][64];
   const int E = (int)a.E, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
     float fp = 0.f;
     uint64_t places = 0, tokens = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
+    if (wave == 0)
+      for (int64_t ch = lane; ch < a.chunks; ch += 64) tokens += a.part_counts[(b * a.chunks + ch) * (a.E + 1) + a.E];
+    int half = 0;
+    for (int e0 = 0; e0 < E; e0 += 64, half ^= 1) {  // the halves take turns: one barrier a round
       const int e = e0 + lane;
       float s = 0.f;
-      uint64_t c = 0;
+      uint32_t c = 0;
       if (e < E) {
 #pragma unroll 4
         for (int64_t ch = wave; ch < a.chunks; ch += WAVES) {
@@ -195,31 +196,31 @@ __global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a) {
           c += a.part_counts[(b * a.chunks + ch) * (a.E + 1) + e];
         }
       }
-      part[wave][lane] = s;
-      partc[wave][lane] = c;
+      part[half][wave][lane] = s;
+      partc[half][wave][lane] = c;
       __syncthreads();
       if (wave == 0 && e < E) {
-        s = 0.f;
-        c = 0;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-          s += part[w][lane];
-          c += partc[w][lane];
+        for (int w = 1; w < WAVES; ++w) {
+          s += part[half][w][lane];
+          c += partc[half][w][lane];
         }
-        a.counts[b * a.E + e] = (int64_t)c;
+        a.counts[b * a.E + e] = c;
         fp = __builtin_fmaf((float)c, s, fp);
         places += c;
       }
-      __syncthreads();
     }
-    for (int64_t ch = threadIdx.x; ch < a.chunks; ch += NT)
-      tokens += a.part_counts[(b * a.chunks + ch) * (a.E + 1) + a.E];
-    places = block_count<NT>(places, redc);
-    tokens = block_count<NT>(tokens, redc);
-    fp = block_sum<NT>(fp, red);
-    if (threadIdx.x == 0) {
-      a.loss[b] = loss_of(fp, places, tokens, a.E);
-      a.tokens[b] = (int64_t)tokens;
+    if (wave == 0) {
+      fp = wave_sum(fp);
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) {
+        places += __shfl_xor(places, off, kWave);
+        tokens += __shfl_xor(tokens, off, kWave);
+      }
+      if (lane == 0) {
+        a.loss[b] = loss_of(fp, places, tokens, a.E);
+        a.tokens[b] = (int64_t)tokens;
+      }
     }
     __syncthreads();
   }
@@ -346,7 +347,7 @@ hipError_t launch_balance_loss(hipStream_t st, int dtype, BalanceArgs a, void* w
   a.part_counts = reinterpret_cast<uint32_t*>(a.part_sums + a.B * a.chunks * a.E);
   const hipError_t e = dtype == 1 ? launch_sums<bf16s>(st, a) : launch_sums<float>(st, a);
   if (e != hipSuccess || a.chunks == 1) return e;
-  k_balance_finish<<<grid_of(a.B), 1024, 0, st>>>(a);
+  k_balance_finish<<<grid_of(a.B), 512, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -36,41 +36,55 @@ namespace dpk {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
-// A distance from the maximum, in powers of two, beyond which 2^-x is 0: it stands for larger ones (and infinite
-// ones) in the products 2^-x x.
+// A distance from the maximum, in powers of two, beyond which 2^t is 0: it stands for larger ones (and infinite ones) in
+// the products 2^t t.
 constexpr float kFar = 256.0f;
 
-// s = sum of 2^-x and u = sum of 2^-x x over the values seen, x = (m - z) k >= 0, k = log2(e) / tau. The initial
-// maximum is finite, so that no difference of infinities arises.
+// s = sum of 2^t and u = sum of 2^t t over the values seen, t = z k - base of the largest of them, m; k = log2(e) / tau.
+// The initial maximum is finite, so that no difference of infinities arises.
 struct Stat {
   float m, s, u;
 };
 __device__ __forceinline__ Stat stat_empty() { return Stat{-FLT_MAX, 0.f, 0.f}; }
 
+// FAST: t = z k - fl(m k), a fused multiply-add; that the base is off m k is made good in the logarithm of the sum.
+// It holds while |m k| < 2^20, where the base is off by 1/16 at most (kept above -2^20: values down to the type's
+// lowest before a larger one is seen are 0 then). Else t = (z - m) k, two operations, for any m.
+constexpr float kFastBase = 0x1p20f;
+template <bool FAST>
+__device__ __forceinline__ float base_of(float m, float k) {
+  return FAST ? fmaxf(m * k, -kFastBase) : m;
+}
+template <bool FAST>
+__device__ __forceinline__ float below(float z, float base, float k) {
+  return FAST ? __builtin_fmaf(z, k, -base) : (z - base) * k;
+}
+
 // r as seen from the maximum m >= r.m
-template <bool ENT>
+template <bool FAST, bool ENT>
 __device__ __forceinline__ void stat_move(Stat& r, float m, float k) {
-  const float x = (m - r.m) * k, f = exp2_hw(-x);
-  if constexpr (ENT) r.u = f * __builtin_fmaf(fminf(x, kFar), r.s, r.u);
+  const float x = FAST ? base_of<FAST>(r.m, k) - base_of<FAST>(m, k) : (r.m - m) * k, f = exp2_hw(x);
+  if constexpr (ENT) r.u = f * __builtin_fmaf(fmaxf(x, -kFar), r.s, r.u);
   r.s *= f;
   r.m = m;
 }
-template <bool ENT>
+template <bool FAST, bool ENT>
 __device__ __forceinline__ Stat stat_join(Stat a, Stat b, float k) {
   const float m = fmaxf(a.m, b.m);
-  stat_move<ENT>(a, m, k);
-  stat_move<ENT>(b, m, k);
+  stat_move<FAST, ENT>(a, m, k);
+  stat_move<FAST, ENT>(b, m, k);
   return Stat{m, a.s + b.s, a.u + b.u};
 }
 // top: the largest of the P values
-template <bool ENT, int P>
+template <bool FAST, bool ENT, int P>
 __device__ __forceinline__ void stat_add(Stat& r, const float* z, float top, float k) {
-  stat_move<ENT>(r, fmaxf(r.m, top), k);
+  stat_move<FAST, ENT>(r, fmaxf(r.m, top), k);
+  const float base = base_of<FAST>(r.m, k);
 #pragma unroll
   for (int e = 0; e < P; ++e) {
-    const float x = (r.m - z[e]) * k, t = exp2_hw(-x);
-    r.s += t;
-    if constexpr (ENT) r.u = __builtin_fmaf(t, fminf(x, kFar), r.u);
+    const float t = below<FAST>(z[e], base, k), p = exp2_hw(t);
+    r.s += p;
+    if constexpr (ENT) r.u = __builtin_fmaf(p, fmaxf(t, -kFar), r.u);
   }
 }
 template <int P>
@@ -80,7 +94,7 @@ __device__ __forceinline__ float largest(const float* z) {
   for (int e = 1; e < P; ++e) m = fmaxf(m, z[e]);
   return m;
 }
-// The largest of eight neighbouring lanes' values, in each of them (a lane that is switched off does not count).
+// The largest of eight neighbouring lanes' values, in each of them. All eight take part.
 __device__ __forceinline__ float largest_of_8(float v) {
   const auto other = [](float x, auto ctrl) {
     const int i = (int)__float_as_uint(x);
@@ -123,12 +137,12 @@ __device__ __forceinline__ float first_lane(float v) {
 }
 
 // Joined over the block; the same value in every thread. Contains barriers.
-template <bool ENT, int NT>
+template <bool FAST, bool ENT, int NT>
 __device__ __forceinline__ Stat block_stat(Stat r, float k, float* red) {
   auto join = [&](Stat& t, int off) {
     Stat o{__shfl_xor(t.m, off, kWave), __shfl_xor(t.s, off, kWave), 0.f};
     if constexpr (ENT) o.u = __shfl_xor(t.u, off, kWave);
-    t = stat_join<ENT>(t, o, k);
+    t = stat_join<FAST, ENT>(t, o, k);
   };
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) join(r, off);
@@ -162,13 +176,13 @@ __device__ __forceinline__ uint64_t place_of(float z, int64_t word) {
   return ((uint64_t)key_of(z) << 32) | (uint32_t)~(uint32_t)word;
 }
 
-constexpr int kGroups = 256, kParts = 2048;
+constexpr int kGroups = 256;
 
 // LDS of the selection: the largest logit of every part of the row (a vector, or 8) or the collected words, the groups'
 // largest keys or digit counts, the parts that reach the floor.
 template <int NT>
 struct TopLds {
-  static constexpr int parts = NT == 64 ? 1024 : kParts, cap = NT == 64 ? 512 : 1024;
+  static constexpr int parts = NT <= 128 ? 1024 : 2048, cap = NT <= 128 ? 512 : 1024;
   union {  // the words are collected once the parts have been looked through
     float part[parts];
     uint64_t found[cap];
@@ -287,6 +301,7 @@ __device__ __forceinline__ uint32_t find_floor(int K, const TopLds<NT>& l) {
 }
 
 // The row's K top words into top_ids and top_logp, from the parts' largest logits in l.part. by8: parts of 8 vectors.
+// r: the largest logit, the sum (0: no distribution, NaN: NaN or +inf in the row) and log of the sum.
 template <typename T, int NT>
 __device__ __forceinline__ void top_words(const LogprobArgs& a, int64_t row, const T* z, bool by8, Stat r, TopLds<NT>& l) {
   constexpr int P = elem_traits<T>::per16;
@@ -364,7 +379,7 @@ __device__ __forceinline__ void top_words(const LogprobArgs& a, int64_t row, con
     __syncthreads();
     n = l.count < (uint32_t)TopLds<NT>::cap ? l.count : (uint32_t)TopLds<NT>::cap;
   }
-  const float inv_tau = 1.0f / a.tau, log_s = logf(r.s);
+  const float inv_tau = 1.0f / a.tau, log_s = r.u;
   for (uint32_t i = threadIdx.x; i < n; i += NT) {
     const uint64_t p = l.found[i];
     uint32_t rank = 0;
@@ -394,33 +409,87 @@ __global__ __launch_bounds__(NT, 8) void k_token_logprob(LogprobArgs a) {
     const bool given = y >= 0 && y < a.V;
     const float zy = given ? to_f32(z[y]) : 0.0f;
     Stat r = stat_empty();
-    // whether a part of the row is 8 vectors, and the vectors that a part number stands for again behind them
-    const bool by8 = TOP && a.V / P > TopLds<NT>::parts;
-    constexpr int kSpan = TopLds<NT>::parts * 8;
-    thread_words<T, NT, 4>(
-        z, a.V, [&](int64_t, float v) { stat_add<ENT, 1>(r, &v, v, k); },
-        [&](int64_t, const float* v, int64_t i) {
-          const float top = largest<P>(v);
-          if (TOP) {
-            if (by8) {
-              const float m = largest_of_8(top);
-              float& part = lds.part[((uint32_t)i & (kSpan - 1)) >> 3];
-              if ((i & 7) == 0) part = i < kSpan ? m : fmaxf(part, m);
-            } else {
-              lds.part[i] = top;
-            }
-          }
-          stat_add<ENT, P>(r, v, top, k);
-        });
-    r = block_stat<ENT, NT>(r, k, red);
+    const Span<T> sn(z, 0, a.V);
+    const u32x4* vz = reinterpret_cast<const u32x4*>(z + sn.head);
+    const bool by8 = TOP && sn.vecs > TopLds<NT>::parts;  // a part of the row is 8 vectors
+    // Round n holds vectors n * NT ..; a part number stands again for parts behind the last one. Both are the wave's.
+    auto keep = [&](float top, int n) {
+      if constexpr (TOP) {
+        if (by8) {
+          const float m = largest_of_8(top);
+          const int at = n * (NT / 8);
+          float& part = lds.part[(at & (TopLds<NT>::parts - 1)) + (threadIdx.x >> 3)];
+          if ((threadIdx.x & 7) == 0) part = at < TopLds<NT>::parts ? m : fmaxf(part, m);
+        } else {
+          lds.part[n * NT + threadIdx.x] = top;
+        }
+      }
+    };
+    constexpr int U = 4;  // vectors in flight
+    const int full = (int)(sn.vecs / NT);  // rounds of all threads
+    const int rest = (int)(sn.vecs - (int64_t)full * NT);
+    int n = 0;
+    for (; n + U <= full; n += U) {
+      u32x4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = vz[(int64_t)(n + u) * NT + threadIdx.x];
+#pragma unroll
+      for (int u = 0; u < U; u += 2) {  // two vectors to a step of the maximum
+        float v[2 * P];
+        unpack16<P>(raw[u], v);
+        unpack16<P>(raw[u + 1], v + P);
+        const float top0 = largest<P>(v), top1 = largest<P>(v + P);
+        keep(top0, n + u);
+        keep(top1, n + u + 1);
+        stat_add<true, ENT, 2 * P>(r, v, fmaxf(top0, top1), k);
+      }
+    }
+    {
+      // The last rounds, the last of them not of all threads: those have -inf there, which counts for nothing, and take
+      // part in the eight lanes' largest.
+      constexpr uint32_t kNothing = P == 8 ? 0xFF80FF80u : 0xFF800000u;
+      u32x4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        raw[u] = u32x4{kNothing, kNothing, kNothing, kNothing};
+        if (n + u < full || (n + u == full && (int)threadIdx.x < rest)) raw[u] = vz[(int64_t)(n + u) * NT + threadIdx.x];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (n + u > full || (n + u == full && rest == 0)) break;  // the same in every thread
+        float v[P];
+        unpack16<P>(raw[u], v);
+        const float top = largest<P>(v);
+        keep(top, n + u);
+        stat_add<true, ENT, P>(r, v, top, k);
+      }
+    }
+    auto single = [&](int64_t j, int64_t end, auto fast) {
+      if (j >= end) return;
+      const float v = to_f32(z[j]);
+      stat_add<decltype(fast)::value, ENT, 1>(r, &v, v, k);
+    };
+    single(threadIdx.x, sn.head, std::true_type{});
+    single(sn.tail0 + threadIdx.x, a.V, std::true_type{});
+    r = block_stat<true, ENT, NT>(r, k, red);
+    float shift = __builtin_fmaf(r.m, k, -base_of<true>(r.m, k));  // m k less the base
+    if (!(fabsf(r.m * k) < kFastBase)) {  // the same in every thread: a mask's value, +inf, a temperature near 0
+      shift = 0.0f;
+      r = stat_empty();
+      thread_words<T, NT, 1>(
+          z, a.V, [&](int64_t, float v) { stat_add<false, ENT, 1>(r, &v, v, k); },
+          [&](int64_t, const float* v, int64_t) { stat_add<false, ENT, P>(r, v, largest<P>(v), k); });
+      r = block_stat<false, ENT, NT>(r, k, red);
+    }
+    const bool none = r.s == 0.0f;  // every logit is -inf
+    const float log_s = none ? 0.0f : __builtin_fmaf(-kLn2, shift, logf(r.s));
     if (threadIdx.x == 0) {
-      const bool none = r.s == 0.0f;  // every logit is -inf
-      const float log_s = none ? 0.0f : logf(r.s);
       a.logp[row] = !given ? 0.0f : none ? -INFINITY : (zy - r.m) / a.tau - log_s;
       a.stats[2 * row] = none ? -INFINITY : r.m;
       a.stats[2 * row + 1] = log_s;
-      if (ENT) a.entropy[row] = none ? 0.0f : log_s + kLn2 * (r.u / r.s);
+      if (ENT) a.entropy[row] = none ? 0.0f : logf(r.s) - kLn2 * (r.u / r.s);
     }
+    r.u = log_s;
     if constexpr (TOP) top_words<T, NT>(a, row, z, by8, r, lds);
   }
 }
@@ -530,9 +599,11 @@ hipError_t launch_bwd(hipStream_t st, const LogprobArgs& a) {
 
 // Threads for a token's words. Few tokens: as many as a workgroup may have, so
 // that a row is few loads of each. Many tokens of a small vocabulary: a wave
-// each.
+// each, or two (20000 tokens of 8000 words, 20 top words: 104 us with two waves,
+// 130 with four; 4096 of 50257 the same).
 int logprob_threads(int64_t rows, int64_t V, int64_t K) {
   if (V <= 256 || (rows > 512 && V <= 4096)) return 64;
+  if (rows > 512 && V <= 16384 && K <= 128) return 128;
   if (rows > 512 || V <= 2048) return 256;
   return rows > 256 || V <= 4096 ? 512 : 1024;
 }
@@ -546,6 +617,7 @@ hipError_t launch_token_logprob(hipStream_t st, int dtype, const LogprobArgs& a)
   };
   switch (logprob_threads(a.rows, a.V, a.K)) {
     case 64: return run(std::integral_constant<int, 64>{});
+    case 128: return run(std::integral_constant<int, 128>{});
     case 256: return run(std::integral_constant<int, 256>{});
     case 512: return run(std::integral_constant<int, 512>{});
     default: return run(std::integral_constant<int, 1024>{});

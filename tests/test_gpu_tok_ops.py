@@ -350,6 +350,22 @@ def test_token_logprob(dtype, rows, V, top, tau, kind):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,V", [(5, 16393), (600, 8205), (600, 16401), (520, 33001)])
+@pytest.mark.parametrize("cut", range(0, 17, 3))
+def test_top_words_at_the_end_of_a_row(dtype, rows, V, cut):
+    """The largest logits in the row's last vectors, which not all lanes have."""
+    V -= cut
+    g = L.gen(V)
+    logits = L.randn(g, rows, V, dtype=L.DT[dtype])
+    logits[:, -29:] += 5.0
+    targets = torch.randint(0, V, (rows,), generator=g).cuda()
+    ti, tl = full(rows, 40, dtype=torch.int64), full(rows, 40)
+    dpc.dp_token_logprob(logits, targets, 1.0, full(rows), full(rows, 2), top_ids=ti, top_logp=tl)
+    want = torch.sort(logits.float(), dim=-1, descending=True, stable=True)[1][..., :40]
+    assert torch.equal(ti, want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,V", [(6, 3000), (600, 3000), (600, 9000)])
 def test_token_logprob_of_nan_and_infinities(dtype, rows, V):
     """A row with NaN or +inf gives NaN, its top words come in order all the
