@@ -746,25 +746,29 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) void k_embed_sum(Embed
     for (int k = 0; k < 5; ++k) at[k] = lane_int64(st, k);
     bool few = at[0] <= at[1] && at[1] <= at[2] && at[2] <= at[3] && at[3] <= at[4] && at[4] - at[0] <= 64;
     if (few) {  // the rows of all four words, read together
-      constexpr int U = 4;
       const int m = (int)(at[4] - at[0]);
       Places p{-1, 0.f, -1};
       if (m > 0) p = places_at<false>(a, at[0] + lane, at[4]);
       const int e1 = (int)(at[1] - at[0]), e2 = (int)(at[2] - at[0]), e3 = (int)(at[3] - at[0]);
+      auto add = [&](auto ahead) {  // rows in flight: four where there are few, sixteen where many
+        constexpr int U = decltype(ahead)::value;
 #pragma unroll 1
-      for (int r = 0; r < m; r += U) {
-        typename C::Raw raw[U];
+        for (int r = 0; r < m; r += U) {
+          typename C::Raw raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = cols.fetch(a.G, lane_int(p.tok, r + u));
+          for (int u = 0; u < U; ++u) raw[u] = cols.fetch(a.G, lane_int(p.tok, r + u));
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float f = lane_float(p.f, r + u);
-          if (r + u < e1) C::add(acc[0], raw[u], f);
-          else if (r + u < e2) C::add(acc[1], raw[u], f);
-          else if (r + u < e3) C::add(acc[2], raw[u], f);
-          else C::add(acc[3], raw[u], f);
+          for (int u = 0; u < U; ++u) {
+            const float f = lane_float(p.f, r + u);
+            if (r + u < e1) C::add(acc[0], raw[u], f);
+            else if (r + u < e2) C::add(acc[1], raw[u], f);
+            else if (r + u < e3) C::add(acc[2], raw[u], f);
+            else C::add(acc[3], raw[u], f);
+          }
         }
-      }
+      };
+      if (m <= 8) add(std::integral_constant<int, 4>{});
+      else add(std::integral_constant<int, 16>{});
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)

@@ -185,7 +185,7 @@ struct TopLds {
   static constexpr int parts = NT <= 128 ? 1024 : 2048, cap = NT <= 128 ? 512 : 1024;
   union {  // the words are collected once the parts have been looked through
     float part[parts];
-    uint64_t found[cap];
+    __attribute__((aligned(16))) uint64_t found[cap];
   };
   union {
     __attribute__((aligned(16))) uint32_t best[kGroups];
@@ -384,7 +384,11 @@ __device__ __forceinline__ void top_words(const LogprobArgs& a, int64_t row, con
     const uint64_t p = l.found[i];
     uint32_t rank = 0;
 #pragma unroll 4
-    for (uint32_t j = 0; j < n; ++j) rank += l.found[j] > p;
+    for (uint32_t j = 0; j + 1 < n; j += 2) {  // two words a read
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(l.found + j);
+      rank += (o.x > p) + (o.y > p);
+    }
+    if (n & 1) rank += l.found[n - 1] > p;
     if (rank < (uint32_t)K) {
       const float v = key_value((uint32_t)(p >> 32));
       a.top_ids[row * K + rank] = (int64_t)(uint32_t)~(uint32_t)p;
@@ -396,9 +400,10 @@ __device__ __forceinline__ void top_words(const LogprobArgs& a, int64_t row, con
 
 }  // namespace
 
-// One workgroup per token.
+// One workgroup per token. (Six waves per SIMD with top words: with eight the compiler spills, 4096 tokens of 50257 take
+// 111 us instead of 98.)
 template <typename T, int NT, bool ENT, bool TOP>
-__global__ __launch_bounds__(NT, 8) void k_token_logprob(LogprobArgs a) {
+__global__ __launch_bounds__(NT, TOP ? 6 : 8) void k_token_logprob(LogprobArgs a) {
   constexpr int P = elem_traits<T>::per16;
   __shared__ float red[3 * NT / 64];
   __shared__ TopLds<TOP ? NT : 0> lds;
