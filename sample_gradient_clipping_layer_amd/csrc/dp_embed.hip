@@ -677,7 +677,8 @@ __global__ __launch_bounds__(256, 4) void k_embed_norm(EmbedGradArgs a, int col_
           if ((lasts >> k) & 1) {
 #pragma unroll
             for (int e = 0; e < P; ++e) {
-              sq[k] = __builtin_fmaf(acc[e], e < cols.skip ? 0.f : acc[e], sq[k]);
+              const float v = e < cols.skip ? 0.f : acc[e];
+              sq[k] = __builtin_fmaf(v, v, sq[k]);
               acc[e] = 0.f;
             }
           }
@@ -685,7 +686,10 @@ __global__ __launch_bounds__(256, 4) void k_embed_norm(EmbedGradArgs a, int col_
         if (tail) {
           add_run<true>(a, cols, acc, i0 + m, end);
 #pragma unroll
-          for (int e = 0; e < P; ++e) sq_tail = __builtin_fmaf(acc[e], e < cols.skip ? 0.f : acc[e], sq_tail);
+          for (int e = 0; e < P; ++e) {
+            const float v = e < cols.skip ? 0.f : acc[e];
+            sq_tail = __builtin_fmaf(v, v, sq_tail);
+          }
         }
       }
     }

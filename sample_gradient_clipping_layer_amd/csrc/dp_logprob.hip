@@ -105,26 +105,19 @@ __device__ __forceinline__ float largest_of_8(float v) {
   return fmaxf(v, other(v, std::integral_constant<int, 0x141>{}));  // the mirrored lane of the eight
 }
 
-// one(word, value) and many(word, P values, vector) over a thread's part of a row: single elements to the first
-// 16-byte boundary, 16-byte vectors, single elements at the end. U vectors in flight.
-template <typename T, int NT, int U, typename F1, typename FP>
+// one(word, value) and many(word, P values) over a thread's part of a row: single elements to the first 16-byte
+// boundary, 16-byte vectors, single elements at the end.
+template <typename T, int NT, typename F1, typename FP>
 __device__ __forceinline__ void thread_words(const T* z, int64_t V, F1 one, FP many) {
   constexpr int P = elem_traits<T>::per16;
   const Span<T> sn(z, 0, V);
   const int64_t j = threadIdx.x;
   if (j < sn.head) one(j, to_f32(z[j]));
   const u32x4* vz = reinterpret_cast<const u32x4*>(z + sn.head);
-  for (int64_t i = threadIdx.x; i < sn.vecs; i += U * NT) {
-    u32x4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = vz[i + u * NT < sn.vecs ? i + u * NT : i];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i + u * NT >= sn.vecs) break;
-      float v[P];
-      unpack16<P>(raw[u], v);
-      many(sn.head + (i + u * NT) * P, v, i + u * NT);
-    }
+  for (int64_t i = threadIdx.x; i < sn.vecs; i += NT) {
+    float v[P];
+    unpack16<P>(vz[i], v);
+    many(sn.head + i * P, v);
   }
   const int64_t jt = sn.tail0 + threadIdx.x;
   if (jt < V) one(jt, to_f32(z[jt]));
@@ -212,7 +205,7 @@ __device__ __forceinline__ void collect(const T* z, int64_t V, uint64_t least, T
       if (at < (uint32_t)TopLds<NT>::cap) l.found[at] = p;
     }
   };
-  thread_words<T, NT, 1>(z, V, one, [&](int64_t j, const float* v, int64_t) {
+  thread_words<T, NT>(z, V, one, [&](int64_t j, const float* v) {
 #pragma unroll
     for (int e = 0; e < P; ++e) one(j + e, v[e]);
   });
@@ -245,7 +238,7 @@ __device__ uint64_t least_place(const T* z, int64_t V, int64_t K, TopLds<NT>& l)
         atomicAdd(&l.bins[digit], 1u);
       }
     };
-    thread_words<T, NT, 1>(z, V, one, [&](int64_t j, const float* v, int64_t) {
+    thread_words<T, NT>(z, V, one, [&](int64_t j, const float* v) {
 #pragma unroll
       for (int e = 0; e < P; ++e) one(j + e, v[e]);
     });
@@ -481,9 +474,9 @@ __global__ __launch_bounds__(NT, TOP ? 6 : 8) void k_token_logprob(LogprobArgs a
     if (!(fabsf(r.m * k) < kFastBase)) {  // the same in every thread: a mask's value, +inf, a temperature near 0
       shift = 0.0f;
       r = stat_empty();
-      thread_words<T, NT, 1>(
+      thread_words<T, NT>(
           z, a.V, [&](int64_t, float v) { stat_add<false, ENT, 1>(r, &v, v, k); },
-          [&](int64_t, const float* v, int64_t) { stat_add<false, ENT, P>(r, v, largest<P>(v), k); });
+          [&](int64_t, const float* v) { stat_add<false, ENT, P>(r, v, largest<P>(v), k); });
       r = block_stat<false, ENT, NT>(r, k, red);
     }
     const bool none = r.s == 0.0f;  // every logit is -inf

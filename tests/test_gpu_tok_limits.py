@@ -156,3 +156,82 @@ def test_balance():
     dpc.dp_balance_loss_backward(z, ids, counts, tokens, z)
     L.check(z[1:, -n:], want, gb, "grad")
     assert torch.count_nonzero(z[0]) == 0 and torch.count_nonzero(z[1, :-n]) == 0
+
+
+# ---- more work items than a launch has workgroups (2^20): they are looped over
+
+
+def test_many_short_rows_of_words():
+    rows, V = 1200000, 5
+    z, y = _randn(17, rows, V), _randint(18, -1, V, rows)
+    logp, stats, ent = torch.empty(rows, device="cuda"), torch.empty(rows, 2, device="cuda"), torch.empty(rows, device="cuda")
+    ti, tl = torch.empty(rows, 3, dtype=torch.int64, device="cuda"), torch.empty(rows, 3, device="cuda")
+    dpc.dp_token_logprob(z, y, 1.0, logp, stats, entropy=ent, top_ids=ti, top_logp=tl)
+    w = K.logprob(z, y, 1.0, 3)
+    L.check(logp, w["logp"], w["logp_bound"], "logp")
+    L.check(ent, w["entropy"], w["entropy_bound"], "entropy")
+    L.check(tl, w["top_logp"], w["top_bound"], "top_logp")
+    assert torch.equal(ti, w["top_ids"])
+    dl, grad = _randn(19, rows, dtype=torch.float32), torch.empty_like(z)
+    dpc.dp_token_logprob_backward(z, y, 1.0, stats, grad, dlogp=dl)
+    want, bound = K.logprob_backward(z, y, 1.0, stats, dl, None, None)
+    L.check(grad, want, bound, "grad")
+
+
+def test_many_samples():
+    B, T, V, d, E = 1200000, 2, 7, 8, 4
+    ids, z = _randint(20, -1, V, B, T), _randn(21, B, T, E)
+    G = _randn(22, B, T, d, dtype=torch.float32)
+    sq = torch.empty(B, device="cuda")
+    dpc.dp_embedding_norm(G, ids, *_order(ids, V), sq)
+    g, on = G.double() * (ids >= 0)[..., None], (ids[:, :1] == ids[:, 1:])
+    want = torch.where(on[:, 0], (g[:, 0] + g[:, 1]).square().sum(-1), g.square().sum((1, 2)))
+    # a sum of two rows, its square's two roundings, the sum of at most 16 squares
+    bound = 64 * L.U * (g[:, 0].abs() + g[:, 1].abs()).square().sum(-1) + 1e-37
+    L.check(sq, want, bound, "sqnorm")
+    route = ids[..., None].clamp(max=E - 1).contiguous()
+    loss, counts = torch.empty(B, device="cuda"), torch.empty(B, E, dtype=torch.int64, device="cuda")
+    tokens, grad = torch.empty(B, dtype=torch.int64, device="cuda"), torch.empty_like(z)
+    dpc.dp_balance_loss(z, route, loss, counts, tokens)
+    wl, wc, wt, bl = K.balance(z, route)
+    assert torch.equal(counts, wc) and torch.equal(tokens, wt)
+    L.check(loss, wl, bl, "loss")
+    dpc.dp_balance_loss_backward(z, route, counts, tokens, grad)
+    L.check(grad, *K.balance_backward(z, route, None), "grad")
+    s, gain = G.view(B, T, d), 1 + 0.1 * _randn(23, d, dtype=torch.float32)
+    rows = [torch.empty(B, d, device="cuda") for _ in range(2)]
+    dpc.dp_layer_norm_backward(G, s, gain, 1e-5, gain_rows=rows[0], bias_rows=rows[1])
+    _, wg, wb, _, bg, bb = K.layer_norm_backward(G, s, None, gain, 1e-5)
+    L.check(rows[0], wg, bg, "gain rows")
+    L.check(rows[1], wb, bb, "bias rows")
+
+
+def test_many_words_of_few_tokens():
+    ids = _randint(24, -1, 300000000, 3, 333)
+    order, starts = _order(ids, 300000000)  # 300 million starts
+    key = torch.where(ids < 0, 300000000, ids).reshape(-1)
+    sorted_keys, places = torch.sort(key, stable=True)
+    assert torch.equal(order, (sorted_keys << 32) + places)
+    at = torch.cat([sorted_keys, sorted_keys + 1, _randint(25, 0, 300000000, 10000)]).clamp(max=300000000)
+    assert torch.equal(starts[at], torch.searchsorted(sorted_keys, at))
+    assert bool((starts[1:] >= starts[:-1]).all())
+    V, d = 20000000, 8
+    ids = _randint(26, -1, V, 3, 333)
+    G, out = _randn(27, 3, 333, d), torch.empty(V, d, device="cuda")
+    c = torch.tensor([0.3, 1.0, 0.9], device="cuda")
+    dpc.dp_embedding_clipped_sum_noise(G, ids, *_order(ids, V), c, 1.0, 0.0, 1.0, 0, 0, 0, out)
+    words, of = torch.unique(ids, return_inverse=True)
+    first = int(words[0] < 0)  # the dropped ones' row
+    want, bound = K.embedding_sum(G, of - first, words.numel() - first, c, 1.0, 1.0)
+    L.check(out[words[first:]], want, bound, "out")
+    out[words[first:]] = 0
+    assert torch.count_nonzero(out) == 0
+
+
+def test_many_wide_rows():
+    N, V, d = 1100000, 5, 8192
+    ids, w = _randint(28, -1, V, N), _randn(29, V, d)
+    rows = torch.empty(N, d, dtype=BF16, device="cuda")
+    dpc.dp_embedding(ids, w, rows)
+    for at in (slice(0, 2000), slice(N - 60000, N)):
+        assert torch.equal(rows[at], torch.where(ids[at, None] < 0, 0, w[ids[at].clamp(min=0)]))

@@ -268,6 +268,20 @@ def test_embedding_gradient_by_differences():
         assert torch.allclose(out[v, v % d].double(), (f(w + e) - f(w - e)) / 2e-5, rtol=1e-5, atol=1e-6)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [5, 64, 333, 777, 2051])
+def test_embedding_norm_of_an_infinite_row(dtype, d):
+    """inf in any one column, and a run whose sum overflows: an infinite norm of its sample, as the formula has it."""
+    B, T, V, g = 3 + d, 20, 9, L.gen(d)
+    ids, G = torch.randint(0, V, (B, T), generator=g).cuda(), L.randn(g, B, T, d, dtype=L.DT[dtype])
+    for c in range(d):
+        G[2 + c, 3, c] = INF if c % 2 else -INF
+    ids[1], G[1] = 4, torch.finfo(torch.bfloat16).max
+    sq = full(B)
+    dpc.dp_embedding_norm(G, ids, *_order(ids, V), sq)
+    assert torch.isinf(sq[1:2 + d]).all() and torch.isfinite(sq[[0, -1]]).all()
+
+
 def test_embedding_with_a_foreign_order_stays_inside():
     """An order and starts that are not of these ids: no meaning, but nothing outside is touched."""
     g = L.gen(8)
