@@ -177,7 +177,7 @@ template <int NT>
 struct TopLds {
   static constexpr int parts = NT <= 128 ? 1024 : 2048, cap = NT <= 128 ? 512 : 1024;
   union {  // the words are collected once the parts have been looked through
-    float part[parts];
+    __attribute__((aligned(16))) float part[parts];
     __attribute__((aligned(16))) uint64_t found[cap];
   };
   union {
@@ -289,18 +289,20 @@ __device__ __forceinline__ uint32_t find_floor(int K, const TopLds<NT>& l) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) n += __popcll(__ballot(best[u] >= t));
     if (n >= K) floor = t;
+    if (n == K) break;
   }
   return floor;
 }
 
-// The row's K top words into top_ids and top_logp, from the parts' largest logits in l.part. by8: parts of 8 vectors.
+// The row's K top words into top_ids and top_logp, from the parts' largest logits in l.part. A part is a vector; by8: 8
+// of them; SMALL: 4 bytes, one word or two.
 // r: the largest logit, the sum (0: no distribution, NaN: NaN or +inf in the row) and log of the sum.
-template <typename T, int NT>
+template <typename T, int NT, bool SMALL>
 __device__ __forceinline__ void top_words(const LogprobArgs& a, int64_t row, const T* z, bool by8, Stat r, TopLds<NT>& l) {
   constexpr int P = elem_traits<T>::per16;
   const int K = (int)a.K;
   const Span<T> sn(z, 0, a.V);
-  const int64_t parts64 = by8 ? (sn.vecs + 7) / 8 : sn.vecs;
+  const int64_t parts64 = SMALL ? 4 * sn.vecs : by8 ? (sn.vecs + 7) / 8 : sn.vecs;
   const int parts = (int)(parts64 < TopLds<NT>::parts ? parts64 : TopLds<NT>::parts);
   __syncthreads();  // l.part is whole
   for (int g = threadIdx.x; g < kGroups; g += NT) {
@@ -334,11 +336,23 @@ __device__ __forceinline__ void top_words(const LogprobArgs& a, int64_t row, con
     if (j < sn.head) one(j, to_f32(z[j]));
     if (jt < a.V) one(jt, to_f32(z[jt]));
     const u32x4* vz = reinterpret_cast<const u32x4*>(z + sn.head);
+    if constexpr (SMALL) {
+      for (uint32_t i = threadIdx.x; i < reaches; i += NT) {
+        const int p = l.reach[i];
+        const uint32_t raw = reinterpret_cast<const uint32_t*>(vz)[p];
+        if constexpr (P == 8) {
+          one(sn.head + 2 * p, __uint_as_float(raw << 16));
+          one(sn.head + 2 * p + 1, __uint_as_float(raw & 0xFFFF0000u));
+        } else {
+          one(sn.head + p, __uint_as_float(raw));
+        }
+      }
+    }
     // a part number stands for all that share it: parts, 2 * parts ... on (rows of very many words)
     const int shift = by8 ? 3 : 0;
     const uint32_t work = reaches << shift;
     constexpr int U = 2;
-    for (int64_t first = 0; first < sn.vecs; first += (int64_t)TopLds<NT>::parts << shift) {
+    for (int64_t first = SMALL ? sn.vecs : 0; first < sn.vecs; first += (int64_t)TopLds<NT>::parts << shift) {
       for (uint32_t i0 = threadIdx.x; i0 < work; i0 += U * NT) {
         u32x4 raw[U];
         int64_t at[U];
@@ -393,9 +407,9 @@ __device__ __forceinline__ void top_words(const LogprobArgs& a, int64_t row, con
 
 }  // namespace
 
-// One workgroup per token. (Six waves per SIMD with top words: with eight the compiler spills, 4096 tokens of 50257 take
+// One workgroup per token. TOP: 0 without top words, 1 with, 2 with parts of 4 bytes. (Six waves per SIMD with top words: with eight the compiler spills, 4096 tokens of 50257 take
 // 111 us instead of 98.)
-template <typename T, int NT, bool ENT, bool TOP>
+template <typename T, int NT, bool ENT, int TOP>
 __global__ __launch_bounds__(NT, TOP ? 6 : 8) void k_token_logprob(LogprobArgs a) {
   constexpr int P = elem_traits<T>::per16;
   __shared__ float red[3 * NT / 64];
@@ -409,10 +423,15 @@ __global__ __launch_bounds__(NT, TOP ? 6 : 8) void k_token_logprob(LogprobArgs a
     Stat r = stat_empty();
     const Span<T> sn(z, 0, a.V);
     const u32x4* vz = reinterpret_cast<const u32x4*>(z + sn.head);
-    const bool by8 = TOP && sn.vecs > TopLds<NT>::parts;  // a part of the row is 8 vectors
+    const bool by8 = TOP == 1 && sn.vecs > TopLds<NT>::parts;  // a part of the row is 8 vectors
     // Round n holds vectors n * NT ..; a part number stands again for parts behind the last one. Both are the wave's.
-    auto keep = [&](float top, int n) {
-      if constexpr (TOP) {
+    auto keep = [&](const float* v, float top, int n) {
+      if constexpr (TOP == 2) {
+        f32x4 m;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = P == 8 ? fmaxf(v[2 * e % P], v[(2 * e + 1) % P]) : v[e];
+        *reinterpret_cast<f32x4*>(lds.part + 4 * (n * NT + threadIdx.x)) = m;
+      } else if constexpr (TOP == 1) {
         if (by8) {
           const float m = largest_of_8(top);
           const int at = n * (NT / 8);
@@ -437,8 +456,8 @@ __global__ __launch_bounds__(NT, TOP ? 6 : 8) void k_token_logprob(LogprobArgs a
         unpack16<P>(raw[u], v);
         unpack16<P>(raw[u + 1], v + P);
         const float top0 = largest<P>(v), top1 = largest<P>(v + P);
-        keep(top0, n + u);
-        keep(top1, n + u + 1);
+        keep(v, top0, n + u);
+        keep(v + P, top1, n + u + 1);
         stat_add<true, ENT, 2 * P>(r, v, fmaxf(top0, top1), k);
       }
     }
@@ -458,7 +477,7 @@ __global__ __launch_bounds__(NT, TOP ? 6 : 8) void k_token_logprob(LogprobArgs a
         float v[P];
         unpack16<P>(raw[u], v);
         const float top = largest<P>(v);
-        keep(top, n + u);
+        keep(v, top, n + u);
         stat_add<true, ENT, P>(r, v, top, k);
       }
     }
@@ -488,7 +507,7 @@ __global__ __launch_bounds__(NT, TOP ? 6 : 8) void k_token_logprob(LogprobArgs a
       if (ENT) a.entropy[row] = none ? 0.0f : logf(r.s) - kLn2 * (r.u / r.s);
     }
     r.u = log_s;
-    if constexpr (TOP) top_words<T, NT>(a, row, z, by8, r, lds);
+    if constexpr (TOP) top_words<T, NT, TOP == 2>(a, row, z, by8, r, lds);
   }
 }
 
@@ -577,14 +596,20 @@ unsigned grid_of(int64_t n) { return (unsigned)std::min<int64_t>(n, 1 << 20); }
 template <typename T, int NT>
 hipError_t launch_fwd(hipStream_t st, const LogprobArgs& a) {
   const unsigned blocks = grid_of(a.rows);
-  if (a.entropy) {
-    if (a.K) k_token_logprob<T, NT, true, true><<<blocks, NT, 0, st>>>(a);
-    else k_token_logprob<T, NT, true, false><<<blocks, NT, 0, st>>>(a);
-  } else {
-    if (a.K) k_token_logprob<T, NT, false, true><<<blocks, NT, 0, st>>>(a);
-    else k_token_logprob<T, NT, false, false><<<blocks, NT, 0, st>>>(a);
-  }
-  return hipGetLastError();
+  auto run = [&](auto top) {
+    constexpr int TOP = decltype(top)::value;
+    if (a.entropy) k_token_logprob<T, NT, true, TOP><<<blocks, NT, 0, st>>>(a);
+    else k_token_logprob<T, NT, false, TOP><<<blocks, NT, 0, st>>>(a);
+    return hipGetLastError();
+  };
+  if (a.K == 0) return run(std::integral_constant<int, 0>{});
+  // Rows of up to 128 vectors, with a top word in every fourth or more: the largest of whole vectors are so few that the
+  // floor lets many others through, and ranking takes the square of them (20000 tokens of 600 bf16: 32 top words 31 us
+  // against 34 with parts of a vector, 100 top words 50 against 90).
+  constexpr int P = elem_traits<T>::per16;
+  if constexpr (NT == 64)
+    if (a.V <= 128 * P && 4 * P * a.K > a.V) return run(std::integral_constant<int, 2>{});
+  return run(std::integral_constant<int, 1>{});
 }
 
 template <typename T, int NT>

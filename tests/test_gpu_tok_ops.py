@@ -380,6 +380,18 @@ def test_top_words_at_the_end_of_a_row(dtype, rows, V, cut):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [3, 8, 64, 67, 256, 257, 300, 511, 512, 513, 1000, 1023, 1024, 1025])
+@pytest.mark.parametrize("kind", ["normal", "ties", "masked", "lowest", "rising"])
+def test_top_words_of_short_rows(dtype, V, kind):
+    """Few to all words of rows around the ends of what is held by 4 bytes, a row at every alignment."""
+    g, rows = L.gen(V), 520
+    logits, targets = _logits(g, (rows, V), L.DT[dtype], kind), torch.randint(0, V, (rows,), generator=g).cuda()
+    for top in sorted({1, max(1, V // 32), V // 16 + 1, V // 8 + 1, V // 3 + 1, V}):
+        if top <= 256:
+            _check_logprob(logits, targets, 1.0, top)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,V", [(6, 3000), (600, 3000), (600, 9000)])
 def test_token_logprob_of_nan_and_infinities(dtype, rows, V):
     """A row with NaN or +inf gives NaN, its top words come in order all the
