@@ -545,8 +545,9 @@ size_t dp_embedding_order_workspace_bytes(int64_t N, int64_t V);
  *  sqnorm   [B] fp32, overwritten (accumulate == 0) or added to.
  *  workspace  at least dp_embedding_workspace_bytes(...) bytes.
  */
-dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const int64_t* order, int64_t B, int64_t T, int64_t V, int64_t d, float scale, void* workspace, size_t ws_bytes,
-                            float* sqnorm, int32_t accumulate);
+dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const int64_t* order, int64_t B, int64_t T,
+                            int64_t V, int64_t d, float scale, void* workspace, size_t ws_bytes, float* sqnorm,
+                            int32_t accumulate);
 
 /*
  * Clipped, noised mean gradient of the whole table:

@@ -252,8 +252,9 @@ size_t dp_embedding_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_
   return dtype_ok(dtype) && check_embedding(B, T, V, d) == DP_OK ? dpk::embed_ws_bytes(dtype, B, T, d) : 0;
 }
 
-dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const int64_t* order, int64_t B, int64_t T, int64_t V, int64_t d, float scale, void* workspace, size_t ws_bytes,
-                            float* sqnorm, int32_t accumulate) {
+dp_status dp_embedding_norm(void* stream, const void* G, dp_dtype dtype, const int64_t* order, int64_t B, int64_t T,
+                            int64_t V, int64_t d, float scale, void* workspace, size_t ws_bytes, float* sqnorm,
+                            int32_t accumulate) {
   if (!G || !order || !sqnorm) return DP_ERR_NULL;
   dp_status s = check_embedding(B, T, V, d);
   if (s != DP_OK) return s;

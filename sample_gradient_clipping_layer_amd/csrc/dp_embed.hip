@@ -10,7 +10,15 @@
 // A per-sample gradient of the table has at most T rows that are not 0, so
 // nothing of its size [B][V][d] is ever formed: in the order, the tokens of
 // one (word, sample) are a run of neighbouring places, and the tokens of one
-// word a run of those. All passes are bound by HBM; each reads G once.
+// word a run of those. The norm and the sum read G once each.
+//
+// The lookup is bound by HBM: 32768 tokens of 1280 bf16 take 26 us, 6.4 TB/s of
+// rows read and written (rows met again come from the caches). The clipping
+// pass of 32 x 1024 such tokens over 50257 words takes 125 us in its eleven
+// launches: the order 28 (four launches), the norm 37 (three), the factors 2,
+// the sum 62 (two; 257 MB of it are the table, written at 5 TB/s). What is not
+// the table's is latency: chains of a place, its row, its run's end. Noise adds
+// 70 us of fp32 work (as much as the noise kernel takes for as many elements).
 //
 // A run may be long (a frequent word, a batch padded with one word). Sums over
 // long runs take the sums of tiles: a first launch adds up every tile of 16
@@ -479,8 +487,8 @@ __device__ __forceinline__ void add_places(const EmbedGradArgs& a, const C& cols
   for (int u = 0; u < U; ++u) C::add(acc, raw[u], lane_float(p.f, r0 + u));
 }
 
-// Rows in flight of a long run. The norm's kernel holds 8 rows' sums beside them: with 16 it has room for four waves
-// instead of five (32768 tokens without a long run: 32 us instead of 28).
+// Rows in flight of a long run. The norm has eight rows of its own in flight already: with 16 it takes 36 us for 32768
+// tokens of Zipf's law, 34 with 8.
 template <bool NORM>
 constexpr int kAhead = NORM ? 8 : 16;
 
@@ -609,7 +617,10 @@ __global__ __launch_bounds__(1024) void k_embed_tiles(EmbedGradArgs a, int l, in
 // Squared norms of the runs that start in a wave's 8 places, over its part of
 // the columns, each written at the token of the run's last of these places, 0
 // at the other tokens. The rows of all 8 places are read together; what
-// follows of the last run behind them is added from its tiles.
+// follows of the last run behind them is added from its tiles. All that a
+// wave decides by is in scalar registers: with branches by lanes the compiler
+// waits for each row before the next (36 us for 32 x 1024 tokens of 1280 bf16,
+// 24 so: 84 MB at 3.5 TB/s).
 template <typename T, bool TINY>
 __global__ __launch_bounds__(256, 4) void k_embed_norm(EmbedGradArgs a, int col_groups) {
   constexpr int R = kEmbedNormPlaces, P = elem_traits<T>::per16;
@@ -723,10 +734,15 @@ __global__ __launch_bounds__(256) void k_embed_norm_finish(EmbedGradArgs a, int 
 }
 
 // The clipped, noised mean of 4 neighbouring words (whose noise shares its
-// blocks) and 256 columns, by a wave: four columns a lane, so that 32 sums leave room for 8 rows in flight beside 16
-// waves a CU (with eight columns: 152 registers and 85 us instead of 62 for 32768 tokens of 1280 bf16).
+// blocks) and 256 columns, by a wave: four columns a lane, so that 16 sums
+// leave room for 16 rows in flight beside 16 to 20 waves a CU (with eight
+// columns 152 registers, and 85 us instead of 62 for 32768 tokens of 1280 bf16
+// before further steps). Past the caches where it can: the table is larger than
+// they are (72 us through them, 55 so). Rows in flight: four up to eight places,
+// else sixteen (55 us by four alone, 50 so).
 template <typename T, bool TINY>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) void k_embed_sum(EmbedGradArgs a, NoiseArgs na, float* __restrict__ out, int col_waves) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) void k_embed_sum(EmbedGradArgs a, NoiseArgs na,
+                                                                           float* __restrict__ out, int col_waves) {
   constexpr int P = 4;
   using C = Cols<T, P, TINY>;
   const int lane = threadIdx.x & 63;
@@ -754,10 +770,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 5 : 4) void k_embed_sum(Embed
       Places p{-1, 0.f, -1};
       if (m > 0) p = places_at<false>(a, at[0] + lane, at[4]);
       const int e1 = (int)(at[1] - at[0]), e2 = (int)(at[2] - at[0]), e3 = (int)(at[3] - at[0]);
-      auto add = [&](auto ahead) {  // rows in flight: four where there are few, sixteen where many
+      auto add = [&](auto ahead) {
         constexpr int U = decltype(ahead)::value;
 #pragma unroll 1
-        for (int r = 0; r < m; r += U) {
+        for (int r = 0; r < m; r += U) {  // lanes past m hold no place
           typename C::Raw raw[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) raw[u] = cols.fetch(a.G, lane_int(p.tok, r + u));

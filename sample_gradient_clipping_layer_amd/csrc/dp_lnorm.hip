@@ -5,8 +5,11 @@
 //   backward:  h = dy * gain,  ds = dsum + rstd * (h - mean(h) - u * mean(h * u)),
 //              gain_rows[b] = sum_t dy[b][t] * u[b][t],  bias_rows[b] = sum_t dy[b][t]
 //
-// A row is held in the registers of one, four or sixteen waves, so one pass
-// over memory serves both its statistics and its outputs. The variance is that
+// Bound by HBM: 32 x 1024 rows of 1280 bf16 with a residual take 58 us forward
+// (336 MB, 5.8 TB/s), 69 + 5 back with both gradients (the rows of 252 MB read
+// and 84 written at 4.9 TB/s, then the workgroups' sums). A row is held in the
+// registers of one, four, eight or sixteen waves, so one pass over memory
+// serves both its statistics and its outputs. The variance is that
 // of the centred row, whose own mean (the rounding of the first one) is taken
 // off again: rows far from zero lose nothing to a difference of large sums.
 // A lane keeps the columns it holds over all its rows, so the per-sample

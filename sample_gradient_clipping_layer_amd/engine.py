@@ -90,8 +90,8 @@ class PrivacyEngine:
     The backward pass must be of the SUM of the per-sample losses, so that the
     kept output gradients are the per-sample ones. A module may run once per
     forward pass; its input's first dimension is the batch (positions given to
-    an Embedding too: one row of them per sample). Any other trainable parameter makes the constructor fail:
-    its per-sample gradient would go unclipped.
+    an Embedding too: one row of them per sample). Any other trainable parameter
+    makes the constructor fail: its per-sample gradient would go unclipped.
 
     mode: the per-layer path rule ('ghost-mixed', 'ghost', 'explicit',
     'time') of the linear and convolution layers; expert layers have the ghost

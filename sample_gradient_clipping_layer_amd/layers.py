@@ -16,6 +16,10 @@ The engine keeps what it needs of the modules during the backward pass; without
 an engine their weights get their ordinary gradients. Everything is computed by
 the library's kernels on the current GPU and torch's current stream;
 activations are float32 or bfloat16.
+
+In a captured HIP graph the backward pass is captured with its forward pass, and
+no eager graph of the same parameters may be alive then (torch runs a leaf's
+accumulation on the stream of the graph that met it first).
 """
 from __future__ import annotations
 
