@@ -32,8 +32,9 @@
 // launch of its own: a workgroup ranks the tokens of its tile by digit (within
 // a wave by ballots, in order), and finds where its share of every digit goes
 // from the counts that all workgroups left. Up to 4096 tokens are sorted by one
-// workgroup in one launch. Places and starts are checked where they are read:
-// whatever they hold, accesses stay inside the tensors.
+// workgroup, and others beside it count the starts. Places and starts are
+// checked where they are read: whatever they hold, accesses stay inside the
+// tensors.
 #include "dp_cols.hpp"
 #include "dp_common.hpp"
 #include "dp_lm.hpp"
@@ -296,11 +297,72 @@ __global__ __launch_bounds__(kSortThreads) void k_order_scatter(const int64_t* _
   }
 }
 
-// All digits of up to 4096 tokens by one workgroup, the tokens in LDS between
-// the passes; the keys in order are left for the starts.
-__global__ __launch_bounds__(kSortThreads) void k_order_small(const int64_t* __restrict__ ids, int N, int64_t V, SortPlan p,
-                                                              uint32_t* __restrict__ keys_out,
-                                                              int64_t* __restrict__ order) {
+namespace {
+
+struct StartsLds {
+  uint32_t count[kSortThreads], waves[kSortWaves], less[kSortWaves];
+};
+
+// The starts of the 1024 words from w0 on, by a workgroup of 1024 threads: how many ids are smaller than w0, and how many
+// are each of the words. All ids are read.
+__device__ __forceinline__ void starts_of_ids(const int64_t* __restrict__ ids, int N, int64_t V, int64_t w0,
+                                              int64_t* __restrict__ starts, StartsLds& l) {
+  constexpr int U = 4;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  l.count[threadIdx.x] = 0;
+  __syncthreads();
+  uint32_t less = 0;
+  for (int i0 = threadIdx.x; i0 < N; i0 += U * kSortThreads) {
+    uint32_t key[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) key[u] = i0 + u * kSortThreads < N ? key_of(ids[i0 + u * kSortThreads], V) : ~0u;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      less += key[u] < (uint32_t)w0;
+      const uint32_t at = key[u] - (uint32_t)w0;  // past the 1024 for a smaller key too
+      if (at < (uint32_t)kSortThreads) {
+        // one add for the lanes with the first one's word: a frequent one's would wait for each other
+        const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+        const uint64_t same = __ballot(at == first);
+        if (at != first) atomicAdd(&l.count[at], 1u);
+        else if (lane == __builtin_ctzll(same)) atomicAdd(&l.count[at], (uint32_t)__popcll(same));
+      }
+    }
+  }
+  __syncthreads();
+  const uint32_t mine = l.count[threadIdx.x];
+  uint32_t run = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t o = __shfl_up(run, off, kWave);
+    if (lane >= off) run += o;
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) less += __shfl_xor(less, off, kWave);
+  if (lane == 63) {
+    l.waves[wave] = run;
+    l.less[wave] = less;
+  }
+  __syncthreads();
+  uint32_t s = run - mine;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) s += l.less[w] + (w < wave ? l.waves[w] : 0u);
+  if (w0 + threadIdx.x <= V) starts[w0 + threadIdx.x] = s;
+}
+
+}  // namespace
+
+// All digits of up to 4096 tokens by one workgroup, the tokens in LDS between the passes; workgroups behind it: the
+// starts (or, without, the keys in order are left for them).
+__global__ __launch_bounds__(kSortThreads) void k_order_small(const int64_t* __restrict__ ids, int N, int64_t V,
+                                                              SortPlan p, uint32_t* __restrict__ keys_out,
+                                                              int64_t* __restrict__ order,
+                                                              int64_t* __restrict__ starts) {
+  __shared__ StartsLds lds;
+  if (blockIdx.x > 0) {
+    starts_of_ids(ids, N, V, (int64_t)(blockIdx.x - 1) * kSortThreads, starts, lds);
+    return;
+  }
   __shared__ uint32_t keys[2][kSortSmall];
   __shared__ uint16_t toks[2][kSortSmall];
   __shared__ uint32_t seen[kSortWaves][kSortMaxDigits];
@@ -952,9 +1014,13 @@ hipError_t launch_embed_order(hipStream_t st, const int64_t* ids, int64_t N, int
     return hipGetLastError();
   };
   if (N <= kSortSmall) {
-    k_order_small<<<1, kSortThreads, 0, st>>>(ids, (int)N, V, p, lists, order);
+    // The starts from the ids beside the sort: every workgroup of 1024 words reads all ids, worth it for few of both
+    // (1001 tokens, 5003 words: 7.1 us, 10.7 in two launches; 32768 tokens beside the first of theirs: 30 and 26).
+    const bool beside = V < (1 << 19);
+    const unsigned more = beside ? (unsigned)((V + kSortThreads) / kSortThreads) : 0;
+    k_order_small<<<1 + more, kSortThreads, 0, st>>>(ids, (int)N, V, p, lists, order, starts);
     const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? find_starts(lists) : e;
+    return e == hipSuccess && !beside ? find_starts(lists) : e;
   }
   k_order_count<<<(unsigned)p.blocks, kSortThreads, 0, st>>>(ids, N, V, p, counts);
   hipError_t e = hipGetLastError();

@@ -188,6 +188,19 @@ def test_embedding_order(B, T, V, kind):
     assert torch.equal(starts.cpu(), wstarts)
 
 
+@pytest.mark.parametrize("V", [1, 63, 1023, 1024, 1025, 2047, 2048, 5003, (1 << 19) - 1, 1 << 19])
+@pytest.mark.parametrize("N", [1, 64, 1001, 4095, 4096, 4097])
+def test_embedding_starts_of_few_tokens(N, V):
+    """Words spread out, in one place of the table, one alone (at either end), all dropped."""
+    g = L.gen(N + V)
+    half = max(1, V // 2)
+    for ids in (torch.randint(-1, V, (N,), generator=g), torch.randint(V - half, V, (N,), generator=g),
+                torch.full((N,), V - 1), torch.zeros(N, dtype=torch.int64), torch.full((N,), V), torch.full((N,), -5)):
+        order, starts = _order(ids.cuda(), V)
+        want, wstarts = K.order(ids, V)
+        assert torch.equal(order.cpu(), want) and torch.equal(starts.cpu(), wstarts)
+
+
 GRADS = [(1, 1, 1, 1, "any"), (2, 3, 5, 7, "any"), (8, 1, 50257, 64, "any"), (3, 40, 11, 33, "any"),
          (2, 1200, 3, 520, "few"), (1, 5000, 1, 72, "few"), (1, 40000, 2, 24, "few"), (32, 64, 1000, 1280, "any"),
          (4100, 2, 50, 24, "any"), (5, 700, 70000, 40, "any"), (2, 33, 7, 8192, "few"), (1, 300, 4, 2051, "few"),
