@@ -14,9 +14,10 @@
 //
 // The lookup is bound by HBM: 32768 tokens of 1280 bf16 take 26 us, 6.4 TB/s of
 // rows read and written (rows met again come from the caches). The clipping
-// pass of 32 x 1024 such tokens over 50257 words takes 125 us in its eleven
+// pass of 32 x 1024 such tokens over 50257 words takes 122 us in its ten
 // launches: the order 28 (four launches), the norm 37 (three), the factors 2,
-// the sum 62 (two; 257 MB of it are the table, written at 5 TB/s). What is not
+// the sum 62 (two; 257 MB of it are the table, written at 5 TB/s), each call by
+// itself. What is not
 // the table's is latency: chains of a place, its row, its run's end. Noise adds
 // 70 us of fp32 work (as much as the noise kernel takes for as many elements).
 //
