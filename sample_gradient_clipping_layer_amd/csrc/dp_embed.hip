@@ -142,7 +142,9 @@ SortPlan sort_plan(int64_t N, int64_t V) {
   return p;
 }
 
-__device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V) { return id < 0 || id >= V ? (uint32_t)V : (uint32_t)id; }
+__device__ __forceinline__ uint32_t key_of(int64_t id, int64_t V) {
+  return id < 0 || id >= V ? (uint32_t)V : (uint32_t)id;
+}
 
 __device__ __forceinline__ int64_t place_of(uint32_t word, uint32_t tok) {
   return (int64_t)(((uint64_t)word << 32) | tok);
@@ -165,8 +167,8 @@ __global__ __launch_bounds__(kSortThreads) void k_order_count(const int64_t* __r
   __shared__ uint32_t bins[kSortMaxDigits];
   const int D = p.digits();
   const int64_t b = blockIdx.x;
-  for (int64_t i = b * kSortThreads + threadIdx.x; i < (int64_t)(p.passes - 1) * p.blocks * D; i += p.blocks * kSortThreads)
-    counts[p.blocks * D + i] = 0;
+  const int64_t later = (int64_t)(p.passes - 1) * p.blocks * D;
+  for (int64_t i = b * kSortThreads + threadIdx.x; i < later; i += p.blocks * kSortThreads) counts[p.blocks * D + i] = 0;
   for (int k = threadIdx.x; k < D; k += kSortThreads) bins[k] = 0;
   __syncthreads();
   const int64_t i0 = b * p.tile();
@@ -179,7 +181,8 @@ __global__ __launch_bounds__(kSortThreads) void k_order_count(const int64_t* __r
 }
 
 // Exclusive sums down the workgroups, per digit, in place, and each digit's total behind them (many workgroups).
-__global__ __launch_bounds__(64) void k_order_scan(SortPlan p, uint32_t* __restrict__ counts, uint32_t* __restrict__ totals) {
+__global__ __launch_bounds__(64) void k_order_scan(SortPlan p, uint32_t* __restrict__ counts,
+                                                   uint32_t* __restrict__ totals) {
   const int D = p.digits();
   const int k = blockIdx.x * 64 + threadIdx.x;
   if (k >= D) return;
@@ -708,7 +711,8 @@ __global__ __launch_bounds__(256, 4) void k_embed_norm(EmbedGradArgs a, int col_
     uint32_t mine = 0, lasts = 0;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const bool in = k < m && (((heads >> (k + 1)) & 1) || (k > 0 && ((goes_on >> (k + 1)) & 1) && ((mine >> (k - 1)) & 1)));
+      const bool on = k > 0 && ((goes_on >> (k + 1)) & 1) && ((mine >> (k - 1)) & 1);
+      const bool in = k < m && (((heads >> (k + 1)) & 1) || on);
       mine |= (uint32_t)in << k;
       const bool more = k + 1 < R && k + 1 < m && ((goes_on >> (k + 2)) & 1);
       lasts |= (uint32_t)(in && !more) << k;

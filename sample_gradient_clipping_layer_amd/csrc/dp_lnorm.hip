@@ -158,7 +158,8 @@ constexpr int backward_waves() {
 // Work items: (sample, chunk of its rows); with `own_groups` every group of
 // a block takes a sample of its own (chunks == 1).
 template <typename T, bool WHOLE, int E, int WPR>
-__global__ __launch_bounds__(row_threads<WPR>(), (backward_waves<T, E, WPR>())) void k_layer_norm_backward(LayerNormBackArgs a) {
+__global__ __launch_bounds__(row_threads<WPR>(),
+                             (backward_waves<T, E, WPR>())) void k_layer_norm_backward(LayerNormBackArgs a) {
   constexpr int NW = row_threads<WPR>() / 64, GROUPS = NW / WPR, LPR = 64 * WPR;
   using M = RowMap<T, WHOLE, E, LPR>;
   __shared__ float red1[64], red2[96];
@@ -312,7 +313,8 @@ __global__ __launch_bounds__(row_threads<WPR>(), (backward_waves<T, E, WPR>())) 
           writes = writes && group == 0;
         }
       }
-      if (writes) M::store_f32(a.chunks == 1 ? rows + item * a.d : a.partial + (which * items + item) * a.d, (int)a.d, lane, acc);
+      float* row = a.chunks == 1 ? rows + item * a.d : a.partial + (which * items + item) * a.d;
+      if (writes) M::store_f32(row, (int)a.d, lane, acc);
     };
     if (a.gain_rows) give(acc_g, a.gain_rows, 0);
     if (a.bias_rows) give(acc_b, a.bias_rows, 1);

@@ -409,8 +409,8 @@ __device__ __forceinline__ void top_words(const LogprobArgs& a, int64_t row, con
 
 }  // namespace
 
-// One workgroup per token. TOP: 0 without top words, 1 with, 2 with parts of 4 bytes. (Six waves per SIMD with top words: with eight the compiler spills, 4096 tokens of 50257 bf16
-// and 64 top words take 121 us instead of 109.)
+// One workgroup per token. TOP: 0 without top words, 1 with, 2 with parts of 4 bytes. (Six waves per SIMD with top words:
+// with eight the compiler spills, 4096 tokens of 50257 bf16 and 64 top words take 121 us instead of 109.)
 template <typename T, int NT, bool ENT, int TOP>
 __global__ __launch_bounds__(NT, TOP ? 6 : 8) void k_token_logprob(LogprobArgs a) {
   constexpr int P = elem_traits<T>::per16;

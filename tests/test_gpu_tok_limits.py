@@ -235,3 +235,36 @@ def test_many_wide_rows():
     dpc.dp_embedding(ids, w, rows)
     for at in (slice(0, 2000), slice(N - 60000, N)):
         assert torch.equal(rows[at], torch.where(ids[at, None] < 0, 0, w[ids[at].clamp(min=0)]))
+
+
+# ---- the widest tables, the most experts and places
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("B,T,V,d", [(2, 3, 3, 1 << 20), (1, 70, 2, (1 << 20) - 1), (3, 1, 5, (1 << 20) - 5)])
+def test_widest_table(dtype, B, T, V, d):
+    ids, w = _randint(30, -1, V, B, T), _randn(31, V, d, dtype=dtype)
+    rows = torch.empty(B, T, d, dtype=dtype, device="cuda")
+    dpc.dp_embedding(ids, w, rows)
+    assert torch.equal(rows, torch.where(ids[..., None] < 0, 0, w[ids.clamp(min=0)]))
+    order, starts = _order(ids, V)
+    sq, c, out = torch.empty(B, device="cuda"), torch.rand(B, device="cuda"), torch.empty(V, d, device="cuda")
+    G = rows.mul_(0.7)
+    dpc.dp_embedding_norm(G, ids, order, starts, sq)
+    L.check(sq, *K.embedding_norm(G, ids, V, 1.0), "sqnorm")
+    dpc.dp_embedding_clipped_sum_noise(G, ids, order, starts, c, 1.0, 0.0, 1.0, 0, 0, 0, out)
+    L.check(out, *K.embedding_sum(G, ids, V, c, 1.0, 1.0), "out")
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_most_experts_and_places(dtype):
+    B, T, E = 2, 37, 1024
+    z, ids = _randn(32, B, T, E, dtype=dtype), _randint(33, -1, E + 1, B, T, 1024)
+    loss, counts = torch.empty(B, device="cuda"), torch.empty(B, E, dtype=torch.int64, device="cuda")
+    tokens, grad = torch.empty(B, dtype=torch.int64, device="cuda"), torch.empty_like(z)
+    dpc.dp_balance_loss(z, ids, loss, counts, tokens)
+    wl, wc, wt, bound = K.balance(z, ids)
+    assert torch.equal(counts, wc) and torch.equal(tokens, wt)
+    L.check(loss, wl, bound, "loss")
+    dpc.dp_balance_loss_backward(z, ids, counts, tokens, grad)
+    L.check(grad, *K.balance_backward(z, ids, None), "grad")
