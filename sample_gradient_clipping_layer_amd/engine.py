@@ -90,8 +90,10 @@ class PrivacyEngine:
     The backward pass must be of the SUM of the per-sample losses, so that the
     kept output gradients are the per-sample ones. A module may run once per
     forward pass; its input's first dimension is the batch (positions given to
-    an Embedding too: one row of them per sample). Any other trainable parameter
-    makes the constructor fail: its per-sample gradient would go unclipped.
+    an Embedding too: one row of them per sample). A torch Embedding's
+    padding_idx keeps its row: its gradient is 0, without noise. Any other
+    trainable parameter makes the constructor fail: its per-sample gradient
+    would go unclipped.
 
     mode: the per-layer path rule ('ghost-mixed', 'ghost', 'explicit',
     'time') of the linear and convolution layers; expert layers have the ghost
@@ -371,6 +373,8 @@ class PrivacyEngine:
             if isinstance(L.module, ExpertLinear):
                 w.grad = out.transpose(1, 2).to(w.dtype).contiguous()  # [E, p, d]
             elif isinstance(L.module, _TABLES):
+                if getattr(L.module, "padding_idx", None) is not None:
+                    out[L.module.padding_idx].zero_()  # no sample has a gradient there: the row needs no noise
                 w.grad = out.to(w.dtype)  # [V, d]
             elif isinstance(L.module, LayerNorm):  # [1, d], or [1, 2d] with the bias
                 d = w.numel()

@@ -1,0 +1,39 @@
+"""Calls at the edges of what the operators from tokens to a per-sample loss
+take: values and routings that other inputs do not reach, against their values
+in 64 bits."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import lm_util as L
+from oracle import noise as N
+from sample_gradient_clipping_layer_amd.engine import PrivacyEngine
+
+pytestmark = pytest.mark.gpu
+
+# ---- a torch table's padding word
+
+
+@pytest.mark.parametrize("padding", [0, 2, 16])
+def test_a_padding_words_row_gets_no_noise(padding):
+    """Its row has no gradient whatever the data, so it needs none; the others carry their layer's stream."""
+    g, v, d, b = L.gen(3), 17, 12, 4
+    m = torch.nn.Embedding(v, d, padding_idx=padding, device="cuda")
+    engine = PrivacyEngine(m, C=0.5, sigma=0.9, seed=21)
+    ids = torch.randint(0, v, (b, 6), generator=g)
+    ids[:, -2:] = padding
+    dy = L.randn(g, b, 6, d)
+    grads = []
+    for sigma in (0.9, 0.0):
+        engine.sigma = sigma
+        (m(ids.cuda()) * dy).sum().backward()
+        engine.step(5)
+        grads.append(m.weight.grad.double().cpu().numpy())
+    engine.detach()
+    assert (grads[0][padding] == 0).all() and (grads[1][padding] == 0).all()
+    z = np.float32(np.float32(0.9) * np.float32(0.5)) * N.weight_noise(v, d, 21, 0, 5) / b
+    z[padding] = 0
+    # the sum's and the mean's rounding on both sides
+    assert np.abs(grads[0] - grads[1] - z).max() <= 8 * L.U * max(np.abs(grads[1]).max(), np.abs(z).max())
