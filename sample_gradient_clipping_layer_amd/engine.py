@@ -90,7 +90,8 @@ class PrivacyEngine:
     The backward pass must be of the SUM of the per-sample losses, so that the
     kept output gradients are the per-sample ones. A module may run once per
     forward pass; its input's first dimension is the batch (positions given to
-    an Embedding too: one row of them per sample). A torch Embedding's
+    an Embedding too: one row of them per sample, [B, T]; ids of one dimension
+    are refused where another layer has several rows per sample). A torch Embedding's
     padding_idx keeps its row: its gradient is 0, without noise. Any other
     trainable parameter makes the constructor fail: its per-sample gradient
     would go unclipped.
@@ -264,6 +265,27 @@ class PrivacyEngine:
             G = g.reshape(B, g.shape[1], -1).transpose(1, 2)
         return A.to(dt).contiguous(), G.to(dt).contiguous()
 
+    def _check_flat_ids(self, ops, B):
+        """A table's ids of one dimension are a token of each sample, or positions
+        whose rows the whole batch shares: as many of them as samples look the
+        same. They are taken where no other layer has several rows per sample."""
+        flat = [k for k, L in enumerate(self.layers) if isinstance(L.module, _TABLES) and L.a.dim() == 1]
+        if not flat or B == 1:
+            return
+        for k, (L, op) in enumerate(zip(self.layers, ops)):
+            if isinstance(L.module, _NORMS):
+                rows = L.a.numel() // L.a.shape[-1]
+            elif isinstance(L.module, ExpertLinear):
+                rows = op[0].shape[0]
+            elif isinstance(L.module, _TABLES):
+                rows = op[0].numel()
+            else:
+                rows = B * op[1].shape[1]
+            if rows > B:
+                raise RuntimeError("an Embedding's ids have one dimension where another layer has several rows per "
+                                   "sample: a row of ids that all samples share has no per-sample gradient. Give each "
+                                   "sample its own, [B, T] (one token of each sample: [B, 1])")
+
     def step(self, step: int, denom: float | None = None):
         """Clipped noised mean gradients into .grad; returns the per-sample norms.
 
@@ -280,6 +302,7 @@ class PrivacyEngine:
         if len(batch) != 1:
             raise RuntimeError(f"all layers must share one batch size, got {sorted(batch)}")
         B = batch.pop()
+        self._check_flat_ids(ops, B)
         dev = ops[0][0].device
         dtypes = {op[0].dtype for k, op in enumerate(ops) if k not in gains and k not in tables}
         if len(dtypes) > 1:

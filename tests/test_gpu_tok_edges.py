@@ -37,3 +37,21 @@ def test_a_padding_words_row_gets_no_noise(padding):
     z[padding] = 0
     # the sum's and the mean's rounding on both sides
     assert np.abs(grads[0] - grads[1] - z).max() <= 8 * L.U * max(np.abs(grads[1]).max(), np.abs(z).max())
+
+
+# ---- positions that every sample shares
+
+
+def test_one_row_of_positions_for_all_samples_is_refused():
+    """[T] positions beside [B, T] words: as many of them as samples, so that their count does not give them away."""
+    words = torch.nn.Embedding(9, 8, device="cuda")
+    places = torch.nn.Embedding(4, 8, device="cuda")
+    engine = PrivacyEngine(torch.nn.ModuleList([words, places]), C=1.0, sigma=0.0)
+    ids = torch.zeros(4, 4, dtype=torch.int64, device="cuda")
+    at = torch.arange(4, device="cuda")
+    (words(ids) + places(at)).sum().backward()
+    with pytest.raises(RuntimeError, match=r"\[B, T\]"):
+        engine.step(0)
+    (words(ids) + places(at.expand(4, 4))).sum().backward()
+    engine.step(0)
+    engine.detach()

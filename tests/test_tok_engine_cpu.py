@@ -40,3 +40,45 @@ def test_a_padding_words_row_gets_no_noise(calls, padding):
     if padding is not None:
         want[padding] = 0
     assert torch.equal(m.weight.grad, want)
+
+
+def _parts(*modules):
+    model = torch.nn.ModuleList(modules)
+    return PrivacyEngine(model, C=1.0, sigma=0.0), modules
+
+
+@pytest.mark.parametrize("other", ["words", "linear", "conv", "norm"])
+def test_one_row_of_positions_for_all_samples_is_refused(calls, monkeypatch, other):
+    """As many positions as samples: the batch sizes agree, but a position's gradient is every sample's. (The other layer
+    alone, and the positions of every sample, are taken.)"""
+    monkeypatch.setattr(eng, "dp_rms_norm_backward", lambda *a, gain_rows=None, **kw: gain_rows.fill_(1))
+    B = T = 4
+    layer, x = {"words": (torch.nn.Embedding(9, 8), torch.zeros(B, T, dtype=torch.int64)),
+                "linear": (torch.nn.Linear(3, 8), torch.ones(B, T, 3)),
+                "conv": (torch.nn.Conv2d(2, 8, 1), torch.ones(B, 2, 1, T)),
+                "norm": (torch.nn.RMSNorm(8), torch.ones(B, T, 8))}[other]
+    engine, (layer, places) = _parts(layer, torch.nn.Embedding(T, 8))
+    engine.library_unfold = False  # torch unfolds on the host
+
+    def loss(at):
+        h = layer(x)
+        return ((h[:, :, 0].transpose(1, 2) if other == "conv" else h) + places(at)).sum()
+
+    loss(torch.arange(T)).backward()
+    with pytest.raises(RuntimeError, match=r"\[B, T\]"):
+        engine.step(0)
+    loss(torch.arange(T).expand(B, T)).backward()
+    engine.step(0)
+    engine.detach()
+
+
+def test_one_token_of_each_sample_is_taken(calls):
+    """Ids [B] beside layers with one row per sample, and of a batch of one."""
+    engine, (labels, head) = _parts(torch.nn.Embedding(5, 8), torch.nn.Linear(8, 2))
+    head(labels(torch.tensor([0, 3, 4]))).sum().backward()
+    assert engine.step(0).shape == (3,)
+    engine.detach()
+    engine, (words, places) = _parts(torch.nn.Embedding(5, 8), torch.nn.Embedding(1, 8))
+    (words(torch.tensor([[0, 3, 4]])) + places(torch.tensor([0]))).sum().backward()
+    assert engine.step(0).shape == (1,)
+    engine.detach()
