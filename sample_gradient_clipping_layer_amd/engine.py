@@ -52,6 +52,7 @@ class _Layer:
         self.g = None   # dL/d(output) of the last backward pass
         self.passed = True  # that forward pass has had its backward pass
         self.segments = None  # ExpertLinear: its rows' (expert, sample) ranges
+        self.version = None  # a table's: that of its ids when they were looked up
 
 
 def _torch_eps(m, dtype):
@@ -67,6 +68,11 @@ _NORMS = (torch.nn.RMSNorm, RMSNorm, LayerNorm)
 _TABLES = (torch.nn.Embedding, Embedding)
 _OWN = (RMSNorm, LayerNorm, Embedding, ExpertLinear)  # modules that know an engine takes their gradients
 _COVERED = (torch.nn.Linear, torch.nn.Conv2d, ExpertLinear) + _NORMS + _TABLES
+
+
+def _version(t):
+    """How often t has been changed in place (a tensor made in inference mode does not say)."""
+    return None if t.is_inference() else t._version
 
 
 def _forget_rows(norm):
@@ -160,6 +166,8 @@ class PrivacyEngine:
                 raise RuntimeError("a module ran twice in one forward pass")
             a = inputs[0] if inputs else next(kwargs[n] for n in ("input", "x", "ids") if n in kwargs)
             L.a = a.detach()
+            if isinstance(module, _TABLES):
+                L.version = _version(a)
             L.g = None
             L.passed = False
             if isinstance(module, ExpertLinear):
@@ -227,6 +235,9 @@ class PrivacyEngine:
         m, ids, g = L.module, L.a, L.g
         if ids is None or g is None:
             raise RuntimeError("step() needs one forward and one backward pass of every layer first")
+        if _version(ids) != L.version:
+            raise RuntimeError("an Embedding's ids were changed in place between its forward pass and step(), which sorts "
+                               "the gradients by them")
         if ids.dim() < 1:
             raise RuntimeError("an Embedding's ids must have one row per sample")
         ids = ids.reshape(ids.shape[0], -1).to(torch.int64)

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import sample_gradient_clipping_layer_amd.engine as eng
+import sample_gradient_clipping_layer_amd.layers as lay
 from sample_gradient_clipping_layer_amd.engine import PrivacyEngine
 
 
@@ -81,4 +82,27 @@ def test_one_token_of_each_sample_is_taken(calls):
     engine, (words, places) = _parts(torch.nn.Embedding(5, 8), torch.nn.Embedding(1, 8))
     (words(torch.tensor([[0, 3, 4]])) + places(torch.tensor([0]))).sum().backward()
     assert engine.step(0).shape == (1,)
+    engine.detach()
+
+
+@pytest.mark.parametrize("table,when", [(torch.nn.Embedding, "after the backward pass"),
+                                        (lay.Embedding, "after the backward pass"),
+                                        (lay.Embedding, "after the forward pass")])  # (where torch's refuses itself)
+def test_ids_changed_in_place_are_refused(calls, monkeypatch, table, when):
+    """step() sorts the gradients by the ids: others than those looked up would give them to other words."""
+    monkeypatch.setattr(lay, "dp_embedding", lambda ids, weight, out, scale: out.copy_(weight[ids]))
+    engine, (m,) = _parts(table(5, 3))
+    ids = torch.tensor([[0, 3], [1, 4]])
+    y = m(ids)
+    if when == "after the forward pass":
+        ids[ids == 4] = 2
+    y.sum().backward()
+    if when == "after the backward pass":
+        ids.copy_(torch.tensor([[1, 1], [1, 1]]))
+    with pytest.raises(RuntimeError, match="in place"):
+        engine.step(0)
+    m(ids.clone()).sum().backward()  # the next batch
+    engine.step(0)
+    with torch.inference_mode():  # ids that do not say how often they were changed
+        m(torch.tensor([[0, 3], [1, 4]]))
     engine.detach()
