@@ -625,7 +625,10 @@ dp_status dp_token_logprob_backward(void* stream, const void* logits, const int6
  * counts[b][e] is the number of places of sample b that name expert e. A place
  * is used when its id lies in [0, E), a token when one of its places is; a
  * sample without a used token has loss 0. (Even routing gives 1.) Tokens that
- * are not used count for nothing, whatever their logits hold.
+ * are not used count for nothing, whatever their logits hold. A used token
+ * whose logits are all -inf has no distribution: it and its places are counted,
+ * with probability 0 of every expert. One with a NaN or +inf makes the sample's
+ * loss NaN.
  *
  *  logits   [B, T, E], dtype, aligned to its element; 1 <= E <= 1024.
  *  ids      [B, T, top] int64, as route() and the expert layers take them;
@@ -644,7 +647,7 @@ size_t dp_balance_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t 
  *
  *   grad[b][t][e] = p_e * (a_e - sum_e' p_e' a_e')    a_e = dloss[b] * E * f_e / tokens[b]
  *
- * and 0 for a token that is not used.
+ * and 0 for a token that is not used or has no distribution.
  *
  *  counts, tokens  as dp_balance_loss left them.
  *  dloss    [B] fp32, or NULL (1 everywhere).

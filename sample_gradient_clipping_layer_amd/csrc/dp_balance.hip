@@ -7,7 +7,8 @@
 //   f_e = counts_e / sum_e' counts_e'      P_e = sum_{t used} p_te / n
 //   loss = E sum_e f_e P_e
 //   dz_te = p_te (a_e - sum_e' p_te' a_e'),  a_e = dloss E f_e / n   (0 for a token that is not used)
-// A sample without a used token has loss 0 and gradient 0. The gradient does
+// A sample without a used token has loss 0 and gradient 0, and a used token
+// whose logits are all -inf has p = 0 and gradient 0. The gradient does
 // not change with a share that all experts have more, so a_e is formed from
 // counts_e - min counts: whole numbers, and an even routing gives exactly 0.
 //
@@ -31,7 +32,8 @@ namespace dpk {
 namespace {
 
 // One token's probabilities from its L lanes' logits: p of every column that this lane holds (its neighbour's among
-// them, which do not count in the sums). A row of -inf alone gives NaN, as a row with a NaN does.
+// them, which do not count in the sums). A row of -inf alone has no distribution, and every p is 0; one with a NaN or
+// +inf gives NaN.
 template <typename C, int P, int L>
 __device__ __forceinline__ void softmax_of(const C& cols, const typename C::Raw& raw, float* v) {
   float m = -INFINITY;
@@ -42,6 +44,7 @@ __device__ __forceinline__ void softmax_of(const C& cols, const typename C::Raw&
   }
 #pragma unroll
   for (int off = L / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
+  m = m == -INFINITY ? 0.f : m;  // no difference of infinities: the terms of such a row are 0
   float s = 0.f;
 #pragma unroll
   for (int e = 0; e < P; ++e) {
@@ -50,7 +53,7 @@ __device__ __forceinline__ void softmax_of(const C& cols, const typename C::Raw&
   }
 #pragma unroll
   for (int off = L / 2; off > 0; off >>= 1) s += __shfl_xor(s, off, kWave);
-  const float inv = 1.0f / s;
+  const float inv = s == 0.f ? 0.f : 1.0f / s;  // with a largest logit s is 1 at least
 #pragma unroll
   for (int e = 0; e < P; ++e) v[e] *= inv;
 }

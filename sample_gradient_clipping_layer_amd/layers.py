@@ -336,10 +336,11 @@ def balance_loss(logits, expert_ids):
         loss[b] = E * sum_e f_e * P_e
 
     f_e is the share of the sample's places that name expert e, P_e the mean
-    probability of e over the sample's tokens that have a place; even routing
-    gives 1. counts are the places per expert. Each sample's loss is its own, so
-    that it can be added to what PrivacyEngine's backward pass sums up.
-    Gradients flow to logits only."""
+    probability of e over the sample's tokens that have a place (0 in a token
+    whose logits are all -inf, and so is its gradient); even routing gives 1.
+    counts are the places per expert. Each sample's loss is its own, so that it
+    can be added to what PrivacyEngine's backward pass sums up. Gradients flow
+    to logits only."""
     return _Balance.apply(logits, expert_ids.contiguous())
 
 

@@ -8,10 +8,21 @@ import pytest
 import torch
 
 import lm_util as L
+import sample_gradient_clipping_layer_amd as dpc
+import tok_util as K
 from oracle import noise as N
 from sample_gradient_clipping_layer_amd.engine import PrivacyEngine
+from sample_gradient_clipping_layer_amd.layers import balance_loss
 
 pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+def full(*shape, dtype=torch.float32, value=None):
+    value = (NAN if dtype.is_floating_point else -9) if value is None else value
+    return torch.full(shape, value, dtype=dtype, device="cuda")
+
 
 # ---- a torch table's padding word
 
@@ -55,3 +66,52 @@ def test_one_row_of_positions_for_all_samples_is_refused():
     (words(ids) + places(at.expand(4, 4))).sum().backward()
     engine.step(0)
     engine.detach()
+
+
+# ---- a routed token whose logits are all -inf
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,E,top", [(2, 3, 4, 2), (3, 40, 9, 2), (2, 600, 64, 2), (1, 3000, 130, 4), (2, 5, 700, 3)])
+def test_balance_of_rows_without_a_distribution(dtype, B, T, E, top):
+    """Such a token has probability 0 of every expert (its places and itself count) and gradient 0."""
+    g, dt = L.gen(B + T + E), L.DT[dtype]
+    z, ids = L.randn(g, B, T, E, scale=2.0, dtype=dt), torch.randint(-1, E, (B, T, top), generator=g).cuda()
+    ids[:, 1, 0] = 0
+    z[:, 1] = -INF
+    z[0, 0, :E - 1] = -INF  # one expert left
+    ids[0, 0, 0] = 1
+    loss, counts, tokens = full(B), full(B, E, dtype=torch.int64), full(B, dtype=torch.int64)
+    dpc.dp_balance_loss(z, ids, loss, counts, tokens)
+    # the same places over logits that have a distribution; the probabilities apart
+    some = z.clone()
+    some[:, 1] = 0
+    _, wc, wt, _ = K.balance(some, ids)
+    assert torch.equal(counts, wc) and torch.equal(tokens, wt)
+    used = (ids >= 0).any(-1)
+    p = torch.softmax(some.double(), -1) * used[..., None]
+    p[:, 1] = 0
+    f = wc.double() / wc.sum(1, keepdim=True)
+    far = torch.where(p > 0, (some.double() - some.double().amax(-1, keepdim=True)).abs(), torch.zeros_like(p))
+    n = wt[:, None]
+    want = E * (f * p.sum(1) / n).sum(1)
+    # as tok_util's balance counts it
+    L.check(loss, want, E * (f * (p * (4 * far + T + E / 8 + 128)).sum(1) / n).sum(1) * L.U + K.TINY, "loss")
+    grad, ref = full(B, T, E, dtype=dt), full(B, T, E, dtype=dt)
+    dpc.dp_balance_loss_backward(z, ids, counts, tokens, grad)
+    dpc.dp_balance_loss_backward(some, ids, counts, tokens, ref)
+    ref[:, 1] = 0
+    assert torch.equal(grad, ref)
+
+
+def test_balance_of_a_sample_of_such_rows_alone():
+    z, ids = full(2, 3, 5, value=-INF), torch.zeros(2, 3, 1, dtype=torch.int64, device="cuda")
+    z[1, 0] = 0
+    zz = z.clone().requires_grad_()
+    loss, counts = balance_loss(zz, ids)
+    loss.sum().backward()
+    assert loss.tolist()[0] == 0 and abs(float(loss[1]) - 1 / 3) <= 8 * L.U and counts[:, 0].tolist() == [3, 3]
+    assert torch.isfinite(zz.grad).all() and (zz.grad[0] == 0).all() and (zz.grad[1, 1:] == 0).all()
+    z[1, 2, 3] = NAN  # NaN and +inf go on as they did
+    z[0, 1, 1] = INF
+    assert torch.isnan(balance_loss(z, ids)[0]).all()
