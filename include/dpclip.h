@@ -542,6 +542,7 @@ size_t dp_embedding_order_workspace_bytes(int64_t N, int64_t V);
  *  G        [B, T, d], dtype, aligned to its element; B*T below 2^31.
  *  order    as dp_embedding_order left it for ids (N = B*T). With other
  *           contents the result means nothing; nothing outside is accessed.
+ *  scale    finite; the sums of G's squares are formed in fp32 before it.
  *  sqnorm   [B] fp32, overwritten (accumulate == 0) or added to.
  *  workspace  at least dp_embedding_workspace_bytes(...) bytes.
  */

@@ -793,7 +793,7 @@ __global__ __launch_bounds__(256) void k_embed_norm_finish(EmbedGradArgs a, int 
       for (int64_t t = threadIdx.x; t < a.T; t += 256) s += a.token_sq[g * a.N + b * a.T + t];
     s = block_sum<256>(s, red);
     if (threadIdx.x == 0) {
-      s *= a.scale * a.scale;
+      s = s * a.scale * a.scale;  // one by one: the scale's square may be out of range where the norm is not
       a.sqnorm[b] = a.accumulate ? a.sqnorm[b] + s : s;
     }
     __syncthreads();

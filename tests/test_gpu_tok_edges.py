@@ -115,3 +115,23 @@ def test_balance_of_a_sample_of_such_rows_alone():
     z[1, 2, 3] = NAN  # NaN and +inf go on as they did
     z[0, 1, 1] = INF
     assert torch.isnan(balance_loss(z, ids)[0]).all()
+
+
+# ---- scales whose square fp32 does not have
+
+
+@pytest.mark.parametrize("scale,size", [(1e20, 1e-16), (-3e19, 1e-15), (1e-25, 1e14), (2.0 ** 100, 2.0 ** -50), (1e-30, 1.0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_table_norm_of_far_scales(dtype, scale, size):
+    g, B, T, V, d = L.gen(7), 4, 90, 11, 72
+    ids = torch.randint(0, V, (B, T), generator=g).cuda()
+    ids[2] = -1  # a sample without a token: 0
+    G = L.randn(g, B, T, d, scale=size, dtype=L.DT[dtype])
+    order, starts = full(B * T, dtype=torch.int64), full(V + 1, dtype=torch.int64)
+    dpc.dp_embedding_order(ids, V, order, starts)
+    sq = full(B)
+    dpc.dp_embedding_norm(G, ids, order, starts, sq, scale=scale)
+    want, bound = K.embedding_norm(G, ids, V, float(np.float32(scale)))
+    assert float(sq[2]) == 0
+    # below 2^-126 fp32 has steps of 2^-149
+    L.check(sq, want, bound + 2.0 ** -148, "sqnorm")
