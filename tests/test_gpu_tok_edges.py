@@ -135,3 +135,36 @@ def test_table_norm_of_far_scales(dtype, scale, size):
     assert float(sq[2]) == 0
     # below 2^-126 fp32 has steps of 2^-149
     L.check(sq, want, bound + 2.0 ** -148, "sqnorm")
+
+
+# ---- rows of one large value
+
+
+CONSTANTS = [3.0, 1e6 + 1, 1.7e8, 3.3e10, 7.7e14, -1.9e16]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [1, 3, 49, 333, 768, 1001, 1280, 1601, 2056, 5000, 10007, 16384, 32767])
+def test_layer_norm_of_rows_of_one_value(dtype, d):
+    """The bias, whatever the value: the row's mean is off by some steps of it, the same for every column, and what is
+    left is taken off exactly. Back: the gradient of a row whose deviation is 0."""
+    g, dt = L.gen(d), L.DT[dtype]
+    rows = torch.tensor(CONSTANTS).to(dt)
+    x = rows[:, None].repeat(1, d).cuda()
+    r = (rows / 3).to(dt)[:, None].repeat(1, d).cuda()
+    gain, bias = 1 + L.randn(g, d, scale=0.3), L.randn(g, d)
+    for res in (None, r):
+        out = full(len(CONSTANTS), d, dtype=dt)
+        dpc.dp_layer_norm(x, gain, bias, 1e-5, out, residual=res)
+        assert torch.equal(out, bias.to(dt).expand_as(out))
+    dpc.dp_layer_norm(x, gain, bias, 0.0, out)
+    assert torch.isnan(out).all()
+    s, dy = x[:, None].contiguous(), L.randn(g, len(CONSTANTS), 1, d, dtype=dt)
+    dx, gr, br = full(*s.shape, dtype=dt), full(len(CONSTANTS), d), full(len(CONSTANTS), d)
+    dpc.dp_layer_norm_backward(dy, s, gain, 1e-5, dx=dx, gain_rows=gr, bias_rows=br)
+    h = dy.double() * gain.double()
+    rstd = float(np.float32(1e-5)) ** -0.5
+    want = rstd * (h - h.mean(-1, keepdim=True))
+    mag = rstd * (h.abs() + h.abs().mean(-1, keepdim=True))
+    L.check(dx, want, 192 * L.U * mag + L.half(dt) * want.abs() + K.TINY, "dx")
+    assert (gr == 0).all() and torch.equal(br, dy[:, 0].float())
