@@ -88,6 +88,15 @@ def _sum_rows(rows):
     return out.view(d)
 
 
+def _row_sums(x, most=4096):
+    """The sums of rows [B, n], long ones from the sums of their parts: torch
+    spreads one row of 131072 or more over workgroups that meet in memory it
+    clears by a memset, which has no place in a captured graph."""
+    while x.shape[1] > most:
+        x = torch.nn.functional.pad(x, (0, -x.shape[1] % most)).view(x.shape[0], -1, most).sum(2)
+    return x.sum(1)
+
+
 class RMSNorm(torch.nn.Module):
     """Root-mean-square norm over the last dimension, with the residual's
     addition fused in: forward(x) gives y; forward(x, residual) gives (y, s)
@@ -397,7 +406,7 @@ def token_loss(logits, targets, weight=None, temperature: float = 1.0):
     if weight is not None:
         weight = weight.detach().float()
         logp = torch.where(weight != 0, weight * logp, torch.zeros_like(logp))
-    return -logp.reshape(logp.shape[0], -1).sum(1)
+    return -_row_sums(logp.reshape(logp.shape[0], -1))
 
 
 class _Distill(torch.autograd.Function):

@@ -12,7 +12,7 @@ import sample_gradient_clipping_layer_amd as dpc
 import tok_util as K
 from oracle import noise as N
 from sample_gradient_clipping_layer_amd.engine import PrivacyEngine
-from sample_gradient_clipping_layer_amd.layers import balance_loss
+from sample_gradient_clipping_layer_amd.layers import balance_loss, token_loss
 
 pytestmark = pytest.mark.gpu
 
@@ -168,3 +168,41 @@ def test_layer_norm_of_rows_of_one_value(dtype, d):
     mag = rstd * (h.abs() + h.abs().mean(-1, keepdim=True))
     L.check(dx, want, 192 * L.U * mag + L.half(dt) * want.abs() + K.TINY, "dx")
     assert (gr == 0).all() and torch.equal(br, dy[:, 0].float())
+
+
+# ---- the loss of very long rows in a graph
+
+
+@pytest.mark.parametrize("B,T", [(1, 1 << 20), (2, 300001), (3, 5000)])
+def test_token_loss_of_long_rows_captured(B, T):
+    """Loss and gradient replayed over other logits, with eager work between: the eager bits, and the sum in 64 bits."""
+    g = torch.Generator("cuda").manual_seed(T)
+    z = torch.randn(B, T, 8, generator=g, device="cuda")
+    y = torch.randint(-1, 8, (B, T), generator=g, device="cuda")
+
+    def work():
+        zz = z.detach().requires_grad_()
+        loss = token_loss(zz, y)
+        return loss.detach(), *torch.autograd.grad(loss.sum(), zz)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for k in range(5):
+        z.mul_(0.9 if k % 2 else -1.1)
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        want = work()
+        torch.cuda.synchronize()
+        assert torch.equal(kept[0], want[0]) and torch.equal(kept[1], want[1]), k
+        lp = K.logprob(z, y, 1.0, 0)
+        # each term, then at most 4096 additions three times over
+        bound = lp["logp_bound"].sum(1) + 3 * 4096 * L.U * lp["logp"].abs().sum(1)
+        L.check(kept[0], -lp["logp"].sum(1), bound, "loss")

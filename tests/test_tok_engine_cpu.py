@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 import sample_gradient_clipping_layer_amd.engine as eng
 import sample_gradient_clipping_layer_amd.layers as lay
@@ -106,3 +107,33 @@ def test_ids_changed_in_place_are_refused(calls, monkeypatch, table, when):
     with torch.inference_mode():  # ids that do not say how often they were changed
         m(torch.tensor([[0, 3], [1, 4]]))
     engine.detach()
+
+
+class _Sums(TorchDispatchMode):
+    """How many values go into one sum, at most."""
+
+    def __init__(self):
+        super().__init__()
+        self.most = 0
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        out = func(*args, **(kwargs or {}))
+        if "sum" in str(func):
+            self.most = max(self.most, args[0].numel() // max(1, out.numel()))
+        return out
+
+
+@pytest.mark.parametrize("B,T", [(1, 1), (3, 4096), (2, 4097), (1, 300001), (1, 1 << 20)])
+def test_long_losses_are_summed_in_parts(monkeypatch, B, T):
+    """Not as one sum of a row of 131072 or more, for which torch records a memset in a captured graph."""
+    monkeypatch.setattr(lay, "token_logprobs", lambda logits, targets, temperature: (logits[..., 0], None))
+    g = torch.Generator().manual_seed(T)
+    z = torch.randn(B, T, 1, generator=g, dtype=torch.float64).requires_grad_()
+    w = torch.rand(B, T, generator=g)
+    with _Sums() as sums:
+        loss = lay.token_loss(z, torch.zeros(B, T, dtype=torch.int64), w)
+    assert sums.most <= 1 << 16
+    want = -(z[..., 0] * w).sum(1)
+    assert loss.shape == (B,) and torch.allclose(loss, want, rtol=1e-12, atol=1e-9)
+    loss.sum().backward()
+    assert torch.equal(z.grad[..., 0], -w.double())
