@@ -177,11 +177,13 @@ class LayerNorm(torch.nn.Module):
 
     @classmethod
     def from_torch(cls, norm: torch.nn.LayerNorm):
-        """A torch.nn.LayerNorm over the last dimension, sharing its parameters."""
+        """A torch.nn.LayerNorm over the last dimension, sharing its parameters
+        and the hooks registered on it (their handles still remove them)."""
         if len(norm.normalized_shape) != 1 or norm.weight is None:
             raise ValueError("LayerNorm must be over the last dimension, with a weight")
         new = cls(1, eps=norm.eps, bias=norm.bias is not None)
         new.weight, new.bias = norm.weight, norm.bias
+        new.__dict__.update((n, v) for n, v in norm.__dict__.items() if "_hook" in n)
         return new.train(norm.training)
 
     def forward(self, x, residual=None):
@@ -190,9 +192,11 @@ class LayerNorm(torch.nn.Module):
 
 def replace_layer_norms(model: torch.nn.Module) -> torch.nn.Module:
     """model with every torch.nn.LayerNorm (over the last dimension, with a
-    weight) replaced by a LayerNorm that shares its parameters, so that an
-    engine can clip them; names and state_dict stay. Changes model and returns
-    it (a model that is a norm itself is returned as a new module)."""
+    weight) replaced by a LayerNorm that shares its parameters and hooks, so
+    that an engine can clip them; names and state_dict stay. Changes model and
+    returns it (a model that is a norm itself is returned as a new module). The
+    new modules take what LayerNorm takes: float32 or bfloat16 on the GPU, with
+    at least one element."""
     new = {}
 
     def of(m):

@@ -137,3 +137,29 @@ def test_long_losses_are_summed_in_parts(monkeypatch, B, T):
     assert loss.shape == (B,) and torch.allclose(loss, want, rtol=1e-12, atol=1e-9)
     loss.sum().backward()
     assert torch.equal(z.grad[..., 0], -w.double())
+
+
+def test_replaced_layer_norms_keep_their_hooks(monkeypatch):
+    """Hooks of every kind run with the module that took the norm's place, in order, until their handles remove them."""
+    monkeypatch.setattr(lay, "dp_layer_norm", lambda x, w, b, eps, out, **kw: out.copy_(torch.layer_norm(x, (4,), w, b, eps)))
+    monkeypatch.setattr(lay, "dp_layer_norm_backward", lambda dy, s, w, eps, dx=None, **kw: dx.copy_(dy))
+    model = torch.nn.Sequential(torch.nn.LayerNorm(4))
+    norm, ran = model[0], []
+    norm.requires_grad_(False)
+    handles = [norm.register_forward_pre_hook(lambda m, a: ran.append((m, "pre"))),
+               norm.register_forward_hook(lambda m, a, k, y: ran.append((m, "forward")), with_kwargs=True),
+               norm.register_forward_hook(lambda m, a, y: ran.append((m, "always")), always_call=True),
+               norm.register_full_backward_pre_hook(lambda m, g: ran.append((m, "backward pre"))),
+               norm.register_full_backward_hook(lambda m, gi, go: ran.append((m, "backward"))),
+               norm.register_state_dict_pre_hook(lambda m, prefix, keep: ran.append((m, "state")))]
+    lay.replace_layer_norms(model)
+    x = torch.arange(8.0).view(2, 4).requires_grad_()
+    model(x).sum().backward()
+    model.state_dict()
+    assert [n for _, n in ran] == ["pre", "forward", "always", "backward pre", "backward", "state"]
+    assert all(m is model[0] and type(m) is lay.LayerNorm for m, _ in ran)
+    for h in handles:
+        h.remove()
+    model(x).sum().backward()
+    model.state_dict()
+    assert len(ran) == 6
