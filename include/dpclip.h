@@ -430,8 +430,9 @@ size_t dp_conv_workspace_bytes(const dp_conv2d* conv, dp_dtype dtype, int64_t B,
  *
  * in fp32, each output rounded once to dtype (out is formed from the sum
  * before its rounding to dtype). A row of zeros gives zeros when eps > 0. The
- * sum of squares is an fp32 value too: elements up to 1e17 do not overflow it,
- * and eps = 0 needs an element of 1e-18 or more in the row.
+ * sum of squares is an fp32 value too: sums s up to 1e17 do not overflow it
+ * (larger ones may, and give zeros), and eps = 0 needs one of 1e-18 or more in
+ * the row.
  *
  *  x, residual  [rows, d], dtype; residual may be NULL (s = x).
  *  gain         [d], gain_dtype (DP_F32 or DP_BF16).
@@ -482,8 +483,9 @@ size_t dp_rms_norm_workspace_bytes(dp_dtype dtype, int64_t B, int64_t T, int64_t
  *  out          [rows, d], dtype; may be x or residual.
  *  sum_out      [rows, d], dtype: s (what the backward pass reads); may be
  *               NULL, x or residual, not out.
- * Tensors aligned to their element. Elements up to 1e17 do not overflow the
- * sum of squares.
+ * Tensors aligned to their element. Sums s up to 1e17 do not overflow the sum
+ * of squares (with a residual of the same size: x and residual up to 5e16);
+ * rows with larger ones have no defined output.
  */
 dp_status dp_layer_norm(void* stream, const void* x, const void* residual, const void* gain, const void* bias,
                         dp_dtype dtype, dp_dtype gain_dtype, int64_t rows, int64_t d, float eps, void* out,

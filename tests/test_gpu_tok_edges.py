@@ -206,3 +206,28 @@ def test_token_loss_of_long_rows_captured(B, T):
         # each term, then at most 4096 additions three times over
         bound = lp["logp_bound"].sum(1) + 3 * 4096 * L.U * lp["logp"].abs().sum(1)
         L.check(kept[0], -lp["logp"].sum(1), bound, "loss")
+
+
+# ---- the largest values
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norms_of_the_largest_values(dtype):
+    """Sums of 1e17 at the largest width."""
+    g, dt, d = L.gen(1), L.DT[dtype], 32768
+    x = (torch.randint(0, 2, (3, d), generator=g) * 2 - 1).float().mul_(0.5e17)
+    x[1, 1:], x[2] = x[1, 1:].abs(), x[2] * torch.rand(d, generator=g)
+    x = x.to(dt).cuda()
+    r = x.clone()
+    assert (x + r).abs().max() <= 1e17 * (1 + L.half(dt))
+    gain, bias = 1 + L.randn(g, d, scale=0.3), L.randn(g, d)
+    out, s = full(3, d, dtype=dt), full(3, d, dtype=dt)
+    dpc.dp_layer_norm(x, gain, bias, 1e-5, out, residual=r, sum_out=s)
+    y, v, by, bv = K.layer_norm(x, r, gain, bias, 1e-5)
+    L.check(out, y, by, "out")
+    L.check(s, v, bv, "sum")
+    dpc.dp_rms_norm(x, gain, 1e-6, out, residual=r, sum_out=s)
+    y, v = L.rms_forward(x, r, gain, 1e-6)
+    by, bv = L.rms_forward_bounds(y, v, dt)
+    L.check(out, y, by, "rms out")
+    L.check(s, v, bv, "rms sum")
