@@ -136,7 +136,7 @@ class _LayerNorm(torch.autograd.Function):
         s, weight = ctx.saved_tensors
         private = ctx.module is not None and ctx.module.private
         has_bias = ctx.bias_dtype is not None
-        B, d = s.shape[0], s.shape[-1]
+        B, d = s.shape[0] if s.dim() > 1 else 1, s.shape[-1]
         dx, rows, dw, db = dsum, [None, None], None, None
         if dy is None:  # only the sum was used: the gradients of weight and bias are zero
             if private:
@@ -147,9 +147,8 @@ class _LayerNorm(torch.autograd.Function):
                 if private or ctx.needs_input_grad[2 + k]:
                     rows[k] = torch.empty(B, d, dtype=torch.float32, device=s.device)
             if dx is not None or rows[0] is not None or rows[1] is not None:
-                dp_layer_norm_backward(dy.contiguous(), s, weight, ctx.eps, dx=dx,
-                                       dsum=None if dsum is None else dsum.contiguous(), gain_rows=rows[0],
-                                       bias_rows=rows[1])
+                dy, v, out, ds = (t if t is None else t.contiguous().view(B, -1, d) for t in (dy, s, dx, dsum))
+                dp_layer_norm_backward(dy, v, weight, ctx.eps, dx=out, dsum=ds, gain_rows=rows[0], bias_rows=rows[1])
             if not private:
                 dw = _sum_rows(rows[0]).to(weight.dtype) if ctx.needs_input_grad[2] else None
                 db = _sum_rows(rows[1]).to(ctx.bias_dtype) if has_bias and ctx.needs_input_grad[3] else None
@@ -162,7 +161,8 @@ class LayerNorm(torch.nn.Module):
     """Layer norm over the last dimension, with the residual's addition fused
     in: forward(x) gives y; forward(x, residual) gives (y, s) with s = x +
     residual, the residual stream after the addition. x is [B, ..., width], a
-    sample per index of the first dimension; weight and bias share one dtype."""
+    sample per index of the first dimension, or one row [width]; weight and bias
+    share one dtype."""
 
     def __init__(self, width: int, eps: float = 1e-5, bias: bool = True, device=None, dtype=None):
         super().__init__()

@@ -12,7 +12,7 @@ import sample_gradient_clipping_layer_amd as dpc
 import tok_util as K
 from oracle import noise as N
 from sample_gradient_clipping_layer_amd.engine import PrivacyEngine
-from sample_gradient_clipping_layer_amd.layers import balance_loss, token_loss
+from sample_gradient_clipping_layer_amd.layers import LayerNorm, balance_loss, token_loss
 
 pytestmark = pytest.mark.gpu
 
@@ -231,3 +231,26 @@ def test_norms_of_the_largest_values(dtype):
     by, bv = L.rms_forward_bounds(y, v, dt)
     L.check(out, y, by, "rms out")
     L.check(s, v, bv, "rms sum")
+
+
+# ---- a row alone
+
+
+def test_layer_norm_of_a_single_row():
+    """A vector without a batch, as torch.nn.LayerNorm takes it, and its gradients."""
+    g = L.gen(2)
+    x, dy = L.randn(g, 40), L.randn(g, 40)
+    for m in (LayerNorm(40, device="cuda"), LayerNorm(40, bias=False, device="cuda")):
+        a, b = x.clone().requires_grad_(), x[None].clone().requires_grad_()
+        (m(a) * dy).sum().backward()
+        got = [a.grad] + [p.grad for p in m.parameters()]
+        m.zero_grad()
+        (m(b) * dy).sum().backward()
+        for u, v in zip(got, [b.grad[0]] + [p.grad for p in m.parameters()]):
+            assert torch.equal(u, v)
+    norm = LayerNorm(40, device="cuda")
+    engine = PrivacyEngine(norm, C=1e9, sigma=0.0)  # one sample
+    (norm(x) * dy).sum().backward()
+    assert engine.step(0).shape == (1,)
+    L.check(norm.bias.grad, dy.double(), 4 * L.U * dy.double().abs() + K.TINY, "bias")
+    engine.detach()
