@@ -358,8 +358,9 @@ namespace {
 // registers a lane; with sixteen waves of 128 the kernel spills, which wider rows put up with.
 template <typename F>
 hipError_t row_dispatch_backward(int64_t d, F f) {
-  if (d > 8192 && d <= 16384) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
-  return row_dispatch(d, f);
+  if (d <= 8192) return row_dispatch_to_8192(d, f);
+  if (d <= 16384) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 16>{});
 }
 
 constexpr int64_t kLnBlocks = 256 * 8;  // blocks that fill the 256 CUs; more rows than that are looped over

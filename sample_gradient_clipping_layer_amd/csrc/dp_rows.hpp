@@ -153,15 +153,19 @@ constexpr int row_threads() {
   return WPR > 4 ? 64 * WPR : 256;
 }
 
-// One instantiation per (elements per lane, waves per row) the width needs.
+// One instantiation per (elements per lane, waves per row) the width needs; up to 8192 columns.
 template <typename F>
-hipError_t row_dispatch(int64_t d, F f) {
+hipError_t row_dispatch_to_8192(int64_t d, F f) {
   if (d <= 512) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
   if (d <= 1024) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
   if (d <= 1536) return f(std::integral_constant<int, 24>{}, std::integral_constant<int, 1>{});
   if (d <= 2048) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
   if (d <= 4096) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
-  if (d <= 8192) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
+}
+template <typename F>
+hipError_t row_dispatch(int64_t d, F f) {
+  if (d <= 8192) return row_dispatch_to_8192(d, f);
   if (d <= 16384) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
   return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 16>{});
 }
