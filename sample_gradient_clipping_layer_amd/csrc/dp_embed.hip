@@ -357,7 +357,7 @@ __device__ __forceinline__ void starts_of_ids(const int64_t* __restrict__ ids, i
 }  // namespace
 
 // All digits of up to 4096 tokens by one workgroup, the tokens in LDS between the passes; workgroups behind it: the
-// starts (or, without, the keys in order are left for them).
+// starts (or, without, the keys in order are left for them in keys_out, null otherwise).
 __global__ __launch_bounds__(kSortThreads) void k_order_small(const int64_t* __restrict__ ids, int N, int64_t V,
                                                               SortPlan p, uint32_t* __restrict__ keys_out,
                                                               int64_t* __restrict__ order,
@@ -429,7 +429,7 @@ __global__ __launch_bounds__(kSortThreads) void k_order_small(const int64_t* __r
       __builtin_amdgcn_wave_barrier();
       if (in) {
         if (last) {
-          keys_out[to] = k;
+          if (keys_out) keys_out[to] = k;
           order[to] = place_of(k, tok[i]);
         } else {
           keys[(pass + 1) & 1][to] = k;
@@ -914,7 +914,7 @@ hipError_t launch_tiles(hipStream_t st, const EmbedGradArgs& a) {
 }
 
 // Parts of the columns that waves of k_embed_norm share out: as many as give about 8192 waves.
-int64_t norm_col_groups(int64_t N, int64_t d, int col_waves) {
+int64_t norm_col_groups(int64_t N, int col_waves) {
   const int64_t waves = (N + kEmbedNormPlaces - 1) / kEmbedNormPlaces;
   return std::max<int64_t>(1, std::min<int64_t>(col_waves, 8192 / waves));
 }
@@ -923,7 +923,7 @@ template <typename T, bool TINY>
 hipError_t launch_norm(hipStream_t st, const EmbedGradArgs& a) {
   hipError_t e = launch_tiles<T, TINY, true>(st, a);
   if (e != hipSuccess) return e;
-  const int64_t groups = norm_col_groups(a.N, a.d, col_waves_of<T>(a.d));
+  const int64_t groups = norm_col_groups(a.N, col_waves_of<T>(a.d));
   const int64_t waves = (a.N + kEmbedNormPlaces - 1) / kEmbedNormPlaces * groups;
   k_embed_norm<T, TINY><<<grid_of((waves + 3) / 4), 256, 0, st>>>(a, (int)groups);
   e = hipGetLastError();
@@ -978,7 +978,7 @@ int64_t level_rows(int64_t N, int levels) {
 // Floats of the tokens' squared norms, a list for each part of the columns.
 int64_t token_floats(int dtype, int64_t N, int64_t d) {
   const int cw = dtype == 1 ? col_waves_of<bf16s>(d) : col_waves_of<float>(d);
-  return (N * norm_col_groups(N, d, cw) + 63) / 64 * 64;
+  return (N * norm_col_groups(N, cw) + 63) / 64 * 64;
 }
 
 }  // namespace
@@ -1023,7 +1023,7 @@ hipError_t launch_embed_order(hipStream_t st, const int64_t* ids, int64_t N, int
     // (1001 tokens, 5003 words: 7.1 us, 10.7 in two launches; 32768 tokens beside the first of theirs: 30 and 26).
     const bool beside = V < (1 << 19);
     const unsigned more = beside ? (unsigned)((V + kSortThreads) / kSortThreads) : 0;
-    k_order_small<<<1 + more, kSortThreads, 0, st>>>(ids, (int)N, V, p, lists, order, starts);
+    k_order_small<<<1 + more, kSortThreads, 0, st>>>(ids, (int)N, V, p, beside ? nullptr : lists, order, starts);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess && !beside ? find_starts(lists) : e;
   }
