@@ -15,19 +15,23 @@
 // The lookup is bound by HBM: 32768 tokens of 1280 bf16 take 26 us, 6.4 TB/s of
 // rows read and written (rows met again come from the caches). The clipping
 // pass of 32 x 1024 such tokens over 50257 words takes 122 us in its ten
-// launches: the order 28 (four launches), the norm 37 (three), the factors 2,
-// the sum 62 (two; 257 MB of it are the table, written at 5 TB/s), each call by
-// itself. What is not
-// the table's is latency: chains of a place, its row, its run's end. Noise adds
-// 70 us of fp32 work (as much as the noise kernel takes for as many elements).
+// launches: the order 26 (four launches), the norm 34 (three), the factors 2,
+// the sum 60 (two; 257 MB of it are the table, written at 5 TB/s). (Whole calls
+// in a loop. A kernel trace, which adds about a microsecond to every launch,
+// sums up to 133.) What is not the table's is latency: chains of a place, its
+// row, its run's end. Noise adds 70 us of fp32 work (as much as the noise kernel
+// takes for as many elements).
 //
 // A run may be long (a frequent word, a batch padded with one word). Sums over
 // long runs take the sums of tiles: a first launch adds up every tile of 16
 // neighbouring places (and of 16 such tiles, and so on) that lies within one
-// run, and what reads a run takes whole tiles from there. Sums are formed in
-// fp32 in an order that the sizes and the ids alone decide; nothing is atomic
-// but the counts of the sort, which are whole numbers. A place holds its word
-// beside its token, so that finding a run's ends takes no second load.
+// run, and what reads a run takes whole tiles from there. (The same batch with
+// one word in the last quarter of every sequence: 133 us, the norm 45 of them;
+// one sequence of 32768 such tokens: 186 and 100, as a wave goes to a run's end
+// 64 places a step.) Sums are formed in fp32 in an order that the sizes and the
+// ids alone decide; nothing is atomic but the counts of the sort, which are
+// whole numbers. A place holds its word beside its token, so that finding a
+// run's ends takes no second load.
 //
 // The sort is by digits of the word, least significant first, each digit in a
 // launch of its own: a workgroup ranks the tokens of its tile by digit (within
@@ -913,7 +917,8 @@ hipError_t launch_tiles(hipStream_t st, const EmbedGradArgs& a) {
   return hipSuccess;
 }
 
-// Parts of the columns that waves of k_embed_norm share out: as many as give about 8192 waves.
+// Parts of the columns that waves of k_embed_norm share out: as many as give about 8192 waves (the norm of 32768 tokens of
+// 1600 bf16 36 us, 42 by one wave for all columns; of 2048 tokens of 1280 16 and 23).
 int64_t norm_col_groups(int64_t N, int col_waves) {
   const int64_t waves = (N + kEmbedNormPlaces - 1) / kEmbedNormPlaces;
   return std::max<int64_t>(1, std::min<int64_t>(col_waves, 8192 / waves));
