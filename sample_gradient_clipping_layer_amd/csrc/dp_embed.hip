@@ -18,7 +18,7 @@
 // launches: the order 26 (four launches), the norm 34 (three), the factors 2,
 // the sum 60 (two; 257 MB of it are the table, written at 5 TB/s). (Whole calls
 // in a loop. A kernel trace, which adds about a microsecond to every launch,
-// sums up to 133.) What is not the table's is latency: chains of a place, its
+// sums up to some 134.) What is not the table's is latency: chains of a place, its
 // row, its run's end. Noise adds 70 us of fp32 work (as much as the noise kernel
 // takes for as many elements).
 //

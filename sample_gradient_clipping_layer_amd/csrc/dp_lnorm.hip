@@ -6,12 +6,12 @@
 //              gain_rows[b] = sum_t dy[b][t] * u[b][t],  bias_rows[b] = sum_t dy[b][t]
 //
 // Bound by HBM: 32 x 1024 rows of 1280 bf16 with a residual take 58 us forward
-// (336 MB, 5.8 TB/s), 69 + 5 back with both gradients (the rows of 252 MB read
-// and 84 written at 4.9 TB/s, then the workgroups' sums). A row is held in the
+// (336 MB, 5.8 TB/s), 72 + 5 back with both gradients (the rows of 252 MB read
+// and 84 written at 4.8 TB/s, then the workgroups' sums). A row is held in the
 // registers of one, four, eight or sixteen waves, so one pass over memory
-// serves both its statistics and its outputs. The variance is that
-// of the centred row, whose own mean (the rounding of the first one) is taken
-// off again: rows far from zero lose nothing to a difference of large sums.
+// serves both its statistics and its outputs. The variance is that of the
+// centred row, whose own mean (the rounding of the first one) is taken off
+// again: rows far from zero lose nothing to a difference of large sums.
 // That mean and the mean square are quotients, not products with 1/d alone: in
 // a row of one value every column is off by the same few steps of it, sums and
 // quotients of those are exact, and the deviation is 0 whatever the value's
